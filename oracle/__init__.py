@@ -11,7 +11,9 @@ never calls it; the product path never calls this package.
 ``oracle.backoff`` is the per-lane miss back-off of a drafter,
 ``oracle.ngram`` the copy-from-the-conversation drafter and
 ``oracle.penalties`` the per-row presence / frequency penalties; all are plain
-Python restatements of the pages' rules.
+Python restatements of the pages' rules.  ``oracle.linear`` is linear attention
+with decay and ``oracle.logprobs`` the log probabilities of given tokens, both
+from their formulas.
 
 Every function is pinned by ``-m "not gpu"`` tests against facts fixed outside
 the oracle itself: the pages' worked examples, exact enumeration of the
@@ -19,7 +21,7 @@ acceptance rule on tiny vocabularies, a closed form, library routines (numpy's
 Philox4x64, scipy's softmax / logsumexp) and invariants.
 """
 
-from . import backoff, metrics, ngram, penalties
+from . import backoff, linear, logprobs, metrics, ngram, penalties
 from .philox import philox4x64_10, round_uniforms, word_to_uniform
 from .verify import (
     DEFAULT_ROW_BUDGET,

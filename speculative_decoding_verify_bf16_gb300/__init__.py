@@ -23,7 +23,8 @@ __all__ = [
     "spec_accept_counts_update", "spec_accept_rates_from_counts", "new_accept_counts", "accept_counts_view",
     "spec_backoff_step", "new_backoff_states", "BACKOFF_FIELDS", "ACCEPT_COUNT_WORDS",
     "spec_ngram_draft", "SPEC_NGRAM_MAX_MATCH", "spec_apply_penalties", "SPEC_VERIFY_META_BEFORE_WAIT",
-    "SPEC_VERIFY_TEST_WITHHOLD_COPY",
+    "SPEC_VERIFY_TEST_WITHHOLD_COPY", "spec_token_logprobs", "SPEC_LOGPROBS_MAX_TOP", "spec_linear_prefill",
+    "spec_linear_verify", "spec_linear_workspace", "new_linear_workspace", "SPEC_LINEAR_MAX_DIM",
 ]
 
 SPEC_OK = 0
@@ -90,6 +91,27 @@ class _AcceptRates(ctypes.Structure):
                 ("depth", ctypes.c_int32), ("reserved", ctypes.c_int32), ("implied_alpha", ctypes.c_double)]
 
 
+class _LogprobsArgs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int), ("ld", ctypes.c_int64), ("V", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("tokens", ctypes.c_void_p), ("temperatures", ctypes.c_void_p),
+                ("logprobs", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("top", ctypes.c_int32),
+                ("top_ids", ctypes.c_void_p), ("top_logprobs", ctypes.c_void_p), ("row_status", ctypes.c_void_p)]
+
+
+class _LinearArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "out")] + \
+        [(f"{n}_{s}_stride", ctypes.c_int64) for n in ("q", "k", "v", "out") for s in ("row", "head")] + \
+        [("log_decay", ctypes.c_void_p), ("decay_row_stride", ctypes.c_int64), ("decay_head_stride", ctypes.c_int64),
+         ("row_offsets", ctypes.c_void_p),
+         ("state_in", ctypes.c_void_p), ("state_in_lane_stride", ctypes.c_int64), ("state_in_head_stride", ctypes.c_int64),
+         ("state_out", ctypes.c_void_p), ("state_out_lane_stride", ctypes.c_int64),
+         ("state_out_col_stride", ctypes.c_int64), ("state_out_head_stride", ctypes.c_int64),
+         ("lane_status", ctypes.c_void_p), ("dtype", ctypes.c_int), ("lanes", ctypes.c_int32), ("rows", ctypes.c_int32),
+         ("max_len", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("v_heads", ctypes.c_int32), ("dk", ctypes.c_int32),
+         ("dv", ctypes.c_int32), ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+         ("workspace_bytes", ctypes.c_uint64)]
+
+
 ACCEPT_COUNT_WORDS = 3 + 2 * SPEC_MAX_DRAFTS
 BACKOFF_FIELDS = ("misses", "backoff", "wait", "reserved")
 
@@ -136,6 +158,13 @@ def load_library():
     lib.spec_backoff_step.restype = ctypes.c_int
     lib.spec_backoff_step.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]
+    lib.spec_token_logprobs.restype = ctypes.c_int
+    lib.spec_token_logprobs.argtypes = [ctypes.POINTER(_LogprobsArgs), ctypes.c_void_p]
+    lib.spec_linear_workspace.restype = ctypes.c_uint64
+    lib.spec_linear_workspace.argtypes = [ctypes.c_int32] * 5
+    for f in (lib.spec_linear_prefill, lib.spec_linear_verify):
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.POINTER(_LinearArgs), ctypes.c_void_p]
     _lib = lib
     return lib
 
@@ -463,3 +492,178 @@ def spec_apply_penalties(target, row_offsets, draft_tokens, draft_lens, pen_toke
                                   _ptr(lane_status), _stream(stream))
     if rc != SPEC_OK:
         raise SpecError(rc, "spec_apply_penalties")
+
+
+# ---------------------------------------------------------------------------
+# Log probabilities of given tokens (include/spec_logprobs.h)
+# ---------------------------------------------------------------------------
+SPEC_LOGPROBS_MAX_TOP = 20
+
+
+def spec_token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, top_logprobs=None, temperatures=None,
+                        row_status=None, rows=None, stream=None):
+    """Log probability of each row's token (see spec_token_logprobs in
+    include/spec_logprobs.h).
+
+    logits: [rows, V] bf16 or float32 CUDA tensor with unit inner stride; tokens
+    int32 [rows] (negative: the row is not asked for); logprobs, entropy
+    float32 [rows]; top_ids int32 and top_logprobs float32 [rows, n], n <=
+    SPEC_LOGPROBS_MAX_TOP; temperatures float32 [rows] (<= 0: unscaled);
+    row_status int32 [rows].  ``rows`` defaults to logits.shape[0].
+    """
+    lib = load_library()
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1) or logits.dtype not in _DTYPES:
+        raise ValueError("logits must be a 2-D bf16/float32 tensor with unit inner stride")
+    dev = logits.device
+    if dev.type != "cuda":
+        raise ValueError("logits must be on a CUDA device")
+    n = logits.shape[0] if rows is None else int(rows)
+    if n > logits.shape[0]:
+        raise ValueError("rows exceeds the rows of logits")
+    _need(tokens, "tokens", torch.int32, dev, n)
+    _need(logprobs, "logprobs", torch.float32, dev, n)
+    for t, name, dtype in ((entropy, "entropy", torch.float32), (temperatures, "temperatures", torch.float32),
+                           (row_status, "row_status", torch.int32)):
+        if t is not None:
+            _need(t, name, dtype, dev, n)
+    top = 0
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs go together")
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape != top_logprobs.shape:
+            raise ValueError("top_ids and top_logprobs must be [rows, n]")
+        top = top_ids.shape[1]
+        _need(top_ids, "top_ids", torch.int32, dev, n * top)
+        _need(top_logprobs, "top_logprobs", torch.float32, dev, n * top)
+    ld = logits.stride(0) if logits.shape[0] > 1 else max(logits.stride(0), logits.shape[1])
+    a = _LogprobsArgs(logits=logits.data_ptr(), dtype=_DTYPES[logits.dtype], ld=ld, V=logits.shape[1], rows=n,
+                      tokens=tokens.data_ptr(), temperatures=None if temperatures is None else temperatures.data_ptr(),
+                      logprobs=logprobs.data_ptr(), entropy=None if entropy is None else entropy.data_ptr(), top=top,
+                      top_ids=None if top == 0 else top_ids.data_ptr(),
+                      top_logprobs=None if top == 0 else top_logprobs.data_ptr(),
+                      row_status=None if row_status is None else row_status.data_ptr())
+    rc = lib.spec_token_logprobs(ctypes.byref(a), _stream(stream))
+    if rc != SPEC_OK:
+        raise SpecError(rc, "spec_token_logprobs")
+
+
+# ---------------------------------------------------------------------------
+# Linear attention with decay (include/spec_linear.h)
+# ---------------------------------------------------------------------------
+SPEC_LINEAR_MAX_DIM = 256
+
+
+def spec_linear_workspace(lanes, v_heads, dk, dv, max_len):
+    """Bytes of scratch memory spec_linear_prefill wants for these sizes."""
+    return int(load_library().spec_linear_workspace(int(lanes), int(v_heads), int(dk), int(dv), int(max_len)))
+
+
+def new_linear_workspace(lanes, v_heads, dk, dv, max_len, device):
+    """A uint8 scratch buffer for spec_linear_prefill (kept by the caller; calls that
+    may run at the same time need one each)."""
+    return torch.empty(spec_linear_workspace(lanes, v_heads, dk, dv, max_len), dtype=torch.uint8, device=device)
+
+
+def _activations(t, name, dtype, device, rows):
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
+    if t.dim() != 3 or t.shape[0] != rows or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name} must be [rows, heads, size] with unit inner stride")
+
+
+def _states(t, name, device, shape):
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32:
+        raise ValueError(f"{name} must be a float32 tensor on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}")
+    # (a size of one leaves its stride free, but the kernels read [dk][dv] rows)
+    if (t.stride(-1) != 1 and shape[-1] > 1) or (t.stride(-2) != shape[-1] and shape[-2] > 1):
+        raise ValueError(f"{name}'s last two dimensions must be contiguous")
+
+
+def _linear_args(q, k, v, log_decay, row_offsets, out, max_len, scale, lane_status):
+    dev, rows = q.device, q.shape[0]
+    if dev.type != "cuda" or q.dtype not in _DTYPES:
+        raise ValueError("q must be a bf16/float32 tensor on a CUDA device")
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+        _activations(t, name, q.dtype, dev, rows)
+    if k.shape != q.shape or out.shape != v.shape:
+        raise ValueError("k must have q's shape, and out v's")
+    hk, dk, hv, dv = q.shape[1], q.shape[2], v.shape[1], v.shape[2]
+    if hk == 0 or hv % hk:
+        raise ValueError("v's heads must be a multiple of q's and k's")
+    if not isinstance(log_decay, torch.Tensor) or log_decay.device != dev or log_decay.dtype != torch.float32 \
+            or tuple(log_decay.shape) != (rows, hv):
+        raise ValueError("log_decay must be a float32 [rows, v_heads] tensor (expanded strides allowed)")
+    _need(row_offsets, "row_offsets", torch.int32, dev, 1)
+    lanes = row_offsets.numel() - 1
+    if lane_status is not None:
+        _need(lane_status, "lane_status", torch.int32, dev, lanes)
+    return _LinearArgs(
+        q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), out=out.data_ptr(),
+        q_row_stride=q.stride(0), q_head_stride=q.stride(1), k_row_stride=k.stride(0), k_head_stride=k.stride(1),
+        v_row_stride=v.stride(0), v_head_stride=v.stride(1), out_row_stride=out.stride(0),
+        out_head_stride=out.stride(1), log_decay=log_decay.data_ptr(), decay_row_stride=log_decay.stride(0),
+        decay_head_stride=log_decay.stride(1), row_offsets=row_offsets.data_ptr(),
+        lane_status=None if lane_status is None else lane_status.data_ptr(), dtype=_DTYPES[q.dtype], lanes=lanes,
+        rows=rows, max_len=int(max_len), k_heads=hk, v_heads=hv, dk=dk, dv=dv,
+        scale=dk ** -0.5 if scale is None else float(scale))
+
+
+def spec_linear_prefill(q, k, v, log_decay, row_offsets, state_in, out, state_out, max_len, scale=None,
+                        lane_status=None, workspace=None, stream=None):
+    """Linear attention with decay over whole prompts (see spec_linear_prefill in
+    include/spec_linear.h).
+
+    q, k: [rows, k_heads, dk], v, out: [rows, v_heads, dv] of one dtype (bf16 or
+    float32), lanes packed one after the other; log_decay: float32 [rows,
+    v_heads] (``decay.expand(rows, -1)`` for one decay a head); row_offsets
+    int32 [lanes + 1]; state_in (None: zeros) and state_out (None: not wanted;
+    may be state_in) float32 [lanes, v_heads, dk, dv]; max_len: an upper bound
+    of the lanes' lengths.  ``scale`` defaults to dk ** -0.5.  lane_status
+    int32 [lanes] is read and updated: fill it with zeros before the first
+    call.  ``workspace`` comes from new_linear_workspace; without one the call
+    takes scratch memory from PyTorch's allocator on the current stream.
+    """
+    lib = load_library()
+    a = _linear_args(q, k, v, log_decay, row_offsets, out, max_len, scale, lane_status)
+    shape = (a.lanes, a.v_heads, a.dk, a.dv)
+    if state_in is not None:
+        _states(state_in, "state_in", q.device, shape)
+        a.state_in, a.state_in_lane_stride, a.state_in_head_stride = state_in.data_ptr(), *state_in.stride()[:2]
+    if state_out is not None:
+        _states(state_out, "state_out", q.device, shape)
+        a.state_out, a.state_out_lane_stride, a.state_out_head_stride = state_out.data_ptr(), *state_out.stride()[:2]
+    if workspace is None:
+        workspace = new_linear_workspace(a.lanes, a.v_heads, a.dk, a.dv, a.max_len, q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    _need(workspace, "workspace", torch.uint8, q.device)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    rc = lib.spec_linear_prefill(ctypes.byref(a), _stream(stream))
+    if rc != SPEC_OK:
+        raise SpecError(rc, "spec_linear_prefill")
+
+
+def spec_linear_verify(q, k, v, log_decay, row_offsets, live, staged, out, scale=None, lane_status=None, stream=None):
+    """Linear attention with decay over a round's columns (see spec_linear_verify in
+    include/spec_linear.h): reads ``live`` [lanes, v_heads, dk, dv] (None:
+    zeros) and writes the state after column c of lane b to ``staged[b, c]``
+    ([lanes, cols, v_heads, dk, dv]), from which spec_commit_state rolls.  For
+    single-token decoding ``staged`` may be ``live.unsqueeze(1)``.  The other
+    arguments are those of spec_linear_prefill.
+    """
+    lib = load_library()
+    if not isinstance(staged, torch.Tensor) or staged.dim() != 5:
+        raise ValueError("staged must be a [lanes, cols, v_heads, dk, dv] tensor")
+    a = _linear_args(q, k, v, log_decay, row_offsets, out, staged.shape[1], scale, lane_status)
+    shape = (a.lanes, a.v_heads, a.dk, a.dv)
+    if live is not None:
+        _states(live, "live", q.device, shape)
+        a.state_in, a.state_in_lane_stride, a.state_in_head_stride = live.data_ptr(), *live.stride()[:2]
+    _states(staged, "staged", q.device, (a.lanes, staged.shape[1], *shape[1:]))
+    a.state_out = staged.data_ptr()
+    a.state_out_lane_stride, a.state_out_col_stride, a.state_out_head_stride = staged.stride()[:3]
+    rc = lib.spec_linear_verify(ctypes.byref(a), _stream(stream))
+    if rc != SPEC_OK:
+        raise SpecError(rc, "spec_linear_verify")
