@@ -1,9 +1,12 @@
 // linear.cu -- host side of include/spec_linear.h: argument checks, the choice of
 // kernel and the launches.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
+#include "linear_chunk.cuh"
 #include "linear_params.h"
 #include "linear_recurrent.cuh"
 
@@ -87,6 +90,25 @@ void* recurrent_kernel_for(int dk) {
   return reinterpret_cast<void*>(&specv::linear_recurrent_kernel<T, 16, STAGED>);
 }
 
+constexpr int kMaxDevices = 64;
+std::mutex g_mutex;
+struct DeviceCache {
+  int sms = 0;
+  bool chunk_attr = false;
+};
+DeviceCache g_cache[kMaxDevices];
+
+int device_cache(DeviceCache** out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SPEC_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceCache& c = g_cache[dev];
+  if (c.sms == 0 && cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  *out = &c;
+  return SPEC_OK;
+}
+
 int launch(void* kernel, unsigned grid, unsigned block, size_t smem, void** args, void* stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
@@ -116,18 +138,128 @@ int launch_recurrent(const LinearParams& p, spec_dtype dtype, bool staged, void*
   return launch(kernel, grid, specv::kRecThreads, 0, args, stream);
 }
 
+// ---------------------------------------------------------------------------
+// Chunked prefill
+// ---------------------------------------------------------------------------
+constexpr int kChunkMinLen = 32;  // shorter prompts run token after token
+
+// Segments a lane's chunks are split into: with fewer (lane, head) pairs than half the
+// SMs, enough for all of them, of four chunks at least (a split lane's k and v are read
+// twice).
+int prefill_segments(int64_t pairs, int max_len, int sms) {
+  const int64_t chunks = (static_cast<int64_t>(max_len) + specv::kChunk - 1) / specv::kChunk;
+  if (pairs <= 0 || 2 * pairs > sms) return 1;
+  const int64_t want = sms / pairs, most = chunks / 4;
+  const int64_t n = want < most ? want : most;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+uint64_t segment_bytes(int segments, int64_t pairs) {
+  if (segments <= 1) return 0;
+  return static_cast<uint64_t>(segments) * pairs * (128 * 128 + 4) * sizeof(float);
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return f;
+}
+
+// Whether a tensor map can describe bf16 activations with these strides.
+bool mappable(const void* base, int64_t row_stride, int64_t head_stride, int heads) {
+  if (!aligned16(base) || row_stride % 8 != 0 || row_stride <= 0 || row_stride >= (int64_t{1} << 38)) return false;
+  return heads == 1 || (head_stride % 8 == 0 && head_stride > 0 && head_stride < (int64_t{1} << 38));
+}
+
+// [rows][heads][128] bf16, copied in boxes of 128 rows of 64 elements of one head.
+bool make_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int64_t row_stride, int64_t head_stride) {
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads == 1 ? 128 : head_stride) * 2,
+                                 static_cast<cuuint64_t>(row_stride) * 2};
+  const cuuint32_t box[3] = {64, 1, specv::kChunk}, step[3] = {1, 1, 1};
+  return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool chunkable(const LinearParams& p, spec_dtype dtype) {
+  const int k_heads = p.v_heads / p.group;
+  return dtype == SPEC_BF16 && p.dk == 128 && p.dv == 128 && p.rows > 0 && p.max_len >= kChunkMinLen &&
+         mappable(p.q, p.q_row, p.q_head, k_heads) && mappable(p.k, p.k_row, p.k_head, k_heads) &&
+         mappable(p.v, p.v_row, p.v_head, p.v_heads) && encode_tiled() != nullptr;
+}
+
+int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args* a, void* stream) {
+  const int64_t pairs = static_cast<int64_t>(p.lanes) * p.v_heads;
+  void* const states = reinterpret_cast<void*>(&specv::linear_chunk_kernel<true>);
+  void* const full = reinterpret_cast<void*>(&specv::linear_chunk_kernel<false>);
+  const int smem = static_cast<int>(sizeof(specv::ChunkSmem));
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!dc->chunk_attr) {
+      for (void* k : {states, full})
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+          cudaGetLastError();
+          return SPEC_ERR_CUDA;
+        }
+      dc->chunk_attr = true;
+    }
+  }
+  specv::ChunkParams cp{};
+  cp.p = p;
+  cp.segments = prefill_segments(pairs, p.max_len, dc->sms);
+  const uint64_t need = segment_bytes(cp.segments, pairs);
+  if (need > 0 && (a->workspace == nullptr || !aligned16(a->workspace) || a->workspace_bytes < need))
+    return SPEC_ERR_INVALID_ARG;
+  cp.local = static_cast<float*>(a->workspace);
+  cp.local_decay = cp.local + static_cast<int64_t>(cp.segments) * pairs * (128 * 128);
+  cp.out_vec = aligned16(p.out) && p.out_row % 8 == 0 && p.out_head % 8 == 0;
+  const int k_heads = p.v_heads / p.group;
+  CUtensorMap q, k, v;
+  if (!make_map(&q, p.q, p.rows, k_heads, p.q_row, p.q_head) || !make_map(&k, p.k, p.rows, k_heads, p.k_row, p.k_head) ||
+      !make_map(&v, p.v, p.rows, p.v_heads, p.v_row, p.v_head))
+    return SPEC_ERR_CUDA;
+  void* args[] = {&cp, &q, &k, &v};
+  if (cp.segments > 1) {
+    const int rc = launch(states, static_cast<unsigned>(pairs * (cp.segments - 1)), specv::kChunkThreads, smem, args, stream);
+    if (rc != SPEC_OK) return rc;
+  }
+  return launch(full, static_cast<unsigned>(pairs * cp.segments), specv::kChunkThreads, smem, args, stream);
+}
+
 }  // namespace
 
 extern "C" {
 
-uint64_t spec_linear_workspace(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+uint64_t spec_linear_workspace(int32_t lanes, int32_t v_heads, int32_t dk, int32_t dv, int32_t max_len) {
+  if (lanes <= 0 || v_heads <= 0 || dk != 128 || dv != 128 || max_len < kChunkMinLen) return 0;
+  DeviceCache* dc = nullptr;
+  if (device_cache(&dc) != SPEC_OK) return 0;
+  const int64_t pairs = static_cast<int64_t>(lanes) * v_heads;
+  return segment_bytes(prefill_segments(pairs, max_len, dc->sms), pairs);
+}
 
 int spec_linear_prefill(const spec_linear_args* a, void* stream) {
   LinearParams p{};
   bool empty = false;
   const int rc = check_args(a, &p, &empty);
   if (rc != SPEC_OK || empty) return rc;
-  return launch_recurrent(p, a->dtype, false, stream);
+  if (!chunkable(p, a->dtype)) return launch_recurrent(p, a->dtype, false, stream);
+  DeviceCache* dc = nullptr;
+  if (device_cache(&dc) != SPEC_OK) return SPEC_ERR_CUDA;
+  return launch_chunk(p, dc, a, stream);
 }
 
 int spec_linear_verify(const spec_linear_args* a, void* stream) {

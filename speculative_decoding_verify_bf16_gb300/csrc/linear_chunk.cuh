@@ -1,0 +1,632 @@
+// linear_chunk.cuh -- linear attention with decay over prompts, a chunk of 128 tokens at
+// a time on the tensor cores (bf16 activations, dk = dv = 128).
+//
+// With G_i the sum of the log decays of the chunk's tokens 0..i (base 2), S the state
+// before the chunk and all sums over the chunk's tokens:
+//
+//   o_i = scale * ( 2^G_i  S^T q_i  +  sum_{j <= i} 2^(G_i - G_j) (q_i . k_j) v_j )
+//   S'  = 2^G_last S + sum_j (2^(G_last - G_j) k_j) v_j^T
+//
+// One CTA walks the chunks of one (lane, head), or of a segment of them.  Its products:
+//
+//   QK  scores [token][token]  = q k^T
+//   QS  D [token][dv]          = q S,      D rows then times 2^G_i
+//   KV  S [dk][dv]            += k'^T v,   k' = 2^(G_last - G_j) k_j, S times 2^G_last before
+//   PV  D                     += P v,      P = weighted scores, 0 above the diagonal
+//
+// S stays in tensor memory in fp32 from the first chunk to the last.  Operands are bf16,
+// so fp32 numbers enter a product in parts: k' in three (all 24 bits, the state is as
+// exact as its fp32 sums), P and S in two (16 bits, far below the rounding of a bf16
+// output).  q, k and v are taken as they are.
+//
+// Tensor memory holds S (128 columns), scores and P (128; P overwrites the scores it came
+// from), D (128) and two buffers of k' for 32 tokens (96).  Shared memory holds a ring of
+// five 32 KB tiles (k, q, v of a chunk; 128-byte swizzled rows, so that a tile serves as
+// an operand along either dimension) and S in two parts.
+//
+// Warps: 0 copies tiles, 1 issues the products, 2 sums the decays, and four groups of
+// four do what lies between the products: scores to P (4-7), D (8-11), S (12-15), k'
+// (16-19).  The products of a chunk take 8 x 512 cycles on the tensor cores, its
+// 128 KB of q, k, v and o about 5,500 at an SM's share of the HBM rate: the groups work
+// beside each other so that the larger of the two counts.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "linear_params.h"
+#include "linear_recurrent.cuh"
+#include "tcgen05_ptx.cuh"
+
+namespace specv {
+
+constexpr int kChunk = 128;
+constexpr int kChunkThreads = 640;
+constexpr int kTile = 32 * 1024;      // 128 rows of 128 bf16: two halves of 64 columns
+constexpr int kHalf = kTile / 2;
+constexpr int kRing = 5;
+constexpr uint32_t kColS = 0, kColP = 128, kColD = 256, kColK = 384;  // columns of tensor memory
+constexpr uint32_t kColKBuf = 48;     // a k' buffer: three parts of 16 columns (32 tokens)
+constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;    // log2(e) in two parts
+// A decay of 2^-160 is 0 in fp32 against everything a state can hold; the clamp keeps
+// resets (-inf) and lowest values out of the sums.
+constexpr float kDecayFloor = -160.f;
+
+struct ChunkSmem {
+  uint8_t ring[kRing][kTile];
+  uint8_t s_hi[kTile];
+  uint8_t s_lo[kTile];
+  float g_hi[2][kChunk];  // G in two parts, chunk c in c % 2
+  float g_lo[2][kChunk];
+  uint64_t full[kRing], empty[kRing];
+  uint64_t g_full[2], g_empty[2];
+  uint64_t scores_full, p_ready, qs_full, d_scaled, o_full, d_free, s_ready, kv_full, v_clean, drain;
+  uint64_t kp_full[2], kp_empty[2];
+  uint32_t tmem;
+  int abort;
+  int status;             // the lane's status on entry
+};
+
+struct ChunkParams {
+  LinearParams p;
+  float* local;       // [segments][lanes][heads][128][128]: 0, the lanes' states before the
+                      // call; r + 1, the state after segment r begun from zero
+  float* local_decay; // [segments][lanes][heads]: whole decay of segment r
+  int32_t segments;
+  int32_t out_vec;    // out rows take 16-byte stores
+};
+
+// Waits for a phase; gives up after the time limit or when another warp has.
+__device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 31u) == 0) {
+      if (*static_cast<volatile int*>(abort)) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        *static_cast<volatile int*>(abort) = 1;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
+  return __all_sync(0xFFFFFFFFu, chunk_wait(bar, parity, abort));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// The upper halves of two fp32 numbers: their bf16 parts by truncation.
+__device__ __forceinline__ uint32_t pack_hi(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float rest(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_rn(float a, float b) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
+
+// Byte offset of 16-byte unit u (of 16) of row r in a tile.
+__device__ __forceinline__ uint32_t tile_unit(uint32_t r, uint32_t u) {
+  return (u >> 3) * kHalf + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+}
+
+// The chunks of a segment, and where they lie.
+struct Segment {
+  int b, h, seg, first, count;  // lane, head, segment, first row and rows of the lane
+  int c0, c1;                   // chunks of the lane
+  bool last;                    // the lane's last segment with rows
+};
+
+// STATES: only the states of all segments but the last, begun from zero (the first of
+// two launches when a lane is split); otherwise outputs and final states.
+template <bool STATES>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    linear_chunk_kernel(const ChunkParams cp, const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>(smem_raw);
+  const LinearParams& p = cp.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Segment sg;
+  sg.h = blockIdx.x % p.v_heads;
+  sg.b = blockIdx.x / p.v_heads % p.lanes;
+  sg.seg = blockIdx.x / p.v_heads / p.lanes;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 5);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.g_full[i], 1);
+      mbar_init(&sm.g_empty[i], STATES ? 8 : 16);
+      mbar_init(&sm.kp_full[i], 4);
+      mbar_init(&sm.kp_empty[i], 1);
+    }
+    mbar_init(&sm.scores_full, 1);
+    mbar_init(&sm.p_ready, 4);
+    mbar_init(&sm.qs_full, 1);
+    mbar_init(&sm.d_scaled, 4);
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.d_free, 4);
+    mbar_init(&sm.s_ready, 4);
+    mbar_init(&sm.kv_full, 1);
+    mbar_init(&sm.v_clean, 4);
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&map_q);
+    tma_prefetch_map(&map_k);
+    tma_prefetch_map(&map_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  // Read once: another head's CTA may write it meanwhile, and all warps must agree.
+  if (threadIdx.x == 0) sm.status = p.lane_status == nullptr ? SPEC_OK : p.lane_status[sg.b];
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = sm.tmem;
+
+  const int rc = linear_lane_rows(p, sg.b, sg.first, sg.count);
+  const bool skip = rc != SPEC_OK || sm.status != SPEC_OK;
+  const int chunks = (sg.count + kChunk - 1) / kChunk;
+  const int per = (chunks + cp.segments - 1) / cp.segments;
+  sg.c0 = min(chunks, sg.seg * per);
+  sg.c1 = min(chunks, sg.c0 + per);
+  sg.last = sg.c1 == chunks && (sg.c0 < chunks || sg.seg == 0);
+  const bool active = !skip && sg.c0 < sg.c1 && !(STATES && sg.last);
+  if (rc != SPEC_OK && threadIdx.x == 0 && p.lane_status != nullptr && sm.status == SPEC_OK) p.lane_status[sg.b] = rc;
+  const int64_t head = static_cast<int64_t>(sg.b) * p.v_heads + sg.h;
+  const int64_t heads = static_cast<int64_t>(p.lanes) * p.v_heads;
+  const float* state_in =
+      p.state_in == nullptr ? nullptr : p.state_in + sg.b * p.state_in_lane + sg.h * p.state_in_head;
+  float* state_out =
+      p.state_out == nullptr ? nullptr : p.state_out + sg.b * p.state_out_lane + sg.h * p.state_out_head;
+
+  if (!STATES && !skip && chunks == 0 && sg.seg == 0 && state_out != nullptr) {  // an empty lane's state passes through
+    for (int i = threadIdx.x; i < 128 * 128 / 4; i += kChunkThreads)
+      reinterpret_cast<float4*>(state_out)[i] =
+          state_in == nullptr ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(state_in)[i];
+  }
+
+  // The last segment writes the final state while others may yet begin, and the two may
+  // be one buffer: with segments the first launch keeps a copy of the initial state.
+  if (STATES && !skip && sg.seg == 0 && state_in != nullptr) {
+    for (int i = threadIdx.x; i < 128 * 128 / 4; i += kChunkThreads)
+      reinterpret_cast<float4*>(cp.local + head * (128 * 128))[i] = reinterpret_cast<const float4*>(state_in)[i];
+  }
+
+  const uint32_t quarter = static_cast<uint32_t>(warp & 3) * 32;  // this warp's lanes of tensor memory
+  const uint32_t row = quarter + lane;
+  const uint32_t tmq = tm + (quarter << 16);
+  const int n_chunks = active ? sg.c1 - sg.c0 : 0;
+  constexpr int kLoads = STATES ? 2 : 3;  // tiles of a chunk: k, (q,) v
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ copies
+    if (lane == 0) {
+      int issued = 0;
+      bool ok = true;
+      for (int c = 0; c < n_chunks && ok; ++c) {
+        const int z = sg.first + (sg.c0 + c) * kChunk;
+        for (int j = 0; j < kLoads; ++j) {
+          const int slot = issued % kRing, turn = issued / kRing;
+          if (turn > 0 && !chunk_wait(&sm.empty[slot], (turn - 1) & 1, &sm.abort)) {
+            ok = false;
+            break;
+          }
+          const CUtensorMap* map = j == 0 ? &map_k : (j == kLoads - 1 ? &map_v : &map_q);
+          const int hh = j == kLoads - 1 ? sg.h : sg.h / p.group;
+          mbar_arrive_expect_tx(&sm.full[slot], kTile);
+          tma_load_3d(sm.ring[slot], map, 0, hh, z, &sm.full[slot]);
+          tma_load_3d(sm.ring[slot] + kHalf, map, 64, hh, z, &sm.full[slot]);
+          ++issued;
+        }
+      }
+      // Every copy lands before the CTA ends (also when a wait gave up).
+      for (int i = max(0, issued - kRing); i < issued; ++i)
+        mbar_wait_bounded(&sm.full[i % kRing], (i / kRing) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t kSame = mma_desc(128, 128, false), kRows = mma_desc(128, 128, true);
+      int step = 0;  // k' buffers used
+      for (int c = 0; c < n_chunks; ++c) {
+        const uint32_t ph = c & 1;
+        const int n = min(kChunk, sg.count - (sg.c0 + c) * kChunk);
+        const int steps = (n + 15) / 16;  // products over the chunk's tokens stop at its last
+        const int lk = kLoads * c, lq = lk + 1, lv = lk + kLoads - 1;
+        uint64_t* const fk = &sm.full[lk % kRing];
+        uint64_t* const fv = &sm.full[lv % kRing];
+        const uint32_t ak = smem_addr(sm.ring[lk % kRing]);
+        const uint32_t av = smem_addr(sm.ring[lv % kRing]);
+        if (!chunk_wait(fk, (lk / kRing) & 1, &sm.abort)) break;
+        if (!STATES) {
+          const uint32_t aq = smem_addr(sm.ring[lq % kRing]);
+          if (!chunk_wait(&sm.full[lq % kRing], (lq / kRing) & 1, &sm.abort)) break;
+          tc_fence_after();
+          for (int s = 0; s < 8; ++s) {
+            const uint32_t off = (s >> 2) * kHalf + (s & 3) * 32;
+            mma_ss(tm + kColP, smem_desc(aq + off, 16, 1024), smem_desc(ak + off, 16, 1024), kSame, s > 0);
+          }
+          mma_commit(&sm.scores_full);
+          mma_commit(&sm.empty[lk % kRing]);
+          if (!chunk_wait(&sm.s_ready, ph, &sm.abort)) break;
+          if (c > 0 && !chunk_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
+          tc_fence_after();
+          const uint32_t ahi = smem_addr(sm.s_hi), alo = smem_addr(sm.s_lo);
+          for (int s = 0; s < 16; ++s) {
+            const uint32_t off = ((s & 7) >> 2) * kHalf + (s & 3) * 32;
+            const uint32_t b = (s < 8 ? alo : ahi) + (s & 7) * 2048;
+            mma_ss(tm + kColD, smem_desc(aq + off, 16, 1024), smem_desc(b, kHalf, 1024), kRows, s > 0);
+          }
+          mma_commit(&sm.qs_full);
+          mma_commit(&sm.empty[lq % kRing]);
+          mbar_arrive_n(&sm.empty[lq % kRing], 4);
+        } else {
+          mbar_arrive(&sm.empty[lk % kRing]);
+          if (!chunk_wait(&sm.s_ready, ph, &sm.abort)) break;
+        }
+        if (!chunk_wait(fv, (lv / kRing) & 1, &sm.abort)) break;
+        if (n < kChunk && !chunk_wait(&sm.v_clean, 0, &sm.abort)) break;
+        bool ok = true;
+        for (int t = 0; t < steps; t += 2, ++step) {
+          const int buf = step & 1;
+          if (!(ok = chunk_wait(&sm.kp_full[buf], (step >> 1) & 1, &sm.abort))) break;
+          tc_fence_after();
+          for (int part = 2; part >= 0; --part)
+            for (int s = t; s < min(t + 2, steps); ++s)
+              mma_ts(tm + kColS, tm + kColK + buf * kColKBuf + part * 16 + (s - t) * 8, smem_desc(av + s * 2048, kHalf, 1024),
+                     kRows, true);
+          mma_commit(&sm.kp_empty[buf]);
+        }
+        if (!ok) break;
+        mma_commit(&sm.kv_full);
+        if (!STATES) {
+          if (!chunk_wait(&sm.p_ready, ph, &sm.abort) || !chunk_wait(&sm.d_scaled, ph, &sm.abort)) break;
+          tc_fence_after();
+          for (int part = 1; part >= 0; --part)
+            for (int s = 0; s < steps; ++s)
+              mma_ts(tm + kColD, tm + kColP + (s >> 1) * 32 + part * 16 + (s & 1) * 8, smem_desc(av + s * 2048, kHalf, 1024),
+                     kRows, true);
+          mma_commit(&sm.o_full);
+        }
+        mma_commit(&sm.empty[lv % kRing]);
+        mbar_arrive_n(&sm.empty[lv % kRing], 4);
+      }
+      // Tensor memory is given back only after the last product.
+      mma_commit(&sm.drain);
+      mbar_wait_bounded(&sm.drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ decays
+    // Fixed point with 32 fractional bits: sums and differences are exact, whatever
+    // large decays stand between two tokens.
+    float g[4];
+    auto fetch = [&](int c) {
+      for (int i = 0; i < 4; ++i) {
+        const int t = (sg.c0 + c) * kChunk + lane * 4 + i;
+        g[i] = t < sg.count ? __ldg(p.log_decay + (sg.first + static_cast<int64_t>(t)) * p.decay_row + sg.h * p.decay_head)
+                            : 0.f;
+      }
+    };
+    if (n_chunks > 0) fetch(0);
+    for (int c = 0; c < n_chunks; ++c) {
+      const int buf = c & 1;
+      long long sum[4];
+      bool bad = false;
+      for (int i = 0; i < 4; ++i) {
+        float hi = g[i] * kLog2eHi;
+        float lo = fmaf(g[i], kLog2eHi, -hi) + g[i] * kLog2eLo;
+        if (!(hi < 128.f)) bad = true;  // NaN, or a decay whose factor is infinite in fp32
+        if (!(hi > kDecayFloor)) {
+          hi = kDecayFloor;
+          lo = 0.f;
+        }
+        sum[i] = bad ? 0 : __float2ll_rn(hi * 4294967296.f) + __float2ll_rn(lo * 4294967296.f);
+        if (i > 0) sum[i] += sum[i - 1];
+      }
+      bad = __any_sync(0xFFFFFFFFu, bad);
+      long long run = sum[3];
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long up = __shfl_up_sync(0xFFFFFFFFu, run, d);
+        if (lane >= d) run += up;
+      }
+      run -= sum[3];
+      if (c + 1 < n_chunks) fetch(c + 1);
+      if (c >= 2 && !warp_wait(&sm.g_empty[buf], ((c >> 1) - 1) & 1, &sm.abort)) break;
+      for (int i = 0; i < 4; ++i) {
+        const float hi = __ll2float_rn(run + sum[i]);
+        const float lo = __ll2float_rn(run + sum[i] - __float2ll_rn(hi));
+        sm.g_hi[buf][lane * 4 + i] = bad ? __uint_as_float(0x7FC00000u) : hi * 0x1p-32f;
+        sm.g_lo[buf][lane * 4 + i] = lo * 0x1p-32f;
+      }
+      __threadfence_block();
+      warp_arrive(&sm.g_full[buf]);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------- scores to P
+    if (!STATES) {
+      for (int c = 0; c < n_chunks; ++c) {
+        const int buf = c & 1;
+        if (!warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort)) break;
+        const float ghi = sm.g_hi[buf][row], glo = sm.g_lo[buf][row];
+        if (!warp_wait(&sm.scores_full, c & 1, &sm.abort)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int piece = 0; piece < 4; ++piece) {
+          uint32_t hi[16], lo[16];
+          if (piece * 32 > static_cast<int>(quarter)) {  // tokens after all of this warp's rows
+#pragma unroll
+            for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0u;
+          } else {
+            uint32_t s[32];
+            tmem_ld32(s, tmq + kColP + piece * 32);
+            tmem_wait_ld();
+            const bool diagonal = piece * 32 == static_cast<int>(quarter);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 jh = *reinterpret_cast<const float4*>(&sm.g_hi[buf][piece * 32 + i]);
+              const float4 jl = *reinterpret_cast<const float4*>(&sm.g_lo[buf][piece * 32 + i]);
+              float w[4] = {(ghi - jh.x) + (glo - jl.x), (ghi - jh.y) + (glo - jl.y), (ghi - jh.z) + (glo - jl.z),
+                            (ghi - jh.w) + (glo - jl.w)};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                w[e] = ex2_approx(w[e]) * __uint_as_float(s[i + e]);
+                if (diagonal && i + e > lane) w[e] = 0.f;  // (a select: what is masked may be NaN)
+              }
+              hi[i / 2] = pack_hi(w[0], w[1]);
+              hi[i / 2 + 1] = pack_hi(w[2], w[3]);
+              lo[i / 2] = pack_rn(rest(w[0]), rest(w[1]));
+              lo[i / 2 + 1] = pack_rn(rest(w[2]), rest(w[3]));
+            }
+          }
+          tmem_st16(tmq + kColP + piece * 32, hi);
+          tmem_st16(tmq + kColP + piece * 32 + 16, lo);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&sm.p_ready);
+        warp_arrive(&sm.g_empty[buf]);
+      }
+    }
+  } else if (warp >= 8 && warp < 12) {
+    // ----------------------------------------------------------------- outputs
+    if (!STATES) {
+      for (int c = 0; c < n_chunks; ++c) {
+        const int buf = c & 1;
+        if (!warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort)) break;
+        const float e = exp2f(sm.g_hi[buf][row] + sm.g_lo[buf][row]);
+        warp_arrive(&sm.g_empty[buf]);
+        if (!warp_wait(&sm.qs_full, c & 1, &sm.abort)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int piece = 0; piece < 4; ++piece) {
+          uint32_t d[32];
+          tmem_ld32(d, tmq + kColD + piece * 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) d[i] = __float_as_uint(__uint_as_float(d[i]) * e);
+          tmem_st32(tmq + kColD + piece * 32, d);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&sm.d_scaled);
+        if (!warp_wait(&sm.o_full, c & 1, &sm.abort)) break;
+        tc_fence_after();
+        const int t = (sg.c0 + c) * kChunk + static_cast<int>(row);
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                             (sg.first + static_cast<int64_t>(t)) * p.out_row + sg.h * p.out_head;
+#pragma unroll 1
+        for (int piece = 0; piece < 4; ++piece) {
+          uint32_t d[32];
+          tmem_ld32(d, tmq + kColD + piece * 32);
+          tmem_wait_ld();
+          if (t < sg.count) {
+            uint32_t o[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[i] = pack_rn(p.scale * __uint_as_float(d[2 * i]), p.scale * __uint_as_float(d[2 * i + 1]));
+            if (cp.out_vec) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(dst + piece * 32 + i * 8) =
+                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                dst[piece * 32 + 2 * i] = __ushort_as_bfloat16(static_cast<unsigned short>(o[i]));
+                dst[piece * 32 + 2 * i + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(o[i] >> 16));
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        warp_arrive(&sm.d_free);
+      }
+    }
+  } else if (warp >= 12 && warp < 16) {
+    // ------------------------------------------------------------------ states
+    bool ok = true;
+    float total = 1.f;  // the segment's whole decay
+    for (int c = 0; c < n_chunks; ++c) {
+      const int buf = c & 1;
+      if (!(ok = warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort))) break;
+      const float decay = exp2f(sm.g_hi[buf][kChunk - 1] + sm.g_lo[buf][kChunk - 1]);
+      total *= decay;
+      warp_arrive(&sm.g_empty[buf]);
+      if (c > 0) {
+        if (!(ok = warp_wait(&sm.kv_full, (c - 1) & 1, &sm.abort))) break;
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int piece = 0; piece < 4; ++piece) {
+        uint32_t s[32];
+        if (c > 0) {
+          tmem_ld32(s, tmq + kColS + piece * 32);
+          tmem_wait_ld();
+        } else {
+          // The state before the segment: the lane's, then every earlier segment's
+          // from zero behind its decay.
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = 0u;
+          if (!STATES) {
+            const int at = static_cast<int>(row) * 128 + piece * 32;
+            const float* begin = cp.segments > 1 ? cp.local + head * (128 * 128) : state_in;
+            if (state_in != nullptr) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(begin + at + i));
+                s[i] = __float_as_uint(x.x);
+                s[i + 1] = __float_as_uint(x.y);
+                s[i + 2] = __float_as_uint(x.z);
+                s[i + 3] = __float_as_uint(x.w);
+              }
+            }
+            for (int r = 0; r < sg.seg; ++r) {
+              const float a = __ldcg(cp.local_decay + r * heads + head);
+              const float* src = cp.local + ((r + 1) * heads + head) * (128 * 128) + at;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(src + i));
+                s[i] = __float_as_uint(fmaf(__uint_as_float(s[i]), a, x.x));
+                s[i + 1] = __float_as_uint(fmaf(__uint_as_float(s[i + 1]), a, x.y));
+                s[i + 2] = __float_as_uint(fmaf(__uint_as_float(s[i + 2]), a, x.z));
+                s[i + 3] = __float_as_uint(fmaf(__uint_as_float(s[i + 3]), a, x.w));
+              }
+            }
+          }
+        }
+        if (!STATES) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint4 hi, lo;
+            uint32_t* ph = &hi.x;
+            uint32_t* pl = &lo.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = __uint_as_float(s[i + 2 * e]), y = __uint_as_float(s[i + 2 * e + 1]);
+              ph[e] = pack_hi(x, y);
+              pl[e] = pack_rn(rest(x), rest(y));
+            }
+            const uint32_t at = tile_unit(row, piece * 4 + i / 8);
+            *reinterpret_cast<uint4*>(sm.s_hi + at) = hi;
+            *reinterpret_cast<uint4*>(sm.s_lo + at) = lo;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * decay);
+        tmem_st32(tmq + kColS + piece * 32, s);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      if (!STATES) fence_async_smem();
+      warp_arrive(&sm.s_ready);
+    }
+    if (n_chunks > 0 && ok && warp_wait(&sm.kv_full, (n_chunks - 1) & 1, &sm.abort)) {
+      tc_fence_after();
+      float* dst = STATES ? cp.local + ((sg.seg + 1) * heads + head) * (128 * 128) : (sg.last ? state_out : nullptr);
+      if (STATES && row == 0) cp.local_decay[sg.seg * heads + head] = total;
+      float bad = 0.f;
+#pragma unroll 1
+      for (int piece = 0; piece < 4; ++piece) {
+        uint32_t s[32];
+        tmem_ld32(s, tmq + kColS + piece * 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          float4 x;
+          x.x = __uint_as_float(s[i]);
+          x.y = __uint_as_float(s[i + 1]);
+          x.z = __uint_as_float(s[i + 2]);
+          x.w = __uint_as_float(s[i + 3]);
+          bad += (x.x - x.x) + (x.y - x.y) + (x.z - x.z) + (x.w - x.w);
+          if (dst != nullptr) *reinterpret_cast<float4*>(dst + row * 128 + piece * 32 + i) = x;
+        }
+      }
+      tc_fence_before();
+      if (!STATES && sg.last && bad != 0.f && p.lane_status != nullptr) p.lane_status[sg.b] = SPEC_ERR_NONFINITE;
+    }
+  } else if (warp >= 16) {
+    // ---------------------------------------------------------------------- k'
+    // Row `row` of k'^T is one of the 128 components of k: a thread reads its component
+    // of every token and writes it, times the token's weight, along its lane.
+    int step = 0;
+    bool ok = true;
+    const uint32_t unit = row >> 3;
+    for (int c = 0; c < n_chunks && ok; ++c) {
+      const int buf = c & 1;
+      const int n = min(kChunk, sg.count - (sg.c0 + c) * kChunk);
+      const int lk = kLoads * c, lv = lk + kLoads - 1;
+      if (!(ok = warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort))) break;
+      if (n < kChunk) {  // rows past the lane take part in products (times 0): make them 0
+        if (!(ok = warp_wait(&sm.full[lv % kRing], (lv / kRing) & 1, &sm.abort))) break;
+        uint8_t* vt = sm.ring[lv % kRing];
+        if (static_cast<int>(row) >= n)
+          for (uint32_t u = 0; u < 16; ++u)
+            *reinterpret_cast<uint4*>(vt + tile_unit(row, u)) = make_uint4(0u, 0u, 0u, 0u);
+        fence_async_smem();
+        warp_arrive(&sm.v_clean);
+      }
+      const float last_hi = sm.g_hi[buf][kChunk - 1], last_lo = sm.g_lo[buf][kChunk - 1];
+      if (!(ok = warp_wait(&sm.full[lk % kRing], (lk / kRing) & 1, &sm.abort))) break;
+      const uint8_t* tile = sm.ring[lk % kRing] + (unit >> 3) * kHalf + (row & 7) * 2;
+      for (int t0 = 0; t0 < n; t0 += 32, ++step) {
+        const int kb = step & 1;
+        uint32_t hi[16], mid[16], lo[16];
+        // Each lane has the weight of one of the 32 tokens.
+        const float weight = exp2f((last_hi - sm.g_hi[buf][t0 + lane]) + (last_lo - sm.g_lo[buf][t0 + lane]));
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float w = __shfl_sync(0xFFFFFFFFu, weight, i + e);
+            const uint32_t raw = *reinterpret_cast<const uint16_t*>(tile + (t0 + i + e) * 128 + ((((unit & 7) ^ ((i + e) & 7))) << 4));
+            x[e] = t0 + i + e < n ? __uint_as_float(raw << 16) * w : 0.f;  // (rows past the lane may be NaN)
+          }
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            hi[(i + e) / 2] = pack_hi(x[e], x[e + 1]);
+            const float r0 = rest(x[e]), r1 = rest(x[e + 1]);
+            mid[(i + e) / 2] = pack_hi(r0, r1);
+            lo[(i + e) / 2] = pack_hi(rest(r0), rest(r1));
+          }
+        }
+        if (step >= 2 && !(ok = warp_wait(&sm.kp_empty[kb], ((step >> 1) - 1) & 1, &sm.abort))) break;
+        tc_fence_after();
+        const uint32_t dst = tmq + kColK + kb * kColKBuf;
+        tmem_st16(dst, hi);
+        tmem_st16(dst + 16, mid);
+        tmem_st16(dst + 32, lo);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&sm.kp_full[kb]);
+      }
+      if (!ok) break;
+      warp_arrive(&sm.g_empty[buf]);
+      warp_arrive(&sm.empty[lk % kRing]);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && sm.abort && p.lane_status != nullptr) p.lane_status[sg.b] = SPEC_ERR_TIMEOUT;
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tm, 512);
+}
+
+}  // namespace specv
