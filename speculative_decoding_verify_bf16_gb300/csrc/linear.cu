@@ -209,11 +209,16 @@ int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args*
   {
     std::lock_guard<std::mutex> lock(g_mutex);
     if (!dc->chunk_attr) {
-      for (void* k : {states, full})
+      for (void* k : {states, full}) {
+        // The warpgroups' shares must not add up to more than the launch brings.
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, k) != cudaSuccess || fa.numRegs * (specv::kChunkThreads / 128) < specv::kChunkRegs)
+          return SPEC_ERR_CUDA;
         if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
           cudaGetLastError();
           return SPEC_ERR_CUDA;
         }
+      }
       dc->chunk_attr = true;
     }
   }
@@ -225,7 +230,7 @@ int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args*
     return SPEC_ERR_INVALID_ARG;
   cp.local = static_cast<float*>(a->workspace);
   cp.local_decay = cp.local + static_cast<int64_t>(cp.segments) * pairs * (128 * 128);
-  cp.out_vec = aligned16(p.out) && p.out_row % 8 == 0 && p.out_head % 8 == 0;
+  cp.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0 && p.out_row % 16 == 0 && p.out_head % 16 == 0;
   const int k_heads = p.v_heads / p.group;
   CUtensorMap q, k, v;
   if (!make_map(&q, p.q, p.rows, k_heads, p.q_row, p.q_head) || !make_map(&k, p.k, p.rows, k_heads, p.k_row, p.k_head) ||

@@ -10,16 +10,18 @@
 // One CTA walks the chunks of one (lane, head), or of a segment of them.  Its products:
 //
 //   QK  scores [token][token]  = q k^T
-//   QS  D [token][dv]          = q S,      D rows then times 2^G_i
-//   KV  S [dk][dv]            += k'^T v,   k' = 2^(G_last - G_j) k_j, S times 2^G_last before
-//   PV  D                     += P v,      P = weighted scores, 0 above the diagonal
+//   QS  D [token][dv]          = q S,     D rows then times 2^G_i
+//   KV  U [dk][dv]             = k'^T v,  k' = 2^(G_last - G_j) k_j
+//   PV  D                     += P v,     P = weighted scores, 0 above the diagonal
 //
-// S stays in tensor memory in fp32 from the first chunk to the last.  Operands are bf16,
-// so fp32 numbers enter a product in parts: k' in three (all 24 bits, the state is as
-// exact as its fp32 sums), P and S in two (16 bits, far below the rounding of a bf16
-// output).  q, k and v are taken as they are.
+// S stays in fp32 in the registers of four warps from the first chunk to the last, and
+// S' = 2^G_last S + U is formed there: the tensor cores truncate each addition to an
+// accumulator, which into S itself cost ten times the precision of its fp32 sums.
+// Operands are bf16, so fp32 numbers enter a product in parts: k' in three (all 24 bits),
+// P and S in two (16 bits, far below the rounding of a bf16 output).  q, k and v are
+// taken as they are.
 //
-// Tensor memory holds S (128 columns), scores and P (128; P overwrites the scores it came
+// Tensor memory holds U (128 columns), scores and P (128; P overwrites the scores it came
 // from), D (128) and two buffers of k' for 32 tokens (96).  Shared memory holds a ring of
 // five 32 KB tiles (k, q, v of a chunk; 128-byte swizzled rows, so that a tile serves as
 // an operand along either dimension) and S in two parts.
@@ -28,7 +30,8 @@
 // four do what lies between the products: scores to P (4-7), D (8-11), S (12-15), k'
 // (16-19).  The products of a chunk take 8 x 512 cycles on the tensor cores, its
 // 128 KB of q, k, v and o about 5,500 at an SM's share of the HBM rate: the groups work
-// beside each other so that the larger of the two counts.
+// beside each other so that the larger of the two counts.  A chunk's products go in the
+// order QK, KV, QS, PV: P is made beside KV and QS, the next S beside QS and PV.
 #pragma once
 
 #include <cuda.h>
@@ -44,10 +47,13 @@ namespace specv {
 
 constexpr int kChunk = 128;
 constexpr int kChunkThreads = 640;
+// Registers a thread of each warpgroup; their sum is what a launch must bring (5 x 96).
+constexpr int kRegsMisc = 80, kRegsScores = 72, kRegsOut = 72, kRegsState = 168, kRegsKey = 88;
+constexpr int kChunkRegs = kRegsMisc + kRegsScores + kRegsOut + kRegsState + kRegsKey;
 constexpr int kTile = 32 * 1024;      // 128 rows of 128 bf16: two halves of 64 columns
 constexpr int kHalf = kTile / 2;
 constexpr int kRing = 5;
-constexpr uint32_t kColS = 0, kColP = 128, kColD = 256, kColK = 384;  // columns of tensor memory
+constexpr uint32_t kColU = 0, kColP = 128, kColD = 256, kColK = 384;  // columns of tensor memory
 constexpr uint32_t kColKBuf = 48;     // a k' buffer: three parts of 16 columns (32 tokens)
 constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;    // log2(e) in two parts
 // A decay of 2^-160 is 0 in fp32 against everything a state can hold; the clamp keeps
@@ -58,11 +64,11 @@ struct ChunkSmem {
   uint8_t ring[kRing][kTile];
   uint8_t s_hi[kTile];
   uint8_t s_lo[kTile];
-  float g_hi[2][kChunk];  // G in two parts, chunk c in c % 2
+  float g_hi[2][kChunk];  // -G in two parts, chunk c in c % 2
   float g_lo[2][kChunk];
   uint64_t full[kRing], empty[kRing];
   uint64_t g_full[2], g_empty[2];
-  uint64_t scores_full, p_ready, qs_full, d_scaled, o_full, d_free, s_ready, kv_full, v_clean, drain;
+  uint64_t scores_full, p_ready, qs_full, d_scaled, o_full, d_free, s_ready, kv_full, u_free, v_clean, drain;
   uint64_t kp_full[2], kp_empty[2];
   uint32_t tmem;
   int abort;
@@ -75,7 +81,7 @@ struct ChunkParams {
                       // call; r + 1, the state after segment r begun from zero
   float* local_decay; // [segments][lanes][heads]: whole decay of segment r
   int32_t segments;
-  int32_t out_vec;    // out rows take 16-byte stores
+  int32_t out_vec;    // out rows take 32-byte stores
 };
 
 // Waits for a phase; gives up after the time limit or when another warp has.
@@ -96,19 +102,32 @@ __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, int* 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
   return __all_sync(0xFFFFFFFFu, chunk_wait(bar, parity, abort));
 }
+// Registers of the calling warpgroup (four warps), within what the CTA was launched with.
+template <int N>
+__device__ __forceinline__ void registers_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// The upper halves of two fp32 numbers: their bf16 parts by truncation.
-__device__ __forceinline__ uint32_t pack_hi(float a, float b) {
-  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+// The upper halves of two fp32 numbers, which are their bf16 parts by truncation; what
+// truncation leaves; and two numbers rounded to bf16.
+__device__ __forceinline__ uint32_t upper(f32x2 v) {
+  return __byte_perm(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32), 0x7632);
 }
-__device__ __forceinline__ float rest(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack_rn(float a, float b) {
+__device__ __forceinline__ f32x2 rest(f32x2 v) {
+  const uint32_t a = static_cast<uint32_t>(v), b = static_cast<uint32_t>(v >> 32);
+  return add2(v, pair(__uint_as_float((a & 0xFFFF0000u) ^ 0x80000000u), __uint_as_float((b & 0xFFFF0000u) ^ 0x80000000u)));
+}
+__device__ __forceinline__ uint32_t rounded(f32x2 v) {
   uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(second_of(v)), "f"(first_of(v)));
   return d;
 }
 
@@ -158,6 +177,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(&sm.d_free, 4);
     mbar_init(&sm.s_ready, 4);
     mbar_init(&sm.kv_full, 1);
+    mbar_init(&sm.u_free, 4);
     mbar_init(&sm.v_clean, 4);
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -214,6 +234,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int n_chunks = active ? sg.c1 - sg.c0 : 0;
   constexpr int kLoads = STATES ? 2 : 3;  // tiles of a chunk: k, (q,) v
 
+  if (warp < 4) registers_shrink<kRegsMisc>();
   if (warp == 0) {
     // ------------------------------------------------------------------ copies
     if (lane == 0) {
@@ -252,57 +273,70 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int lk = kLoads * c, lq = lk + 1, lv = lk + kLoads - 1;
         uint64_t* const fk = &sm.full[lk % kRing];
         uint64_t* const fv = &sm.full[lv % kRing];
-        const uint32_t ak = smem_addr(sm.ring[lk % kRing]);
-        const uint32_t av = smem_addr(sm.ring[lv % kRing]);
+        // One thread issues every product: the loops are unrolled over descriptors that
+        // differ by constants, since address arithmetic between them would hold up the
+        // tensor cores (measured: 300 cycles a product against the 64 it takes).
+        const uint32_t dq = smem_desc(smem_addr(sm.ring[lq % kRing]), 16);
+        const uint32_t dk = smem_desc(smem_addr(sm.ring[lk % kRing]), 16);
+        const uint32_t dv = smem_desc(smem_addr(sm.ring[lv % kRing]), kHalf);
+        // U over the tokens of k' buffers first .. last - 1.
+        auto kv = [&](int first, int last) {
+          for (int t = first * 2; t < min(last * 2, steps); t += 2, ++step) {
+            const int buf = step & 1;
+            if (!chunk_wait(&sm.kp_full[buf], (step >> 1) & 1, &sm.abort)) return false;
+            tc_fence_after();
+            const uint32_t parts = tm + kColK + buf * kColKBuf, rows = dv + t * (2048 / 16);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+              const int part = 2 - i / 2, s = i % 2;
+              if (t + s < steps)
+                mma_ts(tm + kColU, parts + part * 16 + s * 8, rows + s * (2048 / 16), kRows, i > 0 || t > 0);
+            }
+            mma_commit(&sm.kp_empty[buf]);
+          }
+          return true;
+        };
         if (!chunk_wait(fk, (lk / kRing) & 1, &sm.abort)) break;
         if (!STATES) {
-          const uint32_t aq = smem_addr(sm.ring[lq % kRing]);
           if (!chunk_wait(&sm.full[lq % kRing], (lq / kRing) & 1, &sm.abort)) break;
           tc_fence_after();
+#pragma unroll
           for (int s = 0; s < 8; ++s) {
-            const uint32_t off = (s >> 2) * kHalf + (s & 3) * 32;
-            mma_ss(tm + kColP, smem_desc(aq + off, 16, 1024), smem_desc(ak + off, 16, 1024), kSame, s > 0);
+            const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) / 16;
+            mma_ss(tm + kColP, dq + off, dk + off, kSame, s > 0);
           }
           mma_commit(&sm.scores_full);
           mma_commit(&sm.empty[lk % kRing]);
-          if (!chunk_wait(&sm.s_ready, ph, &sm.abort)) break;
-          if (c > 0 && !chunk_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
-          tc_fence_after();
-          const uint32_t ahi = smem_addr(sm.s_hi), alo = smem_addr(sm.s_lo);
-          for (int s = 0; s < 16; ++s) {
-            const uint32_t off = ((s & 7) >> 2) * kHalf + (s & 3) * 32;
-            const uint32_t b = (s < 8 ? alo : ahi) + (s & 7) * 2048;
-            mma_ss(tm + kColD, smem_desc(aq + off, 16, 1024), smem_desc(b, kHalf, 1024), kRows, s > 0);
-          }
-          mma_commit(&sm.qs_full);
-          mma_commit(&sm.empty[lq % kRing]);
-          mbar_arrive_n(&sm.empty[lq % kRing], 4);
         } else {
           mbar_arrive(&sm.empty[lk % kRing]);
-          if (!chunk_wait(&sm.s_ready, ph, &sm.abort)) break;
         }
         if (!chunk_wait(fv, (lv / kRing) & 1, &sm.abort)) break;
         if (n < kChunk && !chunk_wait(&sm.v_clean, 0, &sm.abort)) break;
-        bool ok = true;
-        for (int t = 0; t < steps; t += 2, ++step) {
-          const int buf = step & 1;
-          if (!(ok = chunk_wait(&sm.kp_full[buf], (step >> 1) & 1, &sm.abort))) break;
-          tc_fence_after();
-          for (int part = 2; part >= 0; --part)
-            for (int s = t; s < min(t + 2, steps); ++s)
-              mma_ts(tm + kColS, tm + kColK + buf * kColKBuf + part * 16 + (s - t) * 8, smem_desc(av + s * 2048, kHalf, 1024),
-                     kRows, true);
-          mma_commit(&sm.kp_empty[buf]);
-        }
-        if (!ok) break;
+        if (c > 0 && !chunk_wait(&sm.u_free, ph ^ 1, &sm.abort)) break;
+        if (!kv(0, 4)) break;
         mma_commit(&sm.kv_full);
+        if (!STATES) {
+          if (!chunk_wait(&sm.s_ready, ph, &sm.abort)) break;
+          if (c > 0 && !chunk_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
+          tc_fence_after();
+          const uint32_t dhi = smem_desc(smem_addr(sm.s_hi), kHalf), dlo = smem_desc(smem_addr(sm.s_lo), kHalf);
+#pragma unroll
+          for (int s = 0; s < 16; ++s)
+            mma_ss(tm + kColD, dq + (((s & 7) >> 2) * kHalf + (s & 3) * 32) / 16, (s < 8 ? dlo : dhi) + (s & 7) * (2048 / 16),
+                   kRows, s > 0);
+          mma_commit(&sm.qs_full);
+          mma_commit(&sm.empty[lq % kRing]);
+          mbar_arrive_n(&sm.empty[lq % kRing], 4);
+        }
         if (!STATES) {
           if (!chunk_wait(&sm.p_ready, ph, &sm.abort) || !chunk_wait(&sm.d_scaled, ph, &sm.abort)) break;
           tc_fence_after();
-          for (int part = 1; part >= 0; --part)
-            for (int s = 0; s < steps; ++s)
-              mma_ts(tm + kColD, tm + kColP + (s >> 1) * 32 + part * 16 + (s & 1) * 8, smem_desc(av + s * 2048, kHalf, 1024),
-                     kRows, true);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int part = 1 - i / 8, s = i % 8;
+            if (s < steps)
+              mma_ts(tm + kColD, tm + kColP + (s >> 1) * 32 + part * 16 + (s & 1) * 8, dv + s * (2048 / 16), kRows, true);
+          }
           mma_commit(&sm.o_full);
         }
         mma_commit(&sm.empty[lv % kRing]);
@@ -353,19 +387,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int i = 0; i < 4; ++i) {
         const float hi = __ll2float_rn(run + sum[i]);
         const float lo = __ll2float_rn(run + sum[i] - __float2ll_rn(hi));
-        sm.g_hi[buf][lane * 4 + i] = bad ? __uint_as_float(0x7FC00000u) : hi * 0x1p-32f;
-        sm.g_lo[buf][lane * 4 + i] = lo * 0x1p-32f;
+        sm.g_hi[buf][lane * 4 + i] = bad ? __uint_as_float(0x7FC00000u) : hi * -0x1p-32f;
+        sm.g_lo[buf][lane * 4 + i] = lo * -0x1p-32f;
       }
       __threadfence_block();
       warp_arrive(&sm.g_full[buf]);
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------- scores to P
+    registers_shrink<kRegsScores>();
     if (!STATES) {
       for (int c = 0; c < n_chunks; ++c) {
         const int buf = c & 1;
         if (!warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort)) break;
-        const float ghi = sm.g_hi[buf][row], glo = sm.g_lo[buf][row];
+        const f32x2 ghi = pair(-sm.g_hi[buf][row], -sm.g_hi[buf][row]), glo = pair(-sm.g_lo[buf][row], -sm.g_lo[buf][row]);
         if (!warp_wait(&sm.scores_full, c & 1, &sm.abort)) break;
         tc_fence_after();
 #pragma unroll 1
@@ -381,19 +416,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const bool diagonal = piece * 32 == static_cast<int>(quarter);
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 jh = *reinterpret_cast<const float4*>(&sm.g_hi[buf][piece * 32 + i]);
-              const float4 jl = *reinterpret_cast<const float4*>(&sm.g_lo[buf][piece * 32 + i]);
-              float w[4] = {(ghi - jh.x) + (glo - jl.x), (ghi - jh.y) + (glo - jl.y), (ghi - jh.z) + (glo - jl.z),
-                            (ghi - jh.w) + (glo - jl.w)};
+              const ulonglong2 jh = *reinterpret_cast<const ulonglong2*>(&sm.g_hi[buf][piece * 32 + i]);
+              const ulonglong2 jl = *reinterpret_cast<const ulonglong2*>(&sm.g_lo[buf][piece * 32 + i]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                w[e] = ex2_approx(w[e]) * __uint_as_float(s[i + e]);
-                if (diagonal && i + e > lane) w[e] = 0.f;  // (a select: what is masked may be NaN)
+              for (int e = 0; e < 2; ++e) {
+                // (g arrays hold -G)
+                const f32x2 d = add2(add2(ghi, e ? jh.y : jh.x), add2(glo, e ? jl.y : jl.x));
+                f32x2 w = mul2(pair(ex2_approx(first_of(d)), ex2_approx(second_of(d))),
+                               pair(__uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1])));
+                if (diagonal)  // (a select: what is masked may be NaN)
+                  w = pair(i + 2 * e > lane ? 0.f : first_of(w), i + 2 * e + 1 > lane ? 0.f : second_of(w));
+                hi[i / 2 + e] = upper(w);
+                lo[i / 2 + e] = rounded(rest(w));
               }
-              hi[i / 2] = pack_hi(w[0], w[1]);
-              hi[i / 2 + 1] = pack_hi(w[2], w[3]);
-              lo[i / 2] = pack_rn(rest(w[0]), rest(w[1]));
-              lo[i / 2 + 1] = pack_rn(rest(w[2]), rest(w[3]));
             }
           }
           tmem_st16(tmq + kColP + piece * 32, hi);
@@ -407,11 +442,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else if (warp >= 8 && warp < 12) {
     // ----------------------------------------------------------------- outputs
+    registers_shrink<kRegsOut>();
     if (!STATES) {
       for (int c = 0; c < n_chunks; ++c) {
         const int buf = c & 1;
         if (!warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort)) break;
-        const float e = exp2f(sm.g_hi[buf][row] + sm.g_lo[buf][row]);
+        const float e = exp2f(-(sm.g_hi[buf][row] + sm.g_lo[buf][row]));
         warp_arrive(&sm.g_empty[buf]);
         if (!warp_wait(&sm.qs_full, c & 1, &sm.abort)) break;
         tc_fence_after();
@@ -421,7 +457,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           tmem_ld32(d, tmq + kColD + piece * 32);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) d[i] = __float_as_uint(__uint_as_float(d[i]) * e);
+          for (int i = 0; i < 32; i += 2) {
+            const f32x2 x = mul2(pair(e, e), pair(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
+            d[i] = static_cast<uint32_t>(x);
+            d[i + 1] = static_cast<uint32_t>(x >> 32);
+          }
           tmem_st32(tmq + kColD + piece * 32, d);
         }
         tmem_wait_st();
@@ -432,140 +472,130 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int t = (sg.c0 + c) * kChunk + static_cast<int>(row);
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
                              (sg.first + static_cast<int64_t>(t)) * p.out_row + sg.h * p.out_head;
+        const f32x2 scale = pair(p.scale, p.scale);
 #pragma unroll 1
-        for (int piece = 0; piece < 4; ++piece) {
-          uint32_t d[32];
-          tmem_ld32(d, tmq + kColD + piece * 32);
-          tmem_wait_ld();
-          if (t < sg.count) {
-            uint32_t o[16];
+        for (int half = 0; half < 2; ++half) {
+          uint32_t o[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[i] = pack_rn(p.scale * __uint_as_float(d[2 * i]), p.scale * __uint_as_float(d[2 * i + 1]));
-            if (cp.out_vec) {
+          for (int piece = 0; piece < 4; ++piece) {
+            uint32_t d[16];
+            tmem_ld16(d, tmq + kColD + half * 64 + piece * 16);
+            tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(dst + piece * 32 + i * 8) =
-                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            } else {
+            for (int i = 0; i < 8; ++i)
+              o[piece * 8 + i] = rounded(mul2(scale, pair(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]))));
+          }
+          if (half == 1) {
+            tc_fence_before();
+            warp_arrive(&sm.d_free);
+          }
+          if (t >= sg.count) continue;
+          __nv_bfloat16* at = dst + half * 64;
+          if (cp.out_vec) {  // whole 32-byte sectors
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                dst[piece * 32 + 2 * i] = __ushort_as_bfloat16(static_cast<unsigned short>(o[i]));
-                dst[piece * 32 + 2 * i + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(o[i] >> 16));
-              }
+            for (int i = 0; i < 32; i += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at + 2 * i), "r"(o[i]),
+                           "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]),
+                           "r"(o[i + 7])
+                           : "memory");
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              at[2 * i] = __ushort_as_bfloat16(static_cast<unsigned short>(o[i]));
+              at[2 * i + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(o[i] >> 16));
             }
           }
         }
-        tc_fence_before();
-        warp_arrive(&sm.d_free);
       }
     }
   } else if (warp >= 12 && warp < 16) {
     // ------------------------------------------------------------------ states
+    registers_grow<kRegsState>();
+    f32x2 S[64];  // row `row` of S
+#pragma unroll
+    for (int i = 0; i < 64; ++i) S[i] = 0ull;
+    const int at = static_cast<int>(row) * 128;
+    if (!STATES && n_chunks > 0) {
+      // The state before the segment: the lane's, then every earlier segment's from
+      // zero behind its decay.
+      const float* begin = cp.segments > 1 ? cp.local + head * (128 * 128) : state_in;
+      if (state_in != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(begin + at + 2 * i));
+          S[i] = pair(x.x, x.y);
+          S[i + 1] = pair(x.z, x.w);
+        }
+      }
+      for (int r = 0; r < sg.seg; ++r) {
+        const float a = __ldcg(cp.local_decay + r * heads + head);
+        const float* src = cp.local + ((r + 1) * heads + head) * (128 * 128) + at;
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src + 2 * i));
+          S[i] = fma2(S[i], pair(a, a), pair(x.x, x.y));
+          S[i + 1] = fma2(S[i + 1], pair(a, a), pair(x.z, x.w));
+        }
+      }
+    }
+    // S in two parts to shared memory, for the chunk's QS.
+    auto publish = [&] {
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        const uint32_t unit = tile_unit(row, i / 4);
+        *reinterpret_cast<uint4*>(sm.s_hi + unit) = make_uint4(upper(S[i]), upper(S[i + 1]), upper(S[i + 2]), upper(S[i + 3]));
+        *reinterpret_cast<uint4*>(sm.s_lo + unit) = make_uint4(rounded(rest(S[i])), rounded(rest(S[i + 1])),
+                                                               rounded(rest(S[i + 2])), rounded(rest(S[i + 3])));
+      }
+      fence_async_smem();
+      warp_arrive(&sm.s_ready);
+    };
+    if (!STATES && n_chunks > 0) publish();
     bool ok = true;
     float total = 1.f;  // the segment's whole decay
     for (int c = 0; c < n_chunks; ++c) {
       const int buf = c & 1;
       if (!(ok = warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort))) break;
-      const float decay = exp2f(sm.g_hi[buf][kChunk - 1] + sm.g_lo[buf][kChunk - 1]);
+      const float decay = exp2f(-(sm.g_hi[buf][kChunk - 1] + sm.g_lo[buf][kChunk - 1]));
       total *= decay;
       warp_arrive(&sm.g_empty[buf]);
-      if (c > 0) {
-        if (!(ok = warp_wait(&sm.kv_full, (c - 1) & 1, &sm.abort))) break;
-        tc_fence_after();
-      }
-#pragma unroll 1
-      for (int piece = 0; piece < 4; ++piece) {
-        uint32_t s[32];
-        if (c > 0) {
-          tmem_ld32(s, tmq + kColS + piece * 32);
-          tmem_wait_ld();
-        } else {
-          // The state before the segment: the lane's, then every earlier segment's
-          // from zero behind its decay.
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = 0u;
-          if (!STATES) {
-            const int at = static_cast<int>(row) * 128 + piece * 32;
-            const float* begin = cp.segments > 1 ? cp.local + head * (128 * 128) : state_in;
-            if (state_in != nullptr) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(begin + at + i));
-                s[i] = __float_as_uint(x.x);
-                s[i + 1] = __float_as_uint(x.y);
-                s[i + 2] = __float_as_uint(x.z);
-                s[i + 3] = __float_as_uint(x.w);
-              }
-            }
-            for (int r = 0; r < sg.seg; ++r) {
-              const float a = __ldcg(cp.local_decay + r * heads + head);
-              const float* src = cp.local + ((r + 1) * heads + head) * (128 * 128) + at;
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(src + i));
-                s[i] = __float_as_uint(fmaf(__uint_as_float(s[i]), a, x.x));
-                s[i + 1] = __float_as_uint(fmaf(__uint_as_float(s[i + 1]), a, x.y));
-                s[i + 2] = __float_as_uint(fmaf(__uint_as_float(s[i + 2]), a, x.z));
-                s[i + 3] = __float_as_uint(fmaf(__uint_as_float(s[i + 3]), a, x.w));
-              }
-            }
-          }
-        }
-        if (!STATES) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint4 hi, lo;
-            uint32_t* ph = &hi.x;
-            uint32_t* pl = &lo.x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = __uint_as_float(s[i + 2 * e]), y = __uint_as_float(s[i + 2 * e + 1]);
-              ph[e] = pack_hi(x, y);
-              pl[e] = pack_rn(rest(x), rest(y));
-            }
-            const uint32_t at = tile_unit(row, piece * 4 + i / 8);
-            *reinterpret_cast<uint4*>(sm.s_hi + at) = hi;
-            *reinterpret_cast<uint4*>(sm.s_lo + at) = lo;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * decay);
-        tmem_st32(tmq + kColS + piece * 32, s);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      if (!STATES) fence_async_smem();
-      warp_arrive(&sm.s_ready);
-    }
-    if (n_chunks > 0 && ok && warp_wait(&sm.kv_full, (n_chunks - 1) & 1, &sm.abort)) {
+      if (!(ok = warp_wait(&sm.kv_full, c & 1, &sm.abort))) break;
       tc_fence_after();
+      uint32_t u[2][8];
+      tmem_ld8(u[0], tmq + kColU);
+#pragma unroll
+      for (int piece = 0; piece < 16; ++piece) {
+        tmem_wait_ld();
+        if (piece < 15) tmem_ld8(u[(piece + 1) & 1], tmq + kColU + (piece + 1) * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          S[piece * 4 + i] = fma2(S[piece * 4 + i], pair(decay, decay),
+                                  pair(__uint_as_float(u[piece & 1][2 * i]), __uint_as_float(u[piece & 1][2 * i + 1])));
+      }
+      tc_fence_before();
+      warp_arrive(&sm.u_free);
+      if (!STATES && c + 1 < n_chunks) {
+        if (!(ok = warp_wait(&sm.qs_full, c & 1, &sm.abort))) break;  // the last parts have been read
+        publish();
+      }
+    }
+    if (n_chunks > 0 && ok) {
       float* dst = STATES ? cp.local + ((sg.seg + 1) * heads + head) * (128 * 128) : (sg.last ? state_out : nullptr);
       if (STATES && row == 0) cp.local_decay[sg.seg * heads + head] = total;
       float bad = 0.f;
-#pragma unroll 1
-      for (int piece = 0; piece < 4; ++piece) {
-        uint32_t s[32];
-        tmem_ld32(s, tmq + kColS + piece * 32);
-        tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float4 x;
-          x.x = __uint_as_float(s[i]);
-          x.y = __uint_as_float(s[i + 1]);
-          x.z = __uint_as_float(s[i + 2]);
-          x.w = __uint_as_float(s[i + 3]);
-          bad += (x.x - x.x) + (x.y - x.y) + (x.z - x.z) + (x.w - x.w);
-          if (dst != nullptr) *reinterpret_cast<float4*>(dst + row * 128 + piece * 32 + i) = x;
-        }
+      for (int i = 0; i < 64; i += 2) {
+        const float4 x = make_float4(first_of(S[i]), second_of(S[i]), first_of(S[i + 1]), second_of(S[i + 1]));
+        bad += (x.x - x.x) + (x.y - x.y) + (x.z - x.z) + (x.w - x.w);
+        if (dst != nullptr) *reinterpret_cast<float4*>(dst + at + 2 * i) = x;
       }
-      tc_fence_before();
       if (!STATES && sg.last && bad != 0.f && p.lane_status != nullptr) p.lane_status[sg.b] = SPEC_ERR_NONFINITE;
     }
   } else if (warp >= 16) {
     // ---------------------------------------------------------------------- k'
     // Row `row` of k'^T is one of the 128 components of k: a thread reads its component
     // of every token and writes it, times the token's weight, along its lane.
+    registers_shrink<kRegsKey>();
     int step = 0;
     bool ok = true;
     const uint32_t unit = row >> 3;
@@ -590,23 +620,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int kb = step & 1;
         uint32_t hi[16], mid[16], lo[16];
         // Each lane has the weight of one of the 32 tokens.
-        const float weight = exp2f((last_hi - sm.g_hi[buf][t0 + lane]) + (last_lo - sm.g_lo[buf][t0 + lane]));
+        const float weight = exp2f((sm.g_hi[buf][t0 + lane] - last_hi) + (sm.g_lo[buf][t0 + lane] - last_lo));
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float x[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float w = __shfl_sync(0xFFFFFFFFu, weight, i + e);
-            const uint32_t raw = *reinterpret_cast<const uint16_t*>(tile + (t0 + i + e) * 128 + ((((unit & 7) ^ ((i + e) & 7))) << 4));
-            x[e] = t0 + i + e < n ? __uint_as_float(raw << 16) * w : 0.f;  // (rows past the lane may be NaN)
-          }
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            hi[(i + e) / 2] = pack_hi(x[e], x[e + 1]);
-            const float r0 = rest(x[e]), r1 = rest(x[e + 1]);
-            mid[(i + e) / 2] = pack_hi(r0, r1);
-            lo[(i + e) / 2] = pack_hi(rest(r0), rest(r1));
-          }
+        for (int i = 0; i < 32; i += 2) {
+          const f32x2 w = pair(__shfl_sync(0xFFFFFFFFu, weight, i), __shfl_sync(0xFFFFFFFFu, weight, i + 1));
+          const uint8_t* src = tile + (t0 + i) * 128;
+          const uint32_t raw0 = *reinterpret_cast<const uint16_t*>(src + (((unit ^ i) & 7) << 4));
+          const uint32_t raw1 = *reinterpret_cast<const uint16_t*>(src + 128 + (((unit ^ (i + 1)) & 7) << 4));
+          f32x2 x = mul2(w, pair(__uint_as_float(raw0 << 16), __uint_as_float(raw1 << 16)));
+          if (t0 + 32 > n)  // (rows past the lane may be NaN)
+            x = pair(t0 + i < n ? first_of(x) : 0.f, t0 + i + 1 < n ? second_of(x) : 0.f);
+          hi[i / 2] = upper(x);
+          x = rest(x);
+          mid[i / 2] = upper(x);
+          lo[i / 2] = upper(rest(x));
         }
         if (step >= 2 && !(ok = warp_wait(&sm.kp_empty[kb], ((step >> 1) - 1) & 1, &sm.abort))) break;
         tc_fence_after();
