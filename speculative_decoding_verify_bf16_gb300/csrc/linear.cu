@@ -198,7 +198,8 @@ bool chunkable(const LinearParams& p, spec_dtype dtype) {
   const int k_heads = p.v_heads / p.group;
   return dtype == SPEC_BF16 && p.dk == 128 && p.dv == 128 && p.rows > 0 && p.max_len >= kChunkMinLen &&
          mappable(p.q, p.q_row, p.q_head, k_heads) && mappable(p.k, p.k_row, p.k_head, k_heads) &&
-         mappable(p.v, p.v_row, p.v_head, p.v_heads) && encode_tiled() != nullptr;
+         mappable(p.v, p.v_row, p.v_head, p.v_heads) && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0 &&
+         p.out_row % 16 == 0 && p.out_head % 16 == 0 && encode_tiled() != nullptr;
 }
 
 int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args* a, void* stream) {
@@ -230,7 +231,6 @@ int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args*
     return SPEC_ERR_INVALID_ARG;
   cp.local = static_cast<float*>(a->workspace);
   cp.local_decay = cp.local + static_cast<int64_t>(cp.segments) * pairs * (128 * 128);
-  cp.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0 && p.out_row % 16 == 0 && p.out_head % 16 == 0;
   const int k_heads = p.v_heads / p.group;
   CUtensorMap q, k, v;
   if (!make_map(&q, p.q, p.rows, k_heads, p.q_row, p.q_head) || !make_map(&k, p.k, p.rows, k_heads, p.k_row, p.k_head) ||

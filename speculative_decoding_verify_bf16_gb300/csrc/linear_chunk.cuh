@@ -23,7 +23,7 @@
 //
 // Tensor memory holds U (128 columns), scores and P (128; P overwrites the scores it came
 // from), D (128) and two buffers of k' for 32 tokens (96).  Shared memory holds a ring of
-// five 32 KB tiles (k, q, v of a chunk; 128-byte swizzled rows, so that a tile serves as
+// five 32 KB tiles (k, v, q of a chunk; 128-byte swizzled rows, so that a tile serves as
 // an operand along either dimension) and S in two parts.
 //
 // Warps: 0 copies tiles, 1 issues the products, 2 sums the decays, and four groups of
@@ -31,7 +31,8 @@
 // (16-19).  The products of a chunk take 8 x 512 cycles on the tensor cores, its
 // 128 KB of q, k, v and o about 5,500 at an SM's share of the HBM rate: the groups work
 // beside each other so that the larger of the two counts.  A chunk's products go in the
-// order QK, KV, QS, PV: P is made beside KV and QS, the next S beside QS and PV.
+// order KV (first half), QK, KV (second half), QS, PV: P is made beside the three after
+// QK, the next S beside QS and PV, k' of the next tokens beside whatever is not KV.
 #pragma once
 
 #include <cuda.h>
@@ -48,7 +49,7 @@ namespace specv {
 constexpr int kChunk = 128;
 constexpr int kChunkThreads = 640;
 // Registers a thread of each warpgroup; their sum is what a launch must bring (5 x 96).
-constexpr int kRegsMisc = 80, kRegsScores = 72, kRegsOut = 72, kRegsState = 168, kRegsKey = 88;
+constexpr int kRegsMisc = 80, kRegsScores = 72, kRegsOut = 80, kRegsState = 168, kRegsKey = 80;
 constexpr int kChunkRegs = kRegsMisc + kRegsScores + kRegsOut + kRegsState + kRegsKey;
 constexpr int kTile = 32 * 1024;      // 128 rows of 128 bf16: two halves of 64 columns
 constexpr int kHalf = kTile / 2;
@@ -81,23 +82,19 @@ struct ChunkParams {
                       // call; r + 1, the state after segment r begun from zero
   float* local_decay; // [segments][lanes][heads]: whole decay of segment r
   int32_t segments;
-  int32_t out_vec;    // out rows take 32-byte stores
 };
 
-// Waits for a phase; gives up after the time limit or when another warp has.
+// Waits for a phase; gives up after some seconds or when another warp has.  (Few
+// instructions: the roles' code shares the instruction cache, and a warp that misses there
+// holds up all that wait for it.)
+constexpr uint32_t kPolls = 1u << 27;
 __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 31u) == 0) {
-      if (*static_cast<volatile int*>(abort)) return false;
-      if (global_ns() - t0 > kWaitLimitNs) {
-        *static_cast<volatile int*>(abort) = 1;
-        return false;
-      }
+  for (uint32_t i = 0; !mbar_test_wait(bar, parity); ++i)
+    if (*static_cast<volatile int*>(abort) || i == kPolls) {
+      *static_cast<volatile int*>(abort) = 1;
+      return false;
     }
-  }
+  return true;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
   return __all_sync(0xFFFFFFFFu, chunk_wait(bar, parity, abort));
@@ -232,7 +229,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const uint32_t row = quarter + lane;
   const uint32_t tmq = tm + (quarter << 16);
   const int n_chunks = active ? sg.c1 - sg.c0 : 0;
-  constexpr int kLoads = STATES ? 2 : 3;  // tiles of a chunk: k, (q,) v
+  constexpr int kLoads = STATES ? 2 : 3;  // tiles of a chunk: k, v (, q)
 
   if (warp < 4) registers_shrink<kRegsMisc>();
   if (warp == 0) {
@@ -242,14 +239,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       bool ok = true;
       for (int c = 0; c < n_chunks && ok; ++c) {
         const int z = sg.first + (sg.c0 + c) * kChunk;
+#pragma unroll 1
         for (int j = 0; j < kLoads; ++j) {
           const int slot = issued % kRing, turn = issued / kRing;
           if (turn > 0 && !chunk_wait(&sm.empty[slot], (turn - 1) & 1, &sm.abort)) {
             ok = false;
             break;
           }
-          const CUtensorMap* map = j == 0 ? &map_k : (j == kLoads - 1 ? &map_v : &map_q);
-          const int hh = j == kLoads - 1 ? sg.h : sg.h / p.group;
+          const CUtensorMap* map = j == 0 ? &map_k : (j == 1 ? &map_v : &map_q);
+          const int hh = j == 1 ? sg.h : sg.h / p.group;
           mbar_arrive_expect_tx(&sm.full[slot], kTile);
           tma_load_3d(sm.ring[slot], map, 0, hh, z, &sm.full[slot]);
           tma_load_3d(sm.ring[slot] + kHalf, map, 64, hh, z, &sm.full[slot]);
@@ -263,19 +261,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
+    {
+      const uint32_t lead = elect_one();
       constexpr uint32_t kSame = mma_desc(128, 128, false), kRows = mma_desc(128, 128, true);
       int step = 0;  // k' buffers used
       for (int c = 0; c < n_chunks; ++c) {
         const uint32_t ph = c & 1;
         const int n = min(kChunk, sg.count - (sg.c0 + c) * kChunk);
         const int steps = (n + 15) / 16;  // products over the chunk's tokens stop at its last
-        const int lk = kLoads * c, lq = lk + 1, lv = lk + kLoads - 1;
+        const int lk = kLoads * c, lv = lk + 1, lq = lk + 2;
         uint64_t* const fk = &sm.full[lk % kRing];
         uint64_t* const fv = &sm.full[lv % kRing];
-        // One thread issues every product: the loops are unrolled over descriptors that
-        // differ by constants, since address arithmetic between them would hold up the
-        // tensor cores (measured: 300 cycles a product against the 64 it takes).
+        // (Loops of one product, not unrolled: the warp issues one in less than the 64
+        // cycles it takes, as long as its code stays in the instruction cache.)
         const uint32_t dq = smem_desc(smem_addr(sm.ring[lq % kRing]), 16);
         const uint32_t dk = smem_desc(smem_addr(sm.ring[lk % kRing]), 16);
         const uint32_t dv = smem_desc(smem_addr(sm.ring[lv % kRing]), kHalf);
@@ -283,115 +281,114 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         auto kv = [&](int first, int last) {
           for (int t = first * 2; t < min(last * 2, steps); t += 2, ++step) {
             const int buf = step & 1;
-            if (!chunk_wait(&sm.kp_full[buf], (step >> 1) & 1, &sm.abort)) return false;
+            if (!warp_wait(&sm.kp_full[buf], (step >> 1) & 1, &sm.abort)) return false;
             tc_fence_after();
             const uint32_t parts = tm + kColK + buf * kColKBuf, rows = dv + t * (2048 / 16);
-#pragma unroll
-            for (int i = 0; i < 6; ++i) {
-              const int part = 2 - i / 2, s = i % 2;
-              if (t + s < steps)
-                mma_ts(tm + kColU, parts + part * 16 + s * 8, rows + s * (2048 / 16), kRows, i > 0 || t > 0);
-            }
-            mma_commit(&sm.kp_empty[buf]);
+#pragma unroll 1
+            for (int i = 0; i < 6; ++i)  // the least part first
+              if (t + (i & 1) < steps)
+                mma_ts(lead, tm + kColU, parts + 32 - (i >> 1) * 16 + (i & 1) * 8, rows + (i & 1) * (2048 / 16), kRows,
+                       i + t > 0);
+            mma_commit(lead, &sm.kp_empty[buf]);
           }
           return true;
         };
-        if (!chunk_wait(fk, (lk / kRing) & 1, &sm.abort)) break;
+        if (!warp_wait(fv, (lv / kRing) & 1, &sm.abort)) break;
+        if (n < kChunk && !warp_wait(&sm.v_clean, 0, &sm.abort)) break;
+        if (c > 0 && !warp_wait(&sm.u_free, ph ^ 1, &sm.abort)) break;
+        if (!kv(0, 2)) break;
         if (!STATES) {
-          if (!chunk_wait(&sm.full[lq % kRing], (lq / kRing) & 1, &sm.abort)) break;
+          if (!warp_wait(&sm.full[lq % kRing], (lq / kRing) & 1, &sm.abort)) break;
+          if (!warp_wait(fk, (lk / kRing) & 1, &sm.abort)) break;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int s = 0; s < 8; ++s) {
             const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) / 16;
-            mma_ss(tm + kColP, dq + off, dk + off, kSame, s > 0);
+            mma_ss(lead, tm + kColP, dq + off, dk + off, kSame, s > 0);
           }
-          mma_commit(&sm.scores_full);
-          mma_commit(&sm.empty[lk % kRing]);
+          mma_commit(lead, &sm.scores_full);
+          mma_commit(lead, &sm.empty[lk % kRing]);
         } else {
-          mbar_arrive(&sm.empty[lk % kRing]);
+          if (lead) mbar_arrive(&sm.empty[lk % kRing]);
         }
-        if (!chunk_wait(fv, (lv / kRing) & 1, &sm.abort)) break;
-        if (n < kChunk && !chunk_wait(&sm.v_clean, 0, &sm.abort)) break;
-        if (c > 0 && !chunk_wait(&sm.u_free, ph ^ 1, &sm.abort)) break;
-        if (!kv(0, 4)) break;
-        mma_commit(&sm.kv_full);
+        if (!kv(2, 4)) break;
+        mma_commit(lead, &sm.kv_full);
         if (!STATES) {
-          if (!chunk_wait(&sm.s_ready, ph, &sm.abort)) break;
-          if (c > 0 && !chunk_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
+          if (!warp_wait(&sm.s_ready, ph, &sm.abort)) break;
+          if (c > 0 && !warp_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
           tc_fence_after();
           const uint32_t dhi = smem_desc(smem_addr(sm.s_hi), kHalf), dlo = smem_desc(smem_addr(sm.s_lo), kHalf);
-#pragma unroll
+#pragma unroll 1
           for (int s = 0; s < 16; ++s)
-            mma_ss(tm + kColD, dq + (((s & 7) >> 2) * kHalf + (s & 3) * 32) / 16, (s < 8 ? dlo : dhi) + (s & 7) * (2048 / 16),
-                   kRows, s > 0);
-          mma_commit(&sm.qs_full);
-          mma_commit(&sm.empty[lq % kRing]);
-          mbar_arrive_n(&sm.empty[lq % kRing], 4);
+            mma_ss(lead, tm + kColD, dq + (((s >> 2) & 1) * kHalf + (s & 3) * 32) / 16,
+                   (s < 8 ? dlo : dhi) + (s & 7) * (2048 / 16), kRows, s > 0);
+          mma_commit(lead, &sm.qs_full);
+          mma_commit(lead, &sm.empty[lq % kRing]);
+          if (lead) mbar_arrive_n(&sm.empty[lq % kRing], 4);
         }
         if (!STATES) {
-          if (!chunk_wait(&sm.p_ready, ph, &sm.abort) || !chunk_wait(&sm.d_scaled, ph, &sm.abort)) break;
+          if (!warp_wait(&sm.p_ready, ph, &sm.abort) || !warp_wait(&sm.d_scaled, ph, &sm.abort)) break;
           tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int part = 1 - i / 8, s = i % 8;
-            if (s < steps)
-              mma_ts(tm + kColD, tm + kColP + (s >> 1) * 32 + part * 16 + (s & 1) * 8, dv + s * (2048 / 16), kRows, true);
-          }
-          mma_commit(&sm.o_full);
+#pragma unroll 1
+          for (int part = 1; part >= 0; --part)
+#pragma unroll 1
+            for (int s = 0; s < steps; ++s)
+              mma_ts(lead, tm + kColD, tm + kColP + part * 16 + (s >> 1) * 32 + (s & 1) * 8, dv + s * (2048 / 16), kRows, true);
+          mma_commit(lead, &sm.o_full);
         }
-        mma_commit(&sm.empty[lv % kRing]);
-        mbar_arrive_n(&sm.empty[lv % kRing], 4);
+        mma_commit(lead, &sm.empty[lv % kRing]);
+        if (lead) mbar_arrive_n(&sm.empty[lv % kRing], 4);
       }
       // Tensor memory is given back only after the last product.
-      mma_commit(&sm.drain);
+      mma_commit(lead, &sm.drain);
       mbar_wait_bounded(&sm.drain, 0);
     }
-    __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ decays
     // Fixed point with 32 fractional bits: sums and differences are exact, whatever
-    // large decays stand between two tokens.
-    float g[4];
-    auto fetch = [&](int c) {
-      for (int i = 0; i < 4; ++i) {
-        const int t = (sg.c0 + c) * kChunk + lane * 4 + i;
-        g[i] = t < sg.count ? __ldg(p.log_decay + (sg.first + static_cast<int64_t>(t)) * p.decay_row + sg.h * p.decay_head)
-                            : 0.f;
-      }
+    // large decays stand between two tokens.  32 tokens at a time, a lane each.
+    auto fetch = [&](int t) {
+      t += sg.c0 * kChunk + lane;
+      return t < sg.count ? __ldg(p.log_decay + (sg.first + static_cast<int64_t>(t)) * p.decay_row + sg.h * p.decay_head)
+                          : 0.f;
     };
-    if (n_chunks > 0) fetch(0);
-    for (int c = 0; c < n_chunks; ++c) {
-      const int buf = c & 1;
-      long long sum[4];
-      bool bad = false;
-      for (int i = 0; i < 4; ++i) {
-        float hi = g[i] * kLog2eHi;
-        float lo = fmaf(g[i], kLog2eHi, -hi) + g[i] * kLog2eLo;
-        if (!(hi < 128.f)) bad = true;  // NaN, or a decay whose factor is infinite in fp32
-        if (!(hi > kDecayFloor)) {
-          hi = kDecayFloor;
-          lo = 0.f;
-        }
-        sum[i] = bad ? 0 : __float2ll_rn(hi * 4294967296.f) + __float2ll_rn(lo * 4294967296.f);
-        if (i > 0) sum[i] += sum[i - 1];
+    float next = n_chunks > 0 ? fetch(0) : 0.f;
+    long long before = 0;
+    float poison = 0.f;  // NaN once the chunk holds a NaN or a factor infinite in fp32
+#pragma unroll 1
+    for (int t = 0; t < n_chunks * kChunk; t += 32) {
+      const int c = t / kChunk, buf = c & 1;
+      const float g = next;
+      if (t + 32 < n_chunks * kChunk) next = fetch(t + 32);
+      if (t % kChunk == 0) {
+        if (c >= 2 && !warp_wait(&sm.g_empty[buf], ((c >> 1) - 1) & 1, &sm.abort)) break;
+        before = 0;
+        poison = 0.f;
       }
-      bad = __any_sync(0xFFFFFFFFu, bad);
-      long long run = sum[3];
+      float hi = g * kLog2eHi;
+      float lo = fmaf(g, kLog2eHi, -hi) + g * kLog2eLo;
+      if (__any_sync(0xFFFFFFFFu, !(hi < 128.f))) poison = __uint_as_float(0x7FC00000u);
+      if (!(hi > kDecayFloor)) {
+        hi = kDecayFloor;
+        lo = 0.f;
+      }
+      long long sum = __float2ll_rn(hi * 4294967296.f) + __float2ll_rn(lo * 4294967296.f);
+#pragma unroll 1
       for (int d = 1; d < 32; d <<= 1) {
-        const long long up = __shfl_up_sync(0xFFFFFFFFu, run, d);
-        if (lane >= d) run += up;
+        const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += up;
       }
-      run -= sum[3];
-      if (c + 1 < n_chunks) fetch(c + 1);
-      if (c >= 2 && !warp_wait(&sm.g_empty[buf], ((c >> 1) - 1) & 1, &sm.abort)) break;
-      for (int i = 0; i < 4; ++i) {
-        const float hi = __ll2float_rn(run + sum[i]);
-        const float lo = __ll2float_rn(run + sum[i] - __float2ll_rn(hi));
-        sm.g_hi[buf][lane * 4 + i] = bad ? __uint_as_float(0x7FC00000u) : hi * -0x1p-32f;
-        sm.g_lo[buf][lane * 4 + i] = lo * -0x1p-32f;
+      sum += before;
+      before = __shfl_sync(0xFFFFFFFFu, sum, 31);
+      hi = __ll2float_rn(sum);
+      lo = __ll2float_rn(sum - __float2ll_rn(hi));
+      sm.g_hi[buf][t % kChunk + lane] = fmaf(hi, -0x1p-32f, poison);
+      sm.g_lo[buf][t % kChunk + lane] = lo * -0x1p-32f;
+      if (t % kChunk == kChunk - 32) {
+        // (every use of a chunk's sums takes in the last one, directly or by the state)
+        __threadfence_block();
+        warp_arrive(&sm.g_full[buf]);
       }
-      __threadfence_block();
-      warp_arrive(&sm.g_full[buf]);
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------- scores to P
@@ -403,36 +400,48 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const f32x2 ghi = pair(-sm.g_hi[buf][row], -sm.g_hi[buf][row]), glo = pair(-sm.g_lo[buf][row], -sm.g_lo[buf][row]);
         if (!warp_wait(&sm.scores_full, c & 1, &sm.abort)) break;
         tc_fence_after();
+        uint32_t keep[8];
 #pragma unroll 1
-        for (int piece = 0; piece < 4; ++piece) {
-          uint32_t hi[16], lo[16];
-          if (piece * 32 > static_cast<int>(quarter)) {  // tokens after all of this warp's rows
+        for (int piece = 0; piece < 8; ++piece) {
+          const int j0 = piece * 16;  // tokens j0 .. j0 + 15
+          uint32_t hi[8], lo[8];
+          if (j0 >= static_cast<int>(quarter) + 32) {  // all after this warp's rows
 #pragma unroll
-            for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0u;
+            for (int i = 0; i < 8; ++i) hi[i] = lo[i] = 0u;
           } else {
-            uint32_t s[32];
-            tmem_ld32(s, tmq + kColP + piece * 32);
+            uint32_t s[16];
+            tmem_ld16(s, tmq + kColP + j0);
             tmem_wait_ld();
-            const bool diagonal = piece * 32 == static_cast<int>(quarter);
+            const int seen = static_cast<int>(row) - j0;  // the last token this row sees
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const ulonglong2 jh = *reinterpret_cast<const ulonglong2*>(&sm.g_hi[buf][piece * 32 + i]);
-              const ulonglong2 jl = *reinterpret_cast<const ulonglong2*>(&sm.g_lo[buf][piece * 32 + i]);
+            for (int i = 0; i < 16; i += 4) {
+              const ulonglong2 jh = *reinterpret_cast<const ulonglong2*>(&sm.g_hi[buf][j0 + i]);
+              const ulonglong2 jl = *reinterpret_cast<const ulonglong2*>(&sm.g_lo[buf][j0 + i]);
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                // (g arrays hold -G)
+              for (int e = 0; e < 4; e += 2) {
+                // (the arrays hold -G)
                 const f32x2 d = add2(add2(ghi, e ? jh.y : jh.x), add2(glo, e ? jl.y : jl.x));
                 f32x2 w = mul2(pair(ex2_approx(first_of(d)), ex2_approx(second_of(d))),
-                               pair(__uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1])));
-                if (diagonal)  // (a select: what is masked may be NaN)
-                  w = pair(i + 2 * e > lane ? 0.f : first_of(w), i + 2 * e + 1 > lane ? 0.f : second_of(w));
-                hi[i / 2 + e] = upper(w);
-                lo[i / 2 + e] = rounded(rest(w));
+                               pair(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1])));
+                // (a select: what is masked may be NaN)
+                w = pair(i + e > seen ? 0.f : first_of(w), i + e + 1 > seen ? 0.f : second_of(w));
+                hi[(i + e) / 2] = upper(w);
+                lo[(i + e) / 2] = rounded(rest(w));
               }
             }
           }
-          tmem_st16(tmq + kColP + piece * 32, hi);
-          tmem_st16(tmq + kColP + piece * 32 + 16, lo);
+          // Columns of P: for each 32 tokens 16 of upper and 16 of lower parts.
+          const uint32_t dst = tmq + kColP + (j0 & ~31) + (j0 & 16) / 2;
+          if ((j0 & 16) == 0) {
+            // The scores of the next 16 tokens lie where the lower parts of these go.
+#pragma unroll
+            for (int i = 0; i < 8; ++i) keep[i] = lo[i];
+            tmem_st8(dst, hi);
+          } else {
+            tmem_st8(dst, hi);
+            tmem_st8(dst + 16 - 8, keep);
+            tmem_st8(dst + 16, lo);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -489,21 +498,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             tc_fence_before();
             warp_arrive(&sm.d_free);
           }
-          if (t >= sg.count) continue;
-          __nv_bfloat16* at = dst + half * 64;
-          if (cp.out_vec) {  // whole 32-byte sectors
+          if (t < sg.count) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at + 2 * i), "r"(o[i]),
-                           "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]),
-                           "r"(o[i + 7])
+            for (int i = 0; i < 32; i += 8)  // whole 32-byte sectors
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + half * 64 + 2 * i),
+                           "r"(o[i]), "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]),
+                           "r"(o[i + 6]), "r"(o[i + 7])
                            : "memory");
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              at[2 * i] = __ushort_as_bfloat16(static_cast<unsigned short>(o[i]));
-              at[2 * i + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(o[i] >> 16));
-            }
           }
         }
       }
@@ -538,23 +539,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
     }
-    // S in two parts to shared memory, for the chunk's QS.
-    auto publish = [&] {
-#pragma unroll
-      for (int i = 0; i < 64; i += 4) {
-        const uint32_t unit = tile_unit(row, i / 4);
-        *reinterpret_cast<uint4*>(sm.s_hi + unit) = make_uint4(upper(S[i]), upper(S[i + 1]), upper(S[i + 2]), upper(S[i + 3]));
-        *reinterpret_cast<uint4*>(sm.s_lo + unit) = make_uint4(rounded(rest(S[i])), rounded(rest(S[i + 1])),
-                                                               rounded(rest(S[i + 2])), rounded(rest(S[i + 3])));
-      }
-      fence_async_smem();
-      warp_arrive(&sm.s_ready);
-    };
-    if (!STATES && n_chunks > 0) publish();
     bool ok = true;
     float total = 1.f;  // the segment's whole decay
     for (int c = 0; c < n_chunks; ++c) {
       const int buf = c & 1;
+      if (!STATES) {
+        // S in two parts to shared memory for the chunk's QS, the last chunk's done.
+        if (c > 0 && !(ok = warp_wait(&sm.qs_full, (c - 1) & 1, &sm.abort))) break;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          const uint32_t unit = tile_unit(row, i / 4);
+          *reinterpret_cast<uint4*>(sm.s_hi + unit) = make_uint4(upper(S[i]), upper(S[i + 1]), upper(S[i + 2]), upper(S[i + 3]));
+          *reinterpret_cast<uint4*>(sm.s_lo + unit) = make_uint4(rounded(rest(S[i])), rounded(rest(S[i + 1])),
+                                                                 rounded(rest(S[i + 2])), rounded(rest(S[i + 3])));
+        }
+        fence_async_smem();
+        warp_arrive(&sm.s_ready);
+      }
       if (!(ok = warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort))) break;
       const float decay = exp2f(-(sm.g_hi[buf][kChunk - 1] + sm.g_lo[buf][kChunk - 1]));
       total *= decay;
@@ -574,35 +575,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       tc_fence_before();
       warp_arrive(&sm.u_free);
-      if (!STATES && c + 1 < n_chunks) {
-        if (!(ok = warp_wait(&sm.qs_full, c & 1, &sm.abort))) break;  // the last parts have been read
-        publish();
-      }
     }
     if (n_chunks > 0 && ok) {
       float* dst = STATES ? cp.local + ((sg.seg + 1) * heads + head) * (128 * 128) : (sg.last ? state_out : nullptr);
       if (STATES && row == 0) cp.local_decay[sg.seg * heads + head] = total;
-      float bad = 0.f;
+      f32x2 bad = 0ull;  // 0 times S: NaN where S is not finite
 #pragma unroll
       for (int i = 0; i < 64; i += 2) {
-        const float4 x = make_float4(first_of(S[i]), second_of(S[i]), first_of(S[i + 1]), second_of(S[i + 1]));
-        bad += (x.x - x.x) + (x.y - x.y) + (x.z - x.z) + (x.w - x.w);
-        if (dst != nullptr) *reinterpret_cast<float4*>(dst + at + 2 * i) = x;
+        bad = fma2(S[i], 0ull, fma2(S[i + 1], 0ull, bad));
+        if (dst != nullptr)
+          *reinterpret_cast<float4*>(dst + at + 2 * i) =
+              make_float4(first_of(S[i]), second_of(S[i]), first_of(S[i + 1]), second_of(S[i + 1]));
       }
-      if (!STATES && sg.last && bad != 0.f && p.lane_status != nullptr) p.lane_status[sg.b] = SPEC_ERR_NONFINITE;
+      if (!STATES && sg.last && first_of(bad) + second_of(bad) != 0.f && p.lane_status != nullptr) p.lane_status[sg.b] = SPEC_ERR_NONFINITE;
     }
   } else if (warp >= 16) {
     // ---------------------------------------------------------------------- k'
-    // Row `row` of k'^T is one of the 128 components of k: a thread reads its component
-    // of every token and writes it, times the token's weight, along its lane.
+    // Lane i of k'^T is component i of k, along the tokens.  Transposing loads bring a
+    // thread two tokens of one component, weighted pairs of which go out as they lie.
     registers_shrink<kRegsKey>();
     int step = 0;
     bool ok = true;
-    const uint32_t unit = row >> 3;
     for (int c = 0; c < n_chunks && ok; ++c) {
       const int buf = c & 1;
       const int n = min(kChunk, sg.count - (sg.c0 + c) * kChunk);
-      const int lk = kLoads * c, lv = lk + kLoads - 1;
+      const int lk = kLoads * c, lv = lk + 1;
       if (!(ok = warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort))) break;
       if (n < kChunk) {  // rows past the lane take part in products (times 0): make them 0
         if (!(ok = warp_wait(&sm.full[lv % kRing], (lv / kRing) & 1, &sm.abort))) break;
@@ -615,32 +612,44 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       const float last_hi = sm.g_hi[buf][kChunk - 1], last_lo = sm.g_lo[buf][kChunk - 1];
       if (!(ok = warp_wait(&sm.full[lk % kRing], (lk / kRing) & 1, &sm.abort))) break;
-      const uint8_t* tile = sm.ring[lk % kRing] + (unit >> 3) * kHalf + (row & 7) * 2;
+      const uint32_t tile = smem_addr(sm.ring[lk % kRing]);
       for (int t0 = 0; t0 < n; t0 += 32, ++step) {
         const int kb = step & 1;
-        uint32_t hi[16], mid[16], lo[16];
         // Each lane has the weight of one of the 32 tokens.
         const float weight = exp2f((sm.g_hi[buf][t0 + lane] - last_hi) + (sm.g_lo[buf][t0 + lane] - last_lo));
+        const int pick = 2 * (lane & 3);
+        f32x2 w[4];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const f32x2 w = pair(__shfl_sync(0xFFFFFFFFu, weight, i), __shfl_sync(0xFFFFFFFFu, weight, i + 1));
-          const uint8_t* src = tile + (t0 + i) * 128;
-          const uint32_t raw0 = *reinterpret_cast<const uint16_t*>(src + (((unit ^ i) & 7) << 4));
-          const uint32_t raw1 = *reinterpret_cast<const uint16_t*>(src + 128 + (((unit ^ (i + 1)) & 7) << 4));
-          f32x2 x = mul2(w, pair(__uint_as_float(raw0 << 16), __uint_as_float(raw1 << 16)));
-          if (t0 + 32 > n)  // (rows past the lane may be NaN)
-            x = pair(t0 + i < n ? first_of(x) : 0.f, t0 + i + 1 < n ? second_of(x) : 0.f);
-          hi[i / 2] = upper(x);
-          x = rest(x);
-          mid[i / 2] = upper(x);
-          lo[i / 2] = upper(rest(x));
-        }
-        if (step >= 2 && !(ok = warp_wait(&sm.kp_empty[kb], ((step >> 1) - 1) & 1, &sm.abort))) break;
-        tc_fence_after();
+        for (int m = 0; m < 4; ++m)
+          w[m] = pair(__shfl_sync(0xFFFFFFFFu, weight, 8 * m + pick), __shfl_sync(0xFFFFFFFFu, weight, 8 * m + pick + 1));
         const uint32_t dst = tmq + kColK + kb * kColKBuf;
-        tmem_st16(dst, hi);
-        tmem_st16(dst + 16, mid);
-        tmem_st16(dst + 32, lo);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t raw[4];
+            ldmatrix_trans(raw, tile + tile_unit(t0 + lane, quarter / 8 + half * 2 + i));
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              f32x2 x = mul2(w[m], pair(__uint_as_float(raw[m] << 16), __uint_as_float(raw[m] & 0xFFFF0000u)));
+              if (t0 + 32 > n)  // (rows past the lane may be NaN)
+                x = pair(t0 + 8 * m + pick < n ? first_of(x) : 0.f, t0 + 8 * m + pick + 1 < n ? second_of(x) : 0.f);
+              hi[2 * m + i] = upper(x);
+              x = rest(x);
+              mid[2 * m + i] = upper(x);
+              lo[2 * m + i] = upper(rest(x));
+            }
+          }
+          if (half == 0) {
+            if (step >= 2 && !(ok = warp_wait(&sm.kp_empty[kb], ((step >> 1) - 1) & 1, &sm.abort))) break;
+            tc_fence_after();
+          }
+          tmem_st_16x16(dst + (half << 20), hi);
+          tmem_st_16x16(dst + (half << 20) + 16, mid);
+          tmem_st_16x16(dst + (half << 20) + 32, lo);
+        }
+        if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&sm.kp_full[kb]);
