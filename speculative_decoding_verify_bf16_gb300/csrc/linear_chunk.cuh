@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>(smem_raw);
   const LinearParams& p = cp.p;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   Segment sg;
   sg.h = blockIdx.x % p.v_heads;
   sg.b = blockIdx.x / p.v_heads % p.lanes;
@@ -261,88 +261,101 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products
-    {
-      const uint32_t lead = elect_one();
-      constexpr uint32_t kSame = mma_desc(128, 128, false), kRows = mma_desc(128, 128, true);
-      int step = 0;  // k' buffers used
-      for (int c = 0; c < n_chunks; ++c) {
-        const uint32_t ph = c & 1;
-        const int n = min(kChunk, sg.count - (sg.c0 + c) * kChunk);
-        const int steps = (n + 15) / 16;  // products over the chunk's tokens stop at its last
-        const int lk = kLoads * c, lv = lk + 1, lq = lk + 2;
-        uint64_t* const fk = &sm.full[lk % kRing];
-        uint64_t* const fv = &sm.full[lv % kRing];
-        // (Loops of one product, not unrolled: the warp issues one in less than the 64
-        // cycles it takes, as long as its code stays in the instruction cache.)
-        const uint32_t dq = smem_desc(smem_addr(sm.ring[lq % kRing]), 16);
-        const uint32_t dk = smem_desc(smem_addr(sm.ring[lk % kRing]), 16);
-        const uint32_t dv = smem_desc(smem_addr(sm.ring[lv % kRing]), kHalf);
-        // U over the tokens of k' buffers first .. last - 1.
-        auto kv = [&](int first, int last) {
-          for (int t = first * 2; t < min(last * 2, steps); t += 2, ++step) {
-            const int buf = step & 1;
-            if (!warp_wait(&sm.kp_full[buf], (step >> 1) & 1, &sm.abort)) return false;
+    // What follows from a shuffle is the same in all lanes also to the compiler, which
+    // then keeps loop counters and descriptors in uniform registers: a product is a few
+    // instructions, issued well within the 64 cycles it takes.
+    const uint32_t lead = elect_one();
+    const int loops = __shfl_sync(0xFFFFFFFFu, n_chunks, 0);
+    const int rows_left = __shfl_sync(0xFFFFFFFFu, sg.count - sg.c0 * kChunk, 0);
+    const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0);
+    constexpr uint32_t kSame = mma_desc(128, 128, false), kRows = mma_desc(128, 128, true);
+    const uint32_t ring = smem_desc(smem_addr(sm.ring[0]), kHalf);  // (for K-major tiles the piece distance is not used)
+    const uint32_t dlo = smem_desc(smem_addr(sm.s_lo), kHalf), dhi = smem_desc(smem_addr(sm.s_hi), kHalf);
+    int kb = 0, kphase = 0;  // the k' buffer and its phase
+    int slot = 0, phase = 0; // the ring's slot of this chunk's k and its phase
+    for (int c = 0; c < loops; ++c) {
+      const uint32_t ph = c & 1;
+      const int n = min(kChunk, rows_left - c * kChunk);
+      const int bufs = (n + 31) / 32;  // products over the chunk's tokens stop at the last 32 that hold any
+      const int sk = slot, pk = phase;
+      auto advance = [&] {
+        if (++slot == kRing) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
+      advance();
+      const int sv = slot, pv = phase;
+      advance();
+      const int sq = slot, pq = phase;
+      if (!STATES) advance();
+      const uint32_t dk = ring + sk * (kTile / 16), dv = ring + sv * (kTile / 16), dq = ring + sq * (kTile / 16);
+      if (!warp_wait(&sm.full[sv], pv, &sm.abort)) break;
+      if (n < kChunk && !warp_wait(&sm.v_clean, 0, &sm.abort)) break;
+      if (c > 0 && !warp_wait(&sm.u_free, ph ^ 1, &sm.abort)) break;
+      bool ok = true;
+#pragma unroll 1
+      for (int t = 0; t < bufs || t == 2; ++t) {
+        if (t == 2) {  // QK between the halves of KV (and behind a short chunk's)
+          if (!STATES) {
+            if (!(ok = warp_wait(&sm.full[sq], pq, &sm.abort) && warp_wait(&sm.full[sk], pk, &sm.abort))) break;
             tc_fence_after();
-            const uint32_t parts = tm + kColK + buf * kColKBuf, rows = dv + t * (2048 / 16);
-#pragma unroll 1
-            for (int i = 0; i < 6; ++i)  // the least part first
-              if (t + (i & 1) < steps)
-                mma_ts(lead, tm + kColU, parts + 32 - (i >> 1) * 16 + (i & 1) * 8, rows + (i & 1) * (2048 / 16), kRows,
-                       i + t > 0);
-            mma_commit(lead, &sm.kp_empty[buf]);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+              const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) / 16;
+              mma_ss(lead, tmu + kColP, dq + off, dk + off, kSame, s > 0);
+            }
+            mma_commit(lead, &sm.scores_full);
+            mma_commit(lead, &sm.empty[sk]);
+          } else if (lead) {
+            mbar_arrive(&sm.empty[sk]);
           }
-          return true;
-        };
-        if (!warp_wait(fv, (lv / kRing) & 1, &sm.abort)) break;
-        if (n < kChunk && !warp_wait(&sm.v_clean, 0, &sm.abort)) break;
-        if (c > 0 && !warp_wait(&sm.u_free, ph ^ 1, &sm.abort)) break;
-        if (!kv(0, 2)) break;
-        if (!STATES) {
-          if (!warp_wait(&sm.full[lq % kRing], (lq / kRing) & 1, &sm.abort)) break;
-          if (!warp_wait(fk, (lk / kRing) & 1, &sm.abort)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int s = 0; s < 8; ++s) {
-            const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) / 16;
-            mma_ss(lead, tm + kColP, dq + off, dk + off, kSame, s > 0);
-          }
-          mma_commit(lead, &sm.scores_full);
-          mma_commit(lead, &sm.empty[lk % kRing]);
-        } else {
-          if (lead) mbar_arrive(&sm.empty[lk % kRing]);
+          if (bufs <= 2) break;
         }
-        if (!kv(2, 4)) break;
-        mma_commit(lead, &sm.kv_full);
-        if (!STATES) {
-          if (!warp_wait(&sm.s_ready, ph, &sm.abort)) break;
-          if (c > 0 && !warp_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
-          tc_fence_after();
-          const uint32_t dhi = smem_desc(smem_addr(sm.s_hi), kHalf), dlo = smem_desc(smem_addr(sm.s_lo), kHalf);
-#pragma unroll 1
-          for (int s = 0; s < 16; ++s)
-            mma_ss(lead, tm + kColD, dq + (((s >> 2) & 1) * kHalf + (s & 3) * 32) / 16,
-                   (s < 8 ? dlo : dhi) + (s & 7) * (2048 / 16), kRows, s > 0);
-          mma_commit(lead, &sm.qs_full);
-          mma_commit(lead, &sm.empty[lq % kRing]);
-          if (lead) mbar_arrive_n(&sm.empty[lq % kRing], 4);
-        }
-        if (!STATES) {
-          if (!warp_wait(&sm.p_ready, ph, &sm.abort) || !warp_wait(&sm.d_scaled, ph, &sm.abort)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int part = 1; part >= 0; --part)
-#pragma unroll 1
-            for (int s = 0; s < steps; ++s)
-              mma_ts(lead, tm + kColD, tm + kColP + part * 16 + (s >> 1) * 32 + (s & 1) * 8, dv + s * (2048 / 16), kRows, true);
-          mma_commit(lead, &sm.o_full);
-        }
-        mma_commit(lead, &sm.empty[lv % kRing]);
-        if (lead) mbar_arrive_n(&sm.empty[lv % kRing], 4);
+        if (!(ok = warp_wait(&sm.kp_full[kb], kphase, &sm.abort))) break;
+        tc_fence_after();
+        const uint32_t parts = tmu + kColK + kb * kColKBuf, dvt = dv + t * (2 * 2048 / 16);
+#pragma unroll
+        for (int i = 0; i < 6; ++i)  // the least part first
+          mma_ts(lead, tmu + kColU, parts + 32 - (i >> 1) * 16 + (i & 1) * 8, dvt + (i & 1) * (2048 / 16), kRows, i + t > 0);
+        mma_commit(lead, &sm.kp_empty[kb]);
+        kb ^= 1;
+        kphase ^= kb == 0;
+        if (t == 0 && bufs == 1) t = 1;  // on to QK
       }
-      // Tensor memory is given back only after the last product.
-      mma_commit(lead, &sm.drain);
-      mbar_wait_bounded(&sm.drain, 0);
+      if (!ok) break;
+      mma_commit(lead, &sm.kv_full);
+      if (!STATES) {
+        if (!warp_wait(&sm.s_ready, ph, &sm.abort)) break;
+        if (c > 0 && !warp_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          const uint32_t ds = part == 0 ? dlo : dhi;
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma_ss(lead, tmu + kColD, dq + ((s >> 2) * kHalf + (s & 3) * 32) / 16, ds + s * (2048 / 16), kRows, part + s > 0);
+        }
+        mma_commit(lead, &sm.qs_full);
+        mma_commit(lead, &sm.empty[sq]);
+        if (lead) mbar_arrive_n(&sm.empty[sq], 4);
+        if (!warp_wait(&sm.p_ready, ph, &sm.abort) || !warp_wait(&sm.d_scaled, ph, &sm.abort)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int t = 0; t < bufs; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_ts(lead, tmu + kColD, tmu + kColP + t * 32 + 16 - (i >> 1) * 16 + (i & 1) * 8,
+                   dv + t * (2 * 2048 / 16) + (i & 1) * (2048 / 16), kRows, true);
+        mma_commit(lead, &sm.o_full);
+      }
+      mma_commit(lead, &sm.empty[sv]);
+      if (lead) mbar_arrive_n(&sm.empty[sv], 4);
     }
+    // Tensor memory is given back only after the last product.
+    mma_commit(lead, &sm.drain);
+    mbar_wait_bounded(&sm.drain, 0);
+    __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ decays
     // Fixed point with 32 fractional bits: sums and differences are exact, whatever
