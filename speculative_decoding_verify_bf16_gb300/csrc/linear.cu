@@ -198,8 +198,8 @@ bool chunkable(const LinearParams& p, spec_dtype dtype) {
   const int k_heads = p.v_heads / p.group;
   return dtype == SPEC_BF16 && p.dk == 128 && p.dv == 128 && p.rows > 0 && p.max_len >= kChunkMinLen &&
          mappable(p.q, p.q_row, p.q_head, k_heads) && mappable(p.k, p.k_row, p.k_head, k_heads) &&
-         mappable(p.v, p.v_row, p.v_head, p.v_heads) && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0 &&
-         p.out_row % 16 == 0 && p.out_head % 16 == 0 && encode_tiled() != nullptr;
+         mappable(p.v, p.v_row, p.v_head, p.v_heads) && mappable(p.out, p.out_row, p.out_head, p.v_heads) &&
+         encode_tiled() != nullptr;
 }
 
 int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args* a, void* stream) {
@@ -232,11 +232,12 @@ int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args*
   cp.local = static_cast<float*>(a->workspace);
   cp.local_decay = cp.local + static_cast<int64_t>(cp.segments) * pairs * (128 * 128);
   const int k_heads = p.v_heads / p.group;
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, out;
   if (!make_map(&q, p.q, p.rows, k_heads, p.q_row, p.q_head) || !make_map(&k, p.k, p.rows, k_heads, p.k_row, p.k_head) ||
-      !make_map(&v, p.v, p.rows, p.v_heads, p.v_row, p.v_head))
+      !make_map(&v, p.v, p.rows, p.v_heads, p.v_row, p.v_head) ||
+      !make_map(&out, p.out, p.rows, p.v_heads, p.out_row, p.out_head))
     return SPEC_ERR_CUDA;
-  void* args[] = {&cp, &q, &k, &v};
+  void* args[] = {&cp, &q, &k, &v, &out};
   if (cp.segments > 1) {
     const int rc = launch(states, static_cast<unsigned>(pairs * (cp.segments - 1)), specv::kChunkThreads, smem, args, stream);
     if (rc != SPEC_OK) return rc;

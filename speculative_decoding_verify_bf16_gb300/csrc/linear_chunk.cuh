@@ -26,9 +26,9 @@
 // five 32 KB tiles (k, v, q of a chunk; 128-byte swizzled rows, so that a tile serves as
 // an operand along either dimension) and S in two parts.
 //
-// Warps: 0 copies tiles, 1 issues the products, 2 sums the decays, and four groups of
-// four do what lies between the products: scores to P (4-7), D (8-11), S (12-15), k'
-// (16-19).  The products of a chunk take 8 x 512 cycles on the tensor cores, its
+// Warps: 0 copies tiles, 1 issues the products, 2 sums the decays, and five groups of
+// four do what lies between the products: scores to P (4-7), D (8-11), S (12-15), k' for
+// every other 32 tokens (16-19 and 20-23).  The products of a chunk take 8 x 512 cycles on the tensor cores, its
 // 128 KB of q, k, v and o about 5,500 at an SM's share of the HBM rate: the groups work
 // beside each other so that the larger of the two counts.  A chunk's products go in the
 // order KV (first half), QK, KV (second half), QS, PV: P is made beside the three after
@@ -47,10 +47,10 @@
 namespace specv {
 
 constexpr int kChunk = 128;
-constexpr int kChunkThreads = 640;
-// Registers a thread of each warpgroup; their sum is what a launch must bring (5 x 96).
-constexpr int kRegsMisc = 80, kRegsScores = 72, kRegsOut = 80, kRegsState = 168, kRegsKey = 80;
-constexpr int kChunkRegs = kRegsMisc + kRegsScores + kRegsOut + kRegsState + kRegsKey;
+constexpr int kChunkThreads = 768;
+// Registers a thread of each warpgroup; their sum is what a launch must bring (6 x 80).
+constexpr int kRegsMisc = 64, kRegsScores = 72, kRegsOut = 64, kRegsState = 168, kRegsKey = 56;
+constexpr int kChunkRegs = kRegsMisc + kRegsScores + kRegsOut + kRegsState + 2 * kRegsKey;
 constexpr int kTile = 32 * 1024;      // 128 rows of 128 bf16: two halves of 64 columns
 constexpr int kHalf = kTile / 2;
 constexpr int kRing = 5;
@@ -67,9 +67,10 @@ struct ChunkSmem {
   uint8_t s_lo[kTile];
   float g_hi[2][kChunk];  // -G in two parts, chunk c in c % 2
   float g_lo[2][kChunk];
+  float to_end[4][32];    // the P group's warps: 2^(G at the end of 32 tokens - G_j)
   uint64_t full[kRing], empty[kRing];
   uint64_t g_full[2], g_empty[2];
-  uint64_t scores_full, p_ready, qs_full, d_scaled, o_full, d_free, s_ready, kv_full, u_free, v_clean, drain;
+  uint64_t scores_full, p_ready, qs_full, d_scaled, o_full, d_free, s_ready, kv_full, u_free, v_clean, o_staged, drain;
   uint64_t kp_full[2], kp_empty[2];
   uint32_t tmem;
   int abort;
@@ -87,9 +88,9 @@ struct ChunkParams {
 // Waits for a phase; gives up after some seconds or when another warp has.  (Few
 // instructions: the roles' code shares the instruction cache, and a warp that misses there
 // holds up all that wait for it.)
-constexpr uint32_t kPolls = 1u << 27;
+constexpr uint32_t kPolls = 1u << 24;
 __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, int* abort) {
-  for (uint32_t i = 0; !mbar_test_wait(bar, parity); ++i)
+  for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i)
     if (*static_cast<volatile int*>(abort) || i == kPolls) {
       *static_cast<volatile int*>(abort) = 1;
       return false;
@@ -145,7 +146,8 @@ struct Segment {
 template <bool STATES>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     linear_chunk_kernel(const ChunkParams cp, const __grid_constant__ CUtensorMap map_q,
-                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                        const __grid_constant__ CUtensorMap map_out) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>(smem_raw);
   const LinearParams& p = cp.p;
@@ -158,11 +160,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 5);
+      mbar_init(&sm.empty[i], 9);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.g_full[i], 1);
-      mbar_init(&sm.g_empty[i], STATES ? 8 : 16);
+      mbar_init(&sm.g_empty[i], STATES ? 12 : 20);
       mbar_init(&sm.kp_full[i], 4);
       mbar_init(&sm.kp_empty[i], 1);
     }
@@ -176,6 +178,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(&sm.kv_full, 1);
     mbar_init(&sm.u_free, 4);
     mbar_init(&sm.v_clean, 4);
+    mbar_init(&sm.o_staged, 4);
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
     fence_mbar_init();
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     constexpr uint32_t kSame = mma_desc(128, 128, false), kRows = mma_desc(128, 128, true);
     const uint32_t ring = smem_desc(smem_addr(sm.ring[0]), kHalf);  // (for K-major tiles the piece distance is not used)
     const uint32_t dlo = smem_desc(smem_addr(sm.s_lo), kHalf), dhi = smem_desc(smem_addr(sm.s_hi), kHalf);
-    int kb = 0, kphase = 0;  // the k' buffer and its phase
+    uint32_t kphase = 0;     // bit i: phase of k' buffer i
     int slot = 0, phase = 0; // the ring's slot of this chunk's k and its phase
     for (int c = 0; c < loops; ++c) {
       const uint32_t ph = c & 1;
@@ -312,15 +315,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           if (bufs <= 2) break;
         }
-        if (!(ok = warp_wait(&sm.kp_full[kb], kphase, &sm.abort))) break;
+        const uint32_t kb = t & 1;
+        if (!(ok = warp_wait(&sm.kp_full[kb], (kphase >> kb) & 1, &sm.abort))) break;
         tc_fence_after();
         const uint32_t parts = tmu + kColK + kb * kColKBuf, dvt = dv + t * (2 * 2048 / 16);
 #pragma unroll
         for (int i = 0; i < 6; ++i)  // the least part first
           mma_ts(lead, tmu + kColU, parts + 32 - (i >> 1) * 16 + (i & 1) * 8, dvt + (i & 1) * (2048 / 16), kRows, i + t > 0);
         mma_commit(lead, &sm.kp_empty[kb]);
-        kb ^= 1;
-        kphase ^= kb == 0;
+        kphase ^= 1u << kb;
         if (t == 0 && bufs == 1) t = 1;  // on to QK
       }
       if (!ok) break;
@@ -337,8 +340,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mma_ss(lead, tmu + kColD, dq + ((s >> 2) * kHalf + (s & 3) * 32) / 16, ds + s * (2048 / 16), kRows, part + s > 0);
         }
         mma_commit(lead, &sm.qs_full);
-        mma_commit(lead, &sm.empty[sq]);
-        if (lead) mbar_arrive_n(&sm.empty[sq], 4);
         if (!warp_wait(&sm.p_ready, ph, &sm.abort) || !warp_wait(&sm.d_scaled, ph, &sm.abort)) break;
         tc_fence_after();
 #pragma unroll 1
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mma_commit(lead, &sm.o_full);
       }
       mma_commit(lead, &sm.empty[sv]);
-      if (lead) mbar_arrive_n(&sm.empty[sv], 4);
+      if (lead) mbar_arrive_n(&sm.empty[sv], 8);
     }
     // Tensor memory is given back only after the last product.
     mma_commit(lead, &sm.drain);
@@ -410,51 +411,63 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int c = 0; c < n_chunks; ++c) {
         const int buf = c & 1;
         if (!warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort)) break;
-        const f32x2 ghi = pair(-sm.g_hi[buf][row], -sm.g_hi[buf][row]), glo = pair(-sm.g_lo[buf][row], -sm.g_lo[buf][row]);
+        const float ghi = -sm.g_hi[buf][row], glo = -sm.g_lo[buf][row];
         if (!warp_wait(&sm.scores_full, c & 1, &sm.abort)) break;
         tc_fence_after();
-        uint32_t keep[8];
+        float* const to_end = sm.to_end[warp - 4];
 #pragma unroll 1
-        for (int piece = 0; piece < 8; ++piece) {
-          const int j0 = piece * 16;  // tokens j0 .. j0 + 15
-          uint32_t hi[8], lo[8];
-          if (j0 >= static_cast<int>(quarter) + 32) {  // all after this warp's rows
+        for (int j0 = 0; j0 < kChunk; j0 += 32) {  // tokens j0 .. j0 + 31
+          uint32_t hi[16], lo[16];
+          if (j0 > static_cast<int>(quarter)) {  // all after this warp's rows
 #pragma unroll
-            for (int i = 0; i < 8; ++i) hi[i] = lo[i] = 0u;
+            for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0u;
           } else {
-            uint32_t s[16];
-            tmem_ld16(s, tmq + kColP + j0);
-            tmem_wait_ld();
-            const int seen = static_cast<int>(row) - j0;  // the last token this row sees
+            uint32_t s[32];
+            tmem_ld32(s, tmq + kColP + j0);
+            if (j0 < static_cast<int>(quarter)) {
+              // All before this warp's rows: 2^(G_i - G_j) in two factors, to the end of the
+              // 32 tokens and from there, of which neither can overflow where the whole
+              // does not.
+              const float ehi = sm.g_hi[buf][j0 + 31], elo = sm.g_lo[buf][j0 + 31];
+              const float from_end = ex2_approx((ghi + ehi) + (glo + elo));
+              __syncwarp();
+              to_end[lane] = ex2_approx((sm.g_hi[buf][j0 + lane] - ehi) + (sm.g_lo[buf][j0 + lane] - elo));
+              __syncwarp();
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const ulonglong2 jh = *reinterpret_cast<const ulonglong2*>(&sm.g_hi[buf][j0 + i]);
-              const ulonglong2 jl = *reinterpret_cast<const ulonglong2*>(&sm.g_lo[buf][j0 + i]);
+              for (int i = 0; i < 32; i += 4) {
+                const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(&to_end[i]);
 #pragma unroll
-              for (int e = 0; e < 4; e += 2) {
-                // (the arrays hold -G)
-                const f32x2 d = add2(add2(ghi, e ? jh.y : jh.x), add2(glo, e ? jl.y : jl.x));
-                f32x2 w = mul2(pair(ex2_approx(first_of(d)), ex2_approx(second_of(d))),
-                               pair(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1])));
-                // (a select: what is masked may be NaN)
-                w = pair(i + e > seen ? 0.f : first_of(w), i + e + 1 > seen ? 0.f : second_of(w));
-                hi[(i + e) / 2] = upper(w);
-                lo[(i + e) / 2] = rounded(rest(w));
+                for (int e = 0; e < 4; e += 2) {
+                  const f32x2 w = mul2(mul2(pair(from_end, from_end), e ? t.y : t.x),
+                                       pair(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1])));
+                  hi[(i + e) / 2] = upper(w);
+                  lo[(i + e) / 2] = rounded(rest(w));
+                }
+              }
+            } else {
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const ulonglong2 jh = *reinterpret_cast<const ulonglong2*>(&sm.g_hi[buf][j0 + i]);
+                const ulonglong2 jl = *reinterpret_cast<const ulonglong2*>(&sm.g_lo[buf][j0 + i]);
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                  // (the arrays hold -G)
+                  const f32x2 d = add2(add2(pair(ghi, ghi), e ? jh.y : jh.x), add2(pair(glo, glo), e ? jl.y : jl.x));
+                  f32x2 w = mul2(pair(ex2_approx(first_of(d)), ex2_approx(second_of(d))),
+                                 pair(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1])));
+                  // (a select: what is masked may be NaN)
+                  w = pair(i + e > lane ? 0.f : first_of(w), i + e + 1 > lane ? 0.f : second_of(w));
+                  hi[(i + e) / 2] = upper(w);
+                  lo[(i + e) / 2] = rounded(rest(w));
+                }
               }
             }
           }
           // Columns of P: for each 32 tokens 16 of upper and 16 of lower parts.
-          const uint32_t dst = tmq + kColP + (j0 & ~31) + (j0 & 16) / 2;
-          if ((j0 & 16) == 0) {
-            // The scores of the next 16 tokens lie where the lower parts of these go.
-#pragma unroll
-            for (int i = 0; i < 8; ++i) keep[i] = lo[i];
-            tmem_st8(dst, hi);
-          } else {
-            tmem_st8(dst, hi);
-            tmem_st8(dst + 16 - 8, keep);
-            tmem_st8(dst + 16, lo);
-          }
+          tmem_st16(tmq + kColP + j0, hi);
+          tmem_st16(tmq + kColP + j0 + 16, lo);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -491,36 +504,55 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         warp_arrive(&sm.d_scaled);
         if (!warp_wait(&sm.o_full, c & 1, &sm.abort)) break;
         tc_fence_after();
-        const int t = (sg.c0 + c) * kChunk + static_cast<int>(row);
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                             (sg.first + static_cast<int64_t>(t)) * p.out_row + sg.h * p.out_head;
+        // The chunk's q has been read: its tile takes the outputs on their way out.
+        const int slot = (kLoads * c + 2) % kRing;
+        uint8_t* tile = sm.ring[slot];
+        const int n = sg.count - (sg.c0 + c) * kChunk;
         const f32x2 scale = pair(p.scale, p.scale);
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t o[32];
+        for (int piece = 0; piece < 4; ++piece) {
+          uint32_t d[32], o[16];
+          tmem_ld32(d, tmq + kColD + piece * 32);
+          tmem_wait_ld();
 #pragma unroll
-          for (int piece = 0; piece < 4; ++piece) {
-            uint32_t d[16];
-            tmem_ld16(d, tmq + kColD + half * 64 + piece * 16);
-            tmem_wait_ld();
+          for (int i = 0; i < 16; ++i)
+            o[i] = rounded(mul2(scale, pair(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]))));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              o[piece * 8 + i] = rounded(mul2(scale, pair(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]))));
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<uint4*>(tile + tile_unit(row, piece * 4 + i / 4)) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
+        tc_fence_before();
+        warp_arrive(&sm.d_free);
+        fence_async_smem();
+        if (n >= kChunk) {
+          warp_arrive(&sm.o_staged);
+          if (warp == 8) {
+            if (!warp_wait(&sm.o_staged, c & 1, &sm.abort)) break;
+            if (lane == 0) {
+              const int z = sg.first + (sg.c0 + c) * kChunk;
+              tma_store_3d(&map_out, tile, 0, sg.h, z);
+              tma_store_3d(&map_out, tile + kHalf, 64, sg.h, z);
+              bulk_commit_group();
+              bulk_wait_group_read<0>();
+              mbar_arrive_n(&sm.empty[slot], 9);
+            }
+            __syncwarp();
           }
-          if (half == 1) {
-            tc_fence_before();
-            warp_arrive(&sm.d_free);
-          }
-          if (t < sg.count) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)  // whole 32-byte sectors
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + half * 64 + 2 * i),
-                           "r"(o[i]), "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]),
-                           "r"(o[i + 6]), "r"(o[i + 7])
-                           : "memory");
+        } else {  // (a copy would go on into the next lane's rows)
+          __syncwarp();
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + sg.h * p.out_head;
+#pragma unroll 1
+          for (int i = lane; i < 32 * 16; i += 32) {
+            const int r = static_cast<int>(quarter) + i / 16;
+            if (r < n)
+              *reinterpret_cast<uint4*>(dst + (sg.first + (sg.c0 + c) * static_cast<int64_t>(kChunk) + r) * p.out_row + (i % 16) * 8) =
+                  *reinterpret_cast<const uint4*>(tile + tile_unit(r, i % 16));
           }
         }
       }
+      // (the last copies end before the CTA does)
+      if (lane == 0) bulk_wait_group<0>();
+      __syncwarp();
     }
   } else if (warp >= 12 && warp < 16) {
     // ------------------------------------------------------------------ states
@@ -607,14 +639,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // Lane i of k'^T is component i of k, along the tokens.  Transposing loads bring a
     // thread two tokens of one component, weighted pairs of which go out as they lie.
     registers_shrink<kRegsKey>();
-    int step = 0;
+    const int kb = (warp - 16) >> 2;  // this group's buffer of k'
+    int step = 0;                     // times it has been filled
     bool ok = true;
     for (int c = 0; c < n_chunks && ok; ++c) {
       const int buf = c & 1;
       const int n = min(kChunk, sg.count - (sg.c0 + c) * kChunk);
       const int lk = kLoads * c, lv = lk + 1;
       if (!(ok = warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort))) break;
-      if (n < kChunk) {  // rows past the lane take part in products (times 0): make them 0
+      if (n < kChunk && kb == 0) {  // rows past the lane take part in products (times 0): make them 0
         if (!(ok = warp_wait(&sm.full[lv % kRing], (lv / kRing) & 1, &sm.abort))) break;
         uint8_t* vt = sm.ring[lv % kRing];
         if (static_cast<int>(row) >= n)
@@ -626,8 +659,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const float last_hi = sm.g_hi[buf][kChunk - 1], last_lo = sm.g_lo[buf][kChunk - 1];
       if (!(ok = warp_wait(&sm.full[lk % kRing], (lk / kRing) & 1, &sm.abort))) break;
       const uint32_t tile = smem_addr(sm.ring[lk % kRing]);
-      for (int t0 = 0; t0 < n; t0 += 32, ++step) {
-        const int kb = step & 1;
+      const int used = (n + 31) / 32;
+      for (int t0 = kb * 32; t0 < used * 32; t0 += 64, ++step) {
         // Each lane has the weight of one of the 32 tokens.
         const float weight = exp2f((sm.g_hi[buf][t0 + lane] - last_hi) + (sm.g_lo[buf][t0 + lane] - last_lo));
         const int pick = 2 * (lane & 3);
@@ -655,7 +688,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
           }
           if (half == 0) {
-            if (step >= 2 && !(ok = warp_wait(&sm.kp_empty[kb], ((step >> 1) - 1) & 1, &sm.abort))) break;
+            if (step >= 1 && !(ok = warp_wait(&sm.kp_empty[kb], (step - 1) & 1, &sm.abort))) break;
             tc_fence_after();
           }
           tmem_st_16x16(dst + (half << 20), hi);
