@@ -7,7 +7,9 @@
 //   o_i = scale * ( 2^G_i  S^T q_i  +  sum_{j <= i} 2^(G_i - G_j) (q_i . k_j) v_j )
 //   S'  = 2^G_last S + sum_j (2^(G_last - G_j) k_j) v_j^T
 //
-// One CTA walks the chunks of one (lane, head), or of a segment of them.  Its products:
+// A CTA takes (lane, head) pairs, or segments of their chunks, one after the other, longest
+// lanes first, and walks their chunks; tiles of the next item load while the last one's
+// products run.  A chunk's products:
 //
 //   QK  scores [token][token]  = q k^T
 //   QS  D [token][dv]          = q S,     D rows then times 2^G_i
@@ -26,9 +28,9 @@
 // five 32 KB tiles (k, v, q of a chunk; 128-byte swizzled rows, so that a tile serves as
 // an operand along either dimension) and S in two parts.
 //
-// Warps: 0 copies tiles, 1 issues the products, 2 sums the decays, and five groups of
-// four do what lies between the products: scores to P (4-7), D (8-11), S (12-15), k' for
-// every other 32 tokens (16-19 and 20-23).  The products of a chunk take 8 x 512 cycles on the tensor cores, its
+// Warps: 0 copies tiles, 1 issues the products, 2 sums the decays, 3 hands out the items,
+// and five groups of four do what lies between the products: scores to P (4-7), D (8-11),
+// S (12-15), k' for every other 32 tokens (16-19 and 20-23).  The products of a chunk take 8 x 512 cycles on the tensor cores, its
 // 128 KB of q, k, v and o about 5,500 at an SM's share of the HBM rate: the groups work
 // beside each other so that the larger of the two counts.  A chunk's products go in the
 // order KV (first half), QK, KV (second half), QS, PV: P is made beside the three after
@@ -61,6 +63,16 @@ constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;    // log2(e)
 // resets (-inf) and lowest values out of the sums.
 constexpr float kDecayFloor = -160.f;
 
+constexpr int kSortLanes = 128;       // most lanes that are taken longest first
+
+// What a CTA walks: chunks c0 .. c1 - 1 of a lane's head.
+struct ChunkItem {
+  int b, h, seg;
+  int first, count;  // first row and rows of the lane (count -1: no more items)
+  int c0, c1;
+  int last;          // the lane's last segment
+};
+
 struct ChunkSmem {
   uint8_t ring[kRing][kTile];
   uint8_t s_hi[kTile];
@@ -68,13 +80,16 @@ struct ChunkSmem {
   float g_hi[2][kChunk];  // -G in two parts, chunk c in c % 2
   float g_lo[2][kChunk];
   float to_end[4][32];    // the P group's warps: 2^(G at the end of 32 tokens - G_j)
+  ChunkItem item[2];
+  uint8_t order[kSortLanes];
   uint64_t full[kRing], empty[kRing];
+  uint64_t item_full[2], item_empty[2];
   uint64_t g_full[2], g_empty[2];
   uint64_t scores_full, p_ready, qs_full, d_scaled, o_full, d_free, s_ready, kv_full, u_free, v_clean, o_staged, drain;
   uint64_t kp_full[2], kp_empty[2];
+  uint64_t st_full[2], st_free[2], st_done;
   uint32_t tmem;
   int abort;
-  int status;             // the lane's status on entry
 };
 
 struct ChunkParams {
@@ -83,18 +98,23 @@ struct ChunkParams {
                       // call; r + 1, the state after segment r begun from zero
   float* local_decay; // [segments][lanes][heads]: whole decay of segment r
   int32_t segments;
+  int32_t sort;       // lanes differ in length: longest first
 };
 
-// Waits for a phase; gives up after some seconds or when another warp has.  (Few
+// Waits for a phase; gives up after the time limit or when another warp has.  (Few
 // instructions: the roles' code shares the instruction cache, and a warp that misses there
 // holds up all that wait for it.)
-constexpr uint32_t kPolls = 1u << 24;
 __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, int* abort) {
-  for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i)
-    if (*static_cast<volatile int*>(abort) || i == kPolls) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if (i % 256 != 0) continue;
+    const uint64_t t = global_ns();
+    if (t0 == 0) t0 = t;
+    if (*static_cast<volatile int*>(abort) || t - t0 > kWaitLimitNs) {
       *static_cast<volatile int*>(abort) = 1;
       return false;
     }
+  }
   return true;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
@@ -134,39 +154,63 @@ __device__ __forceinline__ uint32_t tile_unit(uint32_t r, uint32_t u) {
   return (u >> 3) * kHalf + r * 128 + (((u & 7) ^ (r & 7)) << 4);
 }
 
-// The chunks of a segment, and where they lie.
-struct Segment {
-  int b, h, seg, first, count;  // lane, head, segment, first row and rows of the lane
-  int c0, c1;                   // chunks of the lane
-  bool last;                    // the lane's last segment with rows
-};
+// The next item into registers; false when there is none.
+__device__ __forceinline__ bool next_item(ChunkSmem& sm, int& turn, ChunkItem& item) {
+  const int slot = turn & 1;
+  if (!warp_wait(&sm.item_full[slot], (turn >> 1) & 1, &sm.abort)) return false;
+  ++turn;
+  item = sm.item[slot];
+  warp_arrive(&sm.item_empty[slot]);
+  return item.count >= 0;
+}
 
+// Position `i` of this CTA's items among all: rounds of the grid, every other one
+// backwards, so that longest first also evens out the sums.
+__device__ __forceinline__ int item_index(int i) {
+  return i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// A 128 x 128 state by one warp (from == nullptr: zeros).
+__device__ __forceinline__ void copy_state(float* to, const float* from) {
+  for (int i = threadIdx.x & 31; i < 128 * 128 / 4; i += 8 * 32) {
+    float4 x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[j] = from == nullptr ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(reinterpret_cast<const float4*>(from) + i + 32 * j);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) reinterpret_cast<float4*>(to)[i + 32 * j] = x[j];
+  }
+}
+
+// map_begin holds the states before the items: state_in or, with segments, `local` (slot
+// r of lane b in its lane r * lanes + b); map_end takes those after them: state_out or, with
+// STATES, `local`.
 // STATES: only the states of all segments but the last, begun from zero (the first of
 // two launches when a lane is split); otherwise outputs and final states.
 template <bool STATES>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     linear_chunk_kernel(const ChunkParams cp, const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                        const __grid_constant__ CUtensorMap map_out) {
+                        const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_begin,
+                        const __grid_constant__ CUtensorMap map_end) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>(smem_raw);
   const LinearParams& p = cp.p;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  Segment sg;
-  sg.h = blockIdx.x % p.v_heads;
-  sg.b = blockIdx.x / p.v_heads % p.lanes;
-  sg.seg = blockIdx.x / p.v_heads / p.lanes;
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 9);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_empty[i], STATES ? 15 : 23);
       mbar_init(&sm.g_full[i], 1);
       mbar_init(&sm.g_empty[i], STATES ? 12 : 20);
       mbar_init(&sm.kp_full[i], 4);
       mbar_init(&sm.kp_empty[i], 1);
+      mbar_init(&sm.st_full[i], 1);
+      mbar_init(&sm.st_free[i], 4);
     }
     mbar_init(&sm.scores_full, 1);
     mbar_init(&sm.p_ready, 4);
@@ -179,6 +223,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(&sm.u_free, 4);
     mbar_init(&sm.v_clean, 4);
     mbar_init(&sm.o_staged, 4);
+    mbar_init(&sm.st_done, 1);
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
     fence_mbar_init();
@@ -193,74 +238,104 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
   griddep_wait();
   griddep_launch_dependents();
-  // Read once: another head's CTA may write it meanwhile, and all warps must agree.
-  if (threadIdx.x == 0) sm.status = p.lane_status == nullptr ? SPEC_OK : p.lane_status[sg.b];
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = sm.tmem;
-
-  const int rc = linear_lane_rows(p, sg.b, sg.first, sg.count);
-  const bool skip = rc != SPEC_OK || sm.status != SPEC_OK;
-  const int chunks = (sg.count + kChunk - 1) / kChunk;
-  const int per = (chunks + cp.segments - 1) / cp.segments;
-  sg.c0 = min(chunks, sg.seg * per);
-  sg.c1 = min(chunks, sg.c0 + per);
-  sg.last = sg.c1 == chunks && (sg.c0 < chunks || sg.seg == 0);
-  const bool active = !skip && sg.c0 < sg.c1 && !(STATES && sg.last);
-  if (rc != SPEC_OK && threadIdx.x == 0 && p.lane_status != nullptr && sm.status == SPEC_OK) p.lane_status[sg.b] = rc;
-  const int64_t head = static_cast<int64_t>(sg.b) * p.v_heads + sg.h;
-  const int64_t heads = static_cast<int64_t>(p.lanes) * p.v_heads;
-  const float* state_in =
-      p.state_in == nullptr ? nullptr : p.state_in + sg.b * p.state_in_lane + sg.h * p.state_in_head;
-  float* state_out =
-      p.state_out == nullptr ? nullptr : p.state_out + sg.b * p.state_out_lane + sg.h * p.state_out_head;
-
-  if (!STATES && !skip && chunks == 0 && sg.seg == 0 && state_out != nullptr) {  // an empty lane's state passes through
-    for (int i = threadIdx.x; i < 128 * 128 / 4; i += kChunkThreads)
-      reinterpret_cast<float4*>(state_out)[i] =
-          state_in == nullptr ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(state_in)[i];
-  }
-
-  // The last segment writes the final state while others may yet begin, and the two may
-  // be one buffer: with segments the first launch keeps a copy of the initial state.
-  if (STATES && !skip && sg.seg == 0 && state_in != nullptr) {
-    for (int i = threadIdx.x; i < 128 * 128 / 4; i += kChunkThreads)
-      reinterpret_cast<float4*>(cp.local + head * (128 * 128))[i] = reinterpret_cast<const float4*>(state_in)[i];
-  }
-
   const uint32_t quarter = static_cast<uint32_t>(warp & 3) * 32;  // this warp's lanes of tensor memory
   const uint32_t row = quarter + lane;
   const uint32_t tmq = tm + (quarter << 16);
-  const int n_chunks = active ? sg.c1 - sg.c0 : 0;
+  const int heads = p.lanes * p.v_heads;
   constexpr int kLoads = STATES ? 2 : 3;  // tiles of a chunk: k, v (, q)
+  ChunkItem it;
+  int turn = 0;  // items taken
+  int gc = 0;    // chunks done in the items before
 
   if (warp < 4) registers_shrink<kRegsMisc>();
-  if (warp == 0) {
+  if (warp == 3) {
+    // ------------------------------------------------------------------- items
+    const int total = heads * (STATES ? cp.segments - 1 : cp.segments);
+    if (cp.sort) {
+      // A lane's place: how many are longer, or as long and before it.
+      for (int i = lane; i < p.lanes; i += 32) {
+        const int n = p.row_offsets[i + 1] - p.row_offsets[i];
+        int place = 0;
+#pragma unroll 4
+        for (int j = 0; j < p.lanes; ++j) {
+          const int m = __ldg(p.row_offsets + j + 1) - __ldg(p.row_offsets + j);
+          place += m > n || (m == n && j < i) ? 1 : 0;
+        }
+        sm.order[place] = static_cast<uint8_t>(i);
+      }
+      __syncwarp();
+    }
+    auto publish = [&](const ChunkItem& x) {
+      const int slot = turn & 1;
+      if (turn >= 2 && !warp_wait(&sm.item_empty[slot], ((turn >> 1) - 1) & 1, &sm.abort)) return false;
+      if (lane == 0) sm.item[slot] = x;
+      ++turn;
+      __threadfence_block();
+      warp_arrive(&sm.item_full[slot]);
+      return true;
+    };
+    bool ok = true;
+    for (int i = 0; ok && i * static_cast<int64_t>(gridDim.x) < total; ++i) {
+      const int index = item_index(i);
+      if (index >= total) continue;
+      it.h = index % p.v_heads;
+      it.b = index / p.v_heads % p.lanes;
+      if (cp.sort) it.b = sm.order[it.b];
+      it.seg = index / heads;
+      const int rc = linear_lane_rows(p, it.b, it.first, it.count);
+      // (lanes agree on a status that another head's CTA may be writing)
+      const int status = p.lane_status == nullptr ? SPEC_OK : __shfl_sync(0xFFFFFFFFu, p.lane_status[it.b], 0);
+      if (status != SPEC_OK) continue;
+      if (rc != SPEC_OK) {
+        if (lane == 0 && p.lane_status != nullptr) p.lane_status[it.b] = rc;
+        continue;
+      }
+      const int chunks = (it.count + kChunk - 1) / kChunk;
+      const int per = (chunks + cp.segments - 1) / cp.segments;
+      it.c0 = min(chunks, it.seg * per);
+      it.c1 = min(chunks, it.c0 + per);
+      it.last = it.c1 == chunks;
+      if (it.c0 < it.c1 && !(STATES && it.last)) ok = publish(it);
+      if (it.seg != 0) continue;
+      const float* in = p.state_in == nullptr ? nullptr : p.state_in + it.b * p.state_in_lane + it.h * p.state_in_head;
+      // The last segment writes the final state while others may yet begin, and the two
+      // may be one buffer: with segments the first launch keeps a copy of the initial one.
+      if (STATES && in != nullptr) copy_state(cp.local + (it.b * p.v_heads + it.h) * int64_t{128 * 128}, in);
+      // An empty lane's state passes through.
+      if (!STATES && chunks == 0 && p.state_out != nullptr)
+        copy_state(p.state_out + it.b * p.state_out_lane + it.h * p.state_out_head, in);
+    }
+    it.count = -1;
+    publish(it);
+  } else if (warp == 0) {
     // ------------------------------------------------------------------ copies
-    if (lane == 0) {
-      int issued = 0;
-      bool ok = true;
-      for (int c = 0; c < n_chunks && ok; ++c) {
-        const int z = sg.first + (sg.c0 + c) * kChunk;
+    int slot = 0, round = 0, issued = 0;
+    bool ok = true;
+    while (ok && next_item(sm, turn, it)) {
+      for (int c = it.c0; c < it.c1 && ok; ++c) {
 #pragma unroll 1
         for (int j = 0; j < kLoads; ++j) {
-          const int slot = issued % kRing, turn = issued / kRing;
-          if (turn > 0 && !chunk_wait(&sm.empty[slot], (turn - 1) & 1, &sm.abort)) {
-            ok = false;
-            break;
+          if (round > 0 && !(ok = warp_wait(&sm.empty[slot], (round - 1) & 1, &sm.abort))) break;
+          if (lane == 0) {
+            const CUtensorMap* map = j == 0 ? &map_k : (j == 1 ? &map_v : &map_q);
+            const int hh = j == 1 ? it.h : it.h / p.group, z = it.first + c * kChunk;
+            mbar_arrive_expect_tx(&sm.full[slot], kTile);
+            tma_load_3d(sm.ring[slot], map, 0, hh, z, &sm.full[slot]);
+            tma_load_3d(sm.ring[slot] + kHalf, map, 64, hh, z, &sm.full[slot]);
           }
-          const CUtensorMap* map = j == 0 ? &map_k : (j == 1 ? &map_v : &map_q);
-          const int hh = j == 1 ? sg.h : sg.h / p.group;
-          mbar_arrive_expect_tx(&sm.full[slot], kTile);
-          tma_load_3d(sm.ring[slot], map, 0, hh, z, &sm.full[slot]);
-          tma_load_3d(sm.ring[slot] + kHalf, map, 64, hh, z, &sm.full[slot]);
           ++issued;
+          if (++slot == kRing) {
+            slot = 0;
+            ++round;
+          }
         }
       }
-      // Every copy lands before the CTA ends (also when a wait gave up).
-      for (int i = max(0, issued - kRing); i < issued; ++i)
-        mbar_wait_bounded(&sm.full[i % kRing], (i / kRing) & 1);
     }
+    // Every copy lands before the CTA ends (also when a wait gave up).
+    for (int i = max(0, issued - kRing); i < issued; ++i) mbar_wait_bounded(&sm.full[i % kRing], (i / kRing) & 1);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products
@@ -268,16 +343,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // then keeps loop counters and descriptors in uniform registers: a product is a few
     // instructions, issued well within the 64 cycles it takes.
     const uint32_t lead = elect_one();
-    const int loops = __shfl_sync(0xFFFFFFFFu, n_chunks, 0);
-    const int rows_left = __shfl_sync(0xFFFFFFFFu, sg.count - sg.c0 * kChunk, 0);
     const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0);
     constexpr uint32_t kSame = mma_desc(128, 128, false), kRows = mma_desc(128, 128, true);
     const uint32_t ring = smem_desc(smem_addr(sm.ring[0]), kHalf);  // (for K-major tiles the piece distance is not used)
     const uint32_t dlo = smem_desc(smem_addr(sm.s_lo), kHalf), dhi = smem_desc(smem_addr(sm.s_hi), kHalf);
     uint32_t kphase = 0;     // bit i: phase of k' buffer i
     int slot = 0, phase = 0; // the ring's slot of this chunk's k and its phase
-    for (int c = 0; c < loops; ++c) {
-      const uint32_t ph = c & 1;
+    int tails = 0;           // chunks that did not fill a tile
+    bool ok = true;
+    while (ok && next_item(sm, turn, it)) {
+    const int loops = __shfl_sync(0xFFFFFFFFu, it.c1 - it.c0, 0);
+    const int rows_left = __shfl_sync(0xFFFFFFFFu, it.count - it.c0 * kChunk, 0);
+    ok = false;
+    for (int c = 0; c < loops; ++c, ++gc) {
+      const uint32_t ph = gc & 1;
       const int n = min(kChunk, rows_left - c * kChunk);
       const int bufs = (n + 31) / 32;  // products over the chunk's tokens stop at the last 32 that hold any
       const int sk = slot, pk = phase;
@@ -294,14 +373,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (!STATES) advance();
       const uint32_t dk = ring + sk * (kTile / 16), dv = ring + sv * (kTile / 16), dq = ring + sq * (kTile / 16);
       if (!warp_wait(&sm.full[sv], pv, &sm.abort)) break;
-      if (n < kChunk && !warp_wait(&sm.v_clean, 0, &sm.abort)) break;
-      if (c > 0 && !warp_wait(&sm.u_free, ph ^ 1, &sm.abort)) break;
-      bool ok = true;
+      if (n < kChunk && !warp_wait(&sm.v_clean, tails++ & 1, &sm.abort)) break;
+      if (gc > 0 && !warp_wait(&sm.u_free, ph ^ 1, &sm.abort)) break;
+      bool fine = true;
 #pragma unroll 1
       for (int t = 0; t < bufs || t == 2; ++t) {
         if (t == 2) {  // QK between the halves of KV (and behind a short chunk's)
           if (!STATES) {
-            if (!(ok = warp_wait(&sm.full[sq], pq, &sm.abort) && warp_wait(&sm.full[sk], pk, &sm.abort))) break;
+            if (!(fine = warp_wait(&sm.full[sq], pq, &sm.abort) && warp_wait(&sm.full[sk], pk, &sm.abort))) break;
             tc_fence_after();
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
@@ -316,7 +395,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (bufs <= 2) break;
         }
         const uint32_t kb = t & 1;
-        if (!(ok = warp_wait(&sm.kp_full[kb], (kphase >> kb) & 1, &sm.abort))) break;
+        if (!(fine = warp_wait(&sm.kp_full[kb], (kphase >> kb) & 1, &sm.abort))) break;
         tc_fence_after();
         const uint32_t parts = tmu + kColK + kb * kColKBuf, dvt = dv + t * (2 * 2048 / 16);
 #pragma unroll
@@ -326,11 +405,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         kphase ^= 1u << kb;
         if (t == 0 && bufs == 1) t = 1;  // on to QK
       }
-      if (!ok) break;
+      if (!fine) break;
       mma_commit(lead, &sm.kv_full);
       if (!STATES) {
         if (!warp_wait(&sm.s_ready, ph, &sm.abort)) break;
-        if (c > 0 && !warp_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
+        if (gc > 0 && !warp_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
@@ -352,6 +431,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       mma_commit(lead, &sm.empty[sv]);
       if (lead) mbar_arrive_n(&sm.empty[sv], 8);
+      ok = c + 1 == loops;  // the item is done
+    }
     }
     // Tensor memory is given back only after the last product.
     mma_commit(lead, &sm.drain);
@@ -361,58 +442,71 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // ------------------------------------------------------------------ decays
     // Fixed point with 32 fractional bits: sums and differences are exact, whatever
     // large decays stand between two tokens.  32 tokens at a time, a lane each.
-    auto fetch = [&](int t) {
-      t += sg.c0 * kChunk + lane;
-      return t < sg.count ? __ldg(p.log_decay + (sg.first + static_cast<int64_t>(t)) * p.decay_row + sg.h * p.decay_head)
-                          : 0.f;
-    };
-    float next = n_chunks > 0 ? fetch(0) : 0.f;
-    long long before = 0;
-    float poison = 0.f;  // NaN once the chunk holds a NaN or a factor infinite in fp32
+    bool ok = true;
+    while (ok && next_item(sm, turn, it)) {
+      const int rows = it.count - it.c0 * kChunk, end = (it.c1 - it.c0) * kChunk;
+      const float* src = p.log_decay + (it.first + it.c0 * static_cast<int64_t>(kChunk)) * p.decay_row + it.h * p.decay_head;
+      float g4[4], next4[4];  // this chunk's and the next one's
+      auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          next4[i] = t + 32 * i + lane < rows ? __ldg(src + (t + 32 * i + lane) * p.decay_row) : 0.f;
+      };
+      fetch(0);
+      long long before = 0;
+      float poison = 0.f;  // NaN once the chunk holds a NaN or a factor infinite in fp32
 #pragma unroll 1
-    for (int t = 0; t < n_chunks * kChunk; t += 32) {
-      const int c = t / kChunk, buf = c & 1;
-      const float g = next;
-      if (t + 32 < n_chunks * kChunk) next = fetch(t + 32);
-      if (t % kChunk == 0) {
-        if (c >= 2 && !warp_wait(&sm.g_empty[buf], ((c >> 1) - 1) & 1, &sm.abort)) break;
-        before = 0;
-        poison = 0.f;
-      }
-      float hi = g * kLog2eHi;
-      float lo = fmaf(g, kLog2eHi, -hi) + g * kLog2eLo;
-      if (__any_sync(0xFFFFFFFFu, !(hi < 128.f))) poison = __uint_as_float(0x7FC00000u);
-      if (!(hi > kDecayFloor)) {
-        hi = kDecayFloor;
-        lo = 0.f;
-      }
-      long long sum = __float2ll_rn(hi * 4294967296.f) + __float2ll_rn(lo * 4294967296.f);
+      for (int t = 0; t < end; t += 32) {
+        const int buf = gc & 1;
+        if (t % kChunk == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) g4[i] = next4[i];
+          if (t + kChunk < end) fetch(t + kChunk);
+          if (gc >= 2 && !(ok = warp_wait(&sm.g_empty[buf], ((gc >> 1) - 1) & 1, &sm.abort))) break;
+          before = 0;
+          poison = 0.f;
+        }
+        const float g = g4[0];
+        g4[0] = g4[1];
+        g4[1] = g4[2];
+        g4[2] = g4[3];
+        float hi = g * kLog2eHi;
+        float lo = fmaf(g, kLog2eHi, -hi) + g * kLog2eLo;
+        if (__any_sync(0xFFFFFFFFu, !(hi < 128.f))) poison = __uint_as_float(0x7FC00000u);
+        if (!(hi > kDecayFloor)) {
+          hi = kDecayFloor;
+          lo = 0.f;
+        }
+        long long sum = __float2ll_rn(hi * 4294967296.f) + __float2ll_rn(lo * 4294967296.f);
 #pragma unroll 1
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-        if (lane >= d) sum += up;
-      }
-      sum += before;
-      before = __shfl_sync(0xFFFFFFFFu, sum, 31);
-      hi = __ll2float_rn(sum);
-      lo = __ll2float_rn(sum - __float2ll_rn(hi));
-      sm.g_hi[buf][t % kChunk + lane] = fmaf(hi, -0x1p-32f, poison);
-      sm.g_lo[buf][t % kChunk + lane] = lo * -0x1p-32f;
-      if (t % kChunk == kChunk - 32) {
-        // (every use of a chunk's sums takes in the last one, directly or by the state)
-        __threadfence_block();
-        warp_arrive(&sm.g_full[buf]);
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+          if (lane >= d) sum += up;
+        }
+        sum += before;
+        before = __shfl_sync(0xFFFFFFFFu, sum, 31);
+        hi = __ll2float_rn(sum);
+        lo = __ll2float_rn(sum - __float2ll_rn(hi));
+        sm.g_hi[buf][t % kChunk + lane] = fmaf(hi, -0x1p-32f, poison);
+        sm.g_lo[buf][t % kChunk + lane] = lo * -0x1p-32f;
+        if (t % kChunk == kChunk - 32) {
+          // (every use of a chunk's sums takes in the last one, directly or by the state)
+          __threadfence_block();
+          warp_arrive(&sm.g_full[buf]);
+          ++gc;
+        }
       }
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------- scores to P
     registers_shrink<kRegsScores>();
-    if (!STATES) {
-      for (int c = 0; c < n_chunks; ++c) {
-        const int buf = c & 1;
-        if (!warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort)) break;
+    bool ok = !STATES;
+    while (ok && next_item(sm, turn, it)) {
+      for (int c = it.c0; c < it.c1; ++c, ++gc) {
+        const int buf = gc & 1;
+        if (!(ok = warp_wait(&sm.g_full[buf], (gc >> 1) & 1, &sm.abort))) break;
         const float ghi = -sm.g_hi[buf][row], glo = -sm.g_lo[buf][row];
-        if (!warp_wait(&sm.scores_full, c & 1, &sm.abort)) break;
+        if (!(ok = warp_wait(&sm.scores_full, gc & 1, &sm.abort))) break;
         tc_fence_after();
         float* const to_end = sm.to_end[warp - 4];
 #pragma unroll 1
@@ -478,13 +572,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else if (warp >= 8 && warp < 12) {
     // ----------------------------------------------------------------- outputs
     registers_shrink<kRegsOut>();
-    if (!STATES) {
-      for (int c = 0; c < n_chunks; ++c) {
-        const int buf = c & 1;
-        if (!warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort)) break;
+    int slot = 2;     // the ring's slot of the chunk's q
+    int stores = 0;   // chunks that went out as tiles
+    bool ok = !STATES;
+    while (ok && next_item(sm, turn, it)) {
+      for (int c = it.c0; c < it.c1; ++c, ++gc) {
+        const int buf = gc & 1;
+        if (!(ok = warp_wait(&sm.g_full[buf], (gc >> 1) & 1, &sm.abort))) break;
         const float e = exp2f(-(sm.g_hi[buf][row] + sm.g_lo[buf][row]));
         warp_arrive(&sm.g_empty[buf]);
-        if (!warp_wait(&sm.qs_full, c & 1, &sm.abort)) break;
+        if (!(ok = warp_wait(&sm.qs_full, gc & 1, &sm.abort))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int piece = 0; piece < 4; ++piece) {
@@ -502,12 +599,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&sm.d_scaled);
-        if (!warp_wait(&sm.o_full, c & 1, &sm.abort)) break;
+        if (!(ok = warp_wait(&sm.o_full, gc & 1, &sm.abort))) break;
         tc_fence_after();
         // The chunk's q has been read: its tile takes the outputs on their way out.
-        const int slot = (kLoads * c + 2) % kRing;
         uint8_t* tile = sm.ring[slot];
-        const int n = sg.count - (sg.c0 + c) * kChunk;
+        const int n = it.count - c * kChunk;
         const f32x2 scale = pair(p.scale, p.scale);
 #pragma unroll 1
         for (int piece = 0; piece < 4; ++piece) {
@@ -527,11 +623,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (n >= kChunk) {
           warp_arrive(&sm.o_staged);
           if (warp == 8) {
-            if (!warp_wait(&sm.o_staged, c & 1, &sm.abort)) break;
+            if (!(ok = warp_wait(&sm.o_staged, stores++ & 1, &sm.abort))) break;
             if (lane == 0) {
-              const int z = sg.first + (sg.c0 + c) * kChunk;
-              tma_store_3d(&map_out, tile, 0, sg.h, z);
-              tma_store_3d(&map_out, tile + kHalf, 64, sg.h, z);
+              const int z = it.first + c * kChunk;
+              tma_store_3d(&map_out, tile, 0, it.h, z);
+              tma_store_3d(&map_out, tile + kHalf, 64, it.h, z);
               bulk_commit_group();
               bulk_wait_group_read<0>();
               mbar_arrive_n(&sm.empty[slot], 9);
@@ -540,99 +636,161 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         } else {  // (a copy would go on into the next lane's rows)
           __syncwarp();
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + sg.h * p.out_head;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + it.h * p.out_head;
 #pragma unroll 1
           for (int i = lane; i < 32 * 16; i += 32) {
             const int r = static_cast<int>(quarter) + i / 16;
             if (r < n)
-              *reinterpret_cast<uint4*>(dst + (sg.first + (sg.c0 + c) * static_cast<int64_t>(kChunk) + r) * p.out_row + (i % 16) * 8) =
+              *reinterpret_cast<uint4*>(dst + (it.first + c * static_cast<int64_t>(kChunk) + r) * p.out_row + (i % 16) * 8) =
                   *reinterpret_cast<const uint4*>(tile + tile_unit(r, i % 16));
           }
+          fence_async_smem();  // the tile's next content comes by a copy
+          __syncwarp();
+          if (lane == 0) mbar_arrive_n(&sm.empty[slot], warp == 8 ? 6 : 1);
         }
+        slot = slot >= 2 ? slot - 2 : slot + 3;  // three tiles on
       }
-      // (the last copies end before the CTA does)
-      if (lane == 0) bulk_wait_group<0>();
-      __syncwarp();
     }
+    // (the last copies end before the CTA does)
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
   } else if (warp >= 12 && warp < 16) {
     // ------------------------------------------------------------------ states
     registers_grow<kRegsState>();
-    f32x2 S[64];  // row `row` of S
-#pragma unroll
-    for (int i = 0; i < 64; ++i) S[i] = 0ull;
-    const int at = static_cast<int>(row) * 128;
-    if (!STATES && n_chunks > 0) {
-      // The state before the segment: the lane's, then every earlier segment's from
-      // zero behind its decay.
-      const float* begin = cp.segments > 1 ? cp.local + head * (128 * 128) : state_in;
-      if (state_in != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(begin + at + 2 * i));
-          S[i] = pair(x.x, x.y);
-          S[i + 1] = pair(x.z, x.w);
-        }
-      }
-      for (int r = 0; r < sg.seg; ++r) {
-        const float a = __ldcg(cp.local_decay + r * heads + head);
-        const float* src = cp.local + ((r + 1) * heads + head) * (128 * 128) + at;
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src + 2 * i));
-          S[i] = fma2(S[i], pair(a, a), pair(x.x, x.y));
-          S[i + 1] = fma2(S[i + 1], pair(a, a), pair(x.z, x.w));
-        }
-      }
-    }
+    // States come and go by copies through s_hi (columns 0..63) and s_lo, which hold S in
+    // parts only from a chunk's start to its QS; the first warp issues them.
+    const bool has_in = !STATES && p.state_in != nullptr;
+    int loads = 0;       // states loaded so far
+    int frees[2] = {0, 0};  // phases of st_free
+    int stored = 0;      // states stored so far
     bool ok = true;
-    float total = 1.f;  // the segment's whole decay
-    for (int c = 0; c < n_chunks; ++c) {
-      const int buf = c & 1;
+    while (ok && next_item(sm, turn, it)) {
+      const int64_t head = it.b * p.v_heads + it.h;
+      f32x2 S[64];  // row `row` of S
+#pragma unroll
+      for (int i = 0; i < 64; ++i) S[i] = 0ull;
+      if (!STATES && gc > 0 && !(ok = warp_wait(&sm.qs_full, (gc - 1) & 1, &sm.abort))) break;
+      if (stored > 0 && !(ok = warp_wait(&sm.st_done, (stored - 1) & 1, &sm.abort))) break;
       if (!STATES) {
-        // S in two parts to shared memory for the chunk's QS, the last chunk's done.
-        if (c > 0 && !(ok = warp_wait(&sm.qs_full, (c - 1) & 1, &sm.abort))) break;
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const uint32_t unit = tile_unit(row, i / 4);
-          *reinterpret_cast<uint4*>(sm.s_hi + unit) = make_uint4(upper(S[i]), upper(S[i + 1]), upper(S[i + 2]), upper(S[i + 3]));
-          *reinterpret_cast<uint4*>(sm.s_lo + unit) = make_uint4(rounded(rest(S[i])), rounded(rest(S[i + 1])),
-                                                                 rounded(rest(S[i + 2])), rounded(rest(S[i + 3])));
+        // The state before the segment: the lane's, then every earlier segment's from zero
+        // behind its decay.
+        const int n = (has_in ? 1 : 0) + it.seg, slot0 = has_in ? 0 : 1;
+        auto load = [&](int k, int half) {
+          if (lane == 0) {
+            uint8_t* dst = half == 0 ? sm.s_hi : sm.s_lo;
+            const int z = (slot0 + k) * p.lanes + it.b;
+            mbar_arrive_expect_tx(&sm.st_full[half], kTile);
+            tma_load_4d(dst, &map_begin, half * 64, 0, it.h, z, &sm.st_full[half]);
+            tma_load_4d(dst + kHalf, &map_begin, half * 64 + 32, 0, it.h, z, &sm.st_full[half]);
+          }
+          __syncwarp();
+        };
+        if (n > 0 && warp == 12) {
+          load(0, 0);
+          load(0, 1);
         }
-        fence_async_smem();
-        warp_arrive(&sm.s_ready);
-      }
-      if (!(ok = warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort))) break;
-      const float decay = exp2f(-(sm.g_hi[buf][kChunk - 1] + sm.g_lo[buf][kChunk - 1]));
-      total *= decay;
-      warp_arrive(&sm.g_empty[buf]);
-      if (!(ok = warp_wait(&sm.kv_full, c & 1, &sm.abort))) break;
-      tc_fence_after();
-      uint32_t u[2][8];
-      tmem_ld8(u[0], tmq + kColU);
+#pragma unroll 1
+        for (int k = 0; k < n && ok; ++k, ++loads) {
+          const int r = slot0 + k - 1;
+          const float a = r < 0 ? 0.f : __ldcg(cp.local_decay + r * static_cast<int64_t>(heads) + head);
 #pragma unroll
-      for (int piece = 0; piece < 16; ++piece) {
-        tmem_wait_ld();
-        if (piece < 15) tmem_ld8(u[(piece + 1) & 1], tmq + kColU + (piece + 1) * 8);
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = ok && warp_wait(&sm.st_full[half], loads & 1, &sm.abort))) break;
+            const uint8_t* src = half == 0 ? sm.s_hi : sm.s_lo;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          S[piece * 4 + i] = fma2(S[piece * 4 + i], pair(decay, decay),
-                                  pair(__uint_as_float(u[piece & 1][2 * i]), __uint_as_float(u[piece & 1][2 * i + 1])));
+            for (int f = 0; f < 16; ++f) {
+              const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(src + tile_unit(row, f));
+              S[half * 32 + 2 * f] = fma2(S[half * 32 + 2 * f], pair(a, a), x.x);
+              S[half * 32 + 2 * f + 1] = fma2(S[half * 32 + 2 * f + 1], pair(a, a), x.y);
+            }
+            warp_arrive(&sm.st_free[half]);
+            ++frees[half];
+            if (warp == 12 && k + 1 < n) {
+              if (!(ok = warp_wait(&sm.st_free[half], (frees[half] - 1) & 1, &sm.abort))) break;
+              load(k + 1, half);
+            }
+          }
+        }
+        if (!ok) break;
+        if (n > 0 && !(ok = warp_wait(&sm.st_free[0], (frees[0] - 1) & 1, &sm.abort) &&
+                            warp_wait(&sm.st_free[1], (frees[1] - 1) & 1, &sm.abort)))
+          break;
       }
-      tc_fence_before();
-      warp_arrive(&sm.u_free);
-    }
-    if (n_chunks > 0 && ok) {
-      float* dst = STATES ? cp.local + ((sg.seg + 1) * heads + head) * (128 * 128) : (sg.last ? state_out : nullptr);
-      if (STATES && row == 0) cp.local_decay[sg.seg * heads + head] = total;
+      float total = 1.f;  // the segment's whole decay
+      for (int c = it.c0; c < it.c1; ++c, ++gc) {
+        const int buf = gc & 1;
+        if (!STATES) {
+          // S in two parts to shared memory for the chunk's QS, the last chunk's done.
+          if (c > it.c0 && !(ok = warp_wait(&sm.qs_full, (gc - 1) & 1, &sm.abort))) break;
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const uint32_t unit = tile_unit(row, i / 4);
+            *reinterpret_cast<uint4*>(sm.s_hi + unit) =
+                make_uint4(upper(S[i]), upper(S[i + 1]), upper(S[i + 2]), upper(S[i + 3]));
+            *reinterpret_cast<uint4*>(sm.s_lo + unit) = make_uint4(rounded(rest(S[i])), rounded(rest(S[i + 1])),
+                                                                   rounded(rest(S[i + 2])), rounded(rest(S[i + 3])));
+          }
+          fence_async_smem();
+          warp_arrive(&sm.s_ready);
+        }
+        if (!(ok = warp_wait(&sm.g_full[buf], (gc >> 1) & 1, &sm.abort))) break;
+        const float decay = exp2f(-(sm.g_hi[buf][kChunk - 1] + sm.g_lo[buf][kChunk - 1]));
+        total *= decay;
+        warp_arrive(&sm.g_empty[buf]);
+        if (!(ok = warp_wait(&sm.kv_full, gc & 1, &sm.abort))) break;
+        tc_fence_after();
+        uint32_t u[2][8];
+        tmem_ld8(u[0], tmq + kColU);
+#pragma unroll
+        for (int piece = 0; piece < 16; ++piece) {
+          tmem_wait_ld();
+          if (piece < 15) tmem_ld8(u[(piece + 1) & 1], tmq + kColU + (piece + 1) * 8);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            S[piece * 4 + i] = fma2(S[piece * 4 + i], pair(decay, decay),
+                                    pair(__uint_as_float(u[piece & 1][2 * i]), __uint_as_float(u[piece & 1][2 * i + 1])));
+        }
+        tc_fence_before();
+        warp_arrive(&sm.u_free);
+      }
+      if (!ok) break;
       f32x2 bad = 0ull;  // 0 times S: NaN where S is not finite
 #pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        bad = fma2(S[i], 0ull, fma2(S[i + 1], 0ull, bad));
-        if (dst != nullptr)
-          *reinterpret_cast<float4*>(dst + at + 2 * i) =
-              make_float4(first_of(S[i]), second_of(S[i]), first_of(S[i + 1]), second_of(S[i + 1]));
+      for (int i = 0; i < 64; ++i) bad = fma2(S[i], 0ull, bad);
+      if (!STATES && it.last && first_of(bad) + second_of(bad) != 0.f && p.lane_status != nullptr)
+        p.lane_status[it.b] = SPEC_ERR_NONFINITE;
+      if (STATES && row == 0) cp.local_decay[it.seg * static_cast<int64_t>(heads) + head] = total;
+      if (!STATES && !(it.last && p.state_out != nullptr)) continue;
+      if (!STATES && !(ok = warp_wait(&sm.qs_full, (gc - 1) & 1, &sm.abort))) break;
+#pragma unroll
+      for (int f = 0; f < 32; ++f)
+        *reinterpret_cast<ulonglong2*>((f < 16 ? sm.s_hi : sm.s_lo) + tile_unit(row, f & 15)) =
+            make_ulonglong2(S[2 * f], S[2 * f + 1]);
+      fence_async_smem();
+      warp_arrive(&sm.st_free[0]);
+      ++frees[0];
+      ++stored;
+      if (warp == 12) {
+        if (!(ok = warp_wait(&sm.st_free[0], (frees[0] - 1) & 1, &sm.abort))) break;
+        if (lane == 0) {
+          const int z = STATES ? (it.seg + 1) * p.lanes + it.b : it.b;
+          for (int i = 0; i < 4; ++i)
+            tma_store_4d(&map_end, (i < 2 ? sm.s_hi : sm.s_lo) + (i & 1) * kHalf, i * 32, 0, it.h, z);
+          bulk_commit_group();
+          bulk_wait_group_read<0>();
+          mbar_arrive(&sm.st_done);
+        }
+        __syncwarp();
       }
-      if (!STATES && sg.last && first_of(bad) + second_of(bad) != 0.f && p.lane_status != nullptr) p.lane_status[sg.b] = SPEC_ERR_NONFINITE;
+    }
+    // Copies end before the CTA does (loads that a wait gave up on, too).
+    if (warp == 12) {
+      if (sm.abort && loads > 0) {
+        mbar_wait_bounded(&sm.st_full[0], loads & 1);
+        mbar_wait_bounded(&sm.st_full[1], loads & 1);
+      }
+      if (lane == 0) bulk_wait_group<0>();
+      __syncwarp();
     }
   } else if (warp >= 16) {
     // ---------------------------------------------------------------------- k'
@@ -641,15 +799,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     registers_shrink<kRegsKey>();
     const int kb = (warp - 16) >> 2;  // this group's buffer of k'
     int step = 0;                     // times it has been filled
+    int slot = 0, phase = 0;          // the ring's slot of the chunk's k and its phase
     bool ok = true;
-    for (int c = 0; c < n_chunks && ok; ++c) {
-      const int buf = c & 1;
-      const int n = min(kChunk, sg.count - (sg.c0 + c) * kChunk);
-      const int lk = kLoads * c, lv = lk + 1;
-      if (!(ok = warp_wait(&sm.g_full[buf], (c >> 1) & 1, &sm.abort))) break;
+    while (ok && next_item(sm, turn, it))
+    for (int c = it.c0; c < it.c1; ++c, ++gc) {
+      const int buf = gc & 1;
+      const int n = min(kChunk, it.count - c * kChunk);
+      const int sk = slot, pk = phase, sv = slot + 1 == kRing ? 0 : slot + 1, pv = slot + 1 == kRing ? phase ^ 1 : phase;
+      slot += kLoads;
+      if (slot >= kRing) {
+        slot -= kRing;
+        phase ^= 1;
+      }
+      if (!(ok = warp_wait(&sm.g_full[buf], (gc >> 1) & 1, &sm.abort))) break;
       if (n < kChunk && kb == 0) {  // rows past the lane take part in products (times 0): make them 0
-        if (!(ok = warp_wait(&sm.full[lv % kRing], (lv / kRing) & 1, &sm.abort))) break;
-        uint8_t* vt = sm.ring[lv % kRing];
+        if (!(ok = warp_wait(&sm.full[sv], pv, &sm.abort))) break;
+        uint8_t* vt = sm.ring[sv];
         if (static_cast<int>(row) >= n)
           for (uint32_t u = 0; u < 16; ++u)
             *reinterpret_cast<uint4*>(vt + tile_unit(row, u)) = make_uint4(0u, 0u, 0u, 0u);
@@ -657,8 +822,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         warp_arrive(&sm.v_clean);
       }
       const float last_hi = sm.g_hi[buf][kChunk - 1], last_lo = sm.g_lo[buf][kChunk - 1];
-      if (!(ok = warp_wait(&sm.full[lk % kRing], (lk / kRing) & 1, &sm.abort))) break;
-      const uint32_t tile = smem_addr(sm.ring[lk % kRing]);
+      if (!(ok = warp_wait(&sm.full[sk], pk, &sm.abort))) break;
+      const uint32_t tile = smem_addr(sm.ring[sk]);
       const int used = (n + 31) / 32;
       for (int t0 = kb * 32; t0 < used * 32; t0 += 64, ++step) {
         // Each lane has the weight of one of the 32 tokens.
@@ -702,11 +867,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       if (!ok) break;
       warp_arrive(&sm.g_empty[buf]);
-      warp_arrive(&sm.empty[lk % kRing]);
+      warp_arrive(&sm.empty[sk]);
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0 && sm.abort && p.lane_status != nullptr) p.lane_status[sg.b] = SPEC_ERR_TIMEOUT;
+  if (sm.abort && p.lane_status != nullptr) {  // a wait gave up: every lane this CTA had a part of
+    const int total = heads * (STATES ? cp.segments - 1 : cp.segments);
+    for (int i = threadIdx.x; i * static_cast<int64_t>(gridDim.x) < total; i += kChunkThreads) {
+      const int index = item_index(i);
+      if (index >= total) continue;
+      const int b = index / p.v_heads % p.lanes;
+      p.lane_status[cp.sort ? sm.order[b] : b] = SPEC_ERR_TIMEOUT;
+    }
+  }
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tm, 512);
 }
