@@ -29,7 +29,7 @@
 // an operand along either dimension) and S in two parts.
 //
 // Warps: 0 copies tiles, 1 issues the products, 2 sums the decays, 3 hands out the items,
-// and five groups of four do what lies between the products: scores to P (4-7), D (8-11),
+// and five groups of four do what lies between the products: scores to P (4-11), D (8-11),
 // S (12-15), k' for every other 32 tokens (16-19 and 20-23).  The products of a chunk take 8 x 512 cycles on the tensor cores, its
 // 128 KB of q, k, v and o about 5,500 at an SM's share of the HBM rate: the groups work
 // beside each other so that the larger of the two counts.  A chunk's products go in the
@@ -51,8 +51,8 @@ namespace specv {
 constexpr int kChunk = 128;
 constexpr int kChunkThreads = 768;
 // Registers a thread of each warpgroup; their sum is what a launch must bring (6 x 80).
-constexpr int kRegsMisc = 64, kRegsScores = 72, kRegsOut = 64, kRegsState = 168, kRegsKey = 56;
-constexpr int kChunkRegs = kRegsMisc + kRegsScores + kRegsOut + kRegsState + 2 * kRegsKey;
+constexpr int kRegsMisc = 64, kRegsOut = 64, kRegsState = 168, kRegsKey = 56;
+constexpr int kChunkRegs = kRegsMisc + 2 * kRegsOut + kRegsState + 2 * kRegsKey;
 constexpr int kTile = 32 * 1024;      // 128 rows of 128 bf16: two halves of 64 columns
 constexpr int kHalf = kTile / 2;
 constexpr int kRing = 5;
@@ -79,7 +79,7 @@ struct ChunkSmem {
   uint8_t s_lo[kTile];
   float g_hi[2][kChunk];  // -G in two parts, chunk c in c % 2
   float g_lo[2][kChunk];
-  float to_end[4][32];    // the P group's warps: 2^(G at the end of 32 tokens - G_j)
+  float to_end[8][16];    // the P groups' warps: 2^(G at the end of 16 tokens - G_j)
   ChunkItem item[2];
   uint8_t order[kSortLanes];
   uint64_t full[kRing], empty[kRing];
@@ -101,21 +101,16 @@ struct ChunkParams {
   int32_t sort;       // lanes differ in length: longest first
 };
 
-// Waits for a phase; gives up after the time limit or when another warp has.  (Few
-// instructions: the roles' code shares the instruction cache, and a warp that misses there
-// holds up all that wait for it.)
+// Waits for a phase; gives up after some seconds (a try sleeps up to 1.3 us in the barrier,
+// measured).  Few instructions, no clock: the roles' loops together have to stay within
+// the instruction cache, some 32 KB, or every warp waits for its code.
+constexpr uint32_t kTries = 1u << 21;
 __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, int* abort) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-    if (i % 256 != 0) continue;
-    const uint64_t t = global_ns();
-    if (t0 == 0) t0 = t;
-    if (*static_cast<volatile int*>(abort) || t - t0 > kWaitLimitNs) {
-      *static_cast<volatile int*>(abort) = 1;
-      return false;
-    }
-  }
-  return true;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kTries; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  *static_cast<volatile int*>(abort) = 1;
+  return false;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
   return __all_sync(0xFFFFFFFFu, chunk_wait(bar, parity, abort));
@@ -213,7 +208,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sm.st_free[i], 4);
     }
     mbar_init(&sm.scores_full, 1);
-    mbar_init(&sm.p_ready, 4);
+    mbar_init(&sm.p_ready, 8);
     mbar_init(&sm.qs_full, 1);
     mbar_init(&sm.d_scaled, 4);
     mbar_init(&sm.o_full, 1);
@@ -425,7 +420,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int t = 0; t < bufs; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            mma_ts(lead, tmu + kColD, tmu + kColP + t * 32 + 16 - (i >> 1) * 16 + (i & 1) * 8,
+            mma_ts(lead, tmu + kColD, tmu + kColP + t * 32 + (i & 1) * 16 + 8 - (i >> 1) * 8,
                    dv + t * (2 * 2048 / 16) + (i & 1) * (2048 / 16), kRows, true);
         mma_commit(lead, &sm.o_full);
       }
@@ -497,9 +492,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
     }
-  } else if (warp >= 4 && warp < 8) {
-    // ------------------------------------------------------------- scores to P
-    registers_shrink<kRegsScores>();
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------- scores to P; outputs (8-11)
+    registers_shrink<kRegsOut>();
+    const int group = (warp - 4) >> 2;  // which 16 of every 32 tokens
+    float* const to_end = sm.to_end[warp - 4];
+    int slot = 2;    // the ring's slot of the chunk's q
+    int stores = 0;  // chunks that went out as tiles
     bool ok = !STATES;
     while (ok && next_item(sm, turn, it)) {
       for (int c = it.c0; c < it.c1; ++c, ++gc) {
@@ -508,79 +507,60 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const float ghi = -sm.g_hi[buf][row], glo = -sm.g_lo[buf][row];
         if (!(ok = warp_wait(&sm.scores_full, gc & 1, &sm.abort))) break;
         tc_fence_after();
-        float* const to_end = sm.to_end[warp - 4];
 #pragma unroll 1
-        for (int j0 = 0; j0 < kChunk; j0 += 32) {  // tokens j0 .. j0 + 31
-          uint32_t hi[16], lo[16];
-          if (j0 > static_cast<int>(quarter)) {  // all after this warp's rows
+        for (int j0 = group * 16; j0 < kChunk; j0 += 32) {  // tokens j0 .. j0 + 15
+          uint32_t hi[8], lo[8];
+          if (j0 >= static_cast<int>(quarter) + 32) {  // all after this warp's rows
 #pragma unroll
-            for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0u;
+            for (int i = 0; i < 8; ++i) hi[i] = lo[i] = 0u;
           } else {
-            uint32_t s[32];
-            tmem_ld32(s, tmq + kColP + j0);
+            uint32_t s[16];
+            tmem_ld16(s, tmq + kColP + j0);
             if (j0 < static_cast<int>(quarter)) {
               // All before this warp's rows: 2^(G_i - G_j) in two factors, to the end of the
-              // 32 tokens and from there, of which neither can overflow where the whole
+              // 16 tokens and from there, of which neither can overflow where the whole
               // does not.
-              const float ehi = sm.g_hi[buf][j0 + 31], elo = sm.g_lo[buf][j0 + 31];
+              const float ehi = sm.g_hi[buf][j0 + 15], elo = sm.g_lo[buf][j0 + 15];
               const float from_end = ex2_approx((ghi + ehi) + (glo + elo));
               __syncwarp();
-              to_end[lane] = ex2_approx((sm.g_hi[buf][j0 + lane] - ehi) + (sm.g_lo[buf][j0 + lane] - elo));
+              if (lane < 16) to_end[lane] = ex2_approx((sm.g_hi[buf][j0 + lane] - ehi) + (sm.g_lo[buf][j0 + lane] - elo));
               __syncwarp();
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(&to_end[i]);
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                  const f32x2 w = mul2(mul2(pair(from_end, from_end), e ? t.y : t.x),
-                                       pair(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1])));
-                  hi[(i + e) / 2] = upper(w);
-                  lo[(i + e) / 2] = rounded(rest(w));
-                }
+              for (int i = 0; i < 16; i += 2) {
+                const f32x2 w = mul2(mul2(pair(from_end, from_end), *reinterpret_cast<const f32x2*>(&to_end[i])),
+                                     pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+                hi[i / 2] = upper(w);
+                lo[i / 2] = rounded(rest(w));
               }
             } else {
+              const int seen = static_cast<int>(row) - j0;  // the last of the tokens that this row sees
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const ulonglong2 jh = *reinterpret_cast<const ulonglong2*>(&sm.g_hi[buf][j0 + i]);
-                const ulonglong2 jl = *reinterpret_cast<const ulonglong2*>(&sm.g_lo[buf][j0 + i]);
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                  // (the arrays hold -G)
-                  const f32x2 d = add2(add2(pair(ghi, ghi), e ? jh.y : jh.x), add2(pair(glo, glo), e ? jl.y : jl.x));
-                  f32x2 w = mul2(pair(ex2_approx(first_of(d)), ex2_approx(second_of(d))),
-                                 pair(__uint_as_float(s[i + e]), __uint_as_float(s[i + e + 1])));
-                  // (a select: what is masked may be NaN)
-                  w = pair(i + e > lane ? 0.f : first_of(w), i + e + 1 > lane ? 0.f : second_of(w));
-                  hi[(i + e) / 2] = upper(w);
-                  lo[(i + e) / 2] = rounded(rest(w));
-                }
+              for (int i = 0; i < 16; i += 2) {
+                // (the arrays hold -G)
+                const f32x2 d = add2(add2(pair(ghi, ghi), *reinterpret_cast<const f32x2*>(&sm.g_hi[buf][j0 + i])),
+                                     add2(pair(glo, glo), *reinterpret_cast<const f32x2*>(&sm.g_lo[buf][j0 + i])));
+                f32x2 w = mul2(pair(ex2_approx(first_of(d)), ex2_approx(second_of(d))),
+                               pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+                // (a select: what is masked may be NaN)
+                w = pair(i > seen ? 0.f : first_of(w), i + 1 > seen ? 0.f : second_of(w));
+                hi[i / 2] = upper(w);
+                lo[i / 2] = rounded(rest(w));
               }
             }
           }
-          // Columns of P: for each 32 tokens 16 of upper and 16 of lower parts.
-          tmem_st16(tmq + kColP + j0, hi);
-          tmem_st16(tmq + kColP + j0 + 16, lo);
+          // Columns of P: for each 16 tokens 8 of upper and 8 of lower parts.
+          tmem_st8(tmq + kColP + j0, hi);
+          tmem_st8(tmq + kColP + j0 + 8, lo);
         }
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&sm.p_ready);
         warp_arrive(&sm.g_empty[buf]);
-      }
-    }
-  } else if (warp >= 8 && warp < 12) {
-    // ----------------------------------------------------------------- outputs
-    registers_shrink<kRegsOut>();
-    int slot = 2;     // the ring's slot of the chunk's q
-    int stores = 0;   // chunks that went out as tiles
-    bool ok = !STATES;
-    while (ok && next_item(sm, turn, it)) {
-      for (int c = it.c0; c < it.c1; ++c, ++gc) {
-        const int buf = gc & 1;
-        if (!(ok = warp_wait(&sm.g_full[buf], (gc >> 1) & 1, &sm.abort))) break;
-        const float e = exp2f(-(sm.g_hi[buf][row] + sm.g_lo[buf][row]));
-        warp_arrive(&sm.g_empty[buf]);
+        if (group == 0) continue;
+
+        const float e = exp2f(ghi + glo);
         if (!(ok = warp_wait(&sm.qs_full, gc & 1, &sm.abort))) break;
         tc_fence_after();
 #pragma unroll 1
@@ -829,6 +809,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // Each lane has the weight of one of the 32 tokens.
         const float weight = exp2f((sm.g_hi[buf][t0 + lane] - last_hi) + (sm.g_lo[buf][t0 + lane] - last_lo));
         const int pick = 2 * (lane & 3);
+        if (t0 + lane >= n)  // rows past the lane may hold NaN: what this warp reads of them becomes 0
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(sm.ring[sk] + tile_unit(t0 + lane, quarter / 8 + u)) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
         f32x2 w[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m)
@@ -844,8 +828,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               f32x2 x = mul2(w[m], pair(__uint_as_float(raw[m] << 16), __uint_as_float(raw[m] & 0xFFFF0000u)));
-              if (t0 + 32 > n)  // (rows past the lane may be NaN)
-                x = pair(t0 + 8 * m + pick < n ? first_of(x) : 0.f, t0 + 8 * m + pick + 1 < n ? second_of(x) : 0.f);
               hi[2 * m + i] = upper(x);
               x = rest(x);
               mid[2 * m + i] = upper(x);
