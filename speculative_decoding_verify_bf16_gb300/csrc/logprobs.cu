@@ -3,16 +3,18 @@
 //
 // With z = x / T, m = max z, s = sum e^(z - m) and t = sum e^(z - m) (z - m):
 //   log p(i) = z_i - m - log s,     entropy = log s - t / s.
-// One pass over the row gives m, s and t and the largest logit of every block of
-// 512.  The n likeliest tokens lie in the n blocks with the largest maxima (taken
-// by maximum, then lower block: a block outside has n better tokens before it), so
-// the alternatives cost the pass one maximum a block, and afterwards a second look at
-// some n blocks, which L2 still holds.
+// One pass over the row gives m, s and t (fp32, relative to the running maximum of a
+// warp) and the largest logit of every block of 512.  The n likeliest tokens lie in the n
+// blocks with the largest maxima (taken by maximum, then lower block: a block outside has
+// n better tokens before it), so the alternatives cost the pass one maximum a block, and
+// afterwards a second look at some n blocks, which L2 still holds.
 //
-// A row is one thread-block cluster's work; every CTA of it takes a contiguous range
-// of blocks and hands its sums and block maxima to the first one through distributed
-// shared memory.  The pass is bound by HBM; 512 elements of a warp are two or four
-// 16-byte loads a lane.
+// A row is one thread-block cluster's work; every CTA of it takes a contiguous range of
+// blocks and hands its sums and block maxima to the first one through distributed shared
+// memory.  The pass is bound by HBM, with the exponentials close behind (16 a cycle and
+// SM).  Each warp streams for itself: bulk copies of up to 4 KB into its own ring of three
+// slots, so that an SM keeps up to 192 KB on the way without holding registers for it
+// and no barrier stands between warps.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,9 +25,11 @@
 
 #include "device_ptx.cuh"
 #include "spec_logprobs.h"
+#include "tcgen05_ptx.cuh"
 
 namespace {
 
+using specv::add2;
 using specv::bf16_hi;
 using specv::bf16_lo;
 using specv::cluster_arrive_relaxed;
@@ -33,19 +37,29 @@ using specv::cluster_ctarank;
 using specv::cluster_map;
 using specv::cluster_wait_acquire;
 using specv::ex2_approx;
+using specv::f32x2;
+using specv::first_of;
+using specv::fma2;
+using specv::mul2;
+using specv::pair;
+using specv::second_of;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 3;
 constexpr int kBlock = 512;          // logits of a block: 16 a lane
 constexpr int kPerLane = kBlock / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxGroups = 1024;     // block maxima one CTA keeps
-constexpr int kCandidates = 1024;    // tokens the last selection holds
+constexpr int kCandidates = 512;     // tokens the last selection holds
+constexpr int kSlots = 2;            // a warp's ring
+constexpr int kSlotBytes = 4096;
+constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Exponents below this are 0 in fp32 (2^-126 is the smallest normal number and the
-// exponential flushes): weights that far down are dropped, which also keeps
-// 0 * (-inf) out of the entropy's sum.
+// exponential flushes); held there, a masked logit adds 0 * kLowExp to the entropy's sum
+// and not 0 * (-inf).
 constexpr float kLowExp = -140.f;
 
 struct Params {
@@ -62,30 +76,39 @@ struct Params {
   int32_t* row_status;
   int32_t cluster;        // CTAs of a row
   int32_t subs_per_cta;   // blocks of 512 a CTA takes (a multiple of group)
-  int32_t group;          // blocks that share one kept maximum
+  int32_t group;          // blocks that share one kept maximum, a power of two
+  int32_t group_bits;     // its logarithm
   int32_t groups_total;   // kept maxima of a row
+  int32_t chunk;          // blocks of one bulk copy
 };
 
-struct Sums {
+struct alignas(16) Sums {
   float m, s, t;  // largest logit, sum and weighted sum relative to it (log2 units)
-  int bad;        // a NaN or +inf was seen
+  int status;
 };
 
-struct Head {
-  Sums part[kMaxCluster];
-  Sums warp[kWarps];
-  float col_max[kWarps][32];
-  int col_idx[kWarps][32];
-  float thr;
-  int thr_idx;
+// A logit and where it stands: a token, or a group's largest.
+struct alignas(8) Entry {
+  float v;
+  int i;
+};
+// Larger logits first, then lower indices (NaN comes before nothing).  (No || and &&: their
+// branches diverge, and cost the search for a row's alternatives five times its time.)
+__device__ __forceinline__ bool before(const Entry& a, const Entry& b) {
+  return (a.v > b.v) | ((a.v == b.v) & (a.i < b.i));
+}
+constexpr int kNowhere = INT32_MAX;
+
+struct alignas(128) Head {
+  Sums part[kMaxCluster * kWarps];
+  alignas(16) Entry col[kWarps][32];
+  alignas(16) Entry rank[kWarps][32];
+  Entry cand[kCandidates];
+  uint64_t full[kWarps][kSlots], again[kWarps];
+  Sums all;
+  float log_s;
   int nsel, ncand;
-  unsigned long long best[kWarps];
-  float cand_val[kCandidates];
-  int cand_idx[kCandidates];
 };
-
-// (a, i) before (b, j): larger value, then lower index.
-__device__ __forceinline__ bool before(float a, int i, float b, int j) { return a > b || (a == b && i < j); }
 
 __device__ __forceinline__ float warp_max_nan(float v) {
   float r;
@@ -93,77 +116,95 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return r;
 }
 
-// Merge partial sums: both relative to their own maximum, c = log2(e) / T.
-__device__ __forceinline__ Sums merge(const Sums& a, const Sums& b, float c) {
-  Sums r;
-  r.bad = a.bad | b.bad;
-  r.m = fmaxf(a.m, b.m);
-  r.s = r.t = 0.f;
-  if (a.s > 0.f) {
-    const float d = fmaxf((a.m - r.m) * c, kLowExp), f = ex2_approx(d);
-    r.s += a.s * f;
-    r.t += f * fmaf(a.s, d, a.t);
-  }
-  if (b.s > 0.f) {
-    const float d = fmaxf((b.m - r.m) * c, kLowExp), f = ex2_approx(d);
-    r.s += b.s * f;
-    r.t += f * fmaf(b.s, d, b.t);
-  }
-  return r;
+// Places in a list for the lanes that want one; one atomic a warp.
+__device__ __forceinline__ int reserve(int* total, bool want) {
+  const uint32_t all = __ballot_sync(0xFFFFFFFFu, want);
+  if (all == 0) return 0;
+  int base = 0;
+  if ((threadIdx.x & 31) == 0) base = atomicAdd(total, __popc(all));
+  return __shfl_sync(0xFFFFFFFFu, base, 0) + __popc(all & ((1u << (threadIdx.x & 31)) - 1));
 }
 
-// The 16 logits of this lane of block `sub`: element e of them is logit
+// This lane's 16 logits of block `sub`, as they are stored: element e of them is logit
 // index_of(e) of the row.  Past the vocabulary: -inf.
 template <bool BF16, bool VEC>
 struct Block {
+  static constexpr int kWords = BF16 ? kPerLane / 2 : kPerLane;
+  static constexpr int kBytes = kBlock * (BF16 ? 2 : 4);
+  uint32_t w[kWords];
+
   __device__ static __forceinline__ int64_t index_of(int sub, int lane, int e) {
-    constexpr int w = VEC ? (BF16 ? 8 : 4) : 1;  // elements of a load
-    return sub * static_cast<int64_t>(kBlock) + (e / w) * (32 * w) + lane * w + e % w;
+    constexpr int n = VEC ? (BF16 ? 8 : 4) : 1;  // elements of a load
+    return sub * static_cast<int64_t>(kBlock) + (e / n) * (32 * n) + lane * n + e % n;
   }
   __device__ static __forceinline__ float at(const uint8_t* row, int64_t i) {
     if (BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[i]);
     return reinterpret_cast<const float*>(row)[i];
   }
-  __device__ static __forceinline__ void load(const uint8_t* row, int V, int sub, int lane, float (&x)[kPerLane]) {
+  __device__ __forceinline__ float value(int e) const {
+    if (!BF16) return __uint_as_float(w[e]);
+    return e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+  }
+  // A whole block from 16-byte aligned memory, shared or global.
+  __device__ __forceinline__ void load_vec(const uint8_t* block, int lane) {
+#pragma unroll
+    for (int j = 0; j < kWords / 4; ++j) {
+      const uint4 u = *reinterpret_cast<const uint4*>(block + j * 512 + lane * 16);
+      w[4 * j] = u.x;
+      w[4 * j + 1] = u.y;
+      w[4 * j + 2] = u.z;
+      w[4 * j + 3] = u.w;
+    }
+  }
+  __device__ __forceinline__ void load(const uint8_t* row, int V, int sub, int lane) {
     if (VEC && (sub + 1) * static_cast<int64_t>(kBlock) <= V) {
-      constexpr int w = BF16 ? 8 : 4;
-      constexpr int size = BF16 ? 2 : 4;
+      load_vec(row + sub * static_cast<int64_t>(kBytes), lane);
+      return;
+    }
 #pragma unroll
-      for (int j = 0; j < kPerLane / w; ++j) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(
-            row + (static_cast<int64_t>(sub) * kBlock + j * (32 * w) + lane * w) * size));
-        const uint32_t word[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (BF16) {
-            x[j * w + 2 * e] = bf16_lo(word[e]);
-            x[j * w + 2 * e + 1] = bf16_hi(word[e]);
-          } else {
-            x[j * w + e] = __uint_as_float(word[e]);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kPerLane; ++e) {
-        const int64_t i = index_of(sub, lane, e);
-        x[e] = i < V ? at(row, i) : -INFINITY;
+    for (int e = 0; e < kPerLane; ++e) {
+      const int64_t i = index_of(sub, lane, e);
+      if (BF16) {
+        const uint32_t x = i < V ? reinterpret_cast<const uint16_t*>(row)[i] : 0xFF80u;
+        if (e % 2) w[e / 2] |= x << 16;
+        else w[e / 2] = x;
+      } else {
+        w[e] = i < V ? reinterpret_cast<const uint32_t*>(row)[i] : 0xFF800000u;
       }
     }
+  }
+  // The largest, NaN if any is.
+  __device__ __forceinline__ float top() const {
+    if (BF16) {
+      uint32_t m = w[0];
+#pragma unroll
+      for (int j = 1; j < kWords; ++j) m = specv::bf16x2_max_nan(m, w[j]);
+      return specv::f32_max_nan(bf16_lo(m), bf16_hi(m));
+    }
+    float m = __uint_as_float(w[0]);
+#pragma unroll
+    for (int j = 1; j < kWords; ++j) m = specv::f32_max_nan(m, __uint_as_float(w[j]));
+    return m;
   }
 };
 
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(const Params p) {
   using B = Block<BF16, VEC>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   Head& hd = *reinterpret_cast<Head*>(smem);
-  float* maxima = reinterpret_cast<float*>(smem + sizeof(Head));       // [groups_total], the first CTA's
-  int* sel = reinterpret_cast<int*>(maxima + p.groups_total);          // [groups_total]
+  float* maxima = reinterpret_cast<float*>(smem + sizeof(Head));  // [groups_total], whole in the first CTA
+  uint8_t* ring = smem + sizeof(Head) + (p.groups_total * 8 + 127) / 128 * 128;
   const uint32_t rank = p.cluster > 1 ? cluster_ctarank() : 0;
   const int r = blockIdx.x / p.cluster;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (p.cluster > 1) cluster_arrive_relaxed();
+  if (VEC && lane == 0) {
+    for (int i = 0; i < kSlots; ++i) specv::mbar_init(&hd.full[warp][i], 1);
+    specv::mbar_init(&hd.again[warp], 1);
+    specv::fence_mbar_init();
+  }
+  __syncwarp();
   specv::griddep_wait();
   specv::griddep_launch_dependents();
 
@@ -171,192 +212,373 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const Params p
   const bool asked = tok >= 0 && tok < p.V;
   const uint8_t* row = p.logits + r * p.ld_bytes;
   const float T = p.temps != nullptr && p.temps[r] > 0.f ? p.temps[r] : 1.f;
-  const float c = kLog2e / T;
-  const int subs = (p.V + kBlock - 1) / kBlock;
+  const float c = fminf(kLog2e / T, FLT_MAX);
+  const float given = asked && rank == 0 && threadIdx.x == kThreads - 32 ? B::at(row, tok) : 0.f;
+  const int subs = (p.V - 1) / kBlock + 1;
   const int first = rank * p.subs_per_cta;
   const int last = min(subs, first + p.subs_per_cta);
-  const int g0 = first / p.group;
-  const int ngroups = last > first ? (last - first + p.group - 1) / p.group : 0;
-  Sums acc{-INFINITY, 0.f, 0.f, 0};
+  const int g0 = first >> p.group_bits;
+  const int ngroups = last > first ? (last - first + p.group - 1) >> p.group_bits : 0;
+  Sums acc{-INFINITY, 0.f, 0.f, SPEC_OK};
   if (asked) {
     float* mine = maxima + g0;  // kept at the same offsets in every CTA of the cluster
     if (p.group > 1) {
       for (int i = threadIdx.x; i < ngroups; i += kThreads) mine[i] = -INFINITY;
       __syncthreads();
     }
-    for (int sub = first + warp; sub < last; sub += kWarps) {
-      float x[kPerLane];
-      B::load(row, p.V, sub, lane, x);
-      float top = x[0];
-#pragma unroll
-      for (int e = 1; e < kPerLane; ++e) top = specv::f32_max_nan(top, x[e]);
-      top = warp_max_nan(top);
-      if (lane == 0) {
-        if (p.group == 1) {
-          mine[sub - first] = top;
-        } else {  // float order as integer order
-          int* cell = reinterpret_cast<int*>(&mine[(sub - first) / p.group]);
-          int old = *reinterpret_cast<volatile int*>(cell);
-          while (__int_as_float(old) < top) {
-            const int seen = atomicCAS(cell, old, __float_as_int(top));
-            if (seen == old) break;
-            old = seen;
-          }
+    f32x2 s2 = 0ull, t2 = 0ull;
+    auto keep = [&](float top, int sub) {  // block `sub`'s largest
+      if (lane != 0) return;
+      if (p.group == 1) {
+        mine[sub - first] = top;
+      } else {
+        int* cell = reinterpret_cast<int*>(&mine[(sub - first) >> p.group_bits]);
+        int old = *reinterpret_cast<volatile int*>(cell);
+        while (__int_as_float(old) < top) {
+          const int seen = atomicCAS(cell, old, __float_as_int(top));
+          if (seen == old) break;
+          old = seen;
         }
       }
-      if (!(top < INFINITY)) acc.bad = 1;
-      if (!(top > -INFINITY)) continue;
+    };
+    // The running maximum raised to `top`; false where nothing counts.
+    auto raise = [&](float top) {
+      if (!(top < INFINITY)) acc.status = SPEC_ERR_NONFINITE;
+      if (!(top > -INFINITY)) return false;
       if (top > acc.m) {
-        if (acc.s > 0.f) {
-          const float d = fmaxf((acc.m - top) * c, kLowExp), f = ex2_approx(d);
-          acc.t = f * fmaf(acc.s, d, acc.t);
-          acc.s *= f;
-        }
+        const float d = fmaxf((acc.m - top) * c, kLowExp), f = ex2_approx(d);
+        t2 = mul2(pair(f, f), fma2(s2, pair(d, d), t2));
+        s2 = mul2(pair(f, f), s2);
         acc.m = top;
       }
+      return true;
+    };
+    auto add = [&](const B& x) {
+      const f32x2 m2 = pair(-acc.m, -acc.m), c2 = pair(c, c);
 #pragma unroll
-      for (int e = 0; e < kPerLane; ++e) {
-        const float a = fmaxf((x[e] - acc.m) * c, kLowExp);
-        const float w = ex2_approx(a);
-        acc.s += w;
-        acc.t = fmaf(w, a, acc.t);
+      for (int e = 0; e < kPerLane; e += 2) {
+        f32x2 a = mul2(add2(pair(x.value(e), x.value(e + 1)), m2), c2);
+        a = pair(fmaxf(first_of(a), kLowExp), fmaxf(second_of(a), kLowExp));
+        const f32x2 w = pair(ex2_approx(first_of(a)), ex2_approx(second_of(a)));
+        s2 = add2(s2, w);
+        t2 = fma2(w, a, t2);
+      }
+    };
+    auto take = [&](const B& x, int sub) {
+      const float top = warp_max_nan(x.top());
+      keep(top, sub);
+      if (raise(top)) add(x);
+    };
+    if (VEC) {
+      // Whole blocks through the ring, `chunk` of them a copy, the warps in turn.
+      uint8_t* slots = ring + warp * (kSlots * kSlotBytes);
+      const int whole = min(last, p.V / kBlock);
+      const int step = kWarps * p.chunk;
+      auto issue = [&](int sub, int slot) {
+        if (lane == 0 && sub < whole) {
+          const uint32_t bytes = min(p.chunk, whole - sub) * B::kBytes;
+          specv::mbar_arrive_expect_tx(&hd.full[warp][slot], bytes);
+          specv::bulk_g2s(slots + slot * kSlotBytes, row + sub * static_cast<int64_t>(B::kBytes), bytes,
+                          &hd.full[warp][slot]);
+        }
+      };
+      int sub = first + warp * p.chunk;  // (blocks, at most 2^22 of them)
+      for (int i = 0; i < kSlots; ++i) issue(sub + i * step, i);
+      int slot = 0, phase = 0;
+      for (; sub < whole; sub += step) {
+        if (!specv::mbar_wait_bounded(&hd.full[warp][slot], phase)) {
+          acc.status = SPEC_ERR_TIMEOUT;  // (what is on the way still lands before the CTA ends)
+          for (int i = 0; i < kSlots && sub + i * step < whole; ++i) {
+            specv::mbar_wait_bounded(&hd.full[warp][slot], phase);
+            if (++slot == kSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+          break;
+        }
+        const int n = min(p.chunk, whole - sub);
+        const uint8_t* src = slots + slot * kSlotBytes;
+        int i = 0;
+#pragma unroll 1
+        for (; i + 2 <= n; i += 2) {  // (two at a time: their latencies overlap)
+          B x, y;
+          x.load_vec(src + i * B::kBytes, lane);
+          y.load_vec(src + (i + 1) * B::kBytes, lane);
+          const float tx = warp_max_nan(x.top()), ty = warp_max_nan(y.top());
+          keep(tx, sub + i);
+          keep(ty, sub + i + 1);
+          if (raise(specv::f32_max_nan(tx, ty))) {
+            add(x);
+            add(y);
+          }
+        }
+        if (i < n) {
+          B x;
+          x.load_vec(src + i * B::kBytes, lane);
+          take(x, sub + i);
+        }
+        __syncwarp();
+        issue(sub + kSlots * step, slot);
+        if (++slot == kSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+      if (whole < last && warp == 0) {  // the row's last, partial block
+        B x;
+        x.load(row, p.V, whole, lane);
+        take(x, whole);
+      }
+    } else {
+      for (int sub = first + warp; sub < last; sub += kWarps) {
+        B x;
+        x.load(row, p.V, sub, lane);
+        take(x, sub);
       }
     }
     // The maximum is the warp's, so the lanes' sums add directly.
+    acc.s = first_of(s2) + second_of(s2);
+    acc.t = first_of(t2) + second_of(t2);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       acc.s += __shfl_xor_sync(0xFFFFFFFFu, acc.s, d);
       acc.t += __shfl_xor_sync(0xFFFFFFFFu, acc.t, d);
+      acc.status = max(acc.status, __shfl_xor_sync(0xFFFFFFFFu, acc.status, d));
     }
-    if (lane == 0) hd.warp[warp] = acc;
-  }
-  __syncthreads();
-  if (asked && threadIdx.x == 0) {
-    acc = hd.warp[0];
-    for (int w = 1; w < kWarps; ++w) acc = merge(acc, hd.warp[w], c);
-    hd.part[rank] = acc;
   }
   if (p.cluster > 1) {
     cluster_wait_acquire();  // every CTA of the cluster has started
     if (asked && rank != 0) {
+      __syncthreads();
       const uint32_t dst = cluster_map(maxima + g0, 0);
       for (int i = threadIdx.x; i < ngroups; i += kThreads)
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + 4 * i), "f"(maxima[g0 + i]) : "memory");
-      if (threadIdx.x == 0) {
-        const uint32_t s = cluster_map(&hd.part[rank], 0);
+      if (lane == 0) {
+        const uint32_t s = cluster_map(&hd.part[rank * kWarps + warp], 0);
         asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(s), "r"(__float_as_uint(acc.m)),
-                     "r"(__float_as_uint(acc.s)), "r"(__float_as_uint(acc.t)), "r"(acc.bad)
+                     "r"(__float_as_uint(acc.s)), "r"(__float_as_uint(acc.t)), "r"(acc.status)
                      : "memory");
       }
     }
+    if (rank == 0 && lane == 0) hd.part[warp] = acc;
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    if (rank != 0) return;  // (the first CTA waits for those that have not ended)
     cluster_wait_acquire();
-    if (rank != 0) return;
+  } else {
+    if (lane == 0) hd.part[warp] = acc;
+    __syncthreads();
   }
   const int n = p.top;
   int32_t* ids = p.top_ids + static_cast<int64_t>(r) * n;
   float* lps = p.top_logprobs + static_cast<int64_t>(r) * n;
-  __syncthreads();
-  Sums all{-INFINITY, 0.f, 0.f, 0};
-  if (asked)
-    for (int i = 0; i < p.cluster; ++i) all = merge(all, hd.part[i], c);
-  const bool ok = asked && !all.bad && all.s > 0.f;
-  const float log_s = logf(all.s);
-  if (threadIdx.x == 0) {
-    float lp = 0.f, ent = 0.f;
-    if (ok) {
-      lp = (B::at(row, tok) - all.m) / T - log_s;
-      ent = log_s - (all.t / all.s) * kLn2;
-    } else if (tok >= 0) {
-      lp = ent = NAN;
+  if (!asked) {
+    const float none = tok < 0 ? 0.f : NAN;
+    if (threadIdx.x == 0) {
+      p.logprobs[r] = none;
+      if (p.entropy != nullptr) p.entropy[r] = none;
+      if (p.row_status != nullptr) p.row_status[r] = tok < 0 ? SPEC_OK : SPEC_ERR_TOKEN_RANGE;
     }
-    p.logprobs[r] = lp;
-    if (p.entropy != nullptr) p.entropy[r] = ent;
-    if (p.row_status != nullptr)
-      p.row_status[r] = ok || tok < 0 ? SPEC_OK : (asked ? SPEC_ERR_NONFINITE : SPEC_ERR_TOKEN_RANGE);
-  }
-  if (n == 0) return;
-  if (!ok) {
     if (threadIdx.x < n) {
       ids[threadIdx.x] = -1;
-      lps[threadIdx.x] = tok < 0 ? 0.f : NAN;
+      lps[threadIdx.x] = none;
     }
     return;
   }
-
-  // A lower bound of the n-th likeliest token: the groups are dealt to 32 columns,
-  // and the n-th of the columns' maxima has n tokens no worse than it.
-  {
-    float v = -INFINITY;
-    int vi = INT32_MAX;
-    for (int i = threadIdx.x; i < p.groups_total; i += kThreads)
-      if (vi == INT32_MAX || maxima[i] > v) {
-        v = maxima[i];
-        vi = i;
-      }
-    hd.col_max[warp][lane] = v;
-    hd.col_idx[warp][lane] = vi;
-    if (threadIdx.x == 0) hd.nsel = hd.ncand = 0;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    float v = hd.col_max[0][lane];
-    int vi = hd.col_idx[0][lane];
-    for (int w = 1; w < kWarps; ++w)
-      if (before(hd.col_max[w][lane], hd.col_idx[w][lane], v, vi)) {
-        v = hd.col_max[w][lane];
-        vi = hd.col_idx[w][lane];
-      }
-    int pos = 0;
-    for (int j = 0; j < 32; ++j) {
-      const float ov = __shfl_sync(0xFFFFFFFFu, v, j);
-      const int oi = __shfl_sync(0xFFFFFFFFu, vi, j);
-      pos += before(ov, oi, v, vi) || (ov == v && oi == vi && j < lane) ? 1 : 0;
+  // The last warp sums up while the others look for the alternatives' groups.
+  if (threadIdx.x == 0) hd.nsel = hd.ncand = 0;
+  Entry best{-INFINITY, kNowhere};
+  if (n > 0) {  // the groups are dealt to 32 columns: this thread's part of its column's best
+    for (int i = threadIdx.x; i < p.groups_total; i += kThreads) {
+      const Entry x{maxima[i], i};
+      if (before(x, best)) best = x;
     }
-    if (pos == n - 1) {
-      hd.thr = v;
-      hd.thr_idx = vi;
-    }
+    hd.col[warp][lane] = best;
+    __syncthreads();
   }
-  __syncthreads();
-  const float thr = hd.thr;
-  const int thr_idx = hd.thr_idx;
-  for (int i = threadIdx.x; i < p.groups_total; i += kThreads)
-    if (!before(thr, thr_idx, maxima[i], i)) sel[atomicAdd(&hd.nsel, 1)] = i;
-  __syncthreads();
-  const int nsel = hd.nsel;
-  // Tokens equal to the bound count up to the end of its group.
-  const int64_t tie_end = thr_idx == INT32_MAX ? INT64_MAX : (static_cast<int64_t>(thr_idx) + 1) * p.group * kBlock;
-  for (int i = warp; i < nsel * p.group; i += kWarps) {
-    const int sub = sel[i / p.group] * p.group + i % p.group;
-    if (sub >= subs) continue;
-    float x[kPerLane];
-    B::load(row, p.V, sub, lane, x);
+  // The n-th of the 32 columns' best: a lower bound of the n-th best of all, since n are no
+  // worse.  A warp finds it for itself (col is filled, a barrier behind).
+  auto bound = [&] {
+    Entry v = hd.col[0][lane];
 #pragma unroll
-    for (int e = 0; e < kPerLane; ++e) {
-      const int64_t id = B::index_of(sub, lane, e);
-      if (id < p.V && (x[e] > thr || (x[e] == thr && id < tie_end))) {
-        const int at = atomicAdd(&hd.ncand, 1);
-        if (at < kCandidates) {
-          hd.cand_val[at] = x[e];
-          hd.cand_idx[at] = static_cast<int>(id);
-        }
+    for (int w = 1; w < kWarps; ++w) {
+      const Entry x = hd.col[w][lane];
+      const bool b = before(x, v);
+      v.v = b ? x.v : v.v;
+      v.i = b ? x.i : v.i;
+    }
+    Entry* const mine = hd.rank[warp];
+    mine[lane] = v;
+    __syncwarp();
+    int pos = 0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float4 o = *reinterpret_cast<const float4*>(&mine[j]);
+      const int i0 = __float_as_int(o.y), i1 = __float_as_int(o.w);
+      // (columns without entries are alike)
+      pos += (o.x > v.v) | ((o.x == v.v) & ((i0 < v.i) | ((i0 == v.i) & (j < lane))));
+      pos += (o.z > v.v) | ((o.z == v.v) & ((i1 < v.i) | ((i1 == v.i) & (j + 1 < lane))));
+    }
+    __syncwarp();
+    return mine[__ffs(__ballot_sync(0xFFFFFFFFu, pos == n - 1)) - 1];
+  };
+  int* const sel = reinterpret_cast<int*>(maxima + p.groups_total);
+  Entry thr{0.f, 0};
+  if (warp == kWarps - 1) {
+    const int parts = p.cluster * kWarps;
+    Sums a{-INFINITY, 0.f, 0.f, SPEC_OK};
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, hd.part[i].m);
+    a.m = specv::warp_max_f32(m);
+    for (int i = lane; i < parts; i += 32) {
+      const Sums x = hd.part[i];
+      a.status = max(a.status, x.status);
+      if (x.s > 0.f) {
+        const float d = fmaxf((x.m - a.m) * c, kLowExp), f = ex2_approx(d);
+        a.s = fmaf(x.s, f, a.s);
+        a.t = fmaf(f, fmaf(x.s, d, x.t), a.t);
       }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, d);
+      a.t += __shfl_xor_sync(0xFFFFFFFFu, a.t, d);
+    }
+    a.status = __reduce_max_sync(0xFFFFFFFFu, a.status);
+    if (a.status == SPEC_OK && !(a.s > 0.f)) a.status = SPEC_ERR_NONFINITE;
+    const float log_s = logf(a.s);
+    if (lane == 0) {
+      hd.all = a;
+      hd.log_s = log_s;
+      const bool ok = a.status == SPEC_OK;
+      p.logprobs[r] = ok ? (given - a.m) / T - log_s : NAN;
+      if (p.entropy != nullptr) p.entropy[r] = ok ? log_s - (a.t / a.s) * kLn2 : NAN;
+      if (p.row_status != nullptr) p.row_status[r] = a.status;
+    }
+    if (n == 0) return;
+  } else {
+    if (n == 0) return;
+    thr = bound();
+    for (int i0 = 0; i0 < p.groups_total; i0 += kThreads - 32) {
+      const int i = i0 + threadIdx.x;
+      const bool want = i < p.groups_total && !before(thr, Entry{maxima[i], i});
+      const int at = reserve(&hd.nsel, want);
+      if (want) sel[at] = i;
+    }
   }
+  __syncthreads();
+  const Sums all = hd.all;
+  const float log_s = hd.log_s;
+  if (all.status != SPEC_OK) {
+    if (threadIdx.x < n) {
+      ids[threadIdx.x] = -1;
+      lps[threadIdx.x] = NAN;
+    }
+    return;
+  }
+  // The selected groups' blocks, each warp some of them, by way of its part of the ring (in
+  // several batches if need be): f(block, where it lies).
+  using S = Block<BF16, true>;  // (as they lie in the ring)
+  const int nblocks = hd.nsel * p.group;
+  constexpr int kHeld = kSlots * kSlotBytes / S::kBytes;
+  uint8_t* const held = ring + warp * (kSlots * kSlotBytes);
+  int staged = -1, batch = 0;
+  auto blocks = [&](auto f) {
+    for (int i0 = warp; i0 < nblocks; i0 += kWarps * kHeld) {
+      auto block = [&](int j) {  // the j-th block of the batch, or one past the row
+        const int i = i0 + j * kWarps;
+        return i < nblocks ? (sel[i >> p.group_bits] << p.group_bits) + (i & (p.group - 1)) : subs;
+      };
+      if (staged != i0) {
+        __syncwarp();
+        staged = i0;
+        uint32_t bytes = 0;
+#pragma unroll 1
+        for (int j = 0; j < kHeld; ++j) {
+          const int sub = block(j);
+          if (sub >= subs) continue;
+          uint8_t* dst = held + j * S::kBytes;
+          if (VEC && (sub + 1) * static_cast<int64_t>(kBlock) <= p.V) {
+            bytes += S::kBytes;
+          } else {  // NaN past the vocabulary
+#pragma unroll 4
+            for (int e = lane; e < kBlock; e += 32) {
+              const int64_t id = sub * static_cast<int64_t>(kBlock) + e;
+              if (BF16) reinterpret_cast<uint16_t*>(dst)[e] = id < p.V ? reinterpret_cast<const uint16_t*>(row)[id] : 0x7FC0u;
+              else reinterpret_cast<uint32_t*>(dst)[e] = id < p.V ? reinterpret_cast<const uint32_t*>(row)[id] : 0x7FC00000u;
+            }
+          }
+        }
+        if (VEC && bytes > 0) {
+          if (lane == 0) {
+            specv::mbar_arrive_expect_tx(&hd.again[warp], bytes);
+#pragma unroll 1
+            for (int j = 0; j < kHeld; ++j) {
+              const int sub = block(j);
+              if (sub < subs && (sub + 1) * static_cast<int64_t>(kBlock) <= p.V)
+                specv::bulk_g2s(held + j * S::kBytes, row + sub * static_cast<int64_t>(S::kBytes), S::kBytes, &hd.again[warp]);
+            }
+          }
+          if (!specv::mbar_wait_bounded(&hd.again[warp], batch & 1) && lane == 0 && p.row_status != nullptr)
+            p.row_status[r] = SPEC_ERR_TIMEOUT;
+          ++batch;
+        }
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int j = 0; j < kHeld; ++j) {
+        const int sub = block(j);
+        if (sub >= subs) continue;
+        S x;
+        x.load_vec(held + j * S::kBytes, lane);
+        f(x, sub, held + j * S::kBytes);
+      }
+    }
+  };
+  // Once more the n-th of 32 columns, now of tokens, then all that are no worse.
+  best = Entry{-INFINITY, kNowhere};
+  blocks([&](const S& x, int sub, const uint8_t*) {
+    float v = x.value(0);
+    int at = 0;
+#pragma unroll
+    for (int e = 1; e < kPerLane; ++e) {  // (in the order of the tokens: the first of equals stays)
+      const bool b = x.value(e) > v;  // (NaN, past the vocabulary, never is)
+      v = b ? x.value(e) : v;
+      at = b ? e : at;
+    }
+    const Entry k{v, static_cast<int>(S::index_of(sub, lane, at))};
+    if (before(k, best)) best = k;
+  });
+  hd.col[warp][lane] = best;  // (a barrier after the groups' columns were read)
+  __syncthreads();
+  const Entry low = bound();
+  blocks([&](const S& x, int sub, const uint8_t* lies) {
+    uint32_t mask = 0;
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) mask |= static_cast<uint32_t>(x.value(e) >= low.v) << e;
+    while (mask != 0) {
+      const int e = __ffs(mask) - 1;
+      mask &= mask - 1;
+      const int64_t id = S::index_of(sub, lane, e);
+      const Entry k{B::at(lies, id - sub * static_cast<int64_t>(kBlock)), static_cast<int>(id)};
+      if (before(low, k)) continue;
+      const int at = atomicAdd(&hd.ncand, 1);
+      if (at < kCandidates) hd.cand[at] = k;
+    }
+  });
   __syncthreads();
   const int ncand = hd.ncand;
-  auto emit = [&](int pos, float v, int id) {
-    ids[pos] = id;
-    lps[pos] = (v - all.m) / T - log_s;
+  auto emit = [&](int pos, const Entry& k) {
+    ids[pos] = k.i;
+    lps[pos] = (k.v - all.m) / T - log_s;
   };
   if (ncand <= kCandidates) {
     for (int i = threadIdx.x; i < ncand; i += kThreads) {
-      const float v = hd.cand_val[i];
-      const int id = hd.cand_idx[i];
+      const Entry k = hd.cand[i];
       int pos = 0;
-      for (int j = 0; j < ncand; ++j) pos += before(hd.cand_val[j], hd.cand_idx[j], v, id) ? 1 : 0;
-      if (pos < n) emit(pos, v, id);
+#pragma unroll 4
+      for (int j = 0; j < ncand; ++j) pos += before(hd.cand[j], k);
+      if (pos < n) emit(pos, k);
     }
     if (threadIdx.x < n && threadIdx.x >= ncand) {
       ids[threadIdx.x] = -1;
@@ -364,42 +586,27 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const Params p
     }
     return;
   }
-  // Many equal logits: one token after the other, the best behind the last.
-  float lv = INFINITY;
-  int li = -1;
+  // The best tokens crowd in few columns: one after the other, the best behind the last.
+  Entry done{INFINITY, -1};
   for (int pos = 0; pos < n; ++pos) {
-    float v = -INFINITY;
-    int vi = INT32_MAX;
-    for (int i = warp; i < nsel * p.group; i += kWarps) {
-      const int sub = sel[i / p.group] * p.group + i % p.group;
-      if (sub >= subs) continue;
-      float x[kPerLane];
-      B::load(row, p.V, sub, lane, x);
-#pragma unroll
-      for (int e = 0; e < kPerLane; ++e) {
-        const int64_t id = B::index_of(sub, lane, e);
-        if (id < p.V && before(lv, li, x[e], static_cast<int>(id)) && before(x[e], static_cast<int>(id), v, vi)) {
-          v = x[e];
-          vi = static_cast<int>(id);
-        }
+    Entry v{-INFINITY, kNowhere};
+    blocks([&](const S&, int sub, const uint8_t*) {
+#pragma unroll 1
+      for (int e = 0; e < kBlock; e += 32) {  // (from memory: little code for what is rare)
+        const int64_t id = sub * static_cast<int64_t>(kBlock) + e + lane;
+        const Entry k{id < p.V ? B::at(row, id) : NAN, static_cast<int>(id)};
+        if (before(done, k) && before(k, v)) v = k;
       }
-    }
-    const float wv = specv::warp_max_f32(v);
-    const int wi = __reduce_min_sync(0xFFFFFFFFu, v == wv ? vi : INT32_MAX);
+    });
+    const float wv = specv::warp_max_f32(v.v);
+    const int wi = __reduce_min_sync(0xFFFFFFFFu, v.v == wv ? v.i : kNowhere);
+    if (lane == 0) hd.col[warp][0] = Entry{wv, wi};
     __syncthreads();
-    if (lane == 0) {
-      hd.col_max[warp][0] = wv;
-      hd.col_idx[warp][0] = wi;
-    }
-    __syncthreads();
-    lv = hd.col_max[0][0];
-    li = hd.col_idx[0][0];
+    done = hd.col[0][0];
     for (int w = 1; w < kWarps; ++w)
-      if (before(hd.col_max[w][0], hd.col_idx[w][0], lv, li)) {
-        lv = hd.col_max[w][0];
-        li = hd.col_idx[w][0];
-      }
-    if (threadIdx.x == 0) emit(pos, lv, li);
+      if (before(hd.col[w][0], done)) done = hd.col[w][0];
+    __syncthreads();
+    if (threadIdx.x == 0) emit(pos, done);
   }
 }
 
@@ -407,6 +614,11 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mutex;
 int g_sms[kMaxDevices] = {};
 bool g_attr[kMaxDevices][4] = {};
+
+constexpr int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Dynamic shared memory: head, block maxima and the list of those selected, ring.
+int64_t smem_bytes(int64_t groups) { return sizeof(Head) + round_up(groups * 8, 128) + kRingBytes; }
 
 }  // namespace
 
@@ -439,19 +651,22 @@ extern "C" int spec_token_logprobs(const spec_logprobs_args* a, void* stream) {
     if (!g_attr[dev][which]) {
       if (cudaFuncSetAttribute(kernels[which], cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
           cudaFuncSetAttribute(kernels[which], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(sizeof(Head)) + 2 * kMaxCluster * kMaxGroups * 4) != cudaSuccess)
+                               static_cast<int>(smem_bytes(kMaxCluster * kMaxGroups))) != cudaSuccess) {
+        cudaGetLastError();
         return SPEC_ERR_CUDA;
+      }
       g_attr[dev][which] = true;
     }
   }
-  const int subs = (a->V + kBlock - 1) / kBlock;
-  // Enough CTAs for two on every SM, each with a block of 512 a warp at least.
+  const int subs = (a->V - 1) / kBlock + 1;
+  // Enough CTAs for all that the SMs hold, each with a block of 512 a warp at least.
   int cluster = 1;
-  while (cluster < kMaxCluster && static_cast<int64_t>(a->rows) * cluster < 2 * sms && subs > cluster * kWarps) cluster *= 2;
+  while (cluster < kMaxCluster && static_cast<int64_t>(a->rows) * cluster < kCtasPerSm * sms && subs > cluster * kWarps)
+    cluster *= 2;
   int group = 1;
   int per = (subs + cluster - 1) / cluster;
   while ((per + group - 1) / group > kMaxGroups) group *= 2;
-  per = (per + group - 1) / group * group;
+  per = static_cast<int>(round_up(per, group));
 
   Params p{};
   p.logits = static_cast<const uint8_t*>(a->logits);
@@ -468,12 +683,16 @@ extern "C" int spec_token_logprobs(const spec_logprobs_args* a, void* stream) {
   p.cluster = cluster;
   p.subs_per_cta = per;
   p.group = group;
+  while ((1 << p.group_bits) < group) ++p.group_bits;
   p.groups_total = (subs + group - 1) / group;
+  // Copies as large as a slot, or as leave every warp one.
+  const int most = kSlotBytes / (kBlock * esize), share = (per + kWarps - 1) / kWarps;
+  p.chunk = share < most ? share : most;
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a->rows) * cluster, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = sizeof(Head) + 2 * static_cast<size_t>(p.groups_total) * 4;
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(p.groups_total));
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attrs[2];
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -115,6 +115,16 @@ def test_many_equal_logits(dtype, V):
     check(x, [0, 1, V - 1, 7], top=20)
 
 
+@pytest.mark.parametrize("dtype,width", [(torch.bfloat16, 8), (torch.float32, 4)])
+def test_best_tokens_crowded(dtype, width):
+    """The best tokens all at the places of one lane: hundreds tie for the last place."""
+    x = rand(2, 70001, dtype, 6, sigma=0.5)
+    ids = torch.arange(70001, device=DEV)
+    x[0, ids % (32 * width) < width] = 7.0
+    x[1, ids % (32 * width) == 3] = 7.0
+    check(x, [0, 3], top=20)
+
+
 def test_sharp_and_flat_rows():
     x = rand(4, 70000, torch.float32, 8, sigma=30.0)
     x[2] = 0.0
