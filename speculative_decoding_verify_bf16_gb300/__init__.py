@@ -9,6 +9,7 @@ fallback.
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -159,12 +160,12 @@ def load_library():
     lib.spec_backoff_step.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]
     lib.spec_token_logprobs.restype = ctypes.c_int
-    lib.spec_token_logprobs.argtypes = [ctypes.POINTER(_LogprobsArgs), ctypes.c_void_p]
+    lib.spec_token_logprobs.argtypes = [ctypes.c_void_p, ctypes.c_void_p]  # (packed bytes, or a structure)
     lib.spec_linear_workspace.restype = ctypes.c_uint64
     lib.spec_linear_workspace.argtypes = [ctypes.c_int32] * 5
     for f in (lib.spec_linear_prefill, lib.spec_linear_verify):
         f.restype = ctypes.c_int
-        f.argtypes = [ctypes.POINTER(_LinearArgs), ctypes.c_void_p]
+        f.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     _lib = lib
     return lib
 
@@ -500,6 +501,39 @@ def spec_apply_penalties(target, row_offsets, draft_tokens, draft_lens, pen_toke
 SPEC_LOGPROBS_MAX_TOP = 20
 
 
+class _Layout:
+    """Packs a ctypes structure's fields, in order, into bytes in one step (filling a
+    structure of thirty fields takes longer than a small kernel runs)."""
+
+    _CODES = {ctypes.c_void_p: "Q", ctypes.c_int: "i", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_uint64: "Q",
+              ctypes.c_float: "f"}
+
+    def __init__(self, cls):
+        fmt, at = "=", 0
+        for name, kind in cls._fields_:
+            here = getattr(cls, name).offset
+            fmt += "x" * (here - at) + self._CODES[kind]
+            at = here + ctypes.sizeof(kind)
+        fmt += "x" * (ctypes.sizeof(cls) - at)
+        self.pack = struct.Struct(fmt).pack
+
+
+_LOGPROBS_LAYOUT = _Layout(_LogprobsArgs)
+_LINEAR_LAYOUT = _Layout(_LinearArgs)
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _opt(t, name, dtype, device, numel):
+    """Address of an optional tensor, 0 for None."""
+    if t is None:
+        return 0
+    _need(t, name, dtype, device, numel)
+    return t.data_ptr()
+
+
 def spec_token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, top_logprobs=None, temperatures=None,
                         row_status=None, rows=None, stream=None):
     """Log probability of each row's token (see spec_token_logprobs in
@@ -511,38 +545,34 @@ def spec_token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, to
     SPEC_LOGPROBS_MAX_TOP; temperatures float32 [rows] (<= 0: unscaled);
     row_status int32 [rows].  ``rows`` defaults to logits.shape[0].
     """
-    lib = load_library()
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1) or logits.dtype not in _DTYPES:
+    lib = _lib or load_library()
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None or logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError("logits must be a 2-D bf16/float32 tensor with unit inner stride")
     dev = logits.device
     if dev.type != "cuda":
         raise ValueError("logits must be on a CUDA device")
-    n = logits.shape[0] if rows is None else int(rows)
-    if n > logits.shape[0]:
+    have, V = logits.shape
+    n = have if rows is None else int(rows)
+    if n > have:
         raise ValueError("rows exceeds the rows of logits")
     _need(tokens, "tokens", torch.int32, dev, n)
     _need(logprobs, "logprobs", torch.float32, dev, n)
-    for t, name, dtype in ((entropy, "entropy", torch.float32), (temperatures, "temperatures", torch.float32),
-                           (row_status, "row_status", torch.int32)):
-        if t is not None:
-            _need(t, name, dtype, dev, n)
-    top = 0
-    if (top_ids is None) != (top_logprobs is None):
-        raise ValueError("top_ids and top_logprobs go together")
-    if top_ids is not None:
+    top = ids = alts = 0
+    if top_ids is not None and top_logprobs is not None:
         if top_ids.dim() != 2 or top_ids.shape != top_logprobs.shape:
             raise ValueError("top_ids and top_logprobs must be [rows, n]")
         top = top_ids.shape[1]
-        _need(top_ids, "top_ids", torch.int32, dev, n * top)
-        _need(top_logprobs, "top_logprobs", torch.float32, dev, n * top)
-    ld = logits.stride(0) if logits.shape[0] > 1 else max(logits.stride(0), logits.shape[1])
-    a = _LogprobsArgs(logits=logits.data_ptr(), dtype=_DTYPES[logits.dtype], ld=ld, V=logits.shape[1], rows=n,
-                      tokens=tokens.data_ptr(), temperatures=None if temperatures is None else temperatures.data_ptr(),
-                      logprobs=logprobs.data_ptr(), entropy=None if entropy is None else entropy.data_ptr(), top=top,
-                      top_ids=None if top == 0 else top_ids.data_ptr(),
-                      top_logprobs=None if top == 0 else top_logprobs.data_ptr(),
-                      row_status=None if row_status is None else row_status.data_ptr())
-    rc = lib.spec_token_logprobs(ctypes.byref(a), _stream(stream))
+        ids = _opt(top_ids, "top_ids", torch.int32, dev, n * top)
+        alts = _opt(top_logprobs, "top_logprobs", torch.float32, dev, n * top)
+    elif top_ids is not top_logprobs:
+        raise ValueError("top_ids and top_logprobs go together")
+    args = _LOGPROBS_LAYOUT.pack(
+        logits.data_ptr(), dtype, logits.stride(0) if have > 1 else max(logits.stride(0), V), V, n, tokens.data_ptr(),
+        _opt(temperatures, "temperatures", torch.float32, dev, n), logprobs.data_ptr(),
+        _opt(entropy, "entropy", torch.float32, dev, n), top, ids, alts,
+        _opt(row_status, "row_status", torch.int32, dev, n))
+    rc = lib.spec_token_logprobs(args, _raw_stream(stream, dev))
     if rc != SPEC_OK:
         raise SpecError(rc, "spec_token_logprobs")
 
@@ -564,50 +594,59 @@ def new_linear_workspace(lanes, v_heads, dk, dv, max_len, device):
     return torch.empty(spec_linear_workspace(lanes, v_heads, dk, dv, max_len), dtype=torch.uint8, device=device)
 
 
-def _activations(t, name, dtype, device, rows):
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
-    if t.dim() != 3 or t.shape[0] != rows or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise ValueError(f"{name} must be [rows, heads, size] with unit inner stride")
-
-
 def _states(t, name, device, shape):
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32:
+    """Address and strides of a state tensor ([.., dk, dv], the last two contiguous)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device:
         raise ValueError(f"{name} must be a float32 tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
+    s = t.stride()
     # (a size of one leaves its stride free, but the kernels read [dk][dv] rows)
-    if (t.stride(-1) != 1 and shape[-1] > 1) or (t.stride(-2) != shape[-1] and shape[-2] > 1):
+    if (s[-1] != 1 and shape[-1] > 1) or (s[-2] != shape[-1] and shape[-2] > 1):
         raise ValueError(f"{name}'s last two dimensions must be contiguous")
+    return t.data_ptr(), s
 
 
-def _linear_args(q, k, v, log_decay, row_offsets, out, max_len, scale, lane_status):
-    dev, rows = q.device, q.shape[0]
-    if dev.type != "cuda" or q.dtype not in _DTYPES:
+def _linear_call(entry, what, q, k, v, log_decay, row_offsets, out, max_len, scale, lane_status, before, before_name,
+                 after, after_name, cols, workspace, stream):
+    dtype, dev = q.dtype, q.device
+    code = _DTYPES.get(dtype)
+    if code is None or dev.type != "cuda":
         raise ValueError("q must be a bf16/float32 tensor on a CUDA device")
+    rows = q.shape[0]
     for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        _activations(t, name, q.dtype, dev, rows)
+        if t.dtype != dtype or t.device != dev:
+            raise ValueError(f"{name} must be a {dtype} tensor on {dev}")
+        if t.dim() != 3 or t.shape[0] != rows or (t.stride(2) != 1 and t.shape[2] > 1):
+            raise ValueError(f"{name} must be [rows, heads, size] with unit inner stride")
     if k.shape != q.shape or out.shape != v.shape:
         raise ValueError("k must have q's shape, and out v's")
-    hk, dk, hv, dv = q.shape[1], q.shape[2], v.shape[1], v.shape[2]
+    _, hk, dk = q.shape
+    _, hv, dv = v.shape
     if hk == 0 or hv % hk:
         raise ValueError("v's heads must be a multiple of q's and k's")
-    if not isinstance(log_decay, torch.Tensor) or log_decay.device != dev or log_decay.dtype != torch.float32 \
-            or tuple(log_decay.shape) != (rows, hv):
+    if log_decay.dtype != torch.float32 or log_decay.device != dev or log_decay.shape != (rows, hv):
         raise ValueError("log_decay must be a float32 [rows, v_heads] tensor (expanded strides allowed)")
     _need(row_offsets, "row_offsets", torch.int32, dev, 1)
     lanes = row_offsets.numel() - 1
-    if lane_status is not None:
-        _need(lane_status, "lane_status", torch.int32, dev, lanes)
-    return _LinearArgs(
-        q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), out=out.data_ptr(),
-        q_row_stride=q.stride(0), q_head_stride=q.stride(1), k_row_stride=k.stride(0), k_head_stride=k.stride(1),
-        v_row_stride=v.stride(0), v_head_stride=v.stride(1), out_row_stride=out.stride(0),
-        out_head_stride=out.stride(1), log_decay=log_decay.data_ptr(), decay_row_stride=log_decay.stride(0),
-        decay_head_stride=log_decay.stride(1), row_offsets=row_offsets.data_ptr(),
-        lane_status=None if lane_status is None else lane_status.data_ptr(), dtype=_DTYPES[q.dtype], lanes=lanes,
-        rows=rows, max_len=int(max_len), k_heads=hk, v_heads=hv, dk=dk, dv=dv,
-        scale=dk ** -0.5 if scale is None else float(scale))
+    in_ptr = out_ptr = in_lane = in_head = out_lane = out_col = out_head = 0
+    if before is not None:
+        in_ptr, (in_lane, in_head, *_) = _states(before, before_name, dev, (lanes, hv, dk, dv))
+    if after is not None:
+        if cols is None:
+            out_ptr, (out_lane, out_head, *_) = _states(after, after_name, dev, (lanes, hv, dk, dv))
+        else:
+            out_ptr, (out_lane, out_col, out_head, *_) = _states(after, after_name, dev, (lanes, cols, hv, dk, dv))
+    qs, ks, vs, os_, gs = q.stride(), k.stride(), v.stride(), out.stride(), log_decay.stride()
+    args = _LINEAR_LAYOUT.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0],
+        os_[1], log_decay.data_ptr(), gs[0], gs[1], row_offsets.data_ptr(), in_ptr, in_lane, in_head, out_ptr, out_lane,
+        out_col, out_head, _opt(lane_status, "lane_status", torch.int32, dev, lanes), code, lanes, rows, max_len, hk, hv,
+        dk, dv, dk ** -0.5 if scale is None else scale, 0 if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel())
+    rc = entry(args, _raw_stream(stream, dev))
+    if rc != SPEC_OK:
+        raise SpecError(rc, what)
 
 
 def spec_linear_prefill(q, k, v, log_decay, row_offsets, state_in, out, state_out, max_len, scale=None,
@@ -625,24 +664,15 @@ def spec_linear_prefill(q, k, v, log_decay, row_offsets, state_in, out, state_ou
     call.  ``workspace`` comes from new_linear_workspace; without one the call
     takes scratch memory from PyTorch's allocator on the current stream.
     """
-    lib = load_library()
-    a = _linear_args(q, k, v, log_decay, row_offsets, out, max_len, scale, lane_status)
-    shape = (a.lanes, a.v_heads, a.dk, a.dv)
-    if state_in is not None:
-        _states(state_in, "state_in", q.device, shape)
-        a.state_in, a.state_in_lane_stride, a.state_in_head_stride = state_in.data_ptr(), *state_in.stride()[:2]
-    if state_out is not None:
-        _states(state_out, "state_out", q.device, shape)
-        a.state_out, a.state_out_lane_stride, a.state_out_head_stride = state_out.data_ptr(), *state_out.stride()[:2]
+    lib = _lib or load_library()
     if workspace is None:
-        workspace = new_linear_workspace(a.lanes, a.v_heads, a.dk, a.dv, a.max_len, q.device)
-        if stream is not None:
+        workspace = new_linear_workspace(row_offsets.numel() - 1, v.shape[1], q.shape[-1], v.shape[-1], max_len, q.device)
+        if stream is not None and workspace.numel() > 0:
             workspace.record_stream(stream)
-    _need(workspace, "workspace", torch.uint8, q.device)
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    rc = lib.spec_linear_prefill(ctypes.byref(a), _stream(stream))
-    if rc != SPEC_OK:
-        raise SpecError(rc, "spec_linear_prefill")
+    else:
+        _need(workspace, "workspace", torch.uint8, q.device)
+    _linear_call(lib.spec_linear_prefill, "spec_linear_prefill", q, k, v, log_decay, row_offsets, out, int(max_len), scale,
+                 lane_status, state_in, "state_in", state_out, "state_out", None, workspace, stream)
 
 
 def spec_linear_verify(q, k, v, log_decay, row_offsets, live, staged, out, scale=None, lane_status=None, stream=None):
@@ -653,17 +683,9 @@ def spec_linear_verify(q, k, v, log_decay, row_offsets, live, staged, out, scale
     single-token decoding ``staged`` may be ``live.unsqueeze(1)``.  The other
     arguments are those of spec_linear_prefill.
     """
-    lib = load_library()
+    lib = _lib or load_library()
     if not isinstance(staged, torch.Tensor) or staged.dim() != 5:
         raise ValueError("staged must be a [lanes, cols, v_heads, dk, dv] tensor")
-    a = _linear_args(q, k, v, log_decay, row_offsets, out, staged.shape[1], scale, lane_status)
-    shape = (a.lanes, a.v_heads, a.dk, a.dv)
-    if live is not None:
-        _states(live, "live", q.device, shape)
-        a.state_in, a.state_in_lane_stride, a.state_in_head_stride = live.data_ptr(), *live.stride()[:2]
-    _states(staged, "staged", q.device, (a.lanes, staged.shape[1], *shape[1:]))
-    a.state_out = staged.data_ptr()
-    a.state_out_lane_stride, a.state_out_col_stride, a.state_out_head_stride = staged.stride()[:3]
-    rc = lib.spec_linear_verify(ctypes.byref(a), _stream(stream))
-    if rc != SPEC_OK:
-        raise SpecError(rc, "spec_linear_verify")
+    cols = staged.shape[1]
+    _linear_call(lib.spec_linear_verify, "spec_linear_verify", q, k, v, log_decay, row_offsets, out, cols, scale,
+                 lane_status, live, "live", staged, "staged", cols, None, stream)

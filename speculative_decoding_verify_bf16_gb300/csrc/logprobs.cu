@@ -51,7 +51,8 @@ constexpr int kBlock = 512;          // logits of a block: 16 a lane
 constexpr int kPerLane = kBlock / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxGroups = 1024;     // block maxima one CTA keeps
-constexpr int kCandidates = 512;     // tokens the last selection holds
+static_assert(kMaxCluster * kMaxGroups <= 1 << 16, "groups are listed in 16 bits");
+constexpr int kCandidates = 256;     // tokens the last selection holds
 constexpr int kSlots = 2;            // a warp's ring
 constexpr int kSlotBytes = 4096;
 constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
@@ -100,10 +101,12 @@ __device__ __forceinline__ bool before(const Entry& a, const Entry& b) {
 constexpr int kNowhere = INT32_MAX;
 
 struct alignas(128) Head {
-  Sums part[kMaxCluster * kWarps];
+  union {
+    Sums part[kMaxCluster * kWarps];
+    Entry cand[kCandidates];  // (once the parts are summed)
+  };
   alignas(16) Entry col[kWarps][32];
   alignas(16) Entry rank[kWarps][32];
-  Entry cand[kCandidates];
   uint64_t full[kWarps][kSlots], again[kWarps];
   Sums all;
   float log_s;
@@ -131,6 +134,7 @@ template <bool BF16, bool VEC>
 struct Block {
   static constexpr int kWords = BF16 ? kPerLane / 2 : kPerLane;
   static constexpr int kBytes = kBlock * (BF16 ? 2 : 4);
+  static constexpr int kTogether = kSlotBytes / kBytes;
   uint32_t w[kWords];
 
   __device__ static __forceinline__ int64_t index_of(int sub, int lane, int e) {
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
   extern __shared__ __align__(128) uint8_t smem[];
   Head& hd = *reinterpret_cast<Head*>(smem);
   float* maxima = reinterpret_cast<float*>(smem + sizeof(Head));  // [groups_total], whole in the first CTA
-  uint8_t* ring = smem + sizeof(Head) + (p.groups_total * 8 + 127) / 128 * 128;
+  uint8_t* ring = smem + sizeof(Head) + (p.groups_total * 6 + 127) / 128 * 128;
   const uint32_t rank = p.cluster > 1 ? cluster_ctarank() : 0;
   const int r = blockIdx.x / p.cluster;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -227,8 +231,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
       __syncthreads();
     }
     f32x2 s2 = 0ull, t2 = 0ull;
+    float ref = 0.f;   // weights are 2^(c x - ref), ref = c m rounded once: it cancels
+    bool plain = false;
+    uint32_t low = 0;  // (plain) what is below it has weight 0
     auto keep = [&](float top, int sub) {  // block `sub`'s largest
-      if (lane != 0) return;
       if (p.group == 1) {
         mine[sub - first] = top;
       } else {
@@ -246,27 +252,59 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
       if (!(top < INFINITY)) acc.status = SPEC_ERR_NONFINITE;
       if (!(top > -INFINITY)) return false;
       if (top > acc.m) {
-        const float d = fmaxf((acc.m - top) * c, kLowExp), f = ex2_approx(d);
-        t2 = mul2(pair(f, f), fma2(s2, pair(d, d), t2));
-        s2 = mul2(pair(f, f), s2);
+        const float next = top * c;
+        // Far from overflow, and with room below the maximum for all that counts: the plain
+        // form.  Otherwise (x - m) c, every exponent clamped.
+        const float at = (next + kLowExp) / c;
+        const bool was = plain;
+        plain = fabsf(next) < 0x1p100f && at > -0x1p126f && at < top;
+        if (acc.m > -INFINITY) {
+          const float d = fmaxf(was && plain ? ref - next : (acc.m - top) * c, kLowExp), f = ex2_approx(d);
+          t2 = mul2(pair(f, f), fma2(s2, pair(d, d), t2));
+          s2 = mul2(pair(f, f), s2);
+        }
+        ref = next;
         acc.m = top;
+        if (BF16) {
+          low = __bfloat16_as_ushort(__float2bfloat16_rd(at));
+          low |= low << 16;
+        }
       }
       return true;
     };
     auto add = [&](const B& x) {
-      const f32x2 m2 = pair(-acc.m, -acc.m), c2 = pair(c, c);
+      const f32x2 c2 = pair(c, c);
+      if (plain) {
+        const f32x2 r2 = pair(-ref, -ref);
 #pragma unroll
-      for (int e = 0; e < kPerLane; e += 2) {
-        f32x2 a = mul2(add2(pair(x.value(e), x.value(e + 1)), m2), c2);
-        a = pair(fmaxf(first_of(a), kLowExp), fmaxf(second_of(a), kLowExp));
-        const f32x2 w = pair(ex2_approx(first_of(a)), ex2_approx(second_of(a)));
-        s2 = add2(s2, w);
-        t2 = fma2(w, a, t2);
+        for (int e = 0; e < kPerLane; e += 2) {
+          f32x2 a;
+          if (BF16) {
+            const uint32_t w = specv::bf16x2_max_nan(x.w[e / 2], low);
+            a = fma2(pair(bf16_lo(w), bf16_hi(w)), c2, r2);
+          } else {
+            a = fma2(pair(x.value(e), x.value(e + 1)), c2, r2);
+            a = pair(fmaxf(first_of(a), kLowExp), fmaxf(second_of(a), kLowExp));
+          }
+          const f32x2 w = pair(ex2_approx(first_of(a)), ex2_approx(second_of(a)));
+          s2 = add2(s2, w);
+          t2 = fma2(w, a, t2);
+        }
+      } else {
+        const f32x2 m2 = pair(-acc.m, -acc.m);
+#pragma unroll
+        for (int e = 0; e < kPerLane; e += 2) {
+          f32x2 a = mul2(add2(pair(x.value(e), x.value(e + 1)), m2), c2);
+          a = pair(fmaxf(first_of(a), kLowExp), fmaxf(second_of(a), kLowExp));
+          const f32x2 w = pair(ex2_approx(first_of(a)), ex2_approx(second_of(a)));
+          s2 = add2(s2, w);
+          t2 = fma2(w, a, t2);
+        }
       }
     };
     auto take = [&](const B& x, int sub) {
       const float top = warp_max_nan(x.top());
-      keep(top, sub);
+      if (lane == 0) keep(top, sub);
       if (raise(top)) add(x);
     };
     if (VEC) {
@@ -299,24 +337,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
         }
         const int n = min(p.chunk, whole - sub);
         const uint8_t* src = slots + slot * kSlotBytes;
-        int i = 0;
-#pragma unroll 1
-        for (; i + 2 <= n; i += 2) {  // (two at a time: their latencies overlap)
-          B x, y;
-          x.load_vec(src + i * B::kBytes, lane);
-          y.load_vec(src + (i + 1) * B::kBytes, lane);
-          const float tx = warp_max_nan(x.top()), ty = warp_max_nan(y.top());
-          keep(tx, sub + i);
-          keep(ty, sub + i + 1);
-          if (raise(specv::f32_max_nan(tx, ty))) {
-            add(x);
-            add(y);
+        if (n == B::kTogether) {  // (a slot's blocks at once: their latencies overlap)
+          B x[B::kTogether];
+          float top[B::kTogether], most = -INFINITY, own = 0.f;
+#pragma unroll
+          for (int i = 0; i < B::kTogether; ++i) x[i].load_vec(src + i * B::kBytes, lane);
+#pragma unroll
+          for (int i = 0; i < B::kTogether; ++i) {
+            top[i] = warp_max_nan(x[i].top());
+            most = specv::f32_max_nan(most, top[i]);
+            own = lane == i ? top[i] : own;
           }
-        }
-        if (i < n) {
-          B x;
-          x.load_vec(src + i * B::kBytes, lane);
-          take(x, sub + i);
+          if (lane < B::kTogether) keep(own, sub + lane);
+          if (raise(most)) {
+#pragma unroll
+            for (int i = 0; i < B::kTogether; ++i) add(x[i]);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < n; ++i) {
+            B x;
+            x.load_vec(src + i * B::kBytes, lane);
+            take(x, sub + i);
+          }
         }
         __syncwarp();
         issue(sub + kSlots * step, slot);
@@ -340,6 +383,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
     // The maximum is the warp's, so the lanes' sums add directly.
     acc.s = first_of(s2) + second_of(s2);
     acc.t = first_of(t2) + second_of(t2);
+    if (plain) {  // handed on as sums of 2^(c (x - m)): ref is c m but for this rounding
+      const float d = fmaf(-acc.m, c, ref), f = ex2_approx(d);
+      acc.t = f * fmaf(acc.s, d, acc.t);
+      acc.s *= f;
+    }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       acc.s += __shfl_xor_sync(0xFFFFFFFFu, acc.s, d);
@@ -422,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
     __syncwarp();
     return mine[__ffs(__ballot_sync(0xFFFFFFFFu, pos == n - 1)) - 1];
   };
-  int* const sel = reinterpret_cast<int*>(maxima + p.groups_total);
+  uint16_t* const sel = reinterpret_cast<uint16_t*>(maxima + p.groups_total);
   Entry thr{0.f, 0};
   if (warp == kWarps - 1) {
     const int parts = p.cluster * kWarps;
@@ -463,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
       const int i = i0 + threadIdx.x;
       const bool want = i < p.groups_total && !before(thr, Entry{maxima[i], i});
       const int at = reserve(&hd.nsel, want);
-      if (want) sel[at] = i;
+      if (want) sel[at] = static_cast<uint16_t>(i);
     }
   }
   __syncthreads();
@@ -618,7 +666,7 @@ bool g_attr[kMaxDevices][4] = {};
 constexpr int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // Dynamic shared memory: head, block maxima and the list of those selected, ring.
-int64_t smem_bytes(int64_t groups) { return sizeof(Head) + round_up(groups * 8, 128) + kRingBytes; }
+int64_t smem_bytes(int64_t groups) { return sizeof(Head) + round_up(groups * 6, 128) + kRingBytes; }
 
 }  // namespace
 
@@ -659,9 +707,11 @@ extern "C" int spec_token_logprobs(const spec_logprobs_args* a, void* stream) {
     }
   }
   const int subs = (a->V - 1) / kBlock + 1;
-  // Enough CTAs for all that the SMs hold, each with a block of 512 a warp at least.
+  // CTAs for most SMs, each with a block of 512 a warp at least.  More of them a row cost more
+  // than they bring, by their start and the exchange: 64 rows of 151,936 take 18.5, 15.0,
+  // 17.4 and 20.0 us with 1, 2, 4 and 8, a single row of 262,144 20.6 with one and 7.8 with 16.
   int cluster = 1;
-  while (cluster < kMaxCluster && static_cast<int64_t>(a->rows) * cluster < kCtasPerSm * sms && subs > cluster * kWarps)
+  while (cluster < kMaxCluster && 4 * static_cast<int64_t>(a->rows) * cluster < 3 * sms && subs > cluster * kWarps)
     cluster *= 2;
   int group = 1;
   int per = (subs + cluster - 1) / cluster;
