@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kRecThreads) linear_recurrent_kernel(const Lin
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int r = row0 + 16 * i;
-      if (col_in && r < p.dk) *reinterpret_cast<float4*>(dst + static_cast<int64_t>(r) * p.dv + col) = S[i];
+      if (col_in && r < p.dk) __stcs(reinterpret_cast<float4*>(dst + static_cast<int64_t>(r) * p.dv + col), S[i]);
     }
   };
 
