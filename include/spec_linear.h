@@ -96,6 +96,15 @@ uint64_t spec_linear_workspace(int32_t lanes, int32_t v_heads, int32_t dk, int32
  * Errors: SPEC_ERR_INVALID_ARG for NULL required pointers (q, k, v, out, log_decay,
  * row_offsets with lanes and rows > 0), sizes or dtype outside the ranges above,
  * misaligned states or too small a workspace; SPEC_ERR_CUDA if a launch fails.
+ *
+ * Prompts in bf16 with dk = dv = 128 (max_len >= 32; q, k, v and out 16-byte aligned in
+ * base and strides) run in chunks of 128 tokens on the tensor cores; everything else
+ * runs token after token, with the same results up to rounding but slower on long
+ * prompts.  out must not overlap q, k or v.
+ *
+ * SPEC_LINEAR_TEST_WITHHOLD_COPY=1 in the environment, tests of the failure path only: the
+ * chunked kernel's first CTA never issues its first copy, so that its waits give up
+ * after some seconds and its lanes report SPEC_ERR_TIMEOUT.
  */
 int spec_linear_prefill(const spec_linear_args* args, void* stream);
 

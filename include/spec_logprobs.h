@@ -39,8 +39,8 @@ typedef struct {
   float* top_logprobs;         /* out [rows][top]: their log p (-inf with id -1)              */
   int32_t* row_status;         /* out [rows], may be NULL: SPEC_OK; SPEC_ERR_TOKEN_RANGE for a
                                   token >= V; SPEC_ERR_NONFINITE for a row that holds NaN or
-                                  +inf, or -inf only.  Such a row's numbers are NaN, its ids
-                                  -1                                                          */
+                                  +inf, or -inf only; SPEC_ERR_TIMEOUT if a bounded wait gave
+                                  up.  Such a row's numbers are NaN, its ids -1               */
 } spec_logprobs_args;
 
 /*
@@ -50,6 +50,11 @@ typedef struct {
  * NULL required pointers (logits, tokens, logprobs; top_ids and top_logprobs with
  * top > 0), V <= 0, rows < 0, ld < V, top out of range or an unknown dtype;
  * SPEC_ERR_CUDA if the launch fails.  rows = 0 is a no-op.
+ *
+ * Rows whose address is 16-byte aligned (base and ld * element size) are streamed with
+ * bulk copies; other layouts take a slower element-wise path with the same results.
+ * SPEC_LOGPROBS_TEST_WITHHOLD_COPY=1 in the environment, tests of the failure path only:
+ * the first row's first copy is never issued, so that its wait gives up after 2 s.
  */
 int spec_token_logprobs(const spec_logprobs_args* args, void* stream);
 

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 
 #include "linear_chunk.cuh"
@@ -271,6 +272,8 @@ int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args*
   void* args[] = {&cp, &q, &k, &v, &out, &begin, &end};
   void* states_args[] = {&cp, &q, &k, &v, &out, &begin, &local};
   cp.sort = p.lanes > 1 && p.lanes <= specv::kSortLanes && static_cast<int64_t>(p.lanes) * p.max_len != p.rows;
+  const char* withhold = std::getenv("SPEC_LINEAR_TEST_WITHHOLD_COPY");
+  cp.test_withhold = withhold != nullptr && std::atoi(withhold) != 0;
   auto grid = [&](int64_t items) { return static_cast<unsigned>(items < dc->sms ? items : dc->sms); };
   if (split) {
     const int rc = launch(states, grid(pairs * (cp.segments - 1)), specv::kChunkThreads, smem, states_args, stream);

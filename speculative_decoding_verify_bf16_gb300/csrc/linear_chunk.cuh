@@ -99,6 +99,7 @@ struct ChunkParams {
   float* local_decay; // [segments][lanes][heads]: whole decay of segment r
   int32_t segments;
   int32_t sort;       // lanes differ in length: longest first
+  int32_t test_withhold;  // tests only: the first CTA announces its first copy but never issues it
 };
 
 // Waits for a phase; gives up after some seconds (a try sleeps up to 1.3 us in the barrier,
@@ -318,8 +319,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const CUtensorMap* map = j == 0 ? &map_k : (j == 1 ? &map_v : &map_q);
             const int hh = j == 1 ? it.h : it.h / p.group, z = it.first + c * kChunk;
             mbar_arrive_expect_tx(&sm.full[slot], kTile);
-            tma_load_3d(sm.ring[slot], map, 0, hh, z, &sm.full[slot]);
-            tma_load_3d(sm.ring[slot] + kHalf, map, 64, hh, z, &sm.full[slot]);
+            if (!(cp.test_withhold && blockIdx.x == 0 && issued == 0)) {
+              tma_load_3d(sm.ring[slot], map, 0, hh, z, &sm.full[slot]);
+              tma_load_3d(sm.ring[slot] + kHalf, map, 64, hh, z, &sm.full[slot]);
+            }
           }
           ++issued;
           if (++slot == kRing) {

@@ -21,6 +21,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 
 #include "device_ptx.cuh"
@@ -81,6 +82,7 @@ struct Params {
   int32_t group_bits;     // its logarithm
   int32_t groups_total;   // kept maxima of a row
   int32_t chunk;          // blocks of one bulk copy
+  int32_t test_withhold;  // tests only: the first row's first copy is announced but never issued
 };
 
 struct alignas(16) Sums {
@@ -316,8 +318,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
         if (lane == 0 && sub < whole) {
           const uint32_t bytes = min(p.chunk, whole - sub) * B::kBytes;
           specv::mbar_arrive_expect_tx(&hd.full[warp][slot], bytes);
-          specv::bulk_g2s(slots + slot * kSlotBytes, row + sub * static_cast<int64_t>(B::kBytes), bytes,
-                          &hd.full[warp][slot]);
+          if (!(p.test_withhold && blockIdx.x == 0 && sub == 0))
+            specv::bulk_g2s(slots + slot * kSlotBytes, row + sub * static_cast<int64_t>(B::kBytes), bytes,
+                            &hd.full[warp][slot]);
         }
       };
       int sub = first + warp * p.chunk;  // (blocks, at most 2^22 of them)
@@ -738,6 +741,9 @@ extern "C" int spec_token_logprobs(const spec_logprobs_args* a, void* stream) {
   // Copies as large as a slot, or as leave every warp one.
   const int most = kSlotBytes / (kBlock * esize), share = (per + kWarps - 1) / kWarps;
   p.chunk = share < most ? share : most;
+
+  const char* withhold = std::getenv("SPEC_LOGPROBS_TEST_WITHHOLD_COPY");
+  p.test_withhold = withhold != nullptr && std::atoi(withhold) != 0;
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a->rows) * cluster, 1, 1);
