@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0);
     constexpr uint32_t kSame = mma_desc(128, 128, false), kRows = mma_desc(128, 128, true);
     const uint32_t ring = smem_desc(smem_addr(sm.ring[0]), kHalf);  // (for K-major tiles the piece distance is not used)
-    const uint32_t dlo = smem_desc(smem_addr(sm.s_lo), kHalf), dhi = smem_desc(smem_addr(sm.s_hi), kHalf);
+    const uint32_t ds = smem_desc(smem_addr(sm.s_hi), kHalf);
     uint32_t kphase = 0;     // bit i: phase of k' buffer i
     int slot = 0, phase = 0; // the ring's slot of this chunk's k and its phase
     int tails = 0;           // chunks that did not fill a tile
@@ -409,22 +409,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!warp_wait(&sm.s_ready, ph, &sm.abort)) break;
         if (gc > 0 && !warp_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          const uint32_t ds = part == 0 ? dlo : dhi;
 #pragma unroll
-          for (int s = 0; s < 8; ++s)
-            mma_ss(lead, tmu + kColD, dq + ((s >> 2) * kHalf + (s & 3) * 32) / 16, ds + s * (2048 / 16), kRows, part + s > 0);
-        }
+        for (int s = 0; s < 8; ++s)
+          mma_ss(lead, tmu + kColD, dq + ((s >> 2) * kHalf + (s & 3) * 32) / 16, ds + s * (2048 / 16), kRows, s > 0);
         mma_commit(lead, &sm.qs_full);
         if (!warp_wait(&sm.p_ready, ph, &sm.abort) || !warp_wait(&sm.d_scaled, ph, &sm.abort)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int t = 0; t < bufs; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_ts(lead, tmu + kColD, tmu + kColP + t * 32 + (i & 1) * 16 + 8 - (i >> 1) * 8,
-                   dv + t * (2 * 2048 / 16) + (i & 1) * (2048 / 16), kRows, true);
+          for (int i = 0; i < 2; ++i)
+            mma_ts(lead, tmu + kColD, tmu + kColP + t * 32 + i * 16, dv + t * (2 * 2048 / 16) + i * (2048 / 16), kRows, true);
         mma_commit(lead, &sm.o_full);
       }
       mma_commit(lead, &sm.empty[sv]);
@@ -512,10 +507,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc_fence_after();
 #pragma unroll 1
         for (int j0 = group * 16; j0 < kChunk; j0 += 32) {  // tokens j0 .. j0 + 15
-          uint32_t hi[8], lo[8];
+          uint32_t w[8];
           if (j0 >= static_cast<int>(quarter) + 32) {  // all after this warp's rows
 #pragma unroll
-            for (int i = 0; i < 8; ++i) hi[i] = lo[i] = 0u;
+            for (int i = 0; i < 8; ++i) w[i] = 0u;
           } else {
             uint32_t s[16];
             tmem_ld16(s, tmq + kColP + j0);
@@ -531,10 +526,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
-                const f32x2 w = mul2(mul2(pair(from_end, from_end), *reinterpret_cast<const f32x2*>(&to_end[i])),
-                                     pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-                hi[i / 2] = upper(w);
-                lo[i / 2] = rounded(rest(w));
+                w[i / 2] = rounded(mul2(mul2(pair(from_end, from_end), *reinterpret_cast<const f32x2*>(&to_end[i])),
+                                        pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1]))));
               }
             } else {
               const int seen = static_cast<int>(row) - j0;  // the last of the tokens that this row sees
@@ -544,18 +537,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 // (the arrays hold -G)
                 const f32x2 d = add2(add2(pair(ghi, ghi), *reinterpret_cast<const f32x2*>(&sm.g_hi[buf][j0 + i])),
                                      add2(pair(glo, glo), *reinterpret_cast<const f32x2*>(&sm.g_lo[buf][j0 + i])));
-                f32x2 w = mul2(pair(ex2_approx(first_of(d)), ex2_approx(second_of(d))),
-                               pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+                const f32x2 x = mul2(pair(ex2_approx(first_of(d)), ex2_approx(second_of(d))),
+                                     pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
                 // (a select: what is masked may be NaN)
-                w = pair(i > seen ? 0.f : first_of(w), i + 1 > seen ? 0.f : second_of(w));
-                hi[i / 2] = upper(w);
-                lo[i / 2] = rounded(rest(w));
+                w[i / 2] = rounded(pair(i > seen ? 0.f : first_of(x), i + 1 > seen ? 0.f : second_of(x)));
               }
             }
           }
-          // Columns of P: for each 16 tokens 8 of upper and 8 of lower parts.
-          tmem_st8(tmq + kColP + j0, hi);
-          tmem_st8(tmq + kColP + j0 + 8, lo);
+          tmem_st8(tmq + kColP + j0, w);  // (P takes half of the scores' columns)
         }
         tmem_wait_st();
         tc_fence_before();
@@ -709,9 +698,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int i = 0; i < 64; i += 4) {
             const uint32_t unit = tile_unit(row, i / 4);
             *reinterpret_cast<uint4*>(sm.s_hi + unit) =
-                make_uint4(upper(S[i]), upper(S[i + 1]), upper(S[i + 2]), upper(S[i + 3]));
-            *reinterpret_cast<uint4*>(sm.s_lo + unit) = make_uint4(rounded(rest(S[i])), rounded(rest(S[i + 1])),
-                                                                   rounded(rest(S[i + 2])), rounded(rest(S[i + 3])));
+                make_uint4(rounded(S[i]), rounded(S[i + 1]), rounded(S[i + 2]), rounded(S[i + 3]));
           }
           fence_async_smem();
           warp_arrive(&sm.s_ready);
