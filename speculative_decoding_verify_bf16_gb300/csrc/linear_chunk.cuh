@@ -63,7 +63,7 @@ constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;    // log2(e)
 // resets (-inf) and lowest values out of the sums.
 constexpr float kDecayFloor = -160.f;
 
-constexpr int kSortLanes = 128;       // most lanes that are taken longest first
+constexpr int kSortLanes = 64;       // most lanes that are taken longest first
 
 // What a CTA walks: chunks c0 .. c1 - 1 of a lane's head.
 struct ChunkItem {
@@ -85,8 +85,9 @@ struct ChunkSmem {
   uint64_t full[kRing], empty[kRing];
   uint64_t item_full[2], item_empty[2];
   uint64_t g_full[2], g_empty[2];
-  uint64_t scores_full, p_ready, qs_full, d_scaled, o_full, d_free, s_ready, kv_full, u_free, v_clean, o_staged, drain;
-  uint64_t kp_full[2], kp_empty[2];
+  uint64_t scores_full, p_ready, qs_full, d_scaled, o_full, d_free, s_ready, v_clean, o_staged, drain;
+  uint64_t kv_full[2], u_free[2];
+  uint64_t kp_full[4], kp_empty[4];
   uint64_t st_full[2], st_free[2], st_done;
   uint32_t tmem;
   int abort;
@@ -189,6 +190,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                         const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_begin,
                         const __grid_constant__ CUtensorMap map_end) {
+  constexpr int kLoads = STATES ? 2 : 3;  // tiles of a chunk: k, v (, q)
+  // Without outputs their groups make k', too: four buffers of it, and two of U.
+  constexpr int kKeyGroups = STATES ? 4 : 2, kKeyWarps = 4 * kKeyGroups;
+  constexpr uint32_t kColKeys = STATES ? kColP : kColK, kColU2 = STATES ? kColK : kColU;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>(smem_raw);
   const LinearParams& p = cp.p;
@@ -196,17 +201,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 9);
+      mbar_init(&sm.empty[i], 1 + kKeyWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      mbar_init(&sm.item_empty[i], STATES ? 15 : 23);
+      mbar_init(&sm.item_empty[i], 23);
       mbar_init(&sm.g_full[i], 1);
-      mbar_init(&sm.g_empty[i], STATES ? 12 : 20);
-      mbar_init(&sm.kp_full[i], 4);
-      mbar_init(&sm.kp_empty[i], 1);
+      mbar_init(&sm.g_empty[i], 20);
+      mbar_init(&sm.kv_full[i], 1);
+      mbar_init(&sm.u_free[i], 4);
       mbar_init(&sm.st_full[i], 1);
       mbar_init(&sm.st_free[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.kp_full[i], 4);
+      mbar_init(&sm.kp_empty[i], 1);
     }
     mbar_init(&sm.scores_full, 1);
     mbar_init(&sm.p_ready, 8);
@@ -215,8 +224,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.d_free, 4);
     mbar_init(&sm.s_ready, 4);
-    mbar_init(&sm.kv_full, 1);
-    mbar_init(&sm.u_free, 4);
     mbar_init(&sm.v_clean, 4);
     mbar_init(&sm.o_staged, 4);
     mbar_init(&sm.st_done, 1);
@@ -241,7 +248,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const uint32_t row = quarter + lane;
   const uint32_t tmq = tm + (quarter << 16);
   const int heads = p.lanes * p.v_heads;
-  constexpr int kLoads = STATES ? 2 : 3;  // tiles of a chunk: k, v (, q)
   ChunkItem it;
   int turn = 0;  // items taken
   int gc = 0;    // chunks done in the items before
@@ -372,7 +378,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const uint32_t dk = ring + sk * (kTile / 16), dv = ring + sv * (kTile / 16), dq = ring + sq * (kTile / 16);
       if (!warp_wait(&sm.full[sv], pv, &sm.abort)) break;
       if (n < kChunk && !warp_wait(&sm.v_clean, tails++ & 1, &sm.abort)) break;
-      if (gc > 0 && !warp_wait(&sm.u_free, ph ^ 1, &sm.abort)) break;
+      // U alternates between two places with STATES.
+      const uint32_t ub = STATES ? gc & 1 : 0, uph = STATES ? (gc >> 1) & 1 : ph;
+      if (gc > (STATES ? 1 : 0) && !warp_wait(&sm.u_free[ub], uph ^ 1, &sm.abort)) break;
       bool fine = true;
 #pragma unroll 1
       for (int t = 0; t < bufs || t == 2; ++t) {
@@ -392,19 +400,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           if (bufs <= 2) break;
         }
-        const uint32_t kb = t & 1;
+        const uint32_t kb = t % kKeyGroups;
         if (!(fine = warp_wait(&sm.kp_full[kb], (kphase >> kb) & 1, &sm.abort))) break;
         tc_fence_after();
-        const uint32_t parts = tmu + kColK + kb * kColKBuf, dvt = dv + t * (2 * 2048 / 16);
+        const uint32_t parts = tmu + kColKeys + kb * kColKBuf, dvt = dv + t * (2 * 2048 / 16);
 #pragma unroll
         for (int i = 0; i < 6; ++i)  // the least part first
-          mma_ts(lead, tmu + kColU, parts + 32 - (i >> 1) * 16 + (i & 1) * 8, dvt + (i & 1) * (2048 / 16), kRows, i + t > 0);
+          mma_ts(lead, tmu + (ub ? kColU2 : kColU), parts + 32 - (i >> 1) * 16 + (i & 1) * 8, dvt + (i & 1) * (2048 / 16), kRows, i + t > 0);
         mma_commit(lead, &sm.kp_empty[kb]);
         kphase ^= 1u << kb;
         if (t == 0 && bufs == 1) t = 1;  // on to QK
       }
       if (!fine) break;
-      mma_commit(lead, &sm.kv_full);
+      mma_commit(lead, &sm.kv_full[ub]);
       if (!STATES) {
         if (!warp_wait(&sm.s_ready, ph, &sm.abort)) break;
         if (gc > 0 && !warp_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
@@ -423,7 +431,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mma_commit(lead, &sm.o_full);
       }
       mma_commit(lead, &sm.empty[sv]);
-      if (lead) mbar_arrive_n(&sm.empty[sv], 8);
+      if (lead) mbar_arrive_n(&sm.empty[sv], kKeyWarps);
       ok = c + 1 == loops;  // the item is done
     }
     }
@@ -433,71 +441,70 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ decays
-    // Fixed point with 32 fractional bits: sums and differences are exact, whatever
-    // large decays stand between two tokens.  32 tokens at a time, a lane each.
+    // Fixed point with 32 fractional bits: sums and differences are exact, whatever large
+    // decays stand between two tokens.  A lane has four tokens of the chunk; it hands on
+    // whole part and fraction.
     bool ok = true;
     while (ok && next_item(sm, turn, it)) {
       const int rows = it.count - it.c0 * kChunk, end = (it.c1 - it.c0) * kChunk;
       const float* src = p.log_decay + (it.first + it.c0 * static_cast<int64_t>(kChunk)) * p.decay_row + it.h * p.decay_head;
-      float g4[4], next4[4];  // this chunk's and the next one's
+      float next[4];
       auto fetch = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          next4[i] = t + 32 * i + lane < rows ? __ldg(src + (t + 32 * i + lane) * p.decay_row) : 0.f;
+        for (int i = 0; i < 4; ++i) next[i] = t + i < rows ? __ldg(src + (t + i) * p.decay_row) : 0.f;
       };
-      fetch(0);
-      long long before = 0;
-      float poison = 0.f;  // NaN once the chunk holds a NaN or a factor infinite in fp32
+      fetch(lane * 4);
 #pragma unroll 1
-      for (int t = 0; t < end; t += 32) {
+      for (int t = 0; t < end; t += kChunk, ++gc) {
         const int buf = gc & 1;
-        if (t % kChunk == 0) {
+        long long sum[4];
+        bool bad = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) g4[i] = next4[i];
-          if (t + kChunk < end) fetch(t + kChunk);
-          if (gc >= 2 && !(ok = warp_wait(&sm.g_empty[buf], ((gc >> 1) - 1) & 1, &sm.abort))) break;
-          before = 0;
-          poison = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          float hi = next[i] * kLog2eHi;
+          float lo = fmaf(next[i], kLog2eHi, -hi) + next[i] * kLog2eLo;
+          bad |= !(hi < 128.f);  // NaN, or a factor infinite in fp32
+          lo = hi > kDecayFloor ? lo : 0.f;
+          hi = fmaxf(hi, kDecayFloor);
+          const float whole = rintf(hi);
+          sum[i] = (static_cast<long long>(__float2int_rn(whole)) << 32) + __float2int_rn((hi - whole) * 0x1p32f) +
+                   __float2int_rn(lo * 0x1p32f);
+          if (i > 0) sum[i] += sum[i - 1];
         }
-        const float g = g4[0];
-        g4[0] = g4[1];
-        g4[1] = g4[2];
-        g4[2] = g4[3];
-        float hi = g * kLog2eHi;
-        float lo = fmaf(g, kLog2eHi, -hi) + g * kLog2eLo;
-        if (__any_sync(0xFFFFFFFFu, !(hi < 128.f))) poison = __uint_as_float(0x7FC00000u);
-        if (!(hi > kDecayFloor)) {
-          hi = kDecayFloor;
-          lo = 0.f;
-        }
-        long long sum = __float2ll_rn(hi * 4294967296.f) + __float2ll_rn(lo * 4294967296.f);
-#pragma unroll 1
+        if (t + kChunk < end) fetch(t + kChunk + lane * 4);
+        long long run = sum[3];
+#pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-          if (lane >= d) sum += up;
+          const long long up = __shfl_up_sync(0xFFFFFFFFu, run, d);
+          run += lane >= d ? up : 0;
         }
-        sum += before;
-        before = __shfl_sync(0xFFFFFFFFu, sum, 31);
-        hi = __ll2float_rn(sum);
-        lo = __ll2float_rn(sum - __float2ll_rn(hi));
-        sm.g_hi[buf][t % kChunk + lane] = fmaf(hi, -0x1p-32f, poison);
-        sm.g_lo[buf][t % kChunk + lane] = lo * -0x1p-32f;
-        if (t % kChunk == kChunk - 32) {
-          // (every use of a chunk's sums takes in the last one, directly or by the state)
-          __threadfence_block();
-          warp_arrive(&sm.g_full[buf]);
-          ++gc;
+        run -= sum[3];
+        // A NaN makes all the chunk's sums NaN.
+        const float poison = __any_sync(0xFFFFFFFFu, bad) ? __uint_as_float(0x7FC00000u) : 0.f;
+        float4 hi, lo;
+        float* const ph = &hi.x;
+        float* const pl = &lo.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const long long g = -(run + sum[i]);
+          ph[i] = static_cast<float>(static_cast<int>(g >> 32)) + poison;
+          pl[i] = static_cast<float>(static_cast<uint32_t>(g)) * 0x1p-32f;
         }
+        if (gc >= 2 && !(ok = warp_wait(&sm.g_empty[buf], ((gc >> 1) - 1) & 1, &sm.abort))) break;
+        *reinterpret_cast<float4*>(&sm.g_hi[buf][lane * 4]) = hi;
+        *reinterpret_cast<float4*>(&sm.g_lo[buf][lane * 4]) = lo;
+        __threadfence_block();
+        warp_arrive(&sm.g_full[buf]);
       }
     }
-  } else if (warp >= 4 && warp < 12) {
+  } else if (!STATES && warp >= 4 && warp < 12) {
     // ------------------------------------------- scores to P; outputs (8-11)
     registers_shrink<kRegsOut>();
     const int group = (warp - 4) >> 2;  // which 16 of every 32 tokens
     float* const to_end = sm.to_end[warp - 4];
     int slot = 2;    // the ring's slot of the chunk's q
     int stores = 0;  // chunks that went out as tiles
-    bool ok = !STATES;
+    bool ok = true;
     while (ok && next_item(sm, turn, it)) {
       for (int c = it.c0; c < it.c1; ++c, ++gc) {
         const int buf = gc & 1;
@@ -602,7 +609,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               tma_store_3d(&map_out, tile + kHalf, 64, it.h, z);
               bulk_commit_group();
               bulk_wait_group_read<0>();
-              mbar_arrive_n(&sm.empty[slot], 9);
+              mbar_arrive_n(&sm.empty[slot], 1 + kKeyWarps);
             }
             __syncwarp();
           }
@@ -707,21 +714,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const float decay = exp2f(-(sm.g_hi[buf][kChunk - 1] + sm.g_lo[buf][kChunk - 1]));
         total *= decay;
         warp_arrive(&sm.g_empty[buf]);
-        if (!(ok = warp_wait(&sm.kv_full, gc & 1, &sm.abort))) break;
+        const uint32_t ub = STATES ? gc & 1 : 0, uph = STATES ? (gc >> 1) & 1 : gc & 1;
+        if (!(ok = warp_wait(&sm.kv_full[ub], uph, &sm.abort))) break;
         tc_fence_after();
         uint32_t u[2][8];
-        tmem_ld8(u[0], tmq + kColU);
+        const uint32_t from = tmq + (ub ? kColU2 : kColU);
+        tmem_ld8(u[0], from);
 #pragma unroll
         for (int piece = 0; piece < 16; ++piece) {
           tmem_wait_ld();
-          if (piece < 15) tmem_ld8(u[(piece + 1) & 1], tmq + kColU + (piece + 1) * 8);
+          if (piece < 15) tmem_ld8(u[(piece + 1) & 1], from + (piece + 1) * 8);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             S[piece * 4 + i] = fma2(S[piece * 4 + i], pair(decay, decay),
                                     pair(__uint_as_float(u[piece & 1][2 * i]), __uint_as_float(u[piece & 1][2 * i + 1])));
         }
         tc_fence_before();
-        warp_arrive(&sm.u_free);
+        warp_arrive(&sm.u_free[ub]);
       }
       if (!ok) break;
       f32x2 bad = 0ull;  // 0 times S: NaN where S is not finite
@@ -762,12 +771,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (lane == 0) bulk_wait_group<0>();
       __syncwarp();
     }
-  } else if (warp >= 16) {
+  } else {  // (warps 16 .. 23, with STATES also 4 .. 11)
     // ---------------------------------------------------------------------- k'
     // Lane i of k'^T is component i of k, along the tokens.  Transposing loads bring a
     // thread two tokens of one component, weighted pairs of which go out as they lie.
     registers_shrink<kRegsKey>();
-    const int kb = (warp - 16) >> 2;  // this group's buffer of k'
+    const int kb = warp >= 16 ? (warp - 16) >> 2 : (warp + 4) >> 2;  // this group's buffer of k'
     int step = 0;                     // times it has been filled
     int slot = 0, phase = 0;          // the ring's slot of the chunk's k and its phase
     bool ok = true;
@@ -795,7 +804,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (!(ok = warp_wait(&sm.full[sk], pk, &sm.abort))) break;
       const uint32_t tile = smem_addr(sm.ring[sk]);
       const int used = (n + 31) / 32;
-      for (int t0 = kb * 32; t0 < used * 32; t0 += 64, ++step) {
+      for (int t0 = kb * 32; t0 < used * 32; t0 += kKeyGroups * 32, ++step) {
         // Each lane has the weight of one of the 32 tokens.
         const float weight = exp2f((sm.g_hi[buf][t0 + lane] - last_hi) + (sm.g_lo[buf][t0 + lane] - last_lo));
         const int pick = 2 * (lane & 3);
@@ -807,7 +816,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
         for (int m = 0; m < 4; ++m)
           w[m] = pair(__shfl_sync(0xFFFFFFFFu, weight, 8 * m + pick), __shfl_sync(0xFFFFFFFFu, weight, 8 * m + pick + 1));
-        const uint32_t dst = tmq + kColK + kb * kColKBuf;
+        const uint32_t dst = tmq + kColKeys + kb * kColKBuf;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           uint32_t hi[8], mid[8], lo[8];
