@@ -274,12 +274,11 @@ int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args*
   cp.sort = p.lanes > 1 && p.lanes <= specv::kSortLanes && static_cast<int64_t>(p.lanes) * p.max_len != p.rows;
   const char* withhold = std::getenv("SPEC_LINEAR_TEST_WITHHOLD_COPY");
   cp.test_withhold = withhold != nullptr && std::atoi(withhold) != 0;
-  auto grid = [&](int64_t items) { return static_cast<unsigned>(items < dc->sms ? items : dc->sms); };
   if (split) {
-    const int rc = launch(states, grid(pairs * (cp.segments - 1)), specv::kChunkThreads, smem, states_args, stream);
+    const int rc = launch(states, static_cast<unsigned>(pairs * (cp.segments - 1)), specv::kChunkThreads, smem, states_args, stream);
     if (rc != SPEC_OK) return rc;
   }
-  return launch(full, grid(pairs * cp.segments), specv::kChunkThreads, smem, args, stream);
+  return launch(full, static_cast<unsigned>(pairs * cp.segments), specv::kChunkThreads, smem, args, stream);
 }
 
 }  // namespace

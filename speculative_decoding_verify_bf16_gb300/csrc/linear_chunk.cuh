@@ -89,6 +89,7 @@ struct ChunkSmem {
   uint64_t kv_full[2], u_free[2];
   uint64_t kp_full[4], kp_empty[4];
   uint64_t st_full[2], st_free[2], st_done;
+  uint64_t wanted, stolen;
   uint32_t tmem;
   int abort;
 };
@@ -161,12 +162,6 @@ __device__ __forceinline__ bool next_item(ChunkSmem& sm, int& turn, ChunkItem& i
   return item.count >= 0;
 }
 
-// Position `i` of this CTA's items among all: rounds of the grid, every other one
-// backwards, so that longest first also evens out the sums.
-__device__ __forceinline__ int item_index(int i) {
-  return i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-}
-
 // A 128 x 128 state by one warp (from == nullptr: zeros).
 __device__ __forceinline__ void copy_state(float* to, const float* from) {
   for (int i = threadIdx.x & 31; i < 128 * 128 / 4; i += 8 * 32) {
@@ -227,6 +222,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(&sm.v_clean, 4);
     mbar_init(&sm.o_staged, 4);
     mbar_init(&sm.st_done, 1);
+    mbar_init(&sm.wanted, 1);
+    mbar_init(&sm.stolen, 1);
+    sm.item[0].b = sm.item[1].b = -1;
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
     fence_mbar_init();
@@ -255,7 +253,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (warp < 4) registers_shrink<kRegsMisc>();
   if (warp == 3) {
     // ------------------------------------------------------------------- items
-    const int total = heads * (STATES ? cp.segments - 1 : cp.segments);
     if (cp.sort) {
       // A lane's place: how many are longer, or as long and before it.
       for (int i = lane; i < p.lanes; i += 32) {
@@ -270,19 +267,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       __syncwarp();
     }
-    auto publish = [&](const ChunkItem& x) {
-      const int slot = turn & 1;
-      if (turn >= 2 && !warp_wait(&sm.item_empty[slot], ((turn >> 1) - 1) & 1, &sm.abort)) return false;
-      if (lane == 0) sm.item[slot] = x;
-      ++turn;
-      __threadfence_block();
-      warp_arrive(&sm.item_full[slot]);
-      return true;
+    auto slot_free = [&] {
+      return turn < 2 || warp_wait(&sm.item_empty[turn & 1], ((turn >> 1) - 1) & 1, &sm.abort);
     };
-    bool ok = true;
-    for (int i = 0; ok && i * static_cast<int64_t>(gridDim.x) < total; ++i) {
-      const int index = item_index(i);
-      if (index >= total) continue;
+    auto publish = [&](const ChunkItem& x) {
+      if (lane == 0) sm.item[turn & 1] = x;
+      __threadfence_block();
+      warp_arrive(&sm.item_full[turn & 1]);
+      ++turn;
+    };
+    // Items past the first are CTAs that the hardware has not launched yet, in order: a CTA
+    // takes the next one when its copies have run out of work.
+    int index = blockIdx.x;
+    int asked = 0;
+    bool ok = slot_free();
+    while (ok && index >= 0) {
       it.h = index % p.v_heads;
       it.b = index / p.v_heads % p.lanes;
       if (cp.sort) it.b = sm.order[it.b];
@@ -290,28 +289,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int rc = linear_lane_rows(p, it.b, it.first, it.count);
       // (lanes agree on a status that another head's CTA may be writing)
       const int status = p.lane_status == nullptr ? SPEC_OK : __shfl_sync(0xFFFFFFFFu, p.lane_status[it.b], 0);
-      if (status != SPEC_OK) continue;
-      if (rc != SPEC_OK) {
+      if (status == SPEC_OK && rc != SPEC_OK) {
         if (lane == 0 && p.lane_status != nullptr) p.lane_status[it.b] = rc;
-        continue;
+      } else if (status == SPEC_OK) {
+        const int chunks = (it.count + kChunk - 1) / kChunk;
+        const int per = (chunks + cp.segments - 1) / cp.segments;
+        it.c0 = min(chunks, it.seg * per);
+        it.c1 = min(chunks, it.c0 + per);
+        it.last = it.c1 == chunks;
+        const bool work = it.c0 < it.c1 && !(STATES && it.last);
+        if (work) publish(it);
+        if (it.seg == 0) {
+          const float* in =
+              p.state_in == nullptr ? nullptr : p.state_in + it.b * p.state_in_lane + it.h * p.state_in_head;
+          // The last segment writes the final state while others may yet begin, and the two
+          // may be one buffer: with segments the first launch keeps a copy of the initial one.
+          if (STATES && in != nullptr) copy_state(cp.local + (it.b * p.v_heads + it.h) * int64_t{128 * 128}, in);
+          // An empty lane's state passes through.
+          if (!STATES && chunks == 0 && p.state_out != nullptr)
+            copy_state(p.state_out + it.b * p.state_out_lane + it.h * p.state_out_head, in);
+        }
+        if (work && !(ok = warp_wait(&sm.wanted, (turn - 1) & 1, &sm.abort) && slot_free())) break;
       }
-      const int chunks = (it.count + kChunk - 1) / kChunk;
-      const int per = (chunks + cp.segments - 1) / cp.segments;
-      it.c0 = min(chunks, it.seg * per);
-      it.c1 = min(chunks, it.c0 + per);
-      it.last = it.c1 == chunks;
-      if (it.c0 < it.c1 && !(STATES && it.last)) ok = publish(it);
-      if (it.seg != 0) continue;
-      const float* in = p.state_in == nullptr ? nullptr : p.state_in + it.b * p.state_in_lane + it.h * p.state_in_head;
-      // The last segment writes the final state while others may yet begin, and the two
-      // may be one buffer: with segments the first launch keeps a copy of the initial one.
-      if (STATES && in != nullptr) copy_state(cp.local + (it.b * p.v_heads + it.h) * int64_t{128 * 128}, in);
-      // An empty lane's state passes through.
-      if (!STATES && chunks == 0 && p.state_out != nullptr)
-        copy_state(p.state_out + it.b * p.state_out_lane + it.h * p.state_out_head, in);
+      // The response comes into the item's own place.
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sm.stolen, 16);
+        steal_cta(&sm.item[turn & 1], &sm.stolen);
+      }
+      __syncwarp();
+      if (!(ok = warp_wait(&sm.stolen, asked++ & 1, &sm.abort))) break;
+      index = stolen_cta(&sm.item[turn & 1]);
+      fence_async_smem();
+      __syncwarp();
     }
-    it.count = -1;
-    publish(it);
+    if (ok) {
+      it.count = -1;
+      publish(it);
+    }
   } else if (warp == 0) {
     // ------------------------------------------------------------------ copies
     int slot = 0, round = 0, issued = 0;
@@ -337,6 +351,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
       }
+      warp_arrive(&sm.wanted);
     }
     // Every copy lands before the CTA ends (also when a wait gave up).
     for (int i = max(0, issued - kRing); i < issued; ++i) mbar_wait_bounded(&sm.full[i % kRing], (i / kRing) & 1);
@@ -852,14 +867,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   }
   __syncthreads();
-  if (sm.abort && p.lane_status != nullptr) {  // a wait gave up: every lane this CTA had a part of
-    const int total = heads * (STATES ? cp.segments - 1 : cp.segments);
-    for (int i = threadIdx.x; i * static_cast<int64_t>(gridDim.x) < total; i += kChunkThreads) {
-      const int index = item_index(i);
-      if (index >= total) continue;
-      const int b = index / p.v_heads % p.lanes;
-      p.lane_status[cp.sort ? sm.order[b] : b] = SPEC_ERR_TIMEOUT;
-    }
+  // A wait gave up: the lanes of the items that were under way.
+  if (threadIdx.x < 2 && sm.abort && p.lane_status != nullptr) {
+    const int b = sm.item[threadIdx.x].b;
+    if (b >= 0 && b < p.lanes) p.lane_status[b] = SPEC_ERR_TIMEOUT;
   }
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tm, 512);

@@ -203,6 +203,33 @@ __device__ __forceinline__ void tma_store_4d(const void* map, const void* src, i
 __device__ __forceinline__ void tma_prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
+// ---------------------------------------------------------------------------
+// Work stealing: a running CTA takes over one that has not been launched yet.
+// ---------------------------------------------------------------------------
+// Asks for the next CTA's index; 16 bytes come to `response` and count on `bar`.
+__device__ __forceinline__ void steal_cta(void* response, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_addr(response)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+// The index, or -1: none is left (then no further one may be asked for).
+__device__ __forceinline__ int stolen_cta(const void* response) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_addr(response))
+      : "memory");
+  return got ? static_cast<int>(x) : -1;
+}
+
 // Plain writes to shared memory become visible to copies and matrix products.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
