@@ -184,10 +184,12 @@ bool mappable(const void* base, int64_t row_stride, int64_t head_stride, int hea
   return heads == 1 || (head_stride % 8 == 0 && head_stride > 0 && head_stride < (int64_t{1} << 38));
 }
 
-// [rows][heads][128] bf16, copied in boxes of 128 rows of 64 elements of one head.
-bool make_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int64_t row_stride, int64_t head_stride) {
-  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads == 1 ? 128 : head_stride) * 2,
+// [rows][heads][size] bf16, copied in boxes of 128 rows of 64 elements of one head (zeros
+// past the head's size).
+bool make_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int size, int64_t row_stride,
+              int64_t head_stride) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(size), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads == 1 ? row_stride : head_stride) * 2,
                                  static_cast<cuuint64_t>(row_stride) * 2};
   const cuuint32_t box[3] = {64, 1, specv::kChunk}, step[3] = {1, 1, 1};
   return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
@@ -195,17 +197,19 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int64
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// States [lanes][heads][128][128], copied in boxes of 128 rows of 32 numbers.
+// States [lanes][heads][dk][dv], copied in boxes of 128 rows of 32 numbers.
 bool mappable_state(const void* base, int64_t lane_stride, int64_t head_stride, int lanes, int heads) {
   auto fits = [](int64_t s, int n) { return n == 1 || (s > 0 && s < (int64_t{1} << 37)); };
   return base == nullptr || (fits(lane_stride, lanes) && fits(head_stride, heads));
 }
 
-bool make_state_map(CUtensorMap* map, const void* base, int64_t lanes, int heads, int64_t lane_stride,
+bool make_state_map(CUtensorMap* map, const void* base, int64_t lanes, int heads, int dk, int dv, int64_t lane_stride,
                     int64_t head_stride) {
-  const cuuint64_t dims[4] = {128, 128, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(lanes)};
-  const cuuint64_t strides[3] = {128 * 4, static_cast<cuuint64_t>(heads == 1 ? 128 * 128 : head_stride) * 4,
-                                 static_cast<cuuint64_t>(lanes == 1 ? 128 * 128 : lane_stride) * 4};
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dv), static_cast<cuuint64_t>(dk), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(lanes)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(dv) * 4,
+                                 static_cast<cuuint64_t>(heads == 1 ? dk * dv : head_stride) * 4,
+                                 static_cast<cuuint64_t>(lanes == 1 ? dk * dv : lane_stride) * 4};
   const cuuint32_t box[4] = {32, 128, 1, 1}, step[4] = {1, 1, 1, 1};
   return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(base), dims, strides, box, step,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -214,7 +218,7 @@ bool make_state_map(CUtensorMap* map, const void* base, int64_t lanes, int heads
 
 bool chunkable(const LinearParams& p, spec_dtype dtype) {
   const int k_heads = p.v_heads / p.group;
-  return dtype == SPEC_BF16 && p.dk == 128 && p.dv == 128 && p.rows > 0 && p.max_len >= kChunkMinLen &&
+  return dtype == SPEC_BF16 && p.dk <= 128 && p.dv <= 128 && p.rows > 0 && p.max_len >= kChunkMinLen &&
          mappable(p.q, p.q_row, p.q_head, k_heads) && mappable(p.k, p.k_row, p.k_head, k_heads) &&
          mappable(p.v, p.v_row, p.v_head, p.v_heads) && mappable(p.out, p.out_row, p.out_head, p.v_heads) &&
          mappable_state(p.state_in, p.state_in_lane, p.state_in_head, p.lanes, p.v_heads) &&
@@ -253,21 +257,21 @@ int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args*
   cp.local_decay = cp.local + static_cast<int64_t>(cp.segments) * pairs * (128 * 128);
   const int k_heads = p.v_heads / p.group;
   CUtensorMap q, k, v, out, local, begin, end;
-  if (!make_map(&q, p.q, p.rows, k_heads, p.q_row, p.q_head) || !make_map(&k, p.k, p.rows, k_heads, p.k_row, p.k_head) ||
-      !make_map(&v, p.v, p.rows, p.v_heads, p.v_row, p.v_head) ||
-      !make_map(&out, p.out, p.rows, p.v_heads, p.out_row, p.out_head))
+  if (!make_map(&q, p.q, p.rows, k_heads, p.dk, p.q_row, p.q_head) || !make_map(&k, p.k, p.rows, k_heads, p.dk, p.k_row, p.k_head) ||
+      !make_map(&v, p.v, p.rows, p.v_heads, p.dv, p.v_row, p.v_head) ||
+      !make_map(&out, p.out, p.rows, p.v_heads, p.dv, p.out_row, p.out_head))
     return SPEC_ERR_CUDA;
   const bool split = cp.segments > 1;
-  if (split && !make_state_map(&local, cp.local, static_cast<int64_t>(cp.segments) * p.lanes, p.v_heads,
+  if (split && !make_state_map(&local, cp.local, static_cast<int64_t>(cp.segments) * p.lanes, p.v_heads, 128, 128,
                                static_cast<int64_t>(p.v_heads) * 128 * 128, 128 * 128))
     return SPEC_ERR_CUDA;
   begin = split ? local : q;  // (where nothing is read or written, any map will do)
   end = q;
   if (!split && p.state_in != nullptr &&
-      !make_state_map(&begin, p.state_in, p.lanes, p.v_heads, p.state_in_lane, p.state_in_head))
+      !make_state_map(&begin, p.state_in, p.lanes, p.v_heads, p.dk, p.dv, p.state_in_lane, p.state_in_head))
     return SPEC_ERR_CUDA;
   if (p.state_out != nullptr &&
-      !make_state_map(&end, p.state_out, p.lanes, p.v_heads, p.state_out_lane, p.state_out_head))
+      !make_state_map(&end, p.state_out, p.lanes, p.v_heads, p.dk, p.dv, p.state_out_lane, p.state_out_head))
     return SPEC_ERR_CUDA;
   void* args[] = {&cp, &q, &k, &v, &out, &begin, &end};
   void* states_args[] = {&cp, &q, &k, &v, &out, &begin, &local};
@@ -286,7 +290,8 @@ int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args*
 extern "C" {
 
 uint64_t spec_linear_workspace(int32_t lanes, int32_t v_heads, int32_t dk, int32_t dv, int32_t max_len) {
-  if (lanes <= 0 || v_heads <= 0 || dk != 128 || dv != 128 || max_len < kChunkMinLen) return 0;
+  if (lanes <= 0 || v_heads <= 0 || dk <= 0 || dk > 128 || dv <= 0 || dv > 128 || max_len < kChunkMinLen)
+    return 0;
   DeviceCache* dc = nullptr;
   if (device_cache(&dc) != SPEC_OK) return 0;
   const int64_t pairs = static_cast<int64_t>(lanes) * v_heads;

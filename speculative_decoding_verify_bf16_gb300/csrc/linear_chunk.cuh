@@ -1,5 +1,6 @@
 // linear_chunk.cuh -- linear attention with decay over prompts, a chunk of 128 tokens at
-// a time on the tensor cores (bf16 activations, dk = dv = 128).
+// a time on the tensor cores (bf16 activations, dk and dv up to 128; smaller heads are
+// filled up with zeros by the copies).
 //
 // With G_i the sum of the log decays of the chunk's tokens 0..i (base 2), S the state
 // before the chunk and all sums over the chunk's tokens:
@@ -162,15 +163,28 @@ __device__ __forceinline__ bool next_item(ChunkSmem& sm, int& turn, ChunkItem& i
   return item.count >= 0;
 }
 
-// A 128 x 128 state by one warp (from == nullptr: zeros).
-__device__ __forceinline__ void copy_state(float* to, const float* from) {
-  for (int i = threadIdx.x & 31; i < 128 * 128 / 4; i += 8 * 32) {
+// A dk x dv state by one warp, into rows of `ld` numbers of a state of `rows` rows (zeros
+// beyond dk and dv; from == nullptr: zeros).
+__device__ __forceinline__ void copy_state(float* to, int rows, int ld, const float* from, int dk, int dv) {
+  const int wide = ld / 4, n = rows * wide;
+  const bool same = rows == dk && ld == dv;
+  for (int i0 = threadIdx.x & 31; i0 < n; i0 += 8 * 32) {
     float4 x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      x[j] = from == nullptr ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(reinterpret_cast<const float4*>(from) + i + 32 * j);
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + 32 * j;
+      int at = 4 * i;
+      bool in = from != nullptr && i < n;
+      if (!same) {
+        const int r = i / wide, c = i % wide * 4;
+        at = r * dv + c;
+        in = in && r < dk && c < dv;
+      }
+      x[j] = in ? __ldcg(reinterpret_cast<const float4*>(from + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) reinterpret_cast<float4*>(to)[i + 32 * j] = x[j];
+    for (int j = 0; j < 8; ++j)
+      if (i0 + 32 * j < n) reinterpret_cast<float4*>(to)[i0 + 32 * j] = x[j];
   }
 }
 
@@ -304,10 +318,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               p.state_in == nullptr ? nullptr : p.state_in + it.b * p.state_in_lane + it.h * p.state_in_head;
           // The last segment writes the final state while others may yet begin, and the two
           // may be one buffer: with segments the first launch keeps a copy of the initial one.
-          if (STATES && in != nullptr) copy_state(cp.local + (it.b * p.v_heads + it.h) * int64_t{128 * 128}, in);
+          if (STATES && in != nullptr)
+            copy_state(cp.local + (it.b * p.v_heads + it.h) * int64_t{128 * 128}, 128, 128, in, p.dk, p.dv);
           // An empty lane's state passes through.
           if (!STATES && chunks == 0 && p.state_out != nullptr)
-            copy_state(p.state_out + it.b * p.state_out_lane + it.h * p.state_out_head, in);
+            copy_state(p.state_out + it.b * p.state_out_lane + it.h * p.state_out_head, p.dk, p.dv, in, p.dk, p.dv);
         }
         if (work && !(ok = warp_wait(&sm.wanted, (turn - 1) & 1, &sm.abort) && slot_free())) break;
       }
@@ -634,7 +649,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll 1
           for (int i = lane; i < 32 * 16; i += 32) {
             const int r = static_cast<int>(quarter) + i / 16;
-            if (r < n)
+            if (r < n && (i % 16) * 8 < p.dv)
               *reinterpret_cast<uint4*>(dst + (it.first + c * static_cast<int64_t>(kChunk) + r) * p.out_row + (i % 16) * 8) =
                   *reinterpret_cast<const uint4*>(tile + tile_unit(r, i % 16));
           }

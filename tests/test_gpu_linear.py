@@ -102,6 +102,9 @@ def test_prefill_long_and_split():
     """Few heads and a long axis: the work of one head is split."""
     check_prefill([3000], hk=1, hv=2, seed=1)
     check_prefill([2049, 130], hk=1, hv=1, seed=2, slow=1e-4, fast=1e-4)
+    check_prefill([2000, 0, 700], hk=1, hv=1, dk=64, dv=96, seed=3)
+    check_prefill([1500], hk=1, hv=1, dk=72, dv=64, seed=4, in_place=True)
+    check_prefill([1500], hk=1, hv=1, seed=5, in_place=True)
 
 
 @pytest.mark.parametrize("hk,hv", [(1, 1), (2, 4), (3, 9), (16, 16)])
@@ -109,7 +112,8 @@ def test_prefill_head_layouts(hk, hv):
     check_prefill([200, 37], hk=hk, hv=hv, seed=hv)
 
 
-@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (256, 256), (48, 20), (1, 4), (130, 132)])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (256, 256), (48, 20), (1, 4), (130, 132), (24, 40),
+                                   (104, 8), (128, 128)])
 def test_prefill_head_sizes(dk, dv):
     check_prefill([150, 20], dk=dk, dv=dv, seed=dk + dv)
 
