@@ -97,7 +97,7 @@ uint64_t spec_linear_workspace(int32_t lanes, int32_t v_heads, int32_t dk, int32
  * row_offsets with lanes and rows > 0), sizes or dtype outside the ranges above,
  * misaligned states or too small a workspace; SPEC_ERR_CUDA if a launch fails.
  *
- * Prompts in bf16 with dk and dv up to 128 (max_len >= 32; q, k, v and out 16-byte aligned in
+ * Prompts in bf16 with dk and dv up to 128 (max_len >= 8; q, k, v and out 16-byte aligned in
  * base and strides) run in chunks of 128 tokens on the tensor cores; everything else
  * runs token after token, with the same results up to rounding but slower on long
  * prompts.  out must not overlap q, k or v.
