@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
           phase ^= 1;
         }
       }
-      if (whole < last && warp == 0) {  // the row's last, partial block
+      if (first < last && whole < last && warp == 0) {  // the row's last, partial block (a CTA may have none)
         B x;
         x.load(row, p.V, whole, lane);
         take(x, whole);

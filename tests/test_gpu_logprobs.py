@@ -70,6 +70,15 @@ def test_sizes(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,V", [(1, 10104), (5, 50000), (1, 50000), (5, 50008), (2, 99992), (9, 57496), (3, 262136)])
+def test_clusters_whose_last_blocks_have_nothing(rows, V, dtype):
+    """Aligned rows that end inside a block, over more thread blocks than divide them evenly:
+    the last ones have no part, and the partial block counts once."""
+    x = rand(rows, V, dtype, V)
+    check(x, np.random.default_rng(V).integers(0, V, rows), [(0.0, 0.7)[i % 2] for i in range(rows)], top=20)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("pad,shift", [(1, 0), (3, 1), (8, 0), (8, 3), (5, 7)])
 def test_strides_and_alignment(dtype, pad, shift):
     x = rand(4, 3001, dtype, 11, pad, shift)
