@@ -51,8 +51,9 @@ typedef struct {
  * top > 0), V <= 0, rows < 0, ld < V, top out of range or an unknown dtype;
  * SPEC_ERR_CUDA if the launch fails.  rows = 0 is a no-op.
  *
- * Rows whose address is 16-byte aligned (base and ld * element size) are streamed with
- * bulk copies; other layouts take a slower element-wise path with the same results.
+ * Rows whose address is 16-byte aligned (base and ld * element size) are fastest; others are
+ * streamed from the aligned 16 bytes that their start lies in (what is before it is not used)
+ * and taken apart element by element, with the same results.
  * SPEC_LOGPROBS_TEST_WITHHOLD_COPY=1 in the environment, tests of the failure path only:
  * the first row's first copy is never issued, so that its wait gives up after 2 s.
  */

@@ -12,9 +12,18 @@
 // A row is one thread-block cluster's work; every CTA of it takes a contiguous range of
 // blocks and hands its sums and block maxima to the first one through distributed shared
 // memory.  The pass is bound by HBM, with the exponentials close behind (16 a cycle and
-// SM).  Each warp streams for itself: bulk copies of up to 4 KB into its own ring of three
+// SM).  Each warp streams for itself: bulk copies of up to 4 KB into its own ring of two
 // slots, so that an SM keeps up to 192 KB on the way without holding registers for it
-// and no barrier stands between warps.
+// and no barrier stands between warps.  Rows off 16-byte alignment take the same way, their
+// copies from the last boundary before them.
+//
+// Measured (device time, bf16 rows, five alternatives and temperatures, nothing of them in
+// L2): 576 rows of 262,144 at ragged temperatures with rows left out 41.5 us, where the bytes
+// of those asked for take 26.0 at the measured copy rate; 64 of 151,936 with 20 alternatives
+// 15.1 us, of which some 6 are the second look (the exchange, the selection, 20 blocks read
+// again and sorted out: a chain of latencies that few rows leave exposed); one of 262,144
+// 7.6 us; four of 1,024 5.6 us.  576 fp32 rows of 151,937, none but the first aligned, are
+// read at 5.5 TB/s (63 us), and in bf16 at 4.1 TB/s (43 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -56,7 +65,8 @@ static_assert(kMaxCluster * kMaxGroups <= 1 << 16, "groups are listed in 16 bits
 constexpr int kCandidates = 256;     // tokens the last selection holds
 constexpr int kSlots = 2;            // a warp's ring
 constexpr int kSlotBytes = 4096;
-constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
+constexpr int kSlotStride = kSlotBytes + 16;  // (a row off 16-byte alignment starts inside a slot)
+constexpr int kRingBytes = kWarps * kSlots * kSlotStride;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Exponents below this are 0 in fp32 (2^-126 is the smallest normal number and the
@@ -151,22 +161,29 @@ struct Block {
     if (!BF16) return __uint_as_float(w[e]);
     return e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
   }
-  // A whole block from 16-byte aligned memory, shared or global.
-  __device__ __forceinline__ void load_vec(const uint8_t* block, int lane) {
+  // A whole block from shared memory, 16-byte aligned if VEC.
+  __device__ __forceinline__ void load_shared(const uint8_t* block, int lane) {
+    if (VEC) {
 #pragma unroll
-    for (int j = 0; j < kWords / 4; ++j) {
-      const uint4 u = *reinterpret_cast<const uint4*>(block + j * 512 + lane * 16);
-      w[4 * j] = u.x;
-      w[4 * j + 1] = u.y;
-      w[4 * j + 2] = u.z;
-      w[4 * j + 3] = u.w;
+      for (int j = 0; j < kWords / 4; ++j) {
+        const uint4 u = *reinterpret_cast<const uint4*>(block + j * 512 + lane * 16);
+        w[4 * j] = u.x;
+        w[4 * j + 1] = u.y;
+        w[4 * j + 2] = u.z;
+        w[4 * j + 3] = u.w;
+      }
+    } else if (BF16) {
+#pragma unroll
+      for (int e = 0; e < kPerLane; e += 2)
+        w[e / 2] = reinterpret_cast<const uint16_t*>(block)[e * 32 + lane] |
+                   static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(block)[e * 32 + 32 + lane]) << 16;
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) w[e] = reinterpret_cast<const uint32_t*>(block)[e * 32 + lane];
     }
   }
+  // A block that may end past the vocabulary, from the row itself.
   __device__ __forceinline__ void load(const uint8_t* row, int V, int sub, int lane) {
-    if (VEC && (sub + 1) * static_cast<int64_t>(kBlock) <= V) {
-      load_vec(row + sub * static_cast<int64_t>(kBytes), lane);
-      return;
-    }
 #pragma unroll
     for (int e = 0; e < kPerLane; ++e) {
       const int64_t i = index_of(sub, lane, e);
@@ -205,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
   const int r = blockIdx.x / p.cluster;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (p.cluster > 1) cluster_arrive_relaxed();
-  if (VEC && lane == 0) {
+  if (lane == 0) {
     for (int i = 0; i < kSlots; ++i) specv::mbar_init(&hd.full[warp][i], 1);
     specv::mbar_init(&hd.again[warp], 1);
     specv::fence_mbar_init();
@@ -309,79 +326,76 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
       if (lane == 0) keep(top, sub);
       if (raise(top)) add(x);
     };
-    if (VEC) {
-      // Whole blocks through the ring, `chunk` of them a copy, the warps in turn.
-      uint8_t* slots = ring + warp * (kSlots * kSlotBytes);
-      const int whole = min(last, p.V / kBlock);
-      const int step = kWarps * p.chunk;
-      auto issue = [&](int sub, int slot) {
-        if (lane == 0 && sub < whole) {
-          const uint32_t bytes = min(p.chunk, whole - sub) * B::kBytes;
-          specv::mbar_arrive_expect_tx(&hd.full[warp][slot], bytes);
-          if (!(p.test_withhold && blockIdx.x == 0 && sub == 0))
-            specv::bulk_g2s(slots + slot * kSlotBytes, row + sub * static_cast<int64_t>(B::kBytes), bytes,
-                            &hd.full[warp][slot]);
+    // Whole blocks through the ring, `chunk` of them a copy, the warps in turn.  Copies take
+    // whole pieces of 16 aligned bytes: those of a row that starts inside such a piece begin
+    // with it.  (Every piece holds a byte of the row, so that it lies in the same memory page.)
+    uint8_t* slots = ring + warp * (kSlots * kSlotStride);
+    const uint32_t shift = VEC ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15u);
+    const int whole = min(last, p.V / kBlock);
+    const int step = kWarps * p.chunk;
+    auto issue = [&](int sub, int slot) {
+      if (lane == 0 && sub < whole) {
+        const uint32_t bytes = (shift + min(p.chunk, whole - sub) * B::kBytes + 15u) & ~15u;
+        specv::mbar_arrive_expect_tx(&hd.full[warp][slot], bytes);
+        if (!(p.test_withhold && blockIdx.x == 0 && sub == 0))
+          specv::bulk_g2s(slots + slot * kSlotStride, row - shift + sub * static_cast<int64_t>(B::kBytes), bytes,
+                          &hd.full[warp][slot]);
+      }
+    };
+    int sub = first + warp * p.chunk;  // (blocks, at most 2^22 of them)
+    for (int i = 0; i < kSlots; ++i) issue(sub + i * step, i);
+    int slot = 0, phase = 0;
+    for (; sub < whole; sub += step) {
+      if (!specv::mbar_wait_bounded(&hd.full[warp][slot], phase)) {
+        acc.status = SPEC_ERR_TIMEOUT;  // (what is on the way still lands before the CTA ends)
+        for (int i = 0; i < kSlots && sub + i * step < whole; ++i) {
+          specv::mbar_wait_bounded(&hd.full[warp][slot], phase);
+          if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
-      };
-      int sub = first + warp * p.chunk;  // (blocks, at most 2^22 of them)
-      for (int i = 0; i < kSlots; ++i) issue(sub + i * step, i);
-      int slot = 0, phase = 0;
-      for (; sub < whole; sub += step) {
-        if (!specv::mbar_wait_bounded(&hd.full[warp][slot], phase)) {
-          acc.status = SPEC_ERR_TIMEOUT;  // (what is on the way still lands before the CTA ends)
-          for (int i = 0; i < kSlots && sub + i * step < whole; ++i) {
-            specv::mbar_wait_bounded(&hd.full[warp][slot], phase);
-            if (++slot == kSlots) {
-              slot = 0;
-              phase ^= 1;
-            }
-          }
-          break;
+        break;
+      }
+      const int n = min(p.chunk, whole - sub);
+      const uint8_t* src = slots + slot * kSlotStride + shift;
+      // A slot's blocks at once: their latencies overlap.  (Not where bf16 logits come two
+      // bytes a load, whose addresses and halves spill: 576 x 151,937 89 us so, 43 one by one.)
+      if ((VEC || !BF16) && n == B::kTogether) {
+        B x[B::kTogether];
+        float top[B::kTogether], most = -INFINITY, own = 0.f;
+#pragma unroll
+        for (int i = 0; i < B::kTogether; ++i) x[i].load_shared(src + i * B::kBytes, lane);
+#pragma unroll
+        for (int i = 0; i < B::kTogether; ++i) {
+          top[i] = warp_max_nan(x[i].top());
+          most = specv::f32_max_nan(most, top[i]);
+          own = lane == i ? top[i] : own;
         }
-        const int n = min(p.chunk, whole - sub);
-        const uint8_t* src = slots + slot * kSlotBytes;
-        if (n == B::kTogether) {  // (a slot's blocks at once: their latencies overlap)
-          B x[B::kTogether];
-          float top[B::kTogether], most = -INFINITY, own = 0.f;
+        if (lane < B::kTogether) keep(own, sub + lane);
+        if (raise(most)) {
 #pragma unroll
-          for (int i = 0; i < B::kTogether; ++i) x[i].load_vec(src + i * B::kBytes, lane);
-#pragma unroll
-          for (int i = 0; i < B::kTogether; ++i) {
-            top[i] = warp_max_nan(x[i].top());
-            most = specv::f32_max_nan(most, top[i]);
-            own = lane == i ? top[i] : own;
-          }
-          if (lane < B::kTogether) keep(own, sub + lane);
-          if (raise(most)) {
-#pragma unroll
-            for (int i = 0; i < B::kTogether; ++i) add(x[i]);
-          }
-        } else {
+          for (int i = 0; i < B::kTogether; ++i) add(x[i]);
+        }
+      } else {
 #pragma unroll 1
-          for (int i = 0; i < n; ++i) {
-            B x;
-            x.load_vec(src + i * B::kBytes, lane);
-            take(x, sub + i);
-          }
-        }
-        __syncwarp();
-        issue(sub + kSlots * step, slot);
-        if (++slot == kSlots) {
-          slot = 0;
-          phase ^= 1;
+        for (int i = 0; i < n; ++i) {
+          B x;
+          x.load_shared(src + i * B::kBytes, lane);
+          take(x, sub + i);
         }
       }
-      if (first < last && whole < last && warp == 0) {  // the row's last, partial block (a CTA may have none)
-        B x;
-        x.load(row, p.V, whole, lane);
-        take(x, whole);
+      __syncwarp();
+      issue(sub + kSlots * step, slot);
+      if (++slot == kSlots) {
+        slot = 0;
+        phase ^= 1;
       }
-    } else {
-      for (int sub = first + warp; sub < last; sub += kWarps) {
-        B x;
-        x.load(row, p.V, sub, lane);
-        take(x, sub);
-      }
+    }
+    if (first < last && whole < last && warp == 0) {  // the row's last, partial block (a CTA may have none)
+      B x;
+      x.load(row, p.V, whole, lane);
+      take(x, whole);
     }
     // The maximum is the warp's, so the lanes' sums add directly.
     acc.s = first_of(s2) + second_of(s2);
@@ -532,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
   using S = Block<BF16, true>;  // (as they lie in the ring)
   const int nblocks = hd.nsel * p.group;
   constexpr int kHeld = kSlots * kSlotBytes / S::kBytes;
-  uint8_t* const held = ring + warp * (kSlots * kSlotBytes);
+  uint8_t* const held = ring + warp * (kSlots * kSlotStride);
   int staged = -1, batch = 0;
   auto blocks = [&](auto f) {
     for (int i0 = warp; i0 < nblocks; i0 += kWarps * kHeld) {
@@ -581,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
         const int sub = block(j);
         if (sub >= subs) continue;
         S x;
-        x.load_vec(held + j * S::kBytes, lane);
+        x.load_shared(held + j * S::kBytes, lane);
         f(x, sub, held + j * S::kBytes);
       }
     }
