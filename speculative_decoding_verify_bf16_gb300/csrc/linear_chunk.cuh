@@ -20,22 +20,37 @@
 // S stays in fp32 in the registers of four warps from the first chunk to the last, and
 // S' = 2^G_last S + U is formed there: the tensor cores truncate each addition to an
 // accumulator, which into S itself cost ten times the precision of its fp32 sums.
-// Operands are bf16, so fp32 numbers enter a product in parts: k' in three (all 24 bits),
-// P and S in two (16 bits, far below the rounding of a bf16 output).  q, k and v are
-// taken as they are.
+// Operands are bf16, so fp32 numbers enter a product rounded or in parts.  k' comes in three
+// parts that hold all its 24 bits: U is what stays.  P and S are rounded once: they are used
+// for one output, which is rounded to bf16 itself, and with their own roundings its rms error
+// is 0.0023 of its size instead of 0.0017; in two parts each they would cost another 1,024
+// cycles of products a chunk and the room and the registers for them.  q, k and v are taken
+// as they are.  States come out within 4e-7 of 64-bit ones, like those of fp32 sums.
 //
 // Tensor memory holds U (128 columns), scores and P (128; P overwrites the scores it came
 // from), D (128) and two buffers of k' for 32 tokens (96).  Shared memory holds a ring of
 // five 32 KB tiles (k, v, q of a chunk; 128-byte swizzled rows, so that a tile serves as
-// an operand along either dimension) and S in two parts.
+// an operand along either dimension), S in bf16, and with it room for the copies of states
+// in and out.
 //
 // Warps: 0 copies tiles, 1 issues the products, 2 sums the decays, 3 hands out the items,
 // and five groups of four do what lies between the products: scores to P (4-11), D (8-11),
-// S (12-15), k' for every other 32 tokens (16-19 and 20-23).  The products of a chunk take 8 x 512 cycles on the tensor cores, its
-// 128 KB of q, k, v and o about 5,500 at an SM's share of the HBM rate: the groups work
+// S (12-15), k' for every other 32 tokens (16-19 and 20-23).  Where only states are wanted
+// (the first of two launches for a lane cut in segments), 4-11 make k', too, into the room
+// of scores and P, and U has two places.
+//
+// The products of a chunk take 6 x 512 cycles on the tensor cores (k' counts three times),
+// its 128 KB of q, k, v and o about 5,500 at an SM's share of the HBM rate: the groups work
 // beside each other so that the larger of the two counts.  A chunk's products go in the
 // order KV (first half), QK, KV (second half), QS, PV: P is made beside the three after
 // QK, the next S beside QS and PV, k' of the next tokens beside whatever is not KV.
+//
+// Measured (device time, 16 heads of 128): 64 lanes of 2,048 tokens 353 us, 0.93 of the
+// copy rate; 24 grouped lanes of 0 to 3000 tokens 102 us against 68 (what is left is the
+// last items' unequal ends); one lane of 16,384 88 us in two launches, each SM with few
+// chunks and little to overlap their starts with; 200 tokens 10.4 us.  A chunk takes 3.15 us
+// with every SM at work, when HBM bounds it, and 2.75 us with few: then the chain QK, P, PV
+// and the groups' waits for one another do.
 #pragma once
 
 #include <cuda.h>
@@ -76,8 +91,7 @@ struct ChunkItem {
 
 struct ChunkSmem {
   uint8_t ring[kRing][kTile];
-  uint8_t s_hi[kTile];
-  uint8_t s_lo[kTile];
+  uint8_t s[2][kTile];    // S in bf16 in the first; both for states on their way in and out
   float g_hi[2][kChunk];  // -G in two parts, chunk c in c % 2
   float g_lo[2][kChunk];
   float to_end[8][16];    // the P groups' warps: 2^(G at the end of 16 tokens - G_j)
@@ -205,6 +219,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   constexpr uint32_t kColKeys = STATES ? kColP : kColK, kColU2 = STATES ? kColK : kColU;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>(smem_raw);
+  uint64_t* const o_sent = &sm.kp_full[3];  // (STATES has no outputs, the others no fourth buffer of k')
   const LinearParams& p = cp.p;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -223,7 +238,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sm.st_free[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&sm.kp_full[i], 4);
+      mbar_init(&sm.kp_full[i], STATES || i < 3 ? 4 : 1);
       mbar_init(&sm.kp_empty[i], 1);
     }
     mbar_init(&sm.scores_full, 1);
@@ -238,7 +253,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(&sm.st_done, 1);
     mbar_init(&sm.wanted, 1);
     mbar_init(&sm.stolen, 1);
-    sm.item[0].b = sm.item[1].b = -1;
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
     fence_mbar_init();
@@ -380,7 +394,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0);
     constexpr uint32_t kSame = mma_desc(128, 128, false), kRows = mma_desc(128, 128, true);
     const uint32_t ring = smem_desc(smem_addr(sm.ring[0]), kHalf);  // (for K-major tiles the piece distance is not used)
-    const uint32_t ds = smem_desc(smem_addr(sm.s_hi), kHalf);
+    const uint32_t ds = smem_desc(smem_addr(sm.s[0]), kHalf);
     uint32_t kphase = 0;     // bit i: phase of k' buffer i
     int slot = 0, phase = 0; // the ring's slot of this chunk's k and its phase
     int tails = 0;           // chunks that did not fill a tile
@@ -451,6 +465,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int s = 0; s < 8; ++s)
           mma_ss(lead, tmu + kColD, dq + ((s >> 2) * kHalf + (s & 3) * 32) / 16, ds + s * (2048 / 16), kRows, s > 0);
         mma_commit(lead, &sm.qs_full);
+        if (c + 1 < loops) {  // (at the last chunk outputs leave by this tile)
+          mma_commit(lead, &sm.empty[sq]);
+          if (lead) mbar_arrive_n(&sm.empty[sq], kKeyWarps);
+        }
         if (!warp_wait(&sm.p_ready, ph, &sm.abort) || !warp_wait(&sm.d_scaled, ph, &sm.abort)) break;
         tc_fence_after();
 #pragma unroll 1
@@ -534,6 +552,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     float* const to_end = sm.to_end[warp - 4];
     int slot = 2;    // the ring's slot of the chunk's q
     int stores = 0;  // chunks that went out as tiles
+    int sent = 0;    // those that went by sm.s
     bool ok = true;
     while (ok && next_item(sm, turn, it)) {
       for (int c = it.c0; c < it.c1; ++c, ++gc) {
@@ -610,8 +629,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         warp_arrive(&sm.d_scaled);
         if (!(ok = warp_wait(&sm.o_full, gc & 1, &sm.abort))) break;
         tc_fence_after();
-        // The chunk's q has been read: its tile takes the outputs on their way out.
-        uint8_t* tile = sm.ring[slot];
+        // On their way out the outputs stand in the second place for states or, at an item's
+        // last chunk, beside which states may come and go, in the tile of the chunk's q.
+        const bool inner = c + 1 < it.c1;
+        uint8_t* tile = inner ? sm.s[1] : sm.ring[slot];
+        if (inner && sent > 0 && !(ok = warp_wait(o_sent, (sent - 1) & 1, &sm.abort))) break;
         const int n = it.count - c * kChunk;
         const f32x2 scale = pair(p.scale, p.scale);
 #pragma unroll 1
@@ -639,10 +661,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               tma_store_3d(&map_out, tile + kHalf, 64, it.h, z);
               bulk_commit_group();
               bulk_wait_group_read<0>();
-              mbar_arrive_n(&sm.empty[slot], 1 + kKeyWarps);
+              if (inner)
+                mbar_arrive(o_sent);
+              else
+                mbar_arrive_n(&sm.empty[slot], 1 + kKeyWarps);
             }
             __syncwarp();
           }
+          sent += inner ? 1 : 0;
         } else {  // (a copy would go on into the next lane's rows)
           __syncwarp();
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + it.h * p.out_head;
@@ -666,12 +692,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else if (warp >= 12 && warp < 16) {
     // ------------------------------------------------------------------ states
     registers_grow<kRegsState>();
-    // States come and go by copies through s_hi (columns 0..63) and s_lo, which hold S in
-    // parts only from a chunk's start to its QS; the first warp issues them.
+    // States come and go by copies through sm.s (columns 0..63 in the first), which holds S in
+    // bf16 only from a chunk's start to its QS; the group's first warp issues them.
     const bool has_in = !STATES && p.state_in != nullptr;
     int loads = 0;       // states loaded so far
     int frees[2] = {0, 0};  // phases of st_free
     int stored = 0;      // states stored so far
+    int sent = 0;        // chunks whose outputs went by sm.s[1]
     bool ok = true;
     while (ok && next_item(sm, turn, it)) {
       const int64_t head = it.b * p.v_heads + it.h;
@@ -680,13 +707,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int i = 0; i < 64; ++i) S[i] = 0ull;
       if (!STATES && gc > 0 && !(ok = warp_wait(&sm.qs_full, (gc - 1) & 1, &sm.abort))) break;
       if (stored > 0 && !(ok = warp_wait(&sm.st_done, (stored - 1) & 1, &sm.abort))) break;
+      if (!STATES && sent > 0 && !(ok = warp_wait(o_sent, (sent - 1) & 1, &sm.abort))) break;
+      sent += it.c1 - it.c0 - 1;
       if (!STATES) {
         // The state before the segment: the lane's, then every earlier segment's from zero
         // behind its decay.
         const int n = (has_in ? 1 : 0) + it.seg, slot0 = has_in ? 0 : 1;
         auto load = [&](int k, int half) {
           if (lane == 0) {
-            uint8_t* dst = half == 0 ? sm.s_hi : sm.s_lo;
+            uint8_t* dst = sm.s[half];
             const int z = (slot0 + k) * p.lanes + it.b;
             mbar_arrive_expect_tx(&sm.st_full[half], kTile);
             tma_load_4d(dst, &map_begin, half * 64, 0, it.h, z, &sm.st_full[half]);
@@ -705,7 +734,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             if (!(ok = ok && warp_wait(&sm.st_full[half], loads & 1, &sm.abort))) break;
-            const uint8_t* src = half == 0 ? sm.s_hi : sm.s_lo;
+            const uint8_t* src = sm.s[half];
 #pragma unroll
             for (int f = 0; f < 16; ++f) {
               const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(src + tile_unit(row, f));
@@ -729,12 +758,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int c = it.c0; c < it.c1; ++c, ++gc) {
         const int buf = gc & 1;
         if (!STATES) {
-          // S in two parts to shared memory for the chunk's QS, the last chunk's done.
+          // S in bf16 to shared memory for the chunk's QS, the last chunk's done.
           if (c > it.c0 && !(ok = warp_wait(&sm.qs_full, (gc - 1) & 1, &sm.abort))) break;
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
             const uint32_t unit = tile_unit(row, i / 4);
-            *reinterpret_cast<uint4*>(sm.s_hi + unit) =
+            *reinterpret_cast<uint4*>(sm.s[0] + unit) =
                 make_uint4(rounded(S[i]), rounded(S[i + 1]), rounded(S[i + 2]), rounded(S[i + 3]));
           }
           fence_async_smem();
@@ -771,9 +800,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (STATES && row == 0) cp.local_decay[it.seg * static_cast<int64_t>(heads) + head] = total;
       if (!STATES && !(it.last && p.state_out != nullptr)) continue;
       if (!STATES && !(ok = warp_wait(&sm.qs_full, (gc - 1) & 1, &sm.abort))) break;
+      if (!STATES && sent > 0 && !(ok = warp_wait(o_sent, (sent - 1) & 1, &sm.abort))) break;
 #pragma unroll
       for (int f = 0; f < 32; ++f)
-        *reinterpret_cast<ulonglong2*>((f < 16 ? sm.s_hi : sm.s_lo) + tile_unit(row, f & 15)) =
+        *reinterpret_cast<ulonglong2*>(sm.s[f < 16 ? 0 : 1] + tile_unit(row, f & 15)) =
             make_ulonglong2(S[2 * f], S[2 * f + 1]);
       fence_async_smem();
       warp_arrive(&sm.st_free[0]);
@@ -784,7 +814,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (lane == 0) {
           const int z = STATES ? (it.seg + 1) * p.lanes + it.b : it.b;
           for (int i = 0; i < 4; ++i)
-            tma_store_4d(&map_end, (i < 2 ? sm.s_hi : sm.s_lo) + (i & 1) * kHalf, i * 32, 0, it.h, z);
+            tma_store_4d(&map_end, sm.s[i < 2 ? 0 : 1] + (i & 1) * kHalf, i * 32, 0, it.h, z);
           bulk_commit_group();
           bulk_wait_group_read<0>();
           mbar_arrive(&sm.st_done);
@@ -882,11 +912,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   }
   __syncthreads();
-  // A wait gave up: the lanes of the items that were under way.
-  if (threadIdx.x < 2 && sm.abort && p.lane_status != nullptr) {
-    const int b = sm.item[threadIdx.x].b;
-    if (b >= 0 && b < p.lanes) p.lane_status[b] = SPEC_ERR_TIMEOUT;
-  }
+  // A wait gave up: the lanes of the items that were under way.  (No warp is more than one
+  // item behind the copies, nor the copies behind the items' warp.)
+  if (sm.abort && lane == 0 && (turn > 0 || warp == 3) && p.lane_status != nullptr)
+    p.lane_status[it.b] = SPEC_ERR_TIMEOUT;
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tm, 512);
 }
