@@ -522,15 +522,18 @@ _LOGPROBS_LAYOUT = _Layout(_LogprobsArgs)
 _LINEAR_LAYOUT = _Layout(_LinearArgs)
 
 
-def _raw_stream(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+def _raw_stream(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _opt(t, name, dtype, device, numel):
-    """Address of an optional tensor, 0 for None."""
+def _at(t, name, dtype, index, numel):
+    """Address of a tensor that _need accepts, 0 for None.  (Comparing a device's number
+    takes a third of comparing devices; these calls' checks are most of a small call.)"""
     if t is None:
         return 0
-    _need(t, name, dtype, device, numel)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+            and t.numel() >= numel):
+        _need(t, name, dtype, torch.device("cuda", index), numel)
     return t.data_ptr()
 
 
@@ -546,32 +549,33 @@ def spec_token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, to
     row_status int32 [rows].  ``rows`` defaults to logits.shape[0].
     """
     lib = _lib or load_library()
-    dtype = _DTYPES.get(logits.dtype)
-    if dtype is None or logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+    code = _DTYPES.get(logits.dtype)
+    shape, strides = logits.shape, logits.stride()
+    if code is None or len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
         raise ValueError("logits must be a 2-D bf16/float32 tensor with unit inner stride")
-    dev = logits.device
-    if dev.type != "cuda":
+    if not logits.is_cuda:
         raise ValueError("logits must be on a CUDA device")
-    have, V = logits.shape
+    dev = logits.get_device()
+    have, V = shape
     n = have if rows is None else int(rows)
     if n > have:
         raise ValueError("rows exceeds the rows of logits")
-    _need(tokens, "tokens", torch.int32, dev, n)
-    _need(logprobs, "logprobs", torch.float32, dev, n)
+    if tokens is None or logprobs is None:
+        raise ValueError("tokens and logprobs are required")
     top = ids = alts = 0
     if top_ids is not None and top_logprobs is not None:
         if top_ids.dim() != 2 or top_ids.shape != top_logprobs.shape:
             raise ValueError("top_ids and top_logprobs must be [rows, n]")
         top = top_ids.shape[1]
-        ids = _opt(top_ids, "top_ids", torch.int32, dev, n * top)
-        alts = _opt(top_logprobs, "top_logprobs", torch.float32, dev, n * top)
+        ids = _at(top_ids, "top_ids", torch.int32, dev, n * top)
+        alts = _at(top_logprobs, "top_logprobs", torch.float32, dev, n * top)
     elif top_ids is not top_logprobs:
         raise ValueError("top_ids and top_logprobs go together")
     args = _LOGPROBS_LAYOUT.pack(
-        logits.data_ptr(), dtype, logits.stride(0) if have > 1 else max(logits.stride(0), V), V, n, tokens.data_ptr(),
-        _opt(temperatures, "temperatures", torch.float32, dev, n), logprobs.data_ptr(),
-        _opt(entropy, "entropy", torch.float32, dev, n), top, ids, alts,
-        _opt(row_status, "row_status", torch.int32, dev, n))
+        logits.data_ptr(), code, strides[0] if have > 1 else max(strides[0], V), V, n,
+        _at(tokens, "tokens", torch.int32, dev, n), _at(temperatures, "temperatures", torch.float32, dev, n),
+        _at(logprobs, "logprobs", torch.float32, dev, n), _at(entropy, "entropy", torch.float32, dev, n), top, ids, alts,
+        _at(row_status, "row_status", torch.int32, dev, n))
     rc = lib.spec_token_logprobs(args, _raw_stream(stream, dev))
     if rc != SPEC_OK:
         raise SpecError(rc, "spec_token_logprobs")
@@ -594,10 +598,10 @@ def new_linear_workspace(lanes, v_heads, dk, dv, max_len, device):
     return torch.empty(spec_linear_workspace(lanes, v_heads, dk, dv, max_len), dtype=torch.uint8, device=device)
 
 
-def _states(t, name, device, shape):
+def _states(t, name, index, shape):
     """Address and strides of a state tensor ([.., dk, dv], the last two contiguous)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device:
-        raise ValueError(f"{name} must be a float32 tensor on {device}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.get_device() != index:
+        raise ValueError(f"{name} must be a float32 tensor on cuda:{index}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
     s = t.stride()
@@ -609,39 +613,41 @@ def _states(t, name, device, shape):
 
 def _linear_call(entry, what, q, k, v, log_decay, row_offsets, out, max_len, scale, lane_status, before, before_name,
                  after, after_name, cols, workspace, stream):
-    dtype, dev = q.dtype, q.device
+    dtype, dev = q.dtype, q.get_device()
     code = _DTYPES.get(dtype)
-    if code is None or dev.type != "cuda":
+    if code is None or not q.is_cuda:
         raise ValueError("q must be a bf16/float32 tensor on a CUDA device")
-    rows = q.shape[0]
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        if t.dtype != dtype or t.device != dev:
-            raise ValueError(f"{name} must be a {dtype} tensor on {dev}")
-        if t.dim() != 3 or t.shape[0] != rows or (t.stride(2) != 1 and t.shape[2] > 1):
-            raise ValueError(f"{name} must be [rows, heads, size] with unit inner stride")
-    if k.shape != q.shape or out.shape != v.shape:
+    if not (k.dtype is v.dtype is out.dtype is dtype and k.get_device() == v.get_device() == out.get_device() == dev):
+        raise ValueError(f"k, v and out must be {dtype} tensors on cuda:{dev}, like q")
+    qn, vn, qs, ks, vs, os_, gs = q.shape, v.shape, q.stride(), k.stride(), v.stride(), out.stride(), log_decay.stride()
+    if k.shape != qn or out.shape != vn:
         raise ValueError("k must have q's shape, and out v's")
-    _, hk, dk = q.shape
-    _, hv, dv = v.shape
+    if len(qn) != 3 or len(vn) != 3 or qn[0] != vn[0]:
+        raise ValueError("q, k, v and out must be [rows, heads, size]")
+    rows, hk, dk = qn
+    _, hv, dv = vn
+    if (qs[2] != 1 or ks[2] != 1) and dk > 1 or (vs[2] != 1 or os_[2] != 1) and dv > 1:
+        raise ValueError("q, k, v and out must have unit inner stride")
     if hk == 0 or hv % hk:
         raise ValueError("v's heads must be a multiple of q's and k's")
-    if log_decay.dtype != torch.float32 or log_decay.device != dev or log_decay.shape != (rows, hv):
+    if log_decay.dtype is not torch.float32 or log_decay.get_device() != dev or log_decay.shape != (rows, hv):
         raise ValueError("log_decay must be a float32 [rows, v_heads] tensor (expanded strides allowed)")
-    _need(row_offsets, "row_offsets", torch.int32, dev, 1)
+    if row_offsets is None:
+        raise ValueError("row_offsets is required")
+    offsets = _at(row_offsets, "row_offsets", torch.int32, dev, 1)
     lanes = row_offsets.numel() - 1
     in_ptr = out_ptr = in_lane = in_head = out_lane = out_col = out_head = 0
     if before is not None:
-        in_ptr, (in_lane, in_head, *_) = _states(before, before_name, dev, (lanes, hv, dk, dv))
+        in_ptr, (in_lane, in_head, _, _) = _states(before, before_name, dev, (lanes, hv, dk, dv))
     if after is not None:
         if cols is None:
-            out_ptr, (out_lane, out_head, *_) = _states(after, after_name, dev, (lanes, hv, dk, dv))
+            out_ptr, (out_lane, out_head, _, _) = _states(after, after_name, dev, (lanes, hv, dk, dv))
         else:
-            out_ptr, (out_lane, out_col, out_head, *_) = _states(after, after_name, dev, (lanes, cols, hv, dk, dv))
-    qs, ks, vs, os_, gs = q.stride(), k.stride(), v.stride(), out.stride(), log_decay.stride()
+            out_ptr, (out_lane, out_col, out_head, _, _) = _states(after, after_name, dev, (lanes, cols, hv, dk, dv))
     args = _LINEAR_LAYOUT.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0],
-        os_[1], log_decay.data_ptr(), gs[0], gs[1], row_offsets.data_ptr(), in_ptr, in_lane, in_head, out_ptr, out_lane,
-        out_col, out_head, _opt(lane_status, "lane_status", torch.int32, dev, lanes), code, lanes, rows, max_len, hk, hv,
+        os_[1], log_decay.data_ptr(), gs[0], gs[1], offsets, in_ptr, in_lane, in_head, out_ptr, out_lane,
+        out_col, out_head, _at(lane_status, "lane_status", torch.int32, dev, lanes), code, lanes, rows, max_len, hk, hv,
         dk, dv, dk ** -0.5 if scale is None else scale, 0 if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel())
     rc = entry(args, _raw_stream(stream, dev))
@@ -670,7 +676,7 @@ def spec_linear_prefill(q, k, v, log_decay, row_offsets, state_in, out, state_ou
         if stream is not None and workspace.numel() > 0:
             workspace.record_stream(stream)
     else:
-        _need(workspace, "workspace", torch.uint8, q.device)
+        _at(workspace, "workspace", torch.uint8, q.get_device(), 0)
     _linear_call(lib.spec_linear_prefill, "spec_linear_prefill", q, k, v, log_decay, row_offsets, out, int(max_len), scale,
                  lane_status, state_in, "state_in", state_out, "state_out", None, workspace, stream)
 
