@@ -45,12 +45,13 @@
 // order KV (first half), QK, KV (second half), QS, PV: P is made beside the three after
 // QK, the next S beside QS and PV, k' of the next tokens beside whatever is not KV.
 //
-// Measured (device time, 16 heads of 128): 64 lanes of 2,048 tokens 353 us, 0.93 of the
-// copy rate; 24 grouped lanes of 0 to 3000 tokens 102 us against 68 (what is left is the
-// last items' unequal ends); one lane of 16,384 88 us in two launches, each SM with few
-// chunks and little to overlap their starts with; 200 tokens 10.4 us.  A chunk takes 3.15 us
-// with every SM at work, when HBM bounds it, and 2.75 us with few: then the chain QK, P, PV
-// and the groups' waits for one another do.
+// Measured (device time, 16 heads of 128): 64 lanes of 2,048 tokens 350 us, 0.94 of the
+// copy rate; 24 grouped lanes of 0 to 3000 tokens 101 us against 68; one lane of 16,384
+// 88 us in two launches, each SM with few chunks and little to overlap their starts with;
+// 200 tokens 10.8 us.  A chunk takes 3.1 us with every SM at work, when HBM bounds it, and
+// 2.75 us with few: then a chain does, scores to P, D's scaling, PV, outputs.  PV behind the
+// next KV, or QS before KV's second half, shortens that chain but holds v or wants q longer
+// than the ring has tiles for: 372 and 370 us.
 #pragma once
 
 #include <cuda.h>
