@@ -20,18 +20,17 @@
 // S stays in fp32 in the registers of four warps from the first chunk to the last, and
 // S' = 2^G_last S + U is formed there: the tensor cores truncate each addition to an
 // accumulator, which into S itself cost ten times the precision of its fp32 sums.
-// Operands are bf16, so fp32 numbers enter a product rounded or in parts.  k' comes in three
-// parts that hold all its 24 bits: U is what stays.  P and S are rounded once: they are used
-// for one output, which is rounded to bf16 itself, and with their own roundings its rms error
-// is 0.0023 of its size instead of 0.0017; in two parts each they would cost another 1,024
-// cycles of products a chunk and the room and the registers for them.  q, k and v are taken
-// as they are.  States come out within 4e-7 of 64-bit ones, like those of fp32 sums.
+// Operands are bf16, so fp32 numbers enter a product in parts.  k' comes in three parts that
+// hold all its 24 bits: U is what stays.  P and S come in two, 16 bits, far below the rounding
+// of a bf16 output: its rms error is that rounding's, 0.0017 of its size (0.0023 with P and S
+// rounded to one part, which would save 1,024 cycles of products a chunk).  q, k and v are
+// taken as they are.  States come out within 4e-7 of 64-bit ones, like those of fp32 sums.
 //
 // Tensor memory holds U (128 columns), scores and P (128; P overwrites the scores it came
 // from), D (128) and two buffers of k' for 32 tokens (96).  Shared memory holds a ring of
 // five 32 KB tiles (k, v, q of a chunk; 128-byte swizzled rows, so that a tile serves as
-// an operand along either dimension), S in bf16, and with it room for the copies of states
-// in and out.
+// an operand along either dimension) and S in two parts, whose room also takes the copies of
+// states in and out.
 //
 // Warps: 0 copies tiles, 1 issues the products, 2 sums the decays, 3 hands out the items,
 // and five groups of four do what lies between the products: scores to P (4-11), D (8-11),
@@ -39,7 +38,8 @@
 // (the first of two launches for a lane cut in segments), 4-11 make k', too, into the room
 // of scores and P, and U has two places.
 //
-// The products of a chunk take 6 x 512 cycles on the tensor cores (k' counts three times),
+// The products of a chunk take 8 x 512 cycles on the tensor cores (k' counts three times,
+// S and P twice),
 // its 128 KB of q, k, v and o about 5,500 at an SM's share of the HBM rate: the groups work
 // beside each other so that the larger of the two counts.  A chunk's products go in the
 // order KV (first half), QK, KV (second half), QS, PV: P is made beside the three after
@@ -92,7 +92,7 @@ struct ChunkItem {
 
 struct ChunkSmem {
   uint8_t ring[kRing][kTile];
-  uint8_t s[2][kTile];    // S in bf16 in the first; both for states on their way in and out
+  uint8_t s[2][kTile];    // S, upper and lower parts; states on their way in and out
   float g_hi[2][kChunk];  // -G in two parts, chunk c in c % 2
   float g_lo[2][kChunk];
   float to_end[8][16];    // the P groups' warps: 2^(G at the end of 16 tokens - G_j)
@@ -220,7 +220,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   constexpr uint32_t kColKeys = STATES ? kColP : kColK, kColU2 = STATES ? kColK : kColU;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>(smem_raw);
-  uint64_t* const o_sent = &sm.kp_full[3];  // (STATES has no outputs, the others no fourth buffer of k')
   const LinearParams& p = cp.p;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sm.st_free[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&sm.kp_full[i], STATES || i < 3 ? 4 : 1);
+      mbar_init(&sm.kp_full[i], 4);
       mbar_init(&sm.kp_empty[i], 1);
     }
     mbar_init(&sm.scores_full, 1);
@@ -395,7 +394,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0);
     constexpr uint32_t kSame = mma_desc(128, 128, false), kRows = mma_desc(128, 128, true);
     const uint32_t ring = smem_desc(smem_addr(sm.ring[0]), kHalf);  // (for K-major tiles the piece distance is not used)
-    const uint32_t ds = smem_desc(smem_addr(sm.s[0]), kHalf);
+    const uint32_t ds = smem_desc(smem_addr(sm.s[0]), kHalf);  // (the lower part a tile behind)
     uint32_t kphase = 0;     // bit i: phase of k' buffer i
     int slot = 0, phase = 0; // the ring's slot of this chunk's k and its phase
     int tails = 0;           // chunks that did not fill a tile
@@ -462,21 +461,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!warp_wait(&sm.s_ready, ph, &sm.abort)) break;
         if (gc > 0 && !warp_wait(&sm.d_free, ph ^ 1, &sm.abort)) break;
         tc_fence_after();
+#pragma unroll 1
+        for (int part = 1; part >= 0; --part)  // the lower part first
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          mma_ss(lead, tmu + kColD, dq + ((s >> 2) * kHalf + (s & 3) * 32) / 16, ds + s * (2048 / 16), kRows, s > 0);
+          for (int s = 0; s < 8; ++s)
+            mma_ss(lead, tmu + kColD, dq + ((s >> 2) * kHalf + (s & 3) * 32) / 16,
+                   ds + part * (kTile / 16) + s * (2048 / 16), kRows, s > 0 || part == 0);
         mma_commit(lead, &sm.qs_full);
-        if (c + 1 < loops) {  // (at the last chunk outputs leave by this tile)
-          mma_commit(lead, &sm.empty[sq]);
-          if (lead) mbar_arrive_n(&sm.empty[sq], kKeyWarps);
-        }
         if (!warp_wait(&sm.p_ready, ph, &sm.abort) || !warp_wait(&sm.d_scaled, ph, &sm.abort)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int t = 0; t < bufs; ++t)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            mma_ts(lead, tmu + kColD, tmu + kColP + t * 32 + i * 16, dv + t * (2 * 2048 / 16) + i * (2048 / 16), kRows, true);
+          for (int i = 0; i < 4; ++i)
+            mma_ts(lead, tmu + kColD, tmu + kColP + t * 32 + (i & 1) * 16 + 8 - (i >> 1) * 8,
+                   dv + t * (2 * 2048 / 16) + (i & 1) * (2048 / 16), kRows, true);
         mma_commit(lead, &sm.o_full);
       }
       mma_commit(lead, &sm.empty[sv]);
@@ -553,7 +552,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     float* const to_end = sm.to_end[warp - 4];
     int slot = 2;    // the ring's slot of the chunk's q
     int stores = 0;  // chunks that went out as tiles
-    int sent = 0;    // those that went by sm.s
     bool ok = true;
     while (ok && next_item(sm, turn, it)) {
       for (int c = it.c0; c < it.c1; ++c, ++gc) {
@@ -564,10 +562,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc_fence_after();
 #pragma unroll 1
         for (int j0 = group * 16; j0 < kChunk; j0 += 32) {  // tokens j0 .. j0 + 15
-          uint32_t w[8];
+          uint32_t hi[8], lo[8];
           if (j0 >= static_cast<int>(quarter) + 32) {  // all after this warp's rows
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = 0u;
+            for (int i = 0; i < 8; ++i) hi[i] = lo[i] = 0u;
           } else {
             uint32_t s[16];
             tmem_ld16(s, tmq + kColP + j0);
@@ -583,8 +581,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
-                w[i / 2] = rounded(mul2(mul2(pair(from_end, from_end), *reinterpret_cast<const f32x2*>(&to_end[i])),
-                                        pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1]))));
+                const f32x2 x = mul2(mul2(pair(from_end, from_end), *reinterpret_cast<const f32x2*>(&to_end[i])),
+                                     pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+                hi[i / 2] = upper(x);
+                lo[i / 2] = rounded(rest(x));
               }
             } else {
               const int seen = static_cast<int>(row) - j0;  // the last of the tokens that this row sees
@@ -594,14 +594,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 // (the arrays hold -G)
                 const f32x2 d = add2(add2(pair(ghi, ghi), *reinterpret_cast<const f32x2*>(&sm.g_hi[buf][j0 + i])),
                                      add2(pair(glo, glo), *reinterpret_cast<const f32x2*>(&sm.g_lo[buf][j0 + i])));
-                const f32x2 x = mul2(pair(ex2_approx(first_of(d)), ex2_approx(second_of(d))),
-                                     pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+                f32x2 x = mul2(pair(ex2_approx(first_of(d)), ex2_approx(second_of(d))),
+                               pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
                 // (a select: what is masked may be NaN)
-                w[i / 2] = rounded(pair(i > seen ? 0.f : first_of(x), i + 1 > seen ? 0.f : second_of(x)));
+                x = pair(i > seen ? 0.f : first_of(x), i + 1 > seen ? 0.f : second_of(x));
+                hi[i / 2] = upper(x);
+                lo[i / 2] = rounded(rest(x));
               }
             }
           }
-          tmem_st8(tmq + kColP + j0, w);  // (P takes half of the scores' columns)
+          // For each 16 tokens 8 columns of upper and 8 of lower parts.
+          tmem_st8(tmq + kColP + j0, hi);
+          tmem_st8(tmq + kColP + j0 + 8, lo);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -630,11 +634,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         warp_arrive(&sm.d_scaled);
         if (!(ok = warp_wait(&sm.o_full, gc & 1, &sm.abort))) break;
         tc_fence_after();
-        // On their way out the outputs stand in the second place for states or, at an item's
-        // last chunk, beside which states may come and go, in the tile of the chunk's q.
-        const bool inner = c + 1 < it.c1;
-        uint8_t* tile = inner ? sm.s[1] : sm.ring[slot];
-        if (inner && sent > 0 && !(ok = warp_wait(o_sent, (sent - 1) & 1, &sm.abort))) break;
+        // The chunk's q has been read: its tile takes the outputs on their way out.
+        uint8_t* tile = sm.ring[slot];
         const int n = it.count - c * kChunk;
         const f32x2 scale = pair(p.scale, p.scale);
 #pragma unroll 1
@@ -662,14 +663,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               tma_store_3d(&map_out, tile + kHalf, 64, it.h, z);
               bulk_commit_group();
               bulk_wait_group_read<0>();
-              if (inner)
-                mbar_arrive(o_sent);
-              else
-                mbar_arrive_n(&sm.empty[slot], 1 + kKeyWarps);
+              mbar_arrive_n(&sm.empty[slot], 1 + kKeyWarps);
             }
             __syncwarp();
           }
-          sent += inner ? 1 : 0;
         } else {  // (a copy would go on into the next lane's rows)
           __syncwarp();
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + it.h * p.out_head;
@@ -694,12 +691,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // ------------------------------------------------------------------ states
     registers_grow<kRegsState>();
     // States come and go by copies through sm.s (columns 0..63 in the first), which holds S in
-    // bf16 only from a chunk's start to its QS; the group's first warp issues them.
+    // parts only from a chunk's start to its QS; the group's first warp issues them.
     const bool has_in = !STATES && p.state_in != nullptr;
     int loads = 0;       // states loaded so far
     int frees[2] = {0, 0};  // phases of st_free
     int stored = 0;      // states stored so far
-    int sent = 0;        // chunks whose outputs went by sm.s[1]
     bool ok = true;
     while (ok && next_item(sm, turn, it)) {
       const int64_t head = it.b * p.v_heads + it.h;
@@ -708,8 +704,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int i = 0; i < 64; ++i) S[i] = 0ull;
       if (!STATES && gc > 0 && !(ok = warp_wait(&sm.qs_full, (gc - 1) & 1, &sm.abort))) break;
       if (stored > 0 && !(ok = warp_wait(&sm.st_done, (stored - 1) & 1, &sm.abort))) break;
-      if (!STATES && sent > 0 && !(ok = warp_wait(o_sent, (sent - 1) & 1, &sm.abort))) break;
-      sent += it.c1 - it.c0 - 1;
       if (!STATES) {
         // The state before the segment: the lane's, then every earlier segment's from zero
         // behind its decay.
@@ -759,13 +753,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int c = it.c0; c < it.c1; ++c, ++gc) {
         const int buf = gc & 1;
         if (!STATES) {
-          // S in bf16 to shared memory for the chunk's QS, the last chunk's done.
+          // S in two parts to shared memory for the chunk's QS, the last chunk's done.
           if (c > it.c0 && !(ok = warp_wait(&sm.qs_full, (gc - 1) & 1, &sm.abort))) break;
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
             const uint32_t unit = tile_unit(row, i / 4);
             *reinterpret_cast<uint4*>(sm.s[0] + unit) =
-                make_uint4(rounded(S[i]), rounded(S[i + 1]), rounded(S[i + 2]), rounded(S[i + 3]));
+                make_uint4(upper(S[i]), upper(S[i + 1]), upper(S[i + 2]), upper(S[i + 3]));
+            *reinterpret_cast<uint4*>(sm.s[1] + unit) = make_uint4(rounded(rest(S[i])), rounded(rest(S[i + 1])),
+                                                                   rounded(rest(S[i + 2])), rounded(rest(S[i + 3])));
           }
           fence_async_smem();
           warp_arrive(&sm.s_ready);
@@ -801,7 +797,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (STATES && row == 0) cp.local_decay[it.seg * static_cast<int64_t>(heads) + head] = total;
       if (!STATES && !(it.last && p.state_out != nullptr)) continue;
       if (!STATES && !(ok = warp_wait(&sm.qs_full, (gc - 1) & 1, &sm.abort))) break;
-      if (!STATES && sent > 0 && !(ok = warp_wait(o_sent, (sent - 1) & 1, &sm.abort))) break;
 #pragma unroll
       for (int f = 0; f < 32; ++f)
         *reinterpret_cast<ulonglong2*>(sm.s[f < 16 ? 0 : 1] + tile_unit(row, f & 15)) =
