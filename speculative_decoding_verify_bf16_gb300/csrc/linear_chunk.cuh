@@ -864,9 +864,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // Each lane has the weight of one of the 32 tokens.
         const float weight = exp2f((sm.g_hi[buf][t0 + lane] - last_hi) + (sm.g_lo[buf][t0 + lane] - last_lo));
         const int pick = 2 * (lane & 3);
-        if (t0 + lane >= n)  // rows past the lane may hold NaN: what this warp reads of them becomes 0
+        if (t0 + lane >= n) {  // rows past the lane may hold NaN: what this warp reads of them becomes 0
           for (int u = 0; u < 4; ++u)
             *reinterpret_cast<uint4*>(sm.ring[sk] + tile_unit(t0 + lane, quarter / 8 + u)) = make_uint4(0u, 0u, 0u, 0u);
+          fence_async_smem();  // the tile's next content comes by a copy
+        }
         __syncwarp();
         f32x2 w[4];
 #pragma unroll
