@@ -653,7 +653,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc_fence_before();
         warp_arrive(&sm.d_free);
         fence_async_smem();
-        if (n >= kChunk) {
+        // By a copy, unless it would go on into the next lane's rows or, as it ends in steps of 16
+        // bytes, into what lies behind the head.
+        if (n >= kChunk && p.dv % 8 == 0) {
           warp_arrive(&sm.o_staged);
           if (warp == 8) {
             if (!(ok = warp_wait(&sm.o_staged, stores++ & 1, &sm.abort))) break;
@@ -667,15 +669,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             __syncwarp();
           }
-        } else {  // (a copy would go on into the next lane's rows)
+        } else {
           __syncwarp();
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + it.h * p.out_head;
 #pragma unroll 1
           for (int i = lane; i < 32 * 16; i += 32) {
-            const int r = static_cast<int>(quarter) + i / 16;
-            if (r < n && (i % 16) * 8 < p.dv)
-              *reinterpret_cast<uint4*>(dst + (it.first + c * static_cast<int64_t>(kChunk) + r) * p.out_row + (i % 16) * 8) =
-                  *reinterpret_cast<const uint4*>(tile + tile_unit(r, i % 16));
+            const int r = static_cast<int>(quarter) + i / 16, left = p.dv - (i % 16) * 8;
+            if (r >= n || left <= 0) continue;
+            __nv_bfloat16* const to = dst + (it.first + c * static_cast<int64_t>(kChunk) + r) * p.out_row + (i % 16) * 8;
+            const uint8_t* const from = tile + tile_unit(r, i % 16);
+            if (left >= 8)
+              *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+            else  // (dv is a multiple of four)
+              *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
           }
           fence_async_smem();  // the tile's next content comes by a copy
           __syncwarp();
