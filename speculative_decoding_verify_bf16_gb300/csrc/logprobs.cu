@@ -555,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
         return i < nblocks ? (sel[i >> p.group_bits] << p.group_bits) + (i & (p.group - 1)) : subs;
       };
       if (staged != i0) {
+        if (staged >= 0) specv::fence_async_smem();  // (plain stores may have filled what copies fill now)
         __syncwarp();
         staged = i0;
         uint32_t bytes = 0;
