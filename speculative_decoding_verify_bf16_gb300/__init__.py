@@ -644,6 +644,9 @@ def _linear_call(entry, what, q, k, v, log_decay, row_offsets, out, max_len, sca
             out_ptr, (out_lane, out_head, _, _) = _states(after, after_name, dev, (lanes, hv, dk, dv))
         else:
             out_ptr, (out_lane, out_col, out_head, _, _) = _states(after, after_name, dev, (lanes, cols, hv, dk, dv))
+    if workspace is None and cols is None:
+        with torch.cuda.stream(stream):  # (memory of the stream that uses it; None: the current one)
+            workspace = new_linear_workspace(lanes, hv, dk, dv, max_len, q.device)
     args = _LINEAR_LAYOUT.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0],
         os_[1], log_decay.data_ptr(), gs[0], gs[1], offsets, in_ptr, in_lane, in_head, out_ptr, out_lane,
@@ -668,14 +671,10 @@ def spec_linear_prefill(q, k, v, log_decay, row_offsets, state_in, out, state_ou
     of the lanes' lengths.  ``scale`` defaults to dk ** -0.5.  lane_status
     int32 [lanes] is read and updated: fill it with zeros before the first
     call.  ``workspace`` comes from new_linear_workspace; without one the call
-    takes scratch memory from PyTorch's allocator on the current stream.
+    takes scratch memory from PyTorch's allocator, on the stream that it runs on.
     """
     lib = _lib or load_library()
-    if workspace is None:
-        workspace = new_linear_workspace(row_offsets.numel() - 1, v.shape[1], q.shape[-1], v.shape[-1], max_len, q.device)
-        if stream is not None and workspace.numel() > 0:
-            workspace.record_stream(stream)
-    else:
+    if workspace is not None:
         _at(workspace, "workspace", torch.uint8, q.get_device(), 0)
     _linear_call(lib.spec_linear_prefill, "spec_linear_prefill", q, k, v, log_decay, row_offsets, out, int(max_len), scale,
                  lane_status, state_in, "state_in", state_out, "state_out", None, workspace, stream)
