@@ -59,7 +59,8 @@ __global__ void __launch_bounds__(kRecThreads) linear_recurrent_kernel(const Lin
   const int slice = blockIdx.x % slices;
   const int h = (blockIdx.x / slices) % p.v_heads;
   const int b = blockIdx.x / slices / p.v_heads;
-  if (p.lane_status != nullptr && p.lane_status[b] != SPEC_OK) return;
+  // (the warps agree on a status that another head's CTA may be writing)
+  if (p.lane_status != nullptr && __syncthreads_or(p.lane_status[b] != SPEC_OK)) return;
   int first, count;
   const int rc = linear_lane_rows(p, b, first, count);
   if (rc != SPEC_OK) {
