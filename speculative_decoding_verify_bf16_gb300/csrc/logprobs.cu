@@ -73,6 +73,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // exponential flushes); held there, a masked logit adds 0 * kLowExp to the entropy's sum
 // and not 0 * (-inf).
 constexpr float kLowExp = -140.f;
+// Largest logits (times log2(e) / T) up to here take the plain form of the weights.
+constexpr float kPlainExp = 0x1p22f;
 
 struct Params {
   const uint8_t* logits;
@@ -250,7 +252,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
       __syncthreads();
     }
     f32x2 s2 = 0ull, t2 = 0ull;
-    float ref = 0.f;   // weights are 2^(c x - ref), ref = c m rounded once: it cancels
+    // Sums are relative to 2^ref (plain) or to 2^(c m): weights are 2^(c x - ref), where
+    // ref = c m rounded once cancels in the end, or 2^((x - m) c).
+    float ref = 0.f;
     bool plain = false;
     uint32_t low = 0;  // (plain) what is below it has weight 0
     auto keep = [&](float top, int sub) {  // block `sub`'s largest
@@ -272,13 +276,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
       if (!(top > -INFINITY)) return false;
       if (top > acc.m) {
         const float next = top * c;
-        // Far from overflow, and with room below the maximum for all that counts: the plain
-        // form.  Otherwise (x - m) c, every exponent clamped.
+        // The plain form where ref's rounding (at most 2^-3, a factor of 1.1 on all weights) and
+        // its bound on x are small numbers.  Otherwise (x - m) c, every exponent clamped: with
+        // logits around 1e9, or divided by a small temperature, the rounding of ref would be an
+        // exponent of hundreds.
         const float at = (next + kLowExp) / c;
         const bool was = plain;
-        plain = fabsf(next) < 0x1p100f && at > -0x1p126f && at < top;
+        plain = fabsf(next) < kPlainExp && at > -0x1p126f;
         if (acc.m > -INFINITY) {
-          const float d = fmaxf(was && plain ? ref - next : (acc.m - top) * c, kLowExp), f = ex2_approx(d);
+          // From the old reference to the new one, each as exact as it is.
+          const float to = plain ? (was ? ref - next : fmaf(acc.m, c, -next)) : was ? fmaf(-top, c, ref) : (acc.m - top) * c;
+          const float d = fmaxf(to, kLowExp), f = ex2_approx(d);
           t2 = mul2(pair(f, f), fma2(s2, pair(d, d), t2));
           s2 = mul2(pair(f, f), s2);
         }
@@ -498,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
     for (int i = lane; i < parts; i += 32) {
       const Sums x = hd.part[i];
       a.status = max(a.status, x.status);
-      if (x.s > 0.f) {
+      if (!(x.s == 0.f)) {  // (a NaN fails the row)
         const float d = fmaxf((x.m - a.m) * c, kLowExp), f = ex2_approx(d);
         a.s = fmaf(x.s, f, a.s);
         a.t = fmaf(f, fmaf(x.s, d, x.t), a.t);
