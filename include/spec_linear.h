@@ -48,7 +48,8 @@ typedef struct {
   int64_t out_row_stride, out_head_stride;
   /* Log decays g, fp32 [rows][v_heads]; strides in elements, 0 allowed (a decay
    * for each head that is the same for all tokens has row stride 0).  -inf resets
-   * the state before the token; NaN and +inf fail the lane. */
+   * the state before the token; NaN and +inf fail the lane, and so may growth (g > 0)
+   * whose factor, exp of a sum of g over tokens in a row, is infinite in fp32. */
   const float* log_decay;
   int64_t decay_row_stride, decay_head_stride;
   /* Lane b owns rows row_offsets[b] .. row_offsets[b + 1] - 1 (none: an empty lane,

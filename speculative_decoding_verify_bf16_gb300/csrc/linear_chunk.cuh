@@ -76,9 +76,10 @@ constexpr int kRing = 5;
 constexpr uint32_t kColU = 0, kColP = 128, kColD = 256, kColK = 384;  // columns of tensor memory
 constexpr uint32_t kColKBuf = 48;     // a k' buffer: three parts of 16 columns (32 tokens)
 constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;    // log2(e) in two parts
-// A decay of 2^-160 is 0 in fp32 against everything a state can hold; the clamp keeps
-// resets (-inf) and lowest values out of the sums.
-constexpr float kDecayFloor = -160.f;
+// The clamp keeps resets (-inf) and lowest values out of the sums.  A factor is finite, below
+// 2^128, so that no growth over the 127 other tokens of a chunk brings back what this took:
+// 2^-65536 2^(127 * 128) is 0 in fp32.  Sums of 128 of them are exact (2^23).
+constexpr float kDecayFloor = -65536.f;
 
 constexpr int kSortLanes = 64;       // most lanes that are taken longest first
 
