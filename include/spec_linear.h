@@ -77,17 +77,18 @@ typedef struct {
   int32_t k_heads, v_heads;     /* v_heads a multiple of k_heads                               */
   int32_t dk, dv;               /* 1..SPEC_LINEAR_MAX_DIM, dv a multiple of 4                   */
   float scale;
-  /* Prefill only: scratch memory of spec_linear_workspace() bytes, 16-byte aligned,
-   * not shared with a call that may run at the same time (NULL where that is 0). */
+  /* Prefill only: scratch memory, 16-byte aligned, not shared with a call that may run at
+   * the same time; spec_linear_workspace() says how much is of use.  With less of it, or
+   * none (NULL), long prompts of few lanes are cut in fewer segments and take longer. */
   void* workspace;
   uint64_t workspace_bytes;
 } spec_linear_args;
 
 /*
- * spec_linear_workspace -- bytes of scratch memory that spec_linear_prefill wants for
- * this many lanes and heads on the current device (host-only; 0 if none, also for
- * sizes that the prefill refuses).  It grows with lanes * v_heads up to a bound of a
- * few states for each SM; row counts do not enter.
+ * spec_linear_workspace -- the most scratch memory, in bytes, that spec_linear_prefill can
+ * use with up to this many lanes and up to max_len tokens a lane on the current device
+ * (host-only; 0 if none, also for sizes that the prefill refuses): a buffer for the
+ * largest call serves all smaller ones.  It is bounded by one 128 x 128 state for each SM.
  */
 uint64_t spec_linear_workspace(int32_t lanes, int32_t v_heads, int32_t dk, int32_t dv, int32_t max_len);
 
@@ -96,7 +97,7 @@ uint64_t spec_linear_workspace(int32_t lanes, int32_t v_heads, int32_t dk, int32
  *
  * Errors: SPEC_ERR_INVALID_ARG for NULL required pointers (q, k, v, out, log_decay,
  * row_offsets with lanes and rows > 0), sizes or dtype outside the ranges above,
- * misaligned states or too small a workspace; SPEC_ERR_CUDA if a launch fails.
+ * misaligned states or a misaligned workspace; SPEC_ERR_CUDA if a launch fails.
  *
  * Prompts in bf16 with dk and dv up to 128 (max_len >= 8; q, k, v and out 16-byte aligned in
  * base and strides) run in chunks of 128 tokens on the tensor cores; everything else

@@ -588,13 +588,14 @@ SPEC_LINEAR_MAX_DIM = 256
 
 
 def spec_linear_workspace(lanes, v_heads, dk, dv, max_len):
-    """Bytes of scratch memory spec_linear_prefill wants for these sizes."""
+    """Most bytes of scratch memory that spec_linear_prefill can use with up to this many
+    lanes and tokens a lane."""
     return int(load_library().spec_linear_workspace(int(lanes), int(v_heads), int(dk), int(dv), int(max_len)))
 
 
 def new_linear_workspace(lanes, v_heads, dk, dv, max_len, device):
-    """A uint8 scratch buffer for spec_linear_prefill (kept by the caller; calls that
-    may run at the same time need one each)."""
+    """A uint8 scratch buffer for spec_linear_prefill with up to this many lanes and tokens a
+    lane (kept by the caller; calls that may run at the same time need one each)."""
     return torch.empty(spec_linear_workspace(lanes, v_heads, dk, dv, max_len), dtype=torch.uint8, device=device)
 
 
@@ -670,8 +671,8 @@ def spec_linear_prefill(q, k, v, log_decay, row_offsets, state_in, out, state_ou
     may be state_in) float32 [lanes, v_heads, dk, dv]; max_len: an upper bound
     of the lanes' lengths.  ``scale`` defaults to dk ** -0.5.  lane_status
     int32 [lanes] is read and updated: fill it with zeros before the first
-    call.  ``workspace`` comes from new_linear_workspace; without one the call
-    takes scratch memory from PyTorch's allocator, on the stream that it runs on.
+    call.  ``workspace`` comes from new_linear_workspace (any size will do, a
+    smaller one makes long prompts slower); without one the call takes scratch memory from PyTorch's allocator, on the stream that it runs on.
     """
     lib = _lib or load_library()
     if workspace is not None:

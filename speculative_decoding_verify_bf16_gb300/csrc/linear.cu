@@ -152,19 +152,19 @@ constexpr int kChunkMinLen = 8;
 // twice, by two launches, so short lanes and halves do not pay.  Measured with 16 heads,
 // whole against split, in us: 512 tokens, 16.7 / 21.9; 1024, 27.8 / 23.7; 2048, 50 / 29;
 // 16384, 357 / 88; with 64 pairs, in halves: 2048 tokens, 52.4 / 51.7; 4096, 96 / 82.
-int prefill_segments(int64_t pairs, int max_len, int sms) {
-  const int64_t chunks = (static_cast<int64_t>(max_len) + specv::kChunk - 1) / specv::kChunk;
-  if (pairs <= 0 || 2 * pairs > sms || chunks < 8) return 1;
-  const int64_t want = sms / pairs;
+// At most as many as `most`, for which there is scratch memory.
+int prefill_segments(int64_t pairs, int64_t chunks, int sms, int64_t most) {
+  if (pairs <= 0 || 2 * pairs > sms || chunks < 8 || most < 2) return 1;
+  const int64_t want = sms / pairs < most ? sms / pairs : most;
   const int64_t per = (chunks + want - 1) / want < 2 ? 2 : (chunks + want - 1) / want;
   const int64_t n = (chunks + per - 1) / per;
   return n > 2 || chunks > 16 ? static_cast<int>(n) : 1;
 }
 
-uint64_t segment_bytes(int segments, int64_t pairs) {
-  if (segments <= 1) return 0;
-  return static_cast<uint64_t>(segments) * pairs * (128 * 128 + 4) * sizeof(float);
-}
+int64_t chunks_of(int max_len) { return (static_cast<int64_t>(max_len) + specv::kChunk - 1) / specv::kChunk; }
+
+// Scratch memory of a segment of a (lane, head) pair: its state and its decay.
+constexpr uint64_t kSegmentBytes = (128 * 128 + 4) * sizeof(float);
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -255,10 +255,9 @@ int launch_chunk(const LinearParams& p, DeviceCache* dc, const spec_linear_args*
   }
   specv::ChunkParams cp{};
   cp.p = p;
-  cp.segments = prefill_segments(pairs, p.max_len, dc->sms);
-  const uint64_t need = segment_bytes(cp.segments, pairs);
-  if (need > 0 && (a->workspace == nullptr || !aligned16(a->workspace) || a->workspace_bytes < need))
-    return SPEC_ERR_INVALID_ARG;
+  const uint64_t held = a->workspace == nullptr ? 0 : a->workspace_bytes / (kSegmentBytes * pairs);
+  cp.segments = prefill_segments(pairs, chunks_of(p.max_len), dc->sms, static_cast<int64_t>(held));
+  if (cp.segments > 1 && !aligned16(a->workspace)) return SPEC_ERR_INVALID_ARG;
   cp.local = static_cast<float*>(a->workspace);
   cp.local_decay = cp.local + static_cast<int64_t>(cp.segments) * pairs * (128 * 128);
   const int k_heads = p.v_heads / p.group;
@@ -300,8 +299,15 @@ uint64_t spec_linear_workspace(int32_t lanes, int32_t v_heads, int32_t dk, int32
     return 0;
   DeviceCache* dc = nullptr;
   if (device_cache(&dc) != SPEC_OK) return 0;
-  const int64_t pairs = static_cast<int64_t>(lanes) * v_heads;
-  return segment_bytes(prefill_segments(pairs, max_len, dc->sms), pairs);
+  // The most that any call of up to this many lanes and tokens cuts.  (Fewer lanes may be cut
+  // into more segments each, and shorter ones too: segments have two chunks at least.)
+  const int64_t chunks = chunks_of(max_len);
+  int64_t most = 0;
+  for (int64_t pairs = v_heads; pairs <= static_cast<int64_t>(lanes) * v_heads && 2 * pairs <= dc->sms; pairs += v_heads) {
+    const int64_t n = dc->sms / pairs < (chunks + 1) / 2 ? dc->sms / pairs : (chunks + 1) / 2;
+    if (chunks >= 8 && (n > 2 || chunks > 16) && n * pairs > most) most = n * pairs;
+  }
+  return static_cast<uint64_t>(most) * kSegmentBytes;
 }
 
 int spec_linear_prefill(const spec_linear_args* a, void* stream) {
