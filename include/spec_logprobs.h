@@ -55,7 +55,8 @@ typedef struct {
  * streamed from the aligned 16 bytes that their start lies in (what is before it is not used)
  * and taken apart element by element, with the same results.
  * SPEC_LOGPROBS_TEST_WITHHOLD_COPY=1 in the environment, tests of the failure path only:
- * the first row's first copy is never issued, so that its wait gives up after 2 s.
+ * the first row's first copy is never issued, so that its wait gives up after 2 s; with 2
+ * the first copy of its second look, at the blocks that hold the alternatives.
  */
 int spec_token_logprobs(const spec_logprobs_args* args, void* stream);
 

@@ -94,7 +94,8 @@ struct Params {
   int32_t group_bits;     // its logarithm
   int32_t groups_total;   // kept maxima of a row
   int32_t chunk;          // blocks of one bulk copy
-  int32_t test_withhold;  // tests only: the first row's first copy is announced but never issued
+  int32_t test_withhold;  // tests only: the first row's first copy (1), or that of its second
+                          // look (2), is announced but never issued
 };
 
 struct alignas(16) Sums {
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
       if (lane == 0 && sub < whole) {
         const uint32_t bytes = (shift + min(p.chunk, whole - sub) * B::kBytes + 15u) & ~15u;
         specv::mbar_arrive_expect_tx(&hd.full[warp][slot], bytes);
-        if (!(p.test_withhold && blockIdx.x == 0 && sub == 0))
+        if (!(p.test_withhold == 1 && blockIdx.x == 0 && sub == 0))
           specv::bulk_g2s(slots + slot * kSlotStride, row - shift + sub * static_cast<int64_t>(B::kBytes), bytes,
                           &hd.full[warp][slot]);
       }
@@ -556,8 +557,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
   constexpr int kHeld = kSlots * kSlotBytes / S::kBytes;
   uint8_t* const held = ring + warp * (kSlots * kSlotStride);
   int staged = -1, batch = 0;
+  bool late = false;  // a copy did not come
   auto blocks = [&](auto f) {
-    for (int i0 = warp; i0 < nblocks; i0 += kWarps * kHeld) {
+    for (int i0 = warp; i0 < nblocks && !late; i0 += kWarps * kHeld) {
       auto block = [&](int j) {  // the j-th block of the batch, or one past the row
         const int i = i0 + j * kWarps;
         return i < nblocks ? (sel[i >> p.group_bits] << p.group_bits) + (i & (p.group - 1)) : subs;
@@ -589,12 +591,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
 #pragma unroll 1
             for (int j = 0; j < kHeld; ++j) {
               const int sub = block(j);
-              if (sub < subs && (sub + 1) * static_cast<int64_t>(kBlock) <= p.V)
+              if (sub < subs && (sub + 1) * static_cast<int64_t>(kBlock) <= p.V &&
+                  !(p.test_withhold == 2 && blockIdx.x == 0 && warp + batch + j == 0))
                 specv::bulk_g2s(held + j * S::kBytes, row + sub * static_cast<int64_t>(S::kBytes), S::kBytes, &hd.again[warp]);
             }
           }
-          if (!specv::mbar_wait_bounded(&hd.again[warp], batch & 1) && lane == 0 && p.row_status != nullptr)
-            p.row_status[r] = SPEC_ERR_TIMEOUT;
+          late = !__all_sync(0xFFFFFFFFu, specv::mbar_wait_bounded(&hd.again[warp], batch & 1));
+          if (late) {  // (what is on the way still lands before the CTA ends)
+            specv::mbar_wait_bounded(&hd.again[warp], batch & 1);
+            break;
+          }
           ++batch;
         }
         __syncwarp();
@@ -608,6 +614,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
         f(x, sub, held + j * S::kBytes);
       }
     }
+  };
+  // A barrier; the row fails as a whole where a copy did not come.
+  auto gave_up = [&] {
+    if (!__syncthreads_or(late)) return false;
+    if (threadIdx.x == 0) {
+      p.logprobs[r] = NAN;
+      if (p.entropy != nullptr) p.entropy[r] = NAN;
+      if (p.row_status != nullptr) p.row_status[r] = SPEC_ERR_TIMEOUT;
+    }
+    if (threadIdx.x < n) {
+      ids[threadIdx.x] = -1;
+      lps[threadIdx.x] = NAN;
+    }
+    return true;
   };
   // Once more the n-th of 32 columns, now of tokens, then all that are no worse.
   best = Entry{-INFINITY, kNowhere};
@@ -624,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
     if (before(k, best)) best = k;
   });
   hd.col[warp][lane] = best;  // (a barrier after the groups' columns were read)
-  __syncthreads();
+  if (gave_up()) return;
   const Entry low = bound();
   blocks([&](const S& x, int sub, const uint8_t* lies) {
     uint32_t mask = 0;
@@ -640,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
       if (at < kCandidates) hd.cand[at] = k;
     }
   });
-  __syncthreads();
+  if (gave_up()) return;
   const int ncand = hd.ncand;
   auto emit = [&](int pos, const Entry& k) {
     ids[pos] = k.i;
@@ -675,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
     const float wv = specv::warp_max_f32(v.v);
     const int wi = __reduce_min_sync(0xFFFFFFFFu, v.v == wv ? v.i : kNowhere);
     if (lane == 0) hd.col[warp][0] = Entry{wv, wi};
-    __syncthreads();
+    if (gave_up()) return;
     done = hd.col[0][0];
     for (int w = 1; w < kWarps; ++w)
       if (before(hd.col[w][0], done)) done = hd.col[w][0];
@@ -766,7 +786,7 @@ extern "C" int spec_token_logprobs(const spec_logprobs_args* a, void* stream) {
   p.chunk = share < most ? share : most;
 
   const char* withhold = std::getenv("SPEC_LOGPROBS_TEST_WITHHOLD_COPY");
-  p.test_withhold = withhold != nullptr && std::atoi(withhold) != 0;
+  p.test_withhold = withhold != nullptr ? std::atoi(withhold) : 0;
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a->rows) * cluster, 1, 1);
