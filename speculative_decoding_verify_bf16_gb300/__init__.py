@@ -571,11 +571,14 @@ def spec_token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, to
         alts = _at(top_logprobs, "top_logprobs", torch.float32, dev, n * top)
     elif top_ids is not top_logprobs:
         raise ValueError("top_ids and top_logprobs go together")
-    args = _LOGPROBS_LAYOUT.pack(
-        logits.data_ptr(), code, strides[0] if have > 1 else max(strides[0], V), V, n,
-        _at(tokens, "tokens", torch.int32, dev, n), _at(temperatures, "temperatures", torch.float32, dev, n),
-        _at(logprobs, "logprobs", torch.float32, dev, n), _at(entropy, "entropy", torch.float32, dev, n), top, ids, alts,
-        _at(row_status, "row_status", torch.int32, dev, n))
+    try:
+        args = _LOGPROBS_LAYOUT.pack(
+            logits.data_ptr(), code, strides[0] if have > 1 else max(strides[0], V), V, n,
+            _at(tokens, "tokens", torch.int32, dev, n), _at(temperatures, "temperatures", torch.float32, dev, n),
+            _at(logprobs, "logprobs", torch.float32, dev, n), _at(entropy, "entropy", torch.float32, dev, n), top, ids, alts,
+            _at(row_status, "row_status", torch.int32, dev, n))
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"spec_token_logprobs: a size does not fit 32 bits ({e})") from None
     rc = lib.spec_token_logprobs(args, _raw_stream(stream, dev))
     if rc != SPEC_OK:
         raise SpecError(rc, "spec_token_logprobs")
@@ -648,12 +651,15 @@ def _linear_call(entry, what, q, k, v, log_decay, row_offsets, out, max_len, sca
     if workspace is None and cols is None:
         with torch.cuda.stream(stream):  # (memory of the stream that uses it; None: the current one)
             workspace = new_linear_workspace(lanes, hv, dk, dv, max_len, q.device)
-    args = _LINEAR_LAYOUT.pack(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0],
-        os_[1], log_decay.data_ptr(), gs[0], gs[1], offsets, in_ptr, in_lane, in_head, out_ptr, out_lane,
-        out_col, out_head, _at(lane_status, "lane_status", torch.int32, dev, lanes), code, lanes, rows, max_len, hk, hv,
-        dk, dv, dk ** -0.5 if scale is None else scale, 0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel())
+    try:
+        args = _LINEAR_LAYOUT.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0],
+            os_[1], log_decay.data_ptr(), gs[0], gs[1], offsets, in_ptr, in_lane, in_head, out_ptr, out_lane,
+            out_col, out_head, _at(lane_status, "lane_status", torch.int32, dev, lanes), code, lanes, rows, max_len, hk, hv,
+            dk, dv, dk ** -0.5 if scale is None else scale, 0 if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel())
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"{what}: a size does not fit 32 bits, or scale is no number ({e})") from None
     rc = entry(args, _raw_stream(stream, dev))
     if rc != SPEC_OK:
         raise SpecError(rc, what)
@@ -672,7 +678,8 @@ def spec_linear_prefill(q, k, v, log_decay, row_offsets, state_in, out, state_ou
     of the lanes' lengths.  ``scale`` defaults to dk ** -0.5.  lane_status
     int32 [lanes] is read and updated: fill it with zeros before the first
     call.  ``workspace`` comes from new_linear_workspace (any size will do, a
-    smaller one makes long prompts slower); without one the call takes scratch memory from PyTorch's allocator, on the stream that it runs on.
+    smaller one makes long prompts slower); without one the call takes scratch
+    memory from PyTorch's allocator, on the stream that it runs on.
     """
     lib = _lib or load_library()
     if workspace is not None:
