@@ -648,7 +648,7 @@ def _linear_call(entry, what, q, k, v, log_decay, row_offsets, out, max_len, sca
             out_ptr, (out_lane, out_head, _, _) = _states(after, after_name, dev, (lanes, hv, dk, dv))
         else:
             out_ptr, (out_lane, out_col, out_head, _, _) = _states(after, after_name, dev, (lanes, cols, hv, dk, dv))
-    if workspace is None and cols is None:
+    if workspace is None and cols is None and dtype is torch.bfloat16:  # (float32 prompts are never split)
         with torch.cuda.stream(stream):  # (memory of the stream that uses it; None: the current one)
             workspace = new_linear_workspace(lanes, hv, dk, dv, max_len, q.device)
     try:
