@@ -115,6 +115,11 @@ __device__ __forceinline__ bool before(const Entry& a, const Entry& b) {
 }
 constexpr int kNowhere = INT32_MAX;
 
+// log p of logit v; -inf has probability 0 at an infinite temperature, too.
+__device__ __forceinline__ float log_p(float v, float m, float T, float log_s) {
+  return v > -INFINITY ? (v - m) / T - log_s : -INFINITY;
+}
+
 struct alignas(128) Head {
   union {
     Sums part[kMaxCluster * kWarps];
@@ -525,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
       hd.all = a;
       hd.log_s = log_s;
       const bool ok = a.status == SPEC_OK;
-      p.logprobs[r] = ok ? (given - a.m) / T - log_s : NAN;
+      p.logprobs[r] = ok ? log_p(given, a.m, T, log_s) : NAN;
       if (p.entropy != nullptr) p.entropy[r] = ok ? log_s - (a.t / a.s) * kLn2 : NAN;
       if (p.row_status != nullptr) p.row_status[r] = a.status;
     }
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
   const int ncand = hd.ncand;
   auto emit = [&](int pos, const Entry& k) {
     ids[pos] = k.i;
-    lps[pos] = (k.v - all.m) / T - log_s;
+    lps[pos] = log_p(k.v, all.m, T, log_s);
   };
   if (ncand <= kCandidates) {
     for (int i = threadIdx.x; i < ncand; i += kThreads) {
