@@ -143,15 +143,16 @@ int launch_recurrent(const LinearParams& p, spec_dtype dtype, bool staged, void*
 // Chunked prefill
 // ---------------------------------------------------------------------------
 // Shorter prompts run token after token.  Measured, 16 heads of 128, chunked against token
-// after token, in us: 8 tokens, 7.4 / 5.5 with 1 lane, 8.4 / 8.9 with 8, 43 / 60 with 64;
-// 16 tokens, 7.4 / 8.9, 8.5 / 14.3 and 44 / 98; 4 tokens, 7.3 / 4.2, 8.4 / 6.6 and 43 / 42.
+// after token, in us: 8 tokens, 7.7 / 5.5 with 1 lane, 9.1 / 8.9 with 8, 48 / 60 with 64;
+// 16 tokens, 7.9 / 8.8, 9.3 / 14.5 and 49 / 98; 4 tokens, 7.7 / 4.1, 8.9 / 6.6 and 47 / 42.
 constexpr int kChunkMinLen = 8;
 
 // Segments a lane's chunks are split into: with fewer (lane, head) pairs than half the
 // SMs, as many as occupy them, of two chunks at least.  A split lane's k and v are read
-// twice, by two launches, so short lanes and halves do not pay.  Measured with 16 heads,
-// whole against split, in us: 512 tokens, 16.7 / 21.9; 1024, 27.8 / 23.7; 2048, 50 / 29;
-// 16384, 357 / 88; with 64 pairs, in halves: 2048 tokens, 52.4 / 51.7; 4096, 96 / 82.
+// twice, by two launches, so short lanes do not pay, and short halves little.  Measured with
+// 16 heads, whole against split, in us: 512 tokens, 19.0 / 24.4; 1024, 32.8 / 26.3; 2048,
+// 60 / 32; 16384, 436 / 99; with 64 pairs, in halves: 1024 tokens, 33.6 / 39.1; 2048, 63 / 58;
+// 4096, 117 / 94.
 // At most as many as `most`, for which there is scratch memory.
 int prefill_segments(int64_t pairs, int64_t chunks, int sms, int64_t most) {
   if (pairs <= 0 || 2 * pairs > sms || chunks < 8 || most < 2) return 1;

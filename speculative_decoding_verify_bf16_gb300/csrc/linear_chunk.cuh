@@ -41,17 +41,19 @@
 // The products of a chunk take 8 x 512 cycles on the tensor cores (k' counts three times,
 // S and P twice),
 // its 128 KB of q, k, v and o about 5,500 at an SM's share of the HBM rate: the groups work
-// beside each other so that the larger of the two counts.  A chunk's products go in the
-// order KV (first half), QK, KV (second half), QS, PV: P is made beside the three after
+// beside each other, and what counts is the chain from scores to outputs.  A chunk's
+// products go in the order KV (first half), QK, KV (second half), QS, PV: P is made beside the three after
 // QK, the next S beside QS and PV, k' of the next tokens beside whatever is not KV.
 //
-// Measured (device time, 16 heads of 128): 64 lanes of 2,048 tokens 350 us, 0.94 of the
-// copy rate; 24 grouped lanes of 0 to 3000 tokens 101 us against 68; one lane of 16,384
-// 88 us in two launches, each SM with few chunks and little to overlap their starts with;
-// 200 tokens 10.8 us.  A chunk takes 3.1 us with every SM at work, when HBM bounds it, and
-// 2.75 us with few: then a chain does, scores to P, D's scaling, PV, outputs.  PV behind the
-// next KV, or QS before KV's second half, shortens that chain but holds v or wants q longer
-// than the ring has tiles for: 372 and 370 us.
+// Measured (device time, 16 heads of 128): 64 lanes of 2,048 tokens 412 to 433 us, 0.76 to
+// 0.79 of the copy rate (470 where each call finds L2 full of another kernel's writes); 24
+// grouped lanes of 0 to 3000 tokens 120 us against 68; one lane of 16,384 99 us in two
+// launches, each SM with few chunks and little to overlap their starts with; 200 tokens
+// 12.0 us.  A chunk takes 3.6 us (3.9 with every SM at work on heads of 128) where HBM
+// would allow 3.1: a chain bounds it, scores to P, QS, D's scaling, PV, outputs.  PV behind
+// the next KV, or QS before KV's second half (423 us against 417), shortens that chain but
+// holds v or wants q longer than the ring has tiles for.  Outputs straight from registers,
+// which would free q's tile earlier, scatter: 455.
 #pragma once
 
 #include <cuda.h>

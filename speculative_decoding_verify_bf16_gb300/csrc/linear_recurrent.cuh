@@ -10,12 +10,14 @@
 // four row groups of a warp (two shuffles), then across the warps through shared
 // memory, once a block of tokens.
 //
-// With snapshots the kernel is bound by their writes: dk * dv * 4 bytes a column
+// With snapshots most of the kernel's bytes are their writes: dk * dv * 4 bytes a column
 // and head against 5 * dk * dv operations.  Stored around L2 (nothing here reads them again)
-// they leave it to the states: 8 lanes x 8 columns of 16 fp32 heads of 128 take 15.1 us
-// instead of 18.1.  64 lanes x up to 4 columns (238 MB) take 42.5 us, 5.6 TB/s of reads and
-// writes together; plain writes alone reach 3.7 to 4.0 TB/s.  A single token of a single lane
-// takes 3.3 us: one latency of the loads, the sums over dk and a launch.
+// they leave it to the states: 8 lanes x 8 columns of 16 fp32 heads of 128 (78 MB) take 15.2
+// us instead of 18.1; a plain fill of 64 MiB takes 12.4.  64 lanes x up to 4 columns (238 MB)
+// take 43.0 us, 5.5 TB/s of reads and writes together, 0.82 of the copy rate: a CTA waits for
+// its piece of the state before its first column, and there are 4.5 CTAs for each place on
+// an SM.  A single token of a single lane takes 3.3 us: one latency of the loads, the sums
+// over dk and a launch.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -20,9 +20,9 @@
 // Measured (device time, bf16 rows, five alternatives and temperatures, nothing of them in
 // L2): 576 rows of 262,144 at ragged temperatures with rows left out 41.5 us, where the bytes
 // of those asked for take 26.0 at the measured copy rate; 64 of 151,936 with 20 alternatives
-// 15.0 us, of which some 6 are the second look (the exchange, the selection, 20 blocks read
+// 15.2 us, of which some 6 are the second look (the exchange, the selection, 20 blocks read
 // again and sorted out: a chain of latencies that few rows leave exposed); one of 262,144
-// 7.5 us; four of 1,024 in fp32 5.7 us.  576 fp32 rows of 151,937, none but the first aligned, are
+// 7.7 us; four of 1,024 in fp32 5.9 us.  576 fp32 rows of 151,937, none but the first aligned, are
 // read at 5.5 TB/s (63 us), and in bf16 at 4.1 TB/s (43 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
