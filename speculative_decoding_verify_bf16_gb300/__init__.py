@@ -10,6 +10,7 @@ fallback.
 import ctypes
 import os
 import struct
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -26,6 +27,9 @@ __all__ = [
     "spec_ngram_draft", "SPEC_NGRAM_MAX_MATCH", "spec_apply_penalties", "SPEC_VERIFY_META_BEFORE_WAIT",
     "SPEC_VERIFY_TEST_WITHHOLD_COPY", "spec_token_logprobs", "SPEC_LOGPROBS_MAX_TOP", "spec_linear_prefill",
     "spec_linear_verify", "spec_linear_workspace", "new_linear_workspace", "SPEC_LINEAR_MAX_DIM",
+    "PagedCache", "new_paged_cache", "spec_cache_write", "spec_cache_read", "spec_paged_attention",
+    "spec_paged_attention_workspace", "new_paged_attention_workspace", "SPEC_CACHE_MAX_DIM", "SPEC_CACHE_LEAST_EXP",
+    "SPEC_CACHE_MOST_EXP",
 ]
 
 SPEC_OK = 0
@@ -113,6 +117,30 @@ class _LinearArgs(ctypes.Structure):
          ("workspace_bytes", ctypes.c_uint64)]
 
 
+class _PagedCache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("k_exps", ctypes.c_void_p),
+                ("v_exps", ctypes.c_void_p), ("exp_page_stride", ctypes.c_int64), ("exp_slot_stride", ctypes.c_int64),
+                ("exp_head_stride", ctypes.c_int64), ("block_tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("cached_lens", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p), ("lane_status", ctypes.c_void_p),
+                ("type", ctypes.c_int)] + \
+        [(n, ctypes.c_int32) for n in ("pages", "page_size", "table_width", "lanes", "rows", "max_len", "kv_heads", "dim")]
+
+
+class _CacheRowsArgs(ctypes.Structure):
+    _fields_ = [("cache", _PagedCache), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_row_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
+
+
+class _PagedAttentionArgs(ctypes.Structure):
+    _fields_ = [("cache", _PagedCache), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("lse_row_stride", ctypes.c_int64), ("q_heads", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("max_context", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
+
+
 ACCEPT_COUNT_WORDS = 3 + 2 * SPEC_MAX_DRAFTS
 BACKOFF_FIELDS = ("misses", "backoff", "wait", "reserved")
 
@@ -163,7 +191,10 @@ def load_library():
     lib.spec_token_logprobs.argtypes = [ctypes.c_void_p, ctypes.c_void_p]  # (packed bytes, or a structure)
     lib.spec_linear_workspace.restype = ctypes.c_uint64
     lib.spec_linear_workspace.argtypes = [ctypes.c_int32] * 5
-    for f in (lib.spec_linear_prefill, lib.spec_linear_verify):
+    lib.spec_paged_attention_workspace.restype = ctypes.c_uint64
+    lib.spec_paged_attention_workspace.argtypes = [ctypes.c_int32] * 4
+    for f in (lib.spec_linear_prefill, lib.spec_linear_verify, lib.spec_cache_write, lib.spec_cache_read,
+              lib.spec_paged_attention):
         f.restype = ctypes.c_int
         f.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     _lib = lib
@@ -509,17 +540,23 @@ class _Layout:
               ctypes.c_float: "f"}
 
     def __init__(self, cls):
-        fmt, at = "=", 0
-        for name, kind in cls._fields_:
-            here = getattr(cls, name).offset
-            fmt += "x" * (here - at) + self._CODES[kind]
-            at = here + ctypes.sizeof(kind)
-        fmt += "x" * (ctypes.sizeof(cls) - at)
-        self.pack = struct.Struct(fmt).pack
+        self.pack = struct.Struct("=" + self._format(cls)).pack
+
+    @classmethod
+    def _format(cls, kind):
+        fmt, at = "", 0
+        for name, field in kind._fields_:
+            here = getattr(kind, name).offset
+            inner = cls._format(field) if issubclass(field, ctypes.Structure) else cls._CODES[field]
+            fmt += "x" * (here - at) + inner
+            at = here + ctypes.sizeof(field)
+        return fmt + "x" * (ctypes.sizeof(kind) - at)
 
 
 _LOGPROBS_LAYOUT = _Layout(_LogprobsArgs)
 _LINEAR_LAYOUT = _Layout(_LinearArgs)
+_CACHE_ROWS_LAYOUT = _Layout(_CacheRowsArgs)
+_PAGED_ATTENTION_LAYOUT = _Layout(_PagedAttentionArgs)
 
 
 def _raw_stream(stream, index):
@@ -702,3 +739,191 @@ def spec_linear_verify(q, k, v, log_decay, row_offsets, live, staged, out, scale
     cols = staged.shape[1]
     _linear_call(lib.spec_linear_verify, "spec_linear_verify", q, k, v, log_decay, row_offsets, out, cols, scale,
                  lane_status, live, "live", staged, "staged", cols, None, stream)
+
+
+# ---------------------------------------------------------------------------
+# Paged key/value cache and the attention over it (include/spec_cache.h)
+# ---------------------------------------------------------------------------
+SPEC_CACHE_MAX_DIM = 256
+SPEC_CACHE_LEAST_EXP = -48
+SPEC_CACHE_MOST_EXP = 48
+
+_CACHE_TYPES = {torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.int8: 3}
+
+
+class PagedCache(NamedTuple):
+    """Keys and values [pages, page_size, kv_heads, dim] (bf16, float8_e4m3fn or int8; any
+    strides, the same for both, with a contiguous last dimension) and, for the 8-bit types,
+    their exponents' bytes, uint8 [pages, page_size, kv_heads]."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+    k_exps: Optional[torch.Tensor] = None
+    v_exps: Optional[torch.Tensor] = None
+
+
+def new_paged_cache(pages, page_size, kv_heads, dim, dtype, device):
+    """An empty (zeroed) PagedCache; dtype: torch.bfloat16, torch.float8_e4m3fn or torch.int8."""
+    if dtype not in _CACHE_TYPES:
+        raise ValueError("dtype must be torch.bfloat16, torch.float8_e4m3fn or torch.int8")
+    shape = (pages, page_size, kv_heads, dim)
+    # (zeros of one byte are zeros of every type)
+    k, v = (torch.zeros(shape[:3] + (dim * dtype.itemsize,), dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
+    if dtype is torch.bfloat16:
+        return PagedCache(k, v)
+    exps = [torch.full(shape[:3], 127 + SPEC_CACHE_LEAST_EXP, dtype=torch.uint8, device=device) for _ in range(2)]
+    return PagedCache(k, v, *exps)
+
+
+def _cache_fields(cache, block_tables, cached_lens, row_offsets, lane_status, rows, max_len, dev):
+    """The fields of a spec_paged_cache, in order, and (kv_heads, dim)."""
+    k, v, k_exps, v_exps = cache
+    code = _CACHE_TYPES.get(k.dtype)
+    shape, strides = k.shape, k.stride()
+    if code is None or len(shape) != 4 or k.get_device() != dev:
+        raise ValueError(f"cache.k must be a bf16, float8_e4m3fn or int8 [pages, page_size, kv_heads, dim] tensor on cuda:{dev}")
+    if v.dtype is not k.dtype or v.shape != shape or v.stride() != strides or v.get_device() != dev:
+        raise ValueError("cache.v must match cache.k's dtype, device, shape and strides")
+    if strides[3] != 1:
+        raise ValueError("cache.k and cache.v must have unit inner stride")
+    ek = ev = 0
+    es = (0, 0, 0)
+    if code != 1:
+        for t, name in ((k_exps, "k_exps"), (v_exps, "v_exps")):
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or t.get_device() != dev or t.shape != shape[:3]:
+                raise ValueError(f"cache.{name} must be a uint8 [pages, page_size, kv_heads] tensor on cuda:{dev}")
+        es = k_exps.stride()
+        if v_exps.stride() != es:
+            raise ValueError("cache.v_exps must have cache.k_exps' strides")
+        ek, ev = k_exps.data_ptr(), v_exps.data_ptr()
+    elif k_exps is not None or v_exps is not None:
+        raise ValueError("a bf16 cache has no exponents")
+    if row_offsets is None or cached_lens is None or block_tables is None:
+        raise ValueError("block_tables, cached_lens and row_offsets are required")
+    offsets = _at(row_offsets, "row_offsets", torch.int32, dev, 1)
+    lanes = row_offsets.numel() - 1
+    if block_tables.dtype is not torch.int32 or block_tables.get_device() != dev or block_tables.dim() != 2 \
+            or block_tables.shape[0] != lanes or (block_tables.stride(1) != 1 and block_tables.shape[1] > 1 and lanes > 0):
+        raise ValueError(f"block_tables must be an int32 [lanes, width] tensor on cuda:{dev} with unit inner stride")
+    width = block_tables.shape[1]
+    stride = block_tables.stride(0) if lanes > 1 else max(block_tables.stride(0), width)
+    return (k.data_ptr(), v.data_ptr(), strides[0], strides[1], strides[2], ek, ev, es[0], es[1], es[2],
+            block_tables.data_ptr(), stride, _at(cached_lens, "cached_lens", torch.int32, dev, lanes), offsets,
+            _at(lane_status, "lane_status", torch.int32, dev, lanes), code, shape[0], shape[1], width, lanes, rows, max_len,
+            shape[2], shape[3])
+
+
+def _cache_rows_call(entry, what, cache, block_tables, cached_lens, row_offsets, k, v, max_len, lane_status, stream):
+    dtype, shape, dev = k.dtype, k.shape, k.get_device()
+    code = _DTYPES.get(dtype)
+    if code is None or not k.is_cuda or len(shape) != 3:
+        raise ValueError("k must be a bf16/float32 [rows, kv_heads, dim] tensor on a CUDA device")
+    if v.dtype is not dtype or v.shape != shape or v.get_device() != dev:
+        raise ValueError("v must match k's dtype, device and shape")
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1:
+        raise ValueError("k and v must have unit inner stride")
+    fields = _cache_fields(cache, block_tables, cached_lens, row_offsets, lane_status, shape[0], int(max_len), dev)
+    if shape[1:] != fields[-2:]:
+        raise ValueError("k and v must have the cache's heads and head size")
+    try:
+        args = _CACHE_ROWS_LAYOUT.pack(*fields, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], code)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"{what}: a size does not fit 32 bits ({e})") from None
+    rc = entry(args, _raw_stream(stream, dev))
+    if rc != SPEC_OK:
+        raise SpecError(rc, what)
+
+
+def spec_cache_write(cache, block_tables, cached_lens, row_offsets, k, v, max_len, lane_status=None, stream=None):
+    """The lanes' new keys and values into their slots of the cache (see spec_cache_write in
+    include/spec_cache.h).
+
+    cache: a PagedCache; block_tables int32 [lanes, width]: a lane's pages;
+    cached_lens int32 [lanes]: the tokens that a lane's cache holds already, behind which
+    its rows go; row_offsets int32 [lanes + 1]; k, v: [rows, kv_heads, dim] bf16 or float32,
+    lanes packed one after the other, rows and heads at strides of 16 bytes' multiples; max_len: an upper
+    bound of the lanes' rows.  lane_status int32 [lanes] is read and updated: fill it
+    with zeros before the first call.
+    """
+    lib = _lib or load_library()
+    _cache_rows_call(lib.spec_cache_write, "spec_cache_write", cache, block_tables, cached_lens, row_offsets, k, v, max_len,
+                     lane_status, stream)
+
+
+def spec_cache_read(cache, block_tables, cached_lens, row_offsets, k_out, v_out, max_len, lane_status=None, stream=None):
+    """Slots of the cache as the values they stand for (see spec_cache_read in
+    include/spec_cache.h): row i of lane b is the token at position ``cached_lens[b] + i``.
+    k_out and v_out [rows, kv_heads, dim], bf16 or float32, are written; the other arguments
+    are those of spec_cache_write.
+    """
+    lib = _lib or load_library()
+    _cache_rows_call(lib.spec_cache_read, "spec_cache_read", cache, block_tables, cached_lens, row_offsets, k_out, v_out,
+                     max_len, lane_status, stream)
+
+
+def spec_paged_attention_workspace(q_heads, kv_heads, dim, max_len):
+    """Most bytes of scratch memory that spec_paged_attention can use with these heads and up
+    to max_len columns a lane."""
+    return int(load_library().spec_paged_attention_workspace(int(q_heads), int(kv_heads), int(dim), int(max_len)))
+
+
+def new_paged_attention_workspace(q_heads, kv_heads, dim, max_len, device):
+    """A uint8 scratch buffer for spec_paged_attention with these heads and up to max_len columns a
+    lane, whatever the lanes and contexts (kept by the caller; calls that may run at the same
+    time need one each)."""
+    with torch.cuda.device(device):
+        size = spec_paged_attention_workspace(q_heads, kv_heads, dim, max_len)
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def spec_paged_attention(q, cache, block_tables, cached_lens, row_offsets, out, max_len, scale=None, window=0, lse=None,
+                         lane_status=None, max_context=0, workspace=None, stream=None):
+    """Attention of each lane's columns over its paged cache (see spec_paged_attention in
+    include/spec_cache.h): column i of lane b sees positions up to its own,
+    ``cached_lens[b] + i``, where spec_cache_write has put its key and value.
+
+    q, out: [rows, q_heads, dim] bf16, lanes packed one after the other, rows and heads at
+    strides of multiples of 8 elements; q_heads is a multiple of the cache's heads.  ``scale``
+    defaults to dim ** -0.5; ``window`` > 0: the last so many positions, its own
+    among them, are seen; lse: float32 [rows, q_heads] with unit inner stride, or None;
+    ``max_context``: an upper bound of the lanes' positions (0: what the tables hold).
+    ``workspace`` comes from new_paged_attention_workspace (a larger one will do; with a smaller one no
+    context is split over thread blocks); without one the call takes scratch memory from
+    PyTorch's allocator, on the stream that it runs on.  The other arguments are those of
+    spec_cache_write.
+    """
+    lib = _lib or load_library()
+    shape, dev = q.shape, q.get_device()
+    if q.dtype is not torch.bfloat16 or not q.is_cuda or len(shape) != 3:
+        raise ValueError("q must be a bf16 [rows, q_heads, dim] tensor on a CUDA device")
+    if out.dtype is not torch.bfloat16 or out.shape != shape or out.get_device() != dev:
+        raise ValueError("out must match q's dtype, device and shape")
+    rows, hq, dim = shape
+    qs, os_ = q.stride(), out.stride()
+    if qs[2] != 1 or os_[2] != 1:
+        raise ValueError("q and out must have unit inner stride")
+    max_len = int(max_len)
+    fields = _cache_fields(cache, block_tables, cached_lens, row_offsets, lane_status, rows, max_len, dev)
+    kv = fields[-2]
+    if dim != fields[-1] or kv == 0 or hq == 0 or hq % kv:
+        raise ValueError("q must have the cache's head size and a multiple of its heads")
+    lse_ptr = lse_row = 0
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (rows, hq) or (lse.stride(1) != 1 and hq > 1):
+            raise ValueError(f"lse must be a float32 [rows, q_heads] tensor on cuda:{dev} with unit inner stride")
+        lse_ptr, lse_row = lse.data_ptr(), lse.stride(0) if rows > 1 else max(lse.stride(0), hq)
+    if workspace is None:
+        with torch.cuda.stream(stream):  # (memory of the stream that uses it; None: the current one)
+            workspace = new_paged_attention_workspace(hq, kv, dim, max_len, q.device)
+    else:
+        _at(workspace, "workspace", torch.uint8, dev, 0)
+    try:
+        args = _PAGED_ATTENTION_LAYOUT.pack(
+            *fields, q.data_ptr(), out.data_ptr(), qs[0], qs[1], os_[0], os_[1], lse_ptr, lse_row, hq, int(window),
+            int(max_context), dim ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.numel())
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"spec_paged_attention: a size does not fit 32 bits, or scale is no number ({e})") from None
+    rc = lib.spec_paged_attention(args, _raw_stream(stream, dev))
+    if rc != SPEC_OK:
+        raise SpecError(rc, "spec_paged_attention")

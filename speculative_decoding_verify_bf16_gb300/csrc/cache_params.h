@@ -1,0 +1,66 @@
+// cache_params.h -- what the paged cache's kernels are launched with (the checked form of
+// spec_cache.h's structures), and where a lane's tokens lie.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "spec_cache.h"
+
+namespace specv {
+
+// The cache; strides in bytes.
+struct CacheParams {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t page, slot, head;
+  uint8_t* k_exps;
+  uint8_t* v_exps;
+  int64_t exp_page, exp_slot, exp_head;
+  const int32_t* tables;
+  int64_t table_stride;
+  const int32_t* cached;
+  const int32_t* offsets;
+  int32_t* status;
+  int32_t pages, page_size;
+  uint32_t page_magic, page_shift;  // p / page_size, see page_of
+  int32_t lanes, rows, max_len, kv_heads, dim;
+  int32_t most;  // most positions of a lane
+};
+
+// p / page_size for 0 <= p < 2^31.  With 2^s < page_size < 2^(s + 1) and the magic number m =
+// floor(2^(32 + s) / page_size) + 1, p m / 2^(32 + s) exceeds p / page_size by at most p / 2^(32 + s)
+// < 1 / page_size, so its whole part is the same.  Powers of two have magic number 0.
+__host__ __device__ inline int32_t page_of(const CacheParams& c, int32_t p) {
+#ifdef __CUDA_ARCH__
+  return c.page_magic == 0 ? p >> c.page_shift : static_cast<int32_t>(__umulhi(p, c.page_magic) >> c.page_shift);
+#else
+  return c.page_magic == 0 ? p >> c.page_shift
+                           : static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(p)) * c.page_magic >> 32) >> c.page_shift);
+#endif
+}
+inline void set_page_size(CacheParams& c, int32_t page_size) {
+  c.page_size = page_size;
+  c.page_shift = 0;
+  while ((int64_t{2} << c.page_shift) <= page_size) ++c.page_shift;
+  c.page_magic = (page_size & (page_size - 1)) == 0
+                     ? 0u
+                     : static_cast<uint32_t>((uint64_t{1} << (32 + c.page_shift)) / static_cast<uint32_t>(page_size)) + 1u;
+}
+
+// A lane's rows and the tokens before them; false for a lane that is laid out wrongly.
+__device__ __forceinline__ bool cache_lane(const CacheParams& c, int b, int& first, int& count, int& before) {
+  const int o0 = __ldg(c.offsets + b), o1 = __ldg(c.offsets + b + 1), n = __ldg(c.cached + b);
+  first = o0;
+  count = o1 - o0;
+  before = n;
+  return o0 >= 0 && o1 >= o0 && o1 <= c.rows && count <= c.max_len && n >= 0 && n <= c.most - count;
+}
+
+// The first error of a lane stays.
+__device__ __forceinline__ void lane_failed(const CacheParams& c, int b, int code) {
+  if (c.status != nullptr && *static_cast<volatile int32_t*>(c.status + b) == SPEC_OK) c.status[b] = code;
+}
+
+}  // namespace specv

@@ -1,0 +1,231 @@
+// cache_rows.cuh -- rows of keys and values into the slots of a paged cache, and back.
+//
+// A group of 8, 16 or 32 threads takes a token's head, eight numbers a thread, keys and
+// values of it one after the other; the largest number is a few shuffles away.  A CTA takes
+// a run of rows, whose slots its threads look up first, one row each.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "cache_params.h"
+#include "device_ptx.cuh"
+
+namespace specv {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowsMost = 32;  // rows of a CTA
+
+struct CacheRowsParams {
+  CacheParams c;
+  uint8_t* k;  // strides in bytes
+  uint8_t* v;
+  int64_t k_row, k_head, v_row, v_head;
+  int32_t rows_per_cta;
+};
+
+// The row's lane, by bisection of the offsets (which may be in no order at all: then
+// whatever is found does not hold the row, or is laid out rightly for it).
+__device__ __forceinline__ int lane_of_row(const CacheParams& c, int row) {
+  int lo = 0, hi = c.lanes;  // offsets[lo] <= row < offsets[hi], in good order
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(c.offsets + mid) <= row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Two e4m3 numbers as fp16 (exact), and two fp32 numbers rounded to e4m3.
+__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t two) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 s;\n\tcvt.u16.u32 s, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(d) : "r"(two));
+  return d;
+}
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// The exponent's byte of a head whose largest magnitude is `top_bits` (of an fp32 number), 255
+// if it cannot be held: the least e with top * 2^e >= 2^x m (1 <= m < 2), x - whole or one more.
+template <int TYPE>
+__device__ __forceinline__ uint32_t exponent_byte(uint32_t top_bits) {
+  constexpr int kWhole = TYPE == SPEC_CACHE_E4M3 ? 8 : 6;                        // 448 = 1.75 * 2^8, 127 = 1.984375 * 2^6
+  constexpr uint32_t kFraction = TYPE == SPEC_CACHE_E4M3 ? 0x600000u : 0x7E0000u;
+  const int e = static_cast<int>(top_bits >> 23) - kWhole + ((top_bits & 0x7FFFFFu) > kFraction ? 1 : 0);
+  if (e > 127 + SPEC_CACHE_MOST_EXP) return 255u;  // (NaN and infinities among them)
+  return e < 127 + SPEC_CACHE_LEAST_EXP ? 127 + SPEC_CACHE_LEAST_EXP : e;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(float (&x)[8], const uint8_t* from) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(from)), b = __ldcs(reinterpret_cast<const float4*>(from) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(from));
+    x[0] = bf16_lo(a.x), x[1] = bf16_hi(a.x), x[2] = bf16_lo(a.y), x[3] = bf16_hi(a.y);
+    x[4] = bf16_lo(a.z), x[5] = bf16_hi(a.z), x[6] = bf16_lo(a.w), x[7] = bf16_hi(a.w);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(uint8_t* to, const float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(to)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(to) =
+        make_uint4(to_bf16x2(x[0], x[1]), to_bf16x2(x[2], x[3]), to_bf16x2(x[4], x[5]), to_bf16x2(x[6], x[7]));
+  }
+}
+
+// GROUP threads a head (dim <= 8 * GROUP).  WRITE: rows to slots; otherwise slots to rows.
+template <typename T, int TYPE, int GROUP, bool WRITE>
+__global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRowsParams p) {
+  const CacheParams& c = p.c;
+  __shared__ int64_t slot_at[kRowsMost], exp_at[kRowsMost];
+  __shared__ int lane_at[kRowsMost];  // -1: nothing to do
+  griddep_wait();
+  griddep_launch_dependents();
+  const int row0 = blockIdx.x * p.rows_per_cta;
+  const int mine = min(p.rows_per_cta, c.rows - row0);
+  if (static_cast<int>(threadIdx.x) < mine) {
+    const int row = row0 + threadIdx.x, b = lane_of_row(c, row);
+    int first, count, before, lane = -1;
+    int64_t at = 0, ea = 0;
+    if (cache_lane(c, b, first, count, before) && row >= first && row < first + count &&
+        (c.status == nullptr || c.status[b] == SPEC_OK)) {
+      const int pos = before + row - first, page = page_of(c, pos);
+      const int id = __ldg(c.tables + b * c.table_stride + page), in = pos - page * c.page_size;
+      if (static_cast<uint32_t>(id) < static_cast<uint32_t>(c.pages)) {
+        lane = b;
+        at = id * c.page + in * c.slot;
+        ea = id * c.exp_page + in * c.exp_slot;
+      } else {
+        lane_failed(c, b, SPEC_ERR_LAYOUT);
+      }
+    }
+    lane_at[threadIdx.x] = lane;
+    slot_at[threadIdx.x] = at;
+    exp_at[threadIdx.x] = ea;
+  }
+  // Lanes laid out wrongly own no row for certain: the first CTA looks at all of them.
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < c.lanes; b += kRowThreads) {
+      int first, count, before;
+      if (!cache_lane(c, b, first, count, before)) lane_failed(c, b, SPEC_ERR_LAYOUT);
+    }
+  __syncthreads();
+  const int unit = threadIdx.x % GROUP, heads = mine * c.kv_heads;
+  const bool in_head = unit * 8 < c.dim;
+  constexpr int kSize = TYPE == SPEC_CACHE_BF16 ? 2 : 1;
+#pragma unroll 2
+  for (int base = 0; base < heads; base += kRowThreads / GROUP) {
+    const int i = base + threadIdx.x / GROUP;
+    const int r = i / c.kv_heads, h = i - r * c.kv_heads;
+    const int b = i < heads ? lane_at[r] : -1;
+    const bool on = b >= 0 && in_head;
+    const int64_t at = b < 0 ? 0 : slot_at[r] + h * c.head + unit * (8 * kSize);
+    const int64_t ea = b < 0 ? 0 : exp_at[r] + h * c.exp_head;
+    uint8_t* const kr = p.k + (row0 + r) * p.k_row + h * p.k_head + unit * (8 * static_cast<int>(sizeof(T)));
+    uint8_t* const vr = p.v + (row0 + r) * p.v_row + h * p.v_head + unit * (8 * static_cast<int>(sizeof(T)));
+    float x[2][8] = {};
+    if constexpr (WRITE) {
+      if (on) {
+        load8<T>(x[0], kr);
+        load8<T>(x[1], vr);
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        uint8_t* const to = (s ? c.v : c.k) + at;
+        // Magnitudes order as their bits, NaN above all.
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
+        bool bad;
+        if constexpr (TYPE == SPEC_CACHE_BF16) {
+          bad = top > 0x7F7F7FFFu;  // rounds to an infinity in bf16, or is one or NaN
+          if (on) store8<__nv_bfloat16>(to, x[s]);
+          bad = bad && on;
+        } else {
+#pragma unroll
+          for (int d = 1; d < GROUP; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          const uint32_t byte = exponent_byte<TYPE>(top);
+          const float inverse = __uint_as_float((254u - (byte == 255u ? 127u : byte)) << 23);
+          uint32_t w[2];
+          if constexpr (TYPE == SPEC_CACHE_E4M3) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              w[j] = to_e4m3x2(x[s][4 * j] * inverse, x[s][4 * j + 1] * inverse) |
+                     to_e4m3x2(x[s][4 * j + 2] * inverse, x[s][4 * j + 3] * inverse) << 16;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t y[4];
+#pragma unroll
+              for (int i2 = 0; i2 < 4; ++i2) y[i2] = static_cast<uint32_t>(__float2int_rn(x[s][4 * j + i2] * inverse)) & 255u;
+              w[j] = y[0] | y[1] << 8 | y[2] << 16 | y[3] << 24;
+            }
+          }
+          if (on) {
+            *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+            if (unit == 0) (s ? c.v_exps : c.k_exps)[ea] = static_cast<uint8_t>(byte);
+          }
+          bad = byte == 255u && b >= 0 && unit == 0;
+        }
+        if (bad) lane_failed(c, b, SPEC_ERR_NONFINITE);
+      }
+    } else {
+      if constexpr (TYPE == SPEC_CACHE_BF16) {
+        if (on) {
+          load8<__nv_bfloat16>(x[0], c.k + at);
+          load8<__nv_bfloat16>(x[1], c.v + at);
+        }
+      } else {
+        uint2 w[2] = {};
+        uint32_t byte[2] = {};
+        if (on) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            w[s] = __ldcs(reinterpret_cast<const uint2*>((s ? c.v : c.k) + at));
+            byte[s] = (s ? c.v_exps : c.k_exps)[ea];
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const float scale = byte[s] == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte[s] << 23);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t two = ((j < 2 ? w[s].x : w[s].y) >> (16 * (j & 1))) & 0xFFFFu;
+            if constexpr (TYPE == SPEC_CACHE_E4M3) {
+              const uint32_t hh = e4m3_to_half2(two);
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+              x[s][2 * j] = f.x * scale;
+              x[s][2 * j + 1] = f.y * scale;
+            } else {
+              x[s][2 * j] = static_cast<float>(static_cast<int8_t>(two & 255u)) * scale;
+              x[s][2 * j + 1] = static_cast<float>(static_cast<int8_t>(two >> 8)) * scale;
+            }
+          }
+        }
+      }
+      if (on) {
+        store8<T>(kr, x[0]);
+        store8<T>(vr, x[1]);
+      }
+    }
+  }
+}
+
+}  // namespace specv

@@ -1,0 +1,6 @@
+// paged_bf16.cu -- attention over a paged cache of bf16 numbers.
+#include "paged_variants.cuh"
+
+namespace specv {
+PagedVariant paged_rows_bf16(int dim, int64_t rows) { return paged_variant<SPEC_CACHE_BF16>(dim, rows); }
+}  // namespace specv

@@ -1,0 +1,6 @@
+// paged_e4m3.cu -- attention over a paged cache of e4m3 numbers.
+#include "paged_variants.cuh"
+
+namespace specv {
+PagedVariant paged_rows_e4m3(int dim, int64_t rows) { return paged_variant<SPEC_CACHE_E4M3>(dim, rows); }
+}  // namespace specv

@@ -1,0 +1,20 @@
+// paged_launch.h -- the attention kernels of one cache type, each type compiled on its own.
+#pragma once
+
+#include "paged_schedule.cuh"
+
+namespace specv {
+
+// A kernel over blocks of rows and what it is launched with.
+struct PagedVariant {
+  void* kernel;
+  int rows, size;  // rows of an item, head size that the kernel works with
+  int threads, smem;
+};
+
+// The kernel for heads of `dim` and up to `rows` rows of a lane and cache head.
+PagedVariant paged_rows_bf16(int dim, int64_t rows);
+PagedVariant paged_rows_e4m3(int dim, int64_t rows);
+PagedVariant paged_rows_int8(int dim, int64_t rows);
+
+}  // namespace specv

@@ -1,0 +1,21 @@
+// paged_variants.cuh -- which kernel a call takes.
+#pragma once
+
+#include "paged_launch.h"
+#include "paged_rows.cuh"
+
+namespace specv {
+
+template <typename S>
+PagedVariant rows_variant() {
+  return {reinterpret_cast<void*>(&paged_rows_kernel<S>), S::kRows, S::D, S::kThreads, static_cast<int>(sizeof(RowsSmem<S>))};
+}
+
+template <int TYPE>
+PagedVariant paged_variant(int dim, int64_t rows) {
+  if (dim > 128) return rows_variant<RowsShape<TYPE, 256, 1>>();
+  if (dim > 64) return rows > 16 ? rows_variant<RowsShape<TYPE, 128, 2>>() : rows_variant<RowsShape<TYPE, 128, 1>>();
+  return rows > 16 ? rows_variant<RowsShape<TYPE, 64, 2>>() : rows_variant<RowsShape<TYPE, 64, 1>>();
+}
+
+}  // namespace specv
