@@ -161,6 +161,10 @@ uint64_t spec_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int32
  * Errors: SPEC_ERR_INVALID_ARG as above, for q_heads that are no multiple of kv_heads, a
  * negative window or max_context or a misaligned workspace; SPEC_ERR_CUDA if a launch fails.
  * lanes = 0 is a no-op.
+ *
+ * SPEC_PAGED_TEST_WITHHOLD_COPY=1 in the environment, tests of the failure path only: the first thread
+ * block of the kernel for many columns never hands on its first tile of keys, so that its waits give up
+ * after some seconds and its lanes report SPEC_ERR_TIMEOUT.
  */
 int spec_paged_attention(const spec_paged_attention_args* args, void* stream);
 

@@ -123,34 +123,6 @@ struct ChunkParams {
   int32_t test_withhold;  // tests only: the first CTA announces its first copy but never issues it
 };
 
-// Waits for a phase; gives up after some seconds (a try sleeps up to 1.3 us in the barrier,
-// measured).  Few instructions, no clock: the roles' loops together have to stay within
-// the instruction cache, some 32 KB, or every warp waits for its code.
-constexpr uint32_t kTries = 1u << 21;
-__device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, int* abort) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < kTries; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  *static_cast<volatile int*>(abort) = 1;
-  return false;
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
-  return __all_sync(0xFFFFFFFFu, chunk_wait(bar, parity, abort));
-}
-// Registers of the calling warpgroup (four warps), within what the CTA was launched with.
-template <int N>
-__device__ __forceinline__ void registers_grow() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void registers_shrink() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
 // The upper halves of two fp32 numbers, which are their bf16 parts by truncation; what
 // truncation leaves; and two numbers rounded to bf16.
 __device__ __forceinline__ uint32_t upper(f32x2 v) {

@@ -2,5 +2,5 @@
 #include "paged_variants.cuh"
 
 namespace specv {
-PagedVariant paged_rows_bf16(int dim, int64_t rows) { return paged_variant<SPEC_CACHE_BF16>(dim, rows); }
+PagedVariant paged_bf16(int dim, int64_t rows, bool tiles) { return paged_variant<SPEC_CACHE_BF16>(dim, rows, tiles); }
 }  // namespace specv

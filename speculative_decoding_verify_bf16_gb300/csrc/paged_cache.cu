@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 
 #include "cache_rows.cuh"
@@ -105,7 +106,8 @@ int launch(void* kernel, dim3 grid, unsigned block, size_t smem, void** args, vo
   return SPEC_OK;
 }
 
-// Shared memory beyond 48 KB is asked for once for each kernel and device.
+// Shared memory beyond 48 KB is asked for once for each kernel and device (and then the kernel's
+// registers are looked at).
 struct Granted {
   void* kernel;
   int dev;
@@ -113,11 +115,18 @@ struct Granted {
 Granted g_granted[256];
 int g_granted_count = 0;
 
-int grant_smem(void* kernel, int dev, int smem) {
+int grant_smem(const PagedVariant& v, int dev) {
+  void* const kernel = v.kernel;
   std::lock_guard<std::mutex> lock(g_mutex);
   for (int i = 0; i < g_granted_count; ++i)
     if (g_granted[i].kernel == kernel && g_granted[i].dev == dev) return SPEC_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+  // The warpgroups' shares of registers must not add up to more than the launch brings.
+  cudaFuncAttributes fa;
+  if (v.regs > 0 && (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs * (v.threads / 128) < v.regs)) {
+    cudaGetLastError();
+    return SPEC_ERR_CUDA;
+  }
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess) {
     cudaGetLastError();
     return SPEC_ERR_CUDA;
   }
@@ -186,10 +195,10 @@ int cache_rows(const spec_cache_rows_args* a, void* stream) {
 // ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
-PagedVariant variant_for(spec_cache_type type, int dim, int64_t rows) {
-  if (type == SPEC_CACHE_BF16) return specv::paged_rows_bf16(dim, rows);
-  if (type == SPEC_CACHE_E4M3) return specv::paged_rows_e4m3(dim, rows);
-  return specv::paged_rows_int8(dim, rows);
+PagedVariant variant_for(spec_cache_type type, int dim, int64_t rows, bool tiles) {
+  if (type == SPEC_CACHE_BF16) return specv::paged_bf16(dim, rows, tiles);
+  if (type == SPEC_CACHE_E4M3) return specv::paged_e4m3(dim, rows, tiles);
+  return specv::paged_int8(dim, rows, tiles);
 }
 
 uint64_t scratch_bytes(const PagedVariant& v, int sms) {
@@ -218,7 +227,7 @@ uint64_t spec_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int32
   const int64_t rows = static_cast<int64_t>(max_len) * (q_heads / kv_heads);
   uint64_t most = 0;
   for (spec_cache_type type : {SPEC_CACHE_BF16, SPEC_CACHE_E4M3, SPEC_CACHE_INT8}) {
-    const uint64_t n = scratch_bytes(variant_for(type, dim, rows), sms);
+    const uint64_t n = scratch_bytes(variant_for(type, dim, rows, true), sms);
     most = n > most ? n : most;
   }
   return most;
@@ -253,17 +262,21 @@ int spec_paged_attention(const spec_paged_attention_args* a, void* stream) {
   if (a->max_context > 0 && a->max_context < p.c.most) p.c.most = a->max_context;
   int dev, sms;
   if ((rc = device_sms(&dev, &sms)) != SPEC_OK) return rc;
-  const PagedVariant v = variant_for(a->cache.type, p.c.dim, rows);
-  if ((rc = grant_smem(v.kernel, dev, v.smem)) != SPEC_OK) return rc;
+  // The tiles' kernel takes its maxima from unscaled scores: not for a scale of 0 or below (or NaN),
+  // nor for one that is nothing beside the largest numbers.
+  const PagedVariant v = variant_for(a->cache.type, p.c.dim, rows, p.scale >= 0x1p-100f);
+  if ((rc = grant_smem(v, dev)) != SPEC_OK) return rc;
   const bool split = a->workspace != nullptr && a->workspace_bytes >= scratch_bytes(v, sms);
   if (split) {
     p.records = static_cast<specv::PartRecord*>(a->workspace);
     p.parts = reinterpret_cast<float*>(p.records + sms);
   }
-  void* args[] = {&p};
+  const char* const withhold = std::getenv("SPEC_PAGED_TEST_WITHHOLD_COPY");
+  int test_withhold = withhold != nullptr && std::atoi(withhold) != 0;
+  void* args[] = {&p, &test_withhold};  // (the second is the tiles' kernel's)
   rc = launch(v.kernel, dim3(static_cast<unsigned>(sms)), static_cast<unsigned>(v.threads), static_cast<size_t>(v.smem), args, stream);
   if (rc != SPEC_OK || !split) return rc;
-  int rows_of = v.rows, slice = 4;
+  int rows_of = v.rows, slice = v.rows > 32 ? 16 : 4;
   void* join_args[] = {&p, &rows_of, &slice};
   return launch(join_kernel(v.size), dim3(static_cast<unsigned>(sms), static_cast<unsigned>((v.rows + slice - 1) / slice)),
                 specv::kJoinThreads, 0, join_args, stream);

@@ -10,11 +10,13 @@ struct PagedVariant {
   void* kernel;
   int rows, size;  // rows of an item, head size that the kernel works with
   int threads, smem;
+  int regs;  // registers that the warpgroups share out, four of a thread each (0: none are shared out)
 };
 
-// The kernel for heads of `dim` and up to `rows` rows of a lane and cache head.
-PagedVariant paged_rows_bf16(int dim, int64_t rows);
-PagedVariant paged_rows_e4m3(int dim, int64_t rows);
-PagedVariant paged_rows_int8(int dim, int64_t rows);
+// The kernel for heads of `dim` and up to `rows` rows of a lane and cache head; `tiles`: the
+// one of large tiles may be taken.
+PagedVariant paged_bf16(int dim, int64_t rows, bool tiles);
+PagedVariant paged_e4m3(int dim, int64_t rows, bool tiles);
+PagedVariant paged_int8(int dim, int64_t rows, bool tiles);
 
 }  // namespace specv

@@ -1,0 +1,550 @@
+// paged_tile.cuh -- attention of many rows (prompts, wide verify rounds) over a paged cache, on the
+// tensor cores: heads up to 128, two tiles of 128 rows a thread block, 128 positions a step.
+//
+//   S = q k^T (fp32, tensor memory)     P = 2^(scale log2(e) S - M), hidden ones 0     O += P v
+//
+// A row's running maximum M is raised, and O in tensor memory rescaled, only where a score exceeds
+// it by more than 2^8; sums of weights are fp32, in the thread that has the row.
+//
+// Products of a step and tile take 2 x 512 cycles on the tensor cores (heads of 128), the two tiles'
+// take turns: while one's run, the other's scores become weights.  Per step and tile a warp does 32 x 128
+// exponentials and some three further operations a number.
+//
+// Tensor memory: scores of both tiles (2 x 128 columns; the weights overwrite their first half),
+// O of both (2 x 128).  Shared memory: q of both tiles, and a ring of tiles of keys and values, in rows
+// with the 128-byte swizzle, so that a tile serves along either dimension.
+//
+// Warps: 0-3 and 4-7 a tile's rows, a thread each (q into shared memory, weights, rescaling,
+// outputs); 8-11 bring keys and values, 32 positions of a step each, looked up one by one, so that any page size and
+// order will do; 12 issues the products.
+//
+// 8-bit caches become fp16 on the way to shared memory, times 2^(e - r) with r the largest of a warp's 32
+// exponents, and q becomes fp16 times a power of two for each row.  2^r multiplies the keys' scores; the
+// values' r goes into the weights' exponents and out of their sum.  All of it is exact but for numbers
+// more than 2^14 below the largest of their 32 positions, which keep 24 bits behind that one's first.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "paged_rows.cuh"
+#include "paged_schedule.cuh"
+#include "tcgen05_ptx.cuh"
+
+namespace specv {
+
+constexpr int kTileThreads = 512;
+// Registers a thread of each warpgroup; their sum is what a launch must bring (4 x 128).
+constexpr int kTileRegsRows = 176, kTileRegsCopy = 104, kTileRegsIssue = 56;
+constexpr int kTileRegs = 2 * kTileRegsRows + kTileRegsCopy + kTileRegsIssue;
+constexpr int kTileHalf = 128 * 128;  // bytes of 128 rows of 64 numbers
+constexpr int kTileRefs = 8;          // steps whose exponents are held: more than the ring has steps
+
+template <int TYPE_, int D_>
+struct TileShape {
+  static constexpr int TYPE = TYPE_, D = D_;
+  static constexpr bool kEight = TYPE != SPEC_CACHE_BF16;
+  static constexpr int kRows = 256, kTile = 128;
+  static constexpr int kBytes = kTileHalf * (D / 64);
+  static constexpr int kStages = D > 64 ? 5 : 8;
+};
+
+template <typename S>
+struct TileSmem {
+  uint8_t q[2][S::kBytes];
+  uint8_t ring[S::kStages][S::kBytes];
+  float refs[kTileRefs][2][4];  // of a step's keys and values: each 32 positions' exponent
+  typename Schedule<S::kRows, S::kTile>::Shared plan;
+  uint64_t full[S::kStages], empty[S::kStages];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+
+// Descriptor of products of fp16 numbers instead of bf16.
+__host__ __device__ constexpr uint32_t mma_desc_of(bool half, int M, int N, bool b_rows) {
+  return half ? mma_desc(M, N, b_rows) & ~((1u << 7) | (1u << 10)) : mma_desc(M, N, b_rows);
+}
+
+// Byte offset of 16-byte unit u of row r: pieces of 64 numbers one after the other.
+__device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t u) {
+  return (u >> 3) * kTileHalf + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+}
+
+template <typename S>
+__global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const AttendParams p, const int test_withhold) {
+  using Plan = Schedule<S::kRows, S::kTile>;
+  constexpr int D = S::D, kStages = S::kStages;
+  constexpr bool kEight = S::kEight;
+  constexpr uint32_t kColS = 0, kColO = 256;  // columns of tensor memory, 128 a tile
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  TileSmem<S>& sm = *reinterpret_cast<TileSmem<S>*>(smem_raw);
+  const CacheParams& c = p.c;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 4);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 4);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.o_full[i], 1);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  Plan::plan(p, sm.plan);  // (its barriers publish the above)
+  tc_fence_after();
+  if (blockIdx.x == 0)  // lanes laid out wrongly have no units
+    for (int b = threadIdx.x; b < c.lanes; b += kTileThreads) {
+      int first, count, before;
+      if (!cache_lane(c, b, first, count, before)) lane_failed(c, b, SPEC_ERR_LAYOUT);
+    }
+  const uint32_t tm = sm.tmem;
+  const int64_t begin = sm.plan.begin, end = sm.plan.end;
+  int64_t left = begin < end ? end - begin : 0;
+  Cursor at = sm.plan.from;
+  PartRecord record = {0, 0, 0, 0};
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ rows of a tile
+    registers_grow<kTileRegsRows>();
+    const int w = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tms = tm + (static_cast<uint32_t>(warp & 3) << 21) + kColS + w * 128, tmo = tms + (kColO - kColS);
+    float qs = p.scale;  // what a score is multiplied with
+    // This thread's row of q.  (A tile without rows is left out.)
+    auto has_rows = [&] { return at.count * p.group - at.k * S::kRows > w * 128; };
+    auto load_q = [&] {
+      const int r = at.k * S::kRows + w * 128 + row, col = r / p.group;
+      const bool on = col < at.count;
+      const __nv_bfloat16* const from =
+          p.q + (on ? (at.first + col) * p.q_row + (at.h * p.group + r - col * p.group) * p.q_head : 0);
+      uint4 x[D / 8];
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u)
+        x[u] = on && u * 8 < c.dim ? __ldg(reinterpret_cast<const uint4*>(from + u * 8)) : make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (kEight) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+          const uint32_t* const v = &x[u].x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) most = max(most, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
+        }
+        // The largest comes to lie in 2^14 .. 2^15.
+        const int up = max(min(127 + 14 - static_cast<int>(most >> 7), 126), -126);
+        const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+        qs = p.scale / f;
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+          uint32_t* const v = &x[u].x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = to_halfx2(bf16_lo(v[i]) * f, bf16_hi(v[i]) * f);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u) *reinterpret_cast<uint4*>(sm.q[w] + swizzled(row, u)) = x[u];
+      fence_async_smem();
+      warp_arrive(&sm.q_full[w]);
+    };
+    int steps = 0, items = 0, refs = 0;
+    bool ok = true;
+    if (left > 0 && has_rows()) load_q();
+    while (ok && left > 0) {
+      const int n = static_cast<int>(min(static_cast<int64_t>(at.t1 - at.tile), left));
+      const bool starts = at.tile == at.t0, ends = at.tile + n == at.t1;
+      if (!has_rows()) {
+        refs += n;
+        left -= n;
+        at.tile += n - 1;
+        Plan::next_unit(p, at);
+        if (left > 0 && has_rows()) load_q();
+        continue;
+      }
+      const int r = at.k * S::kRows + w * 128 + row, col = r / p.group;
+      const int lim = at.before + col + 1, low = p.window > 0 ? lim - p.window : 0;
+      float top = -INFINITY, sum = 0.f;
+      int p0 = at.tile * S::kTile;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j, p0 += S::kTile, ++refs) {
+        if (!(ok = warp_wait(&sm.s_full[w], steps++ & 1, &sm.abort))) break;
+        tc_fence_after();
+        uint32_t x[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(x[i], tms + i * 32);
+        tmem_wait_ld();
+        if (__any_sync(0xFFFFFFFFu, p0 + S::kTile > lim || p0 < low)) {
+          const int i0 = low - p0, i1 = lim - p0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) x[i / 32][i % 32] = i >= i0 && i < i1 ? x[i / 32][i % 32] : 0xFF800000u;
+        }
+        float by[4], add[4];  // of each 32 positions: a score's factor, and what its exponent gets
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float m[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m[k] = fmaxf(__uint_as_float(x[i][k]), __uint_as_float(x[i][k + 4]));
+#pragma unroll
+          for (int k = 8; k < 32; k += 8)
+#pragma unroll
+            for (int l = 0; l < 4; ++l) m[l] = fmaxf(m[l], fmaxf(__uint_as_float(x[i][k + l]), __uint_as_float(x[i][k + l + 4])));
+          const float mi = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+          if constexpr (kEight) {
+            by[i] = qs * sm.refs[refs % kTileRefs][0][i];
+            add[i] = sm.refs[refs % kTileRefs][1][i];
+            most = fmaxf(most, fmaf(mi, by[i], add[i]));
+          } else {
+            by[i] = qs;
+            add[i] = 0.f;
+            most = fmaxf(most, mi * qs);
+          }
+        }
+        const float raise = most > top + kRowsSlack ? most : top;
+        if (__any_sync(0xFFFFFFFFu, raise != top)) {
+          const float f = raise == top ? 1.f : ex2_approx(top - raise);
+          top = raise;
+          sum *= f;
+          if (j > 0) {
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t o[32];
+              tmem_ld32(o, tmo + i * 32);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st32(tmo + i * 32, o);
+            }
+          }
+        }
+        const float from = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t y[32];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int q4 = half * 2 + i;
+            const f32x2 mul = pair(by[q4], by[q4]), off = pair(add[q4] - from, add[q4] - from);
+            f32x2 part[2] = {0ull, 0ull};
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const f32x2 e = fma2(pair(__uint_as_float(x[q4][k]), __uint_as_float(x[q4][k + 1])), mul, off);
+              const float e0 = ex2_approx(first_of(e)), e1 = ex2_approx(second_of(e));
+              part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], pair(e0, e1));
+              y[i * 16 + k / 2] = kEight ? to_halfx2(e0, e1) : to_bf16x2(e0, e1);
+            }
+            part[0] = add2(part[0], part[1]);
+            const float s = first_of(part[0]) + second_of(part[0]);
+            sum = kEight ? fmaf(s, power_of_minus(add[q4]), sum) : sum + s;
+          }
+          tmem_st32(tms + half * 32, y);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&sm.p_full[w]);
+      }
+      if (!ok) break;
+      // The last scores are there, so q's tile is free: the next item's comes while the last
+      // products run.
+      const Cursor done = at;
+      left -= n;
+      at.tile += n - 1;
+      Plan::next_unit(p, at);
+      if (left > 0 && has_rows()) load_q();
+      if (!(ok = warp_wait(&sm.o_full[w], items++ & 1, &sm.abort))) break;
+      tc_fence_after();
+      const bool whole = starts && ends, on = col < done.count;
+      const int head = done.h * p.group + r - col * p.group;
+      __nv_bfloat16* const out = p.out + (on ? (done.first + col) * p.out_row + head * p.out_head : 0);
+      float* const part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0)) * part_floats(S::kRows, D);
+      const float inv = 1.f / sum;
+      bool fine = true;
+#pragma unroll 1
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[32];
+        tmem_ld32(o, tmo + i * 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          float4 a = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
+          float4 b = make_float4(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5]), __uint_as_float(o[k + 6]), __uint_as_float(o[k + 7]));
+          if (whole) {
+            a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
+            b.x *= inv, b.y *= inv, b.z *= inv, b.w *= inv;
+            if (on && i * 32 + k < c.dim) {
+              *reinterpret_cast<uint4*>(out + i * 32 + k) =
+                  make_uint4(to_bf16x2(a.x, a.y), to_bf16x2(a.z, a.w), to_bf16x2(b.x, b.y), to_bf16x2(b.z, b.w));
+              fine = fine && finite4(a) && finite4(b);
+            }
+          } else {
+            float4* const to = reinterpret_cast<float4*>(part + (w * 128 + row) * D + i * 32 + k);
+            to[0] = a;
+            to[1] = b;
+          }
+        }
+      }
+      tc_fence_before();
+      if (whole) {
+        if (!fine) lane_failed(c, done.b, SPEC_ERR_NONFINITE);
+        if (on && p.lse != nullptr) p.lse[(done.first + col) * p.lse_row + head] = (top + log2f(sum)) * kLn2;
+      } else {
+        part[S::kRows * D + 2 * (w * 128 + row)] = top;
+        part[S::kRows * D + 2 * (w * 128 + row) + 1] = sum;
+      }
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ keys and values
+    registers_shrink<kTileRegsCopy>();
+    constexpr int kUnits = D * (kEight ? 1 : 2) / 16;  // 16-byte units of a token in the cache
+    constexpr int kAtOnce = 32 / kUnits;               // tokens of a warp's access
+    const int mine = warp - 8, used = c.dim * (kEight ? 1 : 2) / 16;
+    const int unit = lane % kUnits, sub = lane / kUnits;
+    const bool in_head = unit < used;
+    // Where this lane's position of the step at the cursor lies (-1: not seen), and its exponents.
+    int64_t from = -1;
+    uint32_t ek = 0, ev = 0;
+    auto look_up = [&] {
+      const int pos = at.tile * S::kTile + mine * 32 + lane;
+      from = -1;
+      ek = ev = 127 + SPEC_CACHE_LEAST_EXP;
+      if (pos >= at.lo && pos < at.hi) {
+        const int page = page_of(c, pos);
+        const int id = __ldg(c.tables + at.b * c.table_stride + page), in = pos - page * c.page_size;
+        if (static_cast<uint32_t>(id) < static_cast<uint32_t>(c.pages)) {
+          from = id * c.page + in * c.slot + at.h * c.head;
+          if constexpr (kEight) {
+            const int64_t e = id * c.exp_page + in * c.exp_slot + at.h * c.exp_head;
+            ek = c.k_exps[e];
+            ev = c.v_exps[e];
+          }
+        } else {
+          lane_failed(c, at.b, SPEC_ERR_LAYOUT);
+        }
+      }
+    };
+    int slot = 0, round = 0;
+    bool ok = true;
+    auto advance = [&] {
+      if (++slot == kStages) {
+        slot = 0;
+        ++round;
+      }
+    };
+    if constexpr (!kEight) {
+      constexpr int kLag = 2;  // tiles on their way before the oldest is waited for
+      int open = 0, open_slot = 0;
+      bool withheld = test_withhold != 0 && blockIdx.x == 0;
+      auto hand_on = [&] {  // the oldest tile, whose copies have landed
+        fence_async_smem();
+        if (!withheld) warp_arrive(&sm.full[open_slot]);
+        withheld = false;
+        if (++open_slot == kStages) open_slot = 0;
+        --open;
+      };
+#pragma unroll 1
+      for (; ok && left > 0; --left, Plan::next_unit(p, at)) {
+        look_up();
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_try_wait(&sm.empty[slot], (round - 1) & 1))) {
+            cp_async_wait<0>();
+            while (open > 0) hand_on();
+            if (!(ok = warp_wait(&sm.empty[slot], (round - 1) & 1, &sm.abort))) break;
+          }
+          const uint32_t to = smem_addr(sm.ring[slot]);
+          const uint8_t* const base = v ? c.v : c.k;
+#pragma unroll
+          for (int i = 0; i < 32 / kAtOnce; ++i) {
+            const int tok = i * kAtOnce + sub;
+            const int64_t f = __shfl_sync(0xFFFFFFFFu, from, tok);
+            const bool on = f >= 0 && in_head;
+            cp_async16_or_zero(to + swizzled(mine * 32 + tok, unit), base + (on ? f + unit * 16 : 0), on);
+          }
+          cp_async_commit();
+          ++open;
+          if (open > kLag) {
+            cp_async_wait<kLag>();
+            hand_on();
+          }
+          advance();
+        }
+      }
+      cp_async_wait<0>();
+      while (open > 0) hand_on();
+    } else {
+      constexpr int kLoads = 32 / kAtOnce;  // of a thread and tile
+      uint4 kx[kLoads], vx[kLoads];
+      auto fetch = [&](uint4 (&x)[kLoads], const uint8_t* base) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int64_t f = __shfl_sync(0xFFFFFFFFu, from, i * kAtOnce + sub);
+          x[i] = f >= 0 && in_head ? __ldg(reinterpret_cast<const uint4*>(base + f + unit * 16)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      // A tile as fp16 into the ring; `byte`: this lane's position's exponent, `ref` the largest.
+      auto store = [&](uint4 (&x)[kLoads], uint32_t byte, uint32_t ref) {
+        if (round > 0 && !(ok = warp_wait(&sm.empty[slot], (round - 1) & 1, &sm.abort))) return;
+        uint8_t* const to = sm.ring[slot];
+        const float f = byte == 255u ? __uint_as_float(0x7FC00000u)
+                                     : __uint_as_float(static_cast<uint32_t>(max(127 + static_cast<int>(byte) - static_cast<int>(ref), 0)) << 23);
+        const uint32_t scale = to_halfx2(f, f);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int tok = i * kAtOnce + sub;
+          const uint32_t s = __shfl_sync(0xFFFFFFFFu, scale, tok);
+          const uint32_t* const in = &x[i].x;
+          uint32_t y[8];
+          if constexpr (S::TYPE == SPEC_CACHE_E4M3) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[k]) : "r"(eight_to_half2<S::TYPE>(in[k / 2], k & 1)), "r"(s));
+          } else {
+            // y = u - 128 with u + 1024 in hand: s (u + 1024) - 1152 s, rounded once.
+            uint32_t less;
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(less) : "r"(s), "r"(0xE480E480u));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t m = __byte_perm(in[k / 2] ^ 0x80808080u, 0x64646464u, (k & 1) == 0 ? 0x4140 : 0x4342);
+              asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y[k]) : "r"(m), "r"(s), "r"(less));
+            }
+          }
+          *reinterpret_cast<uint4*>(to + swizzled(mine * 32 + tok, unit * 2)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(to + swizzled(mine * 32 + tok, unit * 2 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        fence_async_smem();
+        if (test_withhold == 0 || blockIdx.x != 0 || round > 0 || slot > 0) warp_arrive(&sm.full[slot]);
+        advance();
+      };
+      auto largest = [&](uint32_t byte) { return __reduce_max_sync(0xFFFFFFFFu, byte == 255u ? 0u : byte); };
+      if (left > 0) {
+        look_up();
+        fetch(kx, c.k);
+      }
+      int step = 0;
+#pragma unroll 1
+      while (ok && left > 0) {
+        fetch(vx, c.v);
+        const uint32_t kb = ek, vb = ev, kr = largest(kb), vr = largest(vb);
+        if (lane == 0) {
+          sm.refs[step % kTileRefs][0][mine] = __uint_as_float(kr << 23);
+          sm.refs[step % kTileRefs][1][mine] = static_cast<float>(static_cast<int>(vr) - 127);
+        }
+        ++step;
+        store(kx, kb, kr);
+        if (!ok) break;
+        Plan::next_unit(p, at);
+        if (--left > 0) {
+          look_up();
+          fetch(kx, c.k);
+        }
+        store(vx, vb, vr);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ products
+    registers_shrink<kTileRegsIssue>();
+    if (warp == 12) {
+      const uint32_t lead = elect_one();
+      const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0);
+      constexpr uint32_t kScores = mma_desc_of(kEight, 128, 128, false), kOuts = mma_desc_of(kEight, 128, D, true);
+      const uint32_t ring = smem_desc(smem_addr(sm.ring[0]), kTileHalf), qd = smem_desc(smem_addr(sm.q[0]), kTileHalf);
+      int slot = 0, phase = 0;
+      uint32_t parity = 0;  // bits 0, 1: of p_full; 2, 3: of q_full
+      bool ok = true;
+      auto advance = [&] {
+        if (++slot == kStages) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
+      auto scores = [&](int w, uint32_t kd) {
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = ((s >> 2) * kTileHalf + (s & 3) * 32) / 16;
+          mma_ss(lead, tmu + kColS + w * 128, qd + w * (S::kBytes / 16) + off, kd + off, kScores, s > 0);
+        }
+        mma_commit(lead, &sm.s_full[w]);
+      };
+      while (ok && left > 0) {
+        const int n = __shfl_sync(0xFFFFFFFFu, static_cast<int>(min(static_cast<int64_t>(at.t1 - at.tile), left)), 0);
+        const int tiles = __shfl_sync(0xFFFFFFFFu, at.count * p.group - at.k * S::kRows > 128 ? 2 : 1, 0);
+        if (!(ok = warp_wait(&sm.full[slot], phase, &sm.abort))) break;
+#pragma unroll 1
+        for (int w = 0; w < tiles && ok; ++w) {
+          ok = warp_wait(&sm.q_full[w], (parity >> (2 + w)) & 1, &sm.abort);
+          if (!ok) break;
+          parity ^= 4u << w;
+          tc_fence_after();
+          scores(w, ring + slot * (S::kBytes / 16));
+        }
+        if (!ok) break;
+        mma_commit(lead, &sm.empty[slot]);
+        advance();
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j) {
+          const int sv = slot;
+          if (!(ok = warp_wait(&sm.full[sv], phase, &sm.abort))) break;
+          advance();
+          const int sk = slot;
+          const uint32_t vd = ring + sv * (S::kBytes / 16), kd = ring + sk * (S::kBytes / 16);
+          if (j + 1 < n && !(ok = warp_wait(&sm.full[sk], phase, &sm.abort))) break;
+#pragma unroll 1
+          for (int w = 0; w < tiles; ++w) {
+            if (!(ok = warp_wait(&sm.p_full[w], (parity >> w) & 1, &sm.abort))) break;
+            parity ^= 1u << w;
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              mma_ts(lead, tmu + kColO + w * 128, tmu + kColS + w * 128 + s * 8, vd + s * (2048 / 16), kOuts, s + j > 0);
+            if (w + 1 == tiles) mma_commit(lead, &sm.empty[sv]);
+            if (j + 1 < n) {
+              scores(w, kd);
+              if (w + 1 == tiles) mma_commit(lead, &sm.empty[sk]);
+            } else {
+              mma_commit(lead, &sm.o_full[w]);
+            }
+          }
+          if (ok && j + 1 < n) advance();
+        }
+        if (!ok) break;
+        left -= n;
+        at.tile += n - 1;
+        const Cursor done = at;
+        Plan::next_unit(p, at);
+        if (left == 0 && done.tile + 1 < done.t1 && begin <= end - 1 - (done.tile - done.t0)) {
+          record.lane = done.b;
+          record.head = done.h;
+          record.block = done.k;
+          record.parts = Plan::block_of(end - 1 + (done.t1 - done.tile) - 1, sm.plan.total) - static_cast<int>(blockIdx.x) + 1;
+        }
+      }
+      // Tensor memory is given back only after the last product.
+      mma_commit(lead, &sm.drain);
+      mbar_wait_bounded(&sm.drain, 0);
+      __syncwarp();
+      if (lane == 0 && p.parts != nullptr) p.records[blockIdx.x] = record;
+    }
+  }
+  __syncthreads();
+  // A wait gave up: all lanes of the block's range.
+  if (sm.abort && threadIdx.x == 0) {
+    at = sm.plan.from;
+    for (int64_t u = begin; u < end; ++u, Plan::next_unit(p, at))
+      if (c.status != nullptr) c.status[at.b] = SPEC_ERR_TIMEOUT;
+  }
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tm, 512);
+}
+
+}  // namespace specv
