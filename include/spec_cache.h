@@ -50,7 +50,9 @@ typedef enum { SPEC_CACHE_BF16 = 1, SPEC_CACHE_E4M3 = 2, SPEC_CACHE_INT8 = 3 } s
 typedef struct {
   /* Keys and values of `type`, [pages][page_size][kv_heads][dim] in whatever order the
    * strides (in elements, the same for both, >= 0) say, the last dimension contiguous;
-   * bases 16-byte aligned, strides multiples of 16 bytes. */
+   * bases 16-byte aligned, strides multiples of 16 bytes.  With u the largest power of two
+   * up to 64 KB that divides the three strides in bytes, the last head lies less than 2^32 u bytes
+   * behind the first (64 GB at least). */
   void* k_pages;
   void* v_pages;
   int64_t page_stride, slot_stride, head_stride;
@@ -162,9 +164,9 @@ uint64_t spec_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int32
  * negative window or max_context or a misaligned workspace; SPEC_ERR_CUDA if a launch fails.
  * lanes = 0 is a no-op.
  *
- * SPEC_PAGED_TEST_WITHHOLD_COPY=1 in the environment, tests of the failure path only: the first thread
- * block of the kernel for many columns never hands on its first tile of keys, so that its waits give up
- * after some seconds and its lanes report SPEC_ERR_TIMEOUT.
+ * SPEC_PAGED_TEST_WITHHOLD_COPY=1 in the environment, tests of the failure path only: the thread block with
+ * the first position never gets one of its first copies (with many columns: hands on its first tile), so that
+ * its waits give up after some seconds and its lanes report SPEC_ERR_TIMEOUT.
  */
 int spec_paged_attention(const spec_paged_attention_args* args, void* stream);
 

@@ -15,6 +15,10 @@ struct CacheParams {
   uint8_t* k;
   uint8_t* v;
   int64_t page, slot, head;
+  // The same in units of 2^unit_shift bytes, 16 at least, which divide them all; no head lies
+  // 2^32 units or more behind the first.
+  uint32_t page_units, slot_units, head_units;
+  int32_t unit_shift;
   uint8_t* k_exps;
   uint8_t* v_exps;
   int64_t exp_page, exp_slot, exp_head;
@@ -57,6 +61,12 @@ __device__ __forceinline__ bool cache_lane(const CacheParams& c, int b, int& fir
   before = n;
   return o0 >= 0 && o1 >= o0 && o1 <= c.rows && count <= c.max_len && n >= 0 && n <= c.most - count;
 }
+
+// Where a token's head begins, in units.
+__device__ __forceinline__ uint32_t head_at(const CacheParams& c, int page, int slot, int head) {
+  return page * c.page_units + slot * c.slot_units + head * c.head_units;
+}
+constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 
 // The first error of a lane stays.
 __device__ __forceinline__ void lane_failed(const CacheParams& c, int b, int code) {

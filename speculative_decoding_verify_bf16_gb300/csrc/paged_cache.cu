@@ -46,6 +46,15 @@ int check_cache(const spec_paged_cache& a, CacheParams* c) {
   c->page = a.page_stride * size;
   c->slot = a.slot_stride * size;
   c->head = a.head_stride * size;
+  c->unit_shift = 4;
+  while (c->unit_shift < 16 && ((c->page | c->slot | c->head) >> c->unit_shift & 1) == 0) ++c->unit_shift;
+  // (by way of 64-bit floats: the products themselves could overflow)
+  const double last = (a.pages - 1.0) * static_cast<double>(c->page) + (a.page_size - 1.0) * static_cast<double>(c->slot) +
+                      (a.kv_heads - 1.0) * static_cast<double>(c->head);
+  if (last / static_cast<double>(int64_t{1} << c->unit_shift) >= 4294967295.0) return SPEC_ERR_INVALID_ARG;
+  c->page_units = static_cast<uint32_t>(c->page >> c->unit_shift);
+  c->slot_units = static_cast<uint32_t>(c->slot >> c->unit_shift);
+  c->head_units = static_cast<uint32_t>(c->head >> c->unit_shift);
   c->k_exps = a.k_exps;
   c->v_exps = a.v_exps;
   c->exp_page = a.exp_page_stride;
@@ -273,7 +282,7 @@ int spec_paged_attention(const spec_paged_attention_args* a, void* stream) {
   }
   const char* const withhold = std::getenv("SPEC_PAGED_TEST_WITHHOLD_COPY");
   int test_withhold = withhold != nullptr && std::atoi(withhold) != 0;
-  void* args[] = {&p, &test_withhold};  // (the second is the tiles' kernel's)
+  void* args[] = {&p, &test_withhold};
   rc = launch(v.kernel, dim3(static_cast<unsigned>(sms)), static_cast<unsigned>(v.threads), static_cast<size_t>(v.smem), args, stream);
   if (rc != SPEC_OK || !split) return rc;
   int rows_of = v.rows, slice = v.rows > 32 ? 16 : 4;

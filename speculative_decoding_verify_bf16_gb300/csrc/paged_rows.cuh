@@ -4,12 +4,14 @@
 // of a row: one pass over keys and values.
 //
 // What bounds it is reading the cache: 2 * dim numbers a token and head, for the rows of all query
-// heads and columns of that head together.  Every warp streams tokens of its own through a
-// ring of its own in shared memory (16-byte asynchronous copies, whose sources are looked up
-// token by token, so that any page size and order will do), and keeps maxima, sums and the
-// outputs' numerators of all rows in registers: warps wait for nobody until an item ends, when
-// their sums are joined in the ring's last place.  Products are 16 x 8 x 16 ones of a warp: 16 rows are a
-// fraction of a 128-row tile of the large tensor cores, and what they save is not short.
+// heads and columns of that head together.  Every computing warp has tokens of its own, which come
+// through a ring of its own in shared memory, and keeps maxima, sums and the outputs' numerators of
+// all rows in registers: warps wait for nobody until an item ends, when their sums are joined
+// in the ring's last place.  Four warps do nothing but look up where tokens lie, one by one (any page
+// size and order will do), and copy them, 16 bytes a thread.  (Bulk copies of whole heads, 128 or 256 bytes
+// each, are fewer instructions, but one took some 19 cycles of an SM: 142 us for 131,000 tokens
+// where these took 109 from within the computing warps.)  Products are 16 x 8 x 16 ones of a warp: 16 rows are
+// a fraction of a 128-row tile of the large tensor cores, and what they save is not short.
 //
 // 8-bit caches: numbers become fp16 in registers, exactly, and products are fp16.  q is
 // taken times a power of two for each row into fp16's range (exactly, but for what is below
@@ -29,16 +31,12 @@
 #include "cache_rows.cuh"
 #include "device_ptx.cuh"
 #include "paged_schedule.cuh"
+#include "tcgen05_ptx.cuh"
 
 namespace specv {
 
-constexpr uint32_t kRowsRing = 222 * 1024;  // shared memory of all rings
 constexpr float kRowsSlack = 8.f;           // a maximum is raised when it is exceeded by more: weights stay below 2^8
 
-// 16-byte copy of a thread; zeros if not `on`.
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -50,6 +48,14 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// 16-byte copy of a thread; zeros if not `on`.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+// One arrival (of those that the barrier was set up for) when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 template <bool HALF>
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -95,38 +101,52 @@ __device__ __forceinline__ uint32_t eight_to_half2(uint32_t w, int i) {
   }
 }
 
+constexpr int kCopyWarps = 4;
+
 template <int TYPE_, int D_, int MT_>
 struct RowsShape {
   static constexpr int TYPE = TYPE_, D = D_, MT = MT_;  // cache type, head size (at most), blocks of 16 rows
   static constexpr bool kEight = TYPE != SPEC_CACHE_BF16;
   static constexpr int kRows = 16 * MT;
-  static constexpr int kWarps = D > 128 ? 4 : 8;
-  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kWarps = D > 128 ? 4 : 8;  // that compute
+  static constexpr int kThreads = 32 * (kWarps + kCopyWarps);
+  // Registers a thread, and what a launch must bring (0: they are not shared out).
+  static constexpr int kRegsRows = kWarps == 8 ? 208 : 0, kRegsCopy = kWarps == 8 ? 88 : 0;
+  static constexpr int kRegs = kWarps / 4 * kRegsRows + kRegsCopy;
   static constexpr int kRowBytes = D * (kEight ? 1 : 2);
   static constexpr int kPitch = kRowBytes + 16;  // rows on other banks each
-  static constexpr int kTokens = kRowBytes >= 256 && !kEight ? 16 : 32;  // tokens of a warp's step
-  static constexpr int kSub = MT == 1 ? kTokens : 16;         // of them, scores held at a time
+  static constexpr int kTokens = (kEight ? MT > 1 : kRowBytes >= 256) ? 16 : 32;  // tokens of a warp's step
+  static constexpr int kSub = MT == 1 ? kTokens : 16;                             // of them, scores held at a time
   static constexpr int kTile = kTokens * kWarps;
   static constexpr int kStage = 2 * kTokens * kPitch + (kEight ? 2 * kTokens * 4 : 0);
-  static constexpr int kFit = static_cast<int>(kRowsRing) / kWarps / kStage;
+  // With 32 rows q is read from shared memory for each product (registers are short).
+  static constexpr int kFragments = MT > 1 ? MT * (D / 16) * 32 : 0;
+  static constexpr int kRing = (MT == 1 ? 222 : D > 64 ? 214 : 218) * 1024;  // shared memory of all rings
+  static constexpr int kFit = kRing / kWarps / kStage;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static constexpr int kOutPitch = D + 4;  // floats of a row of sums
+  static constexpr int kOutCols = 16 * (D + 4) * 4 <= kStage ? D : D / 2;  // columns of sums joined at a time
+  static constexpr int kOutPitch = kOutCols + 4;
+  static constexpr int kExtra = 1;  // an item's beginning and end, in units
   static_assert(kStages >= 3, "the ring has three places at least");
   static_assert(16 * kOutPitch * 4 <= kStage, "16 rows of sums fit a place of the ring");
+  using Plan = Schedule<kRows, kTile, kExtra>;
 };
 
 template <typename S>
 struct RowsSmem {
   uint8_t ring[S::kWarps][S::kStages][S::kStage];
+  uint4 q[S::kFragments + 1];
   float top[S::kWarps][S::kRows], sum[S::kWarps][S::kRows];
-  typename Schedule<S::kRows, S::kTile>::Shared plan;
+  typename S::Plan::Shared plan;
+  uint64_t full[S::kWarps][S::kStages], empty[S::kWarps][S::kStages];
+  int abort;
 };
 
 constexpr float kLn2 = 0.693147180559945f;
 
 template <typename S>
-__global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const AttendParams p) {
-  using Plan = Schedule<S::kRows, S::kTile>;
+__global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const AttendParams p, const int test_withhold) {
+  using Plan = typename S::Plan;
   constexpr int TYPE = S::TYPE, D = S::D, MT = S::MT, kTokens = S::kTokens, kSub = S::kSub, kStages = S::kStages;
   constexpr bool kEight = S::kEight;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -134,99 +154,142 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
   const CacheParams& c = p.c;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  if (threadIdx.x < S::kWarps * kStages) {
+    // (a full place: each copying thread's copies and, with 8 bits, its warp's exponents)
+    mbar_init(&sm.full[0][0] + threadIdx.x, kEight ? 33 : 32);
+    mbar_init(&sm.empty[0][0] + threadIdx.x, 1);
+  }
+  if (threadIdx.x == 0) sm.abort = 0;
+  fence_mbar_init();
   griddep_wait();
   griddep_launch_dependents();
-  Plan::plan(p, sm.plan);
+  Plan::plan(p, sm.plan);  // (its barriers publish the above)
   if (blockIdx.x == 0)  // lanes laid out wrongly have no units
     for (int b = threadIdx.x; b < c.lanes; b += S::kThreads) {
       int first, count, before;
       if (!cache_lane(c, b, first, count, before)) lane_failed(c, b, SPEC_ERR_LAYOUT);
     }
   const int64_t begin = sm.plan.begin, end = sm.plan.end;
-  PartRecord record = {0, 0, 0, 0};
 
-  if (begin < end) {
-    Cursor ld = sm.plan.from, at = ld;
-    int64_t to_load = end - begin;
-    uint8_t(&ring)[kStages][S::kStage] = sm.ring[warp];
-    const uint32_t ring_at = smem_addr(&ring[0][0]);
+  if (warp >= S::kWarps) {
+    // ------------------------------------------------------------------ copies
+    if constexpr (S::kRegsCopy > 0) registers_shrink<S::kRegsCopy>();
+    constexpr int kUnits = S::kRowBytes / 16, kAtOnce = 32 / kUnits;  // 16-byte units of a token; tokens of an access
+    constexpr int kMine = S::kWarps / kCopyWarps;                     // computing warps of this one
+    const int unit = lane % kUnits, sub = lane / kUnits, first_warp = warp - S::kWarps;
+    const bool in_head = unit * 16 < c.dim * (kEight ? 1 : 2);
+    const uint32_t by = 1u << c.unit_shift;
+    const uint8_t* const k_base = c.k + unit * 16;
+    const uint8_t* const v_base = c.v + unit * 16;
+    Cursor ld = sm.plan.from;
+    int64_t left = begin < end ? end - begin : 0;
+    int id[kMine];  // of each warp's step: the page of this lane's token
+    auto look_up = [&] {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int pos = ld.tile * S::kTile + (first_warp + i * kCopyWarps) * kTokens + lane;
+        id[i] = -1;
+        if (left > 0 && lane < kTokens && pos >= ld.lo && pos < ld.hi) {
+          id[i] = __ldg(c.tables + ld.b * c.table_stride + page_of(c, pos));
+          if (static_cast<uint32_t>(id[i]) >= static_cast<uint32_t>(c.pages)) id[i] = -2;
+        }
+      }
+    };
+    // Exponents come by plain loads, which are put into their place a step later.
     uint32_t pend_k = 127u, pend_v = 127u;
-    int pend_stage = -1;
-
-    // Exponents come by plain loads, which the next call puts into their stage.
+    int pend_warp = -1, pend_stage = 0;
     auto settle = [&] {
-      if constexpr (kEight) {
-        if (pend_stage >= 0 && lane < kTokens) {
-          float* const f = reinterpret_cast<float*>(&ring[pend_stage][2 * kTokens * S::kPitch]);
+      if (kEight && pend_warp >= 0) {
+        if (lane < kTokens) {
+          float* const f = reinterpret_cast<float*>(&sm.ring[pend_warp][pend_stage][2 * kTokens * S::kPitch]);
           const float nan = __uint_as_float(0x7FC00000u);
           f[lane] = pend_k == 255u ? nan : __uint_as_float(pend_k << 23);
           f[kTokens + lane] = pend_v == 255u ? nan : static_cast<float>(static_cast<int>(pend_v) - 127);
         }
-        pend_stage = -1;
+        warp_arrive(&sm.full[pend_warp][pend_stage]);
+        pend_warp = -1;
       }
     };
-    // Copies of this warp's tokens of the unit at `ld` into a place of the ring.
-    auto issue = [&](int stage) {
-      settle();
-      if (to_load > 0) {
-        --to_load;
-        const int p0 = ld.tile * S::kTile + warp * kTokens;
-        if (p0 < ld.hi && p0 + kTokens > ld.lo) {
-          const int pos = p0 + lane % kTokens;
-          bool ok = pos >= ld.lo && pos < ld.hi;
-          int64_t from = -1;
-          pend_k = pend_v = 127u;
-          if (ok) {
-            const int page = page_of(c, pos);
-            const int id = __ldg(c.tables + ld.b * c.table_stride + page), in = pos - page * c.page_size;
-            if (static_cast<uint32_t>(id) < static_cast<uint32_t>(c.pages)) {
-              from = id * c.page + in * c.slot + ld.h * c.head;
-              if constexpr (kEight) {
-                const int64_t e = id * c.exp_page + in * c.exp_slot + ld.h * c.exp_head;
-                pend_k = c.k_exps[e];
-                pend_v = c.v_exps[e];
-              }
-            } else {
-              lane_failed(c, ld.b, SPEC_ERR_LAYOUT);
-            }
-          }
-          pend_stage = stage;
-          constexpr int kUnits = S::kRowBytes / 16;  // 16-byte units of a token
-          const int used = c.dim * (kEight ? 1 : 2) / 16;
-          const uint32_t dst = ring_at + stage * S::kStage;
+    int stage[kMine] = {}, round[kMine] = {};  // of each warp's ring
+    bool ok = true;
+    look_up();
+#pragma unroll 1
+    while (ok && left > 0) {
+      Cursor now = ld;
+      int page_id[kMine];
 #pragma unroll
-          for (int i = 0; i < kTokens * kUnits / 32; ++i) {
-            const int x = i * 32 + lane, tok = x / kUnits, u = x % kUnits;
-            const int64_t f = __shfl_sync(0xFFFFFFFFu, from, tok);
-            const bool on = f >= 0 && u < used;
-            const int64_t off = on ? f + u * 16 : 0;
-            cp_async16_or_zero(dst + tok * S::kPitch + u * 16, c.k + off, on);
-            cp_async16_or_zero(dst + (kTokens + tok) * S::kPitch + u * 16, c.v + off, on);
+      for (int i = 0; i < kMine; ++i) page_id[i] = id[i];
+      --left;
+      if (left > 0) Plan::next_unit(p, ld);
+      look_up();  // of the next unit, which takes its time
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int w = first_warp + i * kCopyWarps, p0 = now.tile * S::kTile + w * kTokens;
+        const bool seen_some = p0 < now.hi && p0 + kTokens > now.lo;  // (if not, a place goes by empty)
+        if (!ok) continue;
+        if (round[i] > 0 && !(ok = warp_wait(&sm.empty[w][stage[i]], (round[i] - 1) & 1, &sm.abort))) continue;
+        uint32_t at = kNowhere, ek = 127u, ev = 127u;
+        if (page_id[i] == -2) lane_failed(c, now.b, SPEC_ERR_LAYOUT);
+        if (page_id[i] >= 0) {
+          const int pos = p0 + lane, in = pos - page_of(c, pos) * c.page_size;
+          at = head_at(c, page_id[i], in, now.h);
+          if constexpr (kEight) {
+            const int64_t e = page_id[i] * c.exp_page + in * c.exp_slot + now.h * c.exp_head;
+            ek = c.k_exps[e];
+            ev = c.v_exps[e];
           }
         }
-        Plan::next_unit(p, ld);
+        const uint32_t to = smem_addr(&sm.ring[w][stage[i]][sub * S::kPitch + unit * 16]);
+#pragma unroll
+        for (int j = 0; j < kTokens / kAtOnce && seen_some; ++j) {
+          const uint32_t from = __shfl_sync(0xFFFFFFFFu, at, j * kAtOnce + sub);
+          const bool on = from != kNowhere && in_head;
+          const uint64_t off = on ? static_cast<uint64_t>(from) * by : 0;
+          if (!(test_withhold != 0 && begin == 0 && w == 0 && j == 0)) {
+            cp_async16_or_zero(to + j * kAtOnce * S::kPitch, k_base + off, on);
+            cp_async16_or_zero(to + (kTokens + j * kAtOnce) * S::kPitch, v_base + off, on);
+          }
+        }
+        if (!(test_withhold != 0 && begin == 0 && w == 0)) cp_async_arrive(&sm.full[w][stage[i]]);
+        // (The step before: no warp waits for it to free a place, as rings have three.)
+        settle();
+        pend_k = ek;
+        pend_v = ev;
+        pend_warp = w;
+        pend_stage = stage[i];
+        if (++stage[i] == kStages) {
+          stage[i] = 0;
+          ++round[i];
+        }
       }
-      cp_async_commit();
-    };
-#pragma unroll 1
-    for (int s = 0; s < kStages - 1; ++s) issue(s);
-
-    uint32_t qf[MT][D / 16][4];
+    }
+    settle();
+    asm volatile("cp.async.wait_all;" ::: "memory");  // copies end before the thread does
+  } else if (begin < end) {
+    // ------------------------------------------------------- scores and outputs
+    if constexpr (S::kRegsRows > 0) registers_grow<S::kRegsRows>();
+    Cursor at = sm.plan.from;
+    bool dead = false;  // a wait gave up: the warp only goes along to the barriers
+    uint8_t(&ring)[kStages][S::kStage] = sm.ring[warp];
+    const uint32_t ring_at = smem_addr(&ring[0][0]);
+    auto all_rows = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * S::kWarps) : "memory"); };
+    uint32_t qf[MT == 1 ? D / 16 : 1][4];
     float o[MT][D / 8][4];
     float top[MT][2], sum[MT][2], qs[MT][2];
     int last[MT][2];  // one past the last position that a row sees
-    bool fresh = true;
-    int stage = 0;
+    bool fresh = true, started = false;
+    int stage = 0, phase = 0;  // of the ring
 #pragma unroll 1
     for (int64_t u = begin; u < end; ++u) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      issue(stage == 0 ? kStages - 1 : stage - 1);
+      const int p0 = at.tile * S::kTile + warp * kTokens;
+      const bool seen_some = p0 < at.hi && p0 + kTokens > at.lo;
       if (fresh) {
         // q as left operands: of each 16 components a thread has four of rows g and g + 8.
         fresh = false;
+        started = at.tile == at.t0;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
+          uint32_t f[D / 16][4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int r = at.k * S::kRows + m * 16 + g + 8 * i, col = r / p.group;
@@ -241,8 +304,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
               // (8 bits: components 16 (t + 4 (s / 4)) + 4 (s % 4) + 0..3)
               const int d = kEight ? 16 * (t + 4 * (s / 4)) + 4 * (s % 4) : 16 * s + 2 * t;
               const int d2 = kEight ? d + 2 : d + 8;
-              qf[m][s][i] = on && d < c.dim ? __ldg(reinterpret_cast<const uint32_t*>(from + d)) : 0u;
-              qf[m][s][i + 2] = on && d2 < c.dim ? __ldg(reinterpret_cast<const uint32_t*>(from + d2)) : 0u;
+              f[s][i] = on && d < c.dim ? __ldg(reinterpret_cast<const uint32_t*>(from + d)) : 0u;
+              f[s][i + 2] = on && d2 < c.dim ? __ldg(reinterpret_cast<const uint32_t*>(from + d2)) : 0u;
             }
           }
           if constexpr (kEight) {
@@ -251,20 +314,28 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
               uint32_t most = 0;
 #pragma unroll
               for (int s = 0; s < D / 16; ++s) {
-                most = max(most, max(qf[m][s][i] & 0x7FFFu, (qf[m][s][i] >> 16) & 0x7FFFu));
-                most = max(most, max(qf[m][s][i + 2] & 0x7FFFu, (qf[m][s][i + 2] >> 16) & 0x7FFFu));
+                most = max(most, max(f[s][i] & 0x7FFFu, (f[s][i] >> 16) & 0x7FFFu));
+                most = max(most, max(f[s][i + 2] & 0x7FFFu, (f[s][i + 2] >> 16) & 0x7FFFu));
               }
               most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
               most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
               // The largest comes to lie in 2^14 .. 2^15.  (Rows of tiny numbers are left smaller.)
               const int up = min(127 + 14 - static_cast<int>(most >> 7), 126);
-              const float f = __uint_as_float(static_cast<uint32_t>(127 + max(up, -126)) << 23);
-              qs[m][i] = p.scale / f;
+              const float by = __uint_as_float(static_cast<uint32_t>(127 + max(up, -126)) << 23);
+              qs[m][i] = p.scale / by;
 #pragma unroll
               for (int s = 0; s < D / 16; ++s)
 #pragma unroll
-                for (int j = i; j < 4; j += 2)
-                  qf[m][s][j] = to_halfx2(bf16_lo(qf[m][s][j]) * f, bf16_hi(qf[m][s][j]) * f);
+                for (int j = i; j < 4; j += 2) f[s][j] = to_halfx2(bf16_lo(f[s][j]) * by, bf16_hi(f[s][j]) * by);
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            if constexpr (MT == 1) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) qf[s][j] = f[s][j];
+            } else if (s % S::kWarps == warp) {  // (all warps have the same)
+              sm.q[(m * (D / 16) + s) * 32 + lane] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
             }
           }
 #pragma unroll
@@ -272,10 +343,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[m][n][i] = 0.f;
         }
+        if constexpr (MT > 1) all_rows();
       }
-      const int p0 = at.tile * S::kTile + warp * kTokens;
+      if (!dead) dead = !warp_wait(&sm.full[warp][stage], phase, &sm.abort);
       const uint32_t ks = ring_at + stage * S::kStage, vs = ks + kTokens * S::kPitch;
-      if (p0 < at.hi && p0 + kTokens > at.lo) {
+      if (seen_some && !dead) {
         const int seen_first = at.before + at.k * S::kRows / p.group;  // the block's first column's position
         const bool whole = p0 + kTokens <= seen_first + 1 && (p.window == 0 || p0 > at.hi - 1 - p.window);
 #pragma unroll
@@ -287,39 +359,59 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
             for (int n = 0; n < kSub / 8; ++n)
 #pragma unroll
               for (int i = 0; i < 4; ++i) x[m][n][i] = 0.f;
+          auto q_of = [&](int m, int s, uint32_t (&a)[4]) {
+            if constexpr (MT == 1) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) a[j] = qf[s][j];
+            } else {
+              const uint4 v = sm.q[(m * (D / 16) + s) * 32 + lane];
+              a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
+            }
+          };
           if constexpr (!kEight) {
             const uint32_t base = ks + (half * kSub + (lane >> 4) * 8 + (lane & 7)) * S::kPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
+            for (int s = 0; s < D / 16; ++s) {
+              uint32_t a[MT][4];
+#pragma unroll
+              for (int m = 0; m < MT; ++m) q_of(m, s, a[m]);
 #pragma unroll
               for (int n = 0; n < kSub / 16; ++n) {
                 uint32_t b[4];
                 ldmatrix_x4(b, base + n * 16 * S::kPitch + s * 32);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                  mma_16816<false>(x[m][2 * n], qf[m][s], b[0], b[1]);
-                  mma_16816<false>(x[m][2 * n + 1], qf[m][s], b[2], b[3]);
+                  mma_16816<false>(x[m][2 * n], a[m], b[0], b[1]);
+                  mma_16816<false>(x[m][2 * n + 1], a[m], b[2], b[3]);
                 }
               }
+            }
           } else {
 #pragma unroll
-            for (int n = 0; n < kSub / 8; ++n)
+            for (int i = 0; i < D / 64; ++i) {
+              uint4 w[kSub / 8];
 #pragma unroll
-              for (int i = 0; i < D / 64; ++i) {
-                uint4 w;
+              for (int n = 0; n < kSub / 8; ++n) {
                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                             : "=r"(w[n].x), "=r"(w[n].y), "=r"(w[n].z), "=r"(w[n].w)
                              : "r"(ks + (half * kSub + n * 8 + g) * S::kPitch + (t + 4 * i) * 16)
                              : "memory");
-                uint32_t* const ws = &w.x;
+              }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  if constexpr (TYPE == SPEC_CACHE_INT8) ws[j] ^= 0x80808080u;
-                  const uint32_t b0 = eight_to_half2<TYPE>(ws[j], 0), b1 = eight_to_half2<TYPE>(ws[j], 1);
+              for (int j = 0; j < 4; ++j) {
+                uint32_t a[MT][4];
 #pragma unroll
-                  for (int m = 0; m < MT; ++m) mma_16816<true>(x[m][n], qf[m][4 * i + j], b0, b1);
+                for (int m = 0; m < MT; ++m) q_of(m, 4 * i + j, a[m]);
+#pragma unroll
+                for (int n = 0; n < kSub / 8; ++n) {
+                  uint32_t v = (&w[n].x)[j];
+                  if constexpr (TYPE == SPEC_CACHE_INT8) v ^= 0x80808080u;
+                  const uint32_t b0 = eight_to_half2<TYPE>(v, 0), b1 = eight_to_half2<TYPE>(v, 1);
+#pragma unroll
+                  for (int m = 0; m < MT; ++m) mma_16816<true>(x[m][n], a[m], b0, b1);
                 }
               }
+            }
           }
           // Scores in powers of two (8 bits: with the value's exponent), hidden ones -inf.
           const float* const exps = reinterpret_cast<const float*>(&ring[stage][2 * kTokens * S::kPitch]) + half * kSub + 2 * t;
@@ -454,7 +546,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
       if (at.tile + 1 == at.t1 || u + 1 == end) {
         // The item ends here, or goes on in the next thread block: the warps' sums are joined, 16
         // rows at a time, in the places of the ring that the warps have just read.
-        const bool started = u - (at.tile - at.t0) >= begin, ends = at.tile + 1 == at.t1;
+        const bool ends = at.tile + 1 == at.t1;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -467,85 +559,104 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
               sm.sum[warp][m * 16 + g + 8 * i] = s;
             }
           }
-        __syncthreads();
+        all_rows();
         float* const part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (started ? 1 : 0)) * part_floats(S::kRows, D);
+        constexpr int kCols = S::kOutCols;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          float* const mine = reinterpret_cast<float*>(&ring[stage][0]);
+          float factor[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int r = m * 16 + g + 8 * i;
             float most = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) most = fmaxf(most, sm.top[w][r]);
-            const float f = top[m][i] == -INFINITY ? 0.f : ex2_approx(top[m][i] - most);
-            float* const to = mine + (g + 8 * i) * S::kOutPitch;
-            if constexpr (!kEight) {
-#pragma unroll
-              for (int n = 0; n < D / 8; ++n)
-                *reinterpret_cast<float2*>(to + n * 8 + 2 * t) = make_float2(o[m][n][2 * i] * f, o[m][n][2 * i + 1] * f);
-            } else {
-              constexpr int kBytes = D >= 128 ? 16 : 8;
-#pragma unroll
-              for (int n = 0; n < D / 8; n += 4)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  *reinterpret_cast<float4*>(to + (2 * t + e + 8 * (n / kBytes)) * kBytes + n % kBytes) =
-                      make_float4(o[m][n][2 * i + e] * f, o[m][n + 1][2 * i + e] * f, o[m][n + 2][2 * i + e] * f,
-                                  o[m][n + 3][2 * i + e] * f);
-            }
+            for (int w = 0; w < S::kWarps; ++w) most = fmaxf(most, sm.top[w][m * 16 + g + 8 * i]);
+            factor[i] = top[m][i] == -INFINITY ? 0.f : ex2_approx(top[m][i] - most);
           }
-          __syncthreads();
+#pragma unroll
+          for (int d0 = 0; d0 < D; d0 += kCols) {
+            // (8 bits: a thread's numbers of n = 0, 8, .. go to components all over the head: those of
+            // a half are the ones whose place in it is even or odd, n % 8 below 4 or not)
+            float* const mine = reinterpret_cast<float*>(&ring[stage][0]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float* const to = mine + (g + 8 * i) * S::kOutPitch;
+              const float f = factor[i];
+              if constexpr (!kEight) {
+#pragma unroll
+                for (int n = d0 / 8; n < (d0 + kCols) / 8; ++n)
+                  *reinterpret_cast<float2*>(to + n * 8 - d0 + 2 * t) = make_float2(o[m][n][2 * i] * f, o[m][n][2 * i + 1] * f);
+              } else {
+                constexpr int kBytes = D >= 128 ? 16 : 8;
+#pragma unroll
+                for (int n = 0; n < D / 8; n += 4)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    // Components 4 y .. 4 y + 3 of the head; a half takes every other four.
+                    const int y = (2 * t + e + 8 * (n / kBytes)) * (kBytes / 4) + n % kBytes / 4;
+                    if (kCols == D || (n / 4) % 2 == d0 / kCols)
+                      *reinterpret_cast<float4*>(to + (kCols == D ? y : y / 2) * 4) =
+                          make_float4(o[m][n][2 * i + e] * f, o[m][n + 1][2 * i + e] * f, o[m][n + 2][2 * i + e] * f,
+                                      o[m][n + 3][2 * i + e] * f);
+                  }
+              }
+            }
+            all_rows();
 #pragma unroll 1
-          for (int x = threadIdx.x; x < 16 * (D / 4); x += S::kThreads) {
-            const int r = x / (D / 4), d = x % (D / 4) * 4;
-            float most = -INFINITY, total = 0.f;
+            for (int x = threadIdx.x; x < 16 * (kCols / 4); x += 32 * S::kWarps) {
+              const int r = x / (kCols / 4), y = x % (kCols / 4);
+              const int d = kCols == D ? y * 4 : kEight ? (2 * y + d0 / kCols) * 4 : d0 + y * 4;
+              float most = -INFINITY, total = 0.f;
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) most = fmaxf(most, sm.top[w][m * 16 + r]);
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int w = 0; w < S::kWarps; ++w) most = fmaxf(most, sm.top[w][m * 16 + r]);
+              float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) {
-              const float mw = sm.top[w][m * 16 + r];
-              total += mw == -INFINITY ? 0.f : sm.sum[w][m * 16 + r] * ex2_approx(mw - most);
-              const float4 b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(&sm.ring[w][stage][0]) +
-                                                                r * S::kOutPitch + d);
-              a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
-            }
-            if (started && ends) {
-              const int row = at.k * S::kRows + m * 16 + r, col = row / p.group, head = at.h * p.group + row - col * p.group;
-              if (col < at.count && d < c.dim) {
-                const float inv = 1.f / total;
-                a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
-                *reinterpret_cast<uint2*>(p.out + (at.first + col) * p.out_row + head * p.out_head + d) =
-                    make_uint2(to_bf16x2(a.x, a.y), to_bf16x2(a.z, a.w));
-                if (!finite4(a)) lane_failed(c, at.b, SPEC_ERR_NONFINITE);
-                if (p.lse != nullptr && d == 0)
-                  p.lse[(at.first + col) * p.lse_row + head] = (most + log2f(total)) * kLn2;
+              for (int w = 0; w < S::kWarps; ++w) {
+                const float mw = sm.top[w][m * 16 + r];
+                total += mw == -INFINITY ? 0.f : sm.sum[w][m * 16 + r] * ex2_approx(mw - most);
+                const float4 b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(&sm.ring[w][stage][0]) +
+                                                                  r * S::kOutPitch + y * 4);
+                a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
               }
-            } else {
-              *reinterpret_cast<float4*>(part + (m * 16 + r) * D + d) = a;
-              if (d == 0) {
-                part[S::kRows * D + 2 * (m * 16 + r)] = most;
-                part[S::kRows * D + 2 * (m * 16 + r) + 1] = total;
+              if (started && ends) {
+                const int row = at.k * S::kRows + m * 16 + r, col = row / p.group, head = at.h * p.group + row - col * p.group;
+                if (col < at.count && d < c.dim) {
+                  const float inv = 1.f / total;
+                  a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
+                  *reinterpret_cast<uint2*>(p.out + (at.first + col) * p.out_row + head * p.out_head + d) =
+                      make_uint2(to_bf16x2(a.x, a.y), to_bf16x2(a.z, a.w));
+                  if (!finite4(a)) lane_failed(c, at.b, SPEC_ERR_NONFINITE);
+                  if (p.lse != nullptr && d == 0)
+                    p.lse[(at.first + col) * p.lse_row + head] = (most + log2f(total)) * kLn2;
+                }
+              } else {
+                *reinterpret_cast<float4*>(part + (m * 16 + r) * D + d) = a;
+                if (d == 0) {
+                  part[S::kRows * D + 2 * (m * 16 + r)] = most;
+                  part[S::kRows * D + 2 * (m * 16 + r) + 1] = total;
+                }
               }
             }
+            all_rows();
           }
-          __syncthreads();
         }
         fresh = true;
-        if (started && !ends) {
-          record.lane = at.b;
-          record.head = at.h;
-          record.block = at.k;
-          record.parts = Plan::block_of(u + (at.t1 - at.tile) - 1, sm.plan.total) - static_cast<int>(blockIdx.x) + 1;
-        }
       }
       Plan::next_unit(p, at);
-      if (++stage == kStages) stage = 0;
+      warp_arrive(&sm.empty[warp][stage]);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
-    cp_async_wait<0>();
   }
-  if (p.parts != nullptr && threadIdx.x == 0) p.records[blockIdx.x] = record;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (p.parts != nullptr) p.records[blockIdx.x] = sm.plan.record;
+    if (sm.abort && c.status != nullptr) {  // a wait gave up: all lanes of the block's range
+      Cursor x = sm.plan.from;
+      for (int64_t u = begin; u < end; ++u, Plan::next_unit(p, x)) c.status[x.b] = SPEC_ERR_TIMEOUT;
+    }
+  }
 }
 
 // Joins the parts of items that were split.  blockIdx.x: the thread block that an item begins in;

@@ -2,12 +2,13 @@
 //
 // The query heads of one cache head and a lane's columns make up its rows: row r is column
 // r / group, query head r % group of the group.  An item is a block of rows of a lane and cache
-// head, a unit an item's step over a tile of positions.  All units stand in one order (lanes, heads, row blocks,
-// tiles), and thread block c of g takes units total * c / g up to total * (c + 1) / g: every one has the
-// same work to within a unit (and, of few units, one), however ragged the lanes are.  An item whose
-// units fall to several blocks leaves partial sums, which a second launch joins; without scratch memory for
-// them the borders move up to the next item.  Lanes' lengths are read on the device, so
-// that a captured launch serves every round.
+// head, a unit an item's step over a tile of positions.  All units stand in one order (lanes, heads,
+// row blocks, tiles); an item costs its units and EXTRA for what it takes to begin and to end it, and thread
+// block c of g takes what lies between total * c / g and total * (c + 1) / g of the costs: all have
+// the same work to within a unit, however ragged the lanes are.  An item whose units
+// fall to several blocks leaves partial sums, which a second launch joins; without scratch
+// memory for them the borders move up to the next item.  Lanes' lengths are read on the device,
+// so that a captured launch serves every round.
 #pragma once
 
 #include <cstdint>
@@ -49,7 +50,13 @@ struct Cursor {
   int tile, t0, t1;          // tiles of positions
 };
 
-template <int ROWS, int TILE>
+// n / d for 0 <= n < 2^62, d > 0; most are small, and take a fraction of the time then.
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  if (static_cast<uint64_t>(n | d) >> 32 == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+  return n / d;
+}
+
+template <int ROWS, int TILE, int EXTRA>
 struct Schedule {
   static __device__ __forceinline__ void set_block(const AttendParams& p, Cursor& x) {
     const int i0 = x.k * ROWS / p.group, i1 = min(x.count - 1, (x.k * ROWS + ROWS - 1) / p.group);
@@ -59,15 +66,13 @@ struct Schedule {
     x.t1 = (x.hi + TILE - 1) / TILE;
     x.tile = x.t0;
   }
-  // The lane at x.b or the first one after it that has work.
-  static __device__ __forceinline__ void set_lane(const AttendParams& p, Cursor& x) {
+  // The lane at x.b, if it has work, at its first item.
+  static __device__ __forceinline__ bool try_lane(const AttendParams& p, Cursor& x) {
+    if (!cache_lane(p.c, x.b, x.first, x.count, x.before) || x.count == 0) return false;
+    x.blocks = (x.count * p.group + ROWS - 1) / ROWS;
     x.h = x.k = 0;
-    for (; x.b < p.c.lanes; ++x.b)
-      if (cache_lane(p.c, x.b, x.first, x.count, x.before) && x.count > 0) {
-        x.blocks = (x.count * p.group + ROWS - 1) / ROWS;
-        set_block(p, x);
-        return;
-      }
+    set_block(p, x);
+    return true;
   }
   static __device__ __forceinline__ void next_item(const AttendParams& p, Cursor& x) {
     if (++x.k < x.blocks) {
@@ -76,14 +81,14 @@ struct Schedule {
       x.k = 0;
       set_block(p, x);
     } else {
-      ++x.b;
-      set_lane(p, x);
+      while (++x.b < p.c.lanes && !try_lane(p, x)) {
+      }
     }
   }
   static __device__ __forceinline__ void next_unit(const AttendParams& p, Cursor& x) {
     if (++x.tile == x.t1) next_item(p, x);
   }
-  // Units of one head of the lane at x (its other fields are set on the way).
+  // Units of one head of the lane at x (whose block moves on the way).
   static __device__ __forceinline__ int64_t head_units(const AttendParams& p, Cursor& x) {
     int64_t n = 0;
     for (x.k = 0; x.k < x.blocks; ++x.k) {
@@ -92,97 +97,127 @@ struct Schedule {
     }
     return n;
   }
-  static __device__ __forceinline__ int64_t lane_units(const AttendParams& p, int b) {
+  // Units and costs of lane b.
+  static __device__ __forceinline__ void lane_sums(const AttendParams& p, int b, int64_t& units, int64_t& cost) {
     Cursor x;
     x.b = b;
-    if (!cache_lane(p.c, b, x.first, x.count, x.before) || x.count == 0) return 0;
-    x.blocks = (x.count * p.group + ROWS - 1) / ROWS;
-    return head_units(p, x) * p.c.kv_heads;
+    units = cost = 0;
+    if (!try_lane(p, x)) return;
+    units = head_units(p, x) * p.c.kv_heads;
+    cost = units + static_cast<int64_t>(EXTRA) * x.blocks * p.c.kv_heads;
   }
 
   struct Shared {
-    int64_t warp_sum[32];
-    int64_t begin, end, total;
-    Cursor from;
+    int64_t units[32], cost[32];
+    int64_t begin, end;  // units of this thread block
+    Cursor from;         // at the first of them
+    PartRecord record;
   };
+
+  // Thread blocks that get work: each a cost of one at least.
+  static __device__ __forceinline__ int64_t blocks_for(int64_t total, int64_t grid) { return total < grid ? total : grid; }
+  // The thread block that a cost falls to.
+  static __device__ __forceinline__ int block_of(int64_t u, int64_t total, int64_t g) {
+    return static_cast<int>(quotient((u + 1) * g - 1, total));
+  }
+
+  // What lies `left` costs behind the beginning of lane b0: the cursor there (in an item's EXTRA: at its
+  // first unit; where items stay whole and one has begun: at the next), and the units
+  // before it.  `in`: costs of the item up to there, `all`: its costs.
+  static __device__ __forceinline__ int64_t find(const AttendParams& p, int b0, int64_t left, Cursor& x, int64_t& in,
+                                                 int64_t& all) {
+    int64_t before = 0;
+    x.b = b0;
+    for (;; ++x.b) {
+      int64_t units, cost;
+      lane_sums(p, x.b, units, cost);
+      if (left < cost) break;
+      left -= cost;
+      before += units;
+    }
+    try_lane(p, x);
+    const int64_t per_units = head_units(p, x), per_cost = per_units + static_cast<int64_t>(EXTRA) * x.blocks;
+    x.h = static_cast<int>(quotient(left, per_cost));
+    left -= x.h * per_cost;
+    before += x.h * per_units;
+    for (x.k = 0;; ++x.k) {
+      set_block(p, x);
+      all = x.t1 - x.t0 + EXTRA;
+      if (left < all) break;
+      left -= all;
+      before += all - EXTRA;
+    }
+    in = left;
+    if (left <= EXTRA) return before;
+    if (p.parts == nullptr) {
+      next_item(p, x);
+      return before + all - EXTRA;
+    }
+    x.tile = x.t0 + static_cast<int>(left - EXTRA);
+    return before + left - EXTRA;
+  }
 
   // The whole thread block: its range of units and the cursor at the first of them.
   static __device__ void plan(const AttendParams& p, Shared& sh) {
     const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.c.lanes + threads - 1) / threads;
     const int b0 = min(p.c.lanes, static_cast<int>(threadIdx.x) * per), b1 = min(p.c.lanes, b0 + per);
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += lane_units(p, b);
-    int64_t run = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t up = __shfl_up_sync(0xFFFFFFFFu, run, d);
-      run += lane >= d ? up : 0;
+    int64_t units = 0, cost = 0;
+    for (int b = b0; b < b1; ++b) {
+      int64_t u, n;
+      lane_sums(p, b, u, n);
+      units += u;
+      cost += n;
     }
-    if (lane == 31) sh.warp_sum[warp] = run;
+    int64_t run_units = units, run_cost = cost;
+    if (warp * 32 * per < p.c.lanes)
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, run_units, d), n = __shfl_up_sync(0xFFFFFFFFu, run_cost, d);
+        run_units += lane >= d ? u : 0;
+        run_cost += lane >= d ? n : 0;
+      }
+    if (lane == 31) {
+      sh.units[warp] = run_units;
+      sh.cost[warp] = run_cost;
+    }
     if (threadIdx.x == 0) {
       sh.begin = sh.end = 0;
-      sh.from.b = p.c.lanes;
+      sh.record.parts = 0;
     }
     __syncthreads();
-    int64_t total = 0, before = run - sum;
+    int64_t total = 0, all_units = 0, before = run_cost - cost, before_units = run_units - units;
     for (int w = 0; w < threads / 32; ++w) {
-      before += w < warp ? sh.warp_sum[w] : 0;
-      total += sh.warp_sum[w];
+      before += w < warp ? sh.cost[w] : 0;
+      before_units += w < warp ? sh.units[w] : 0;
+      total += sh.cost[w];
+      all_units += sh.units[w];
     }
-    if (threadIdx.x == 0) sh.total = total;
     const int64_t g = blocks_for(total, gridDim.x), c = blockIdx.x;
     if (c < g) {
+      const int64_t border[2] = {quotient(total * c, g), quotient(total * (c + 1), g)};
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
-        const int64_t u = total * (c + i) / g;
+        const int64_t u = border[i];
         if (u == total) {
-          if (threadIdx.x == 0) sh.end = total;
-        } else if (u >= before && u < before + sum) {  // the border lies in one of this thread's lanes
+          if (threadIdx.x == 0) sh.end = all_units;
+        } else if (u >= before && u < before + cost) {  // the border lies in one of this thread's lanes
           Cursor x;
-          const int64_t at = u + find(p, b0, u - before, x);
+          int64_t in, all;
+          const int64_t at = before_units + find(p, b0, u - before, x, in, all);
           if (i == 0) {
             sh.begin = at;
             sh.from = x;
           } else {
             sh.end = at;
+            // An item that goes on, and that this block begins.
+            if (p.parts != nullptr && in > EXTRA && border[0] <= u - in + EXTRA)
+              sh.record = {x.b, x.h, x.k, block_of(u - in + all - 1, total, g) - static_cast<int>(c) + 1};
           }
         }
       }
     }
     __syncthreads();
-  }
-  // Unit `left` of those of lanes b0 and after: the cursor there or, where items stay whole,
-  // at the first item that begins there or later; how many units later that is.
-  static __device__ __forceinline__ int64_t find(const AttendParams& p, int b0, int64_t left, Cursor& x) {
-    x.b = b0;
-    set_lane(p, x);
-    for (int64_t n; left >= (n = lane_units(p, x.b));) {
-      left -= n;
-      ++x.b;
-      set_lane(p, x);
-    }
-    const int64_t per_head = head_units(p, x);
-    x.h = static_cast<int>(left / per_head);
-    left -= x.h * per_head;
-    for (x.k = 0;; ++x.k) {
-      set_block(p, x);
-      if (left < x.t1 - x.t0) break;
-      left -= x.t1 - x.t0;
-    }
-    if (p.parts == nullptr && left > 0) {
-      const int64_t later = x.t1 - x.t0 - left;
-      next_item(p, x);
-      return later;
-    }
-    x.tile = x.t0 + static_cast<int>(left);
-    return 0;
-  }
-  // Thread blocks that get units: each at least one.
-  static __device__ __forceinline__ int64_t blocks_for(int64_t total, int64_t grid) { return total < grid ? total : grid; }
-  // The thread block that unit u falls to.
-  static __device__ __forceinline__ int block_of(int64_t u, int64_t total) {
-    return static_cast<int>(((u + 1) * blocks_for(total, gridDim.x) - 1) / total);
   }
 };
 

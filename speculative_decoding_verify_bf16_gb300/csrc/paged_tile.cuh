@@ -48,6 +48,8 @@ struct TileShape {
   static constexpr int kRows = 256, kTile = 128;
   static constexpr int kBytes = kTileHalf * (D / 64);
   static constexpr int kStages = D > 64 ? 5 : 8;
+  static constexpr int kExtra = 2;  // an item's beginning and end, in units
+  using Plan = Schedule<kRows, kTile, kExtra>;
 };
 
 template <typename S>
@@ -55,7 +57,7 @@ struct TileSmem {
   uint8_t q[2][S::kBytes];
   uint8_t ring[S::kStages][S::kBytes];
   float refs[kTileRefs][2][4];  // of a step's keys and values: each 32 positions' exponent
-  typename Schedule<S::kRows, S::kTile>::Shared plan;
+  typename S::Plan::Shared plan;
   uint64_t full[S::kStages], empty[S::kStages];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
   uint32_t tmem;
@@ -74,12 +76,12 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t u) {
 
 template <typename S>
 __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const AttendParams p, const int test_withhold) {
-  using Plan = Schedule<S::kRows, S::kTile>;
+  using Plan = typename S::Plan;
   constexpr int D = S::D, kStages = S::kStages;
   constexpr bool kEight = S::kEight;
   constexpr uint32_t kColS = 0, kColO = 256;  // columns of tensor memory, 128 a tile
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  TileSmem<S>& sm = *reinterpret_cast<TileSmem<S>*>(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];
+  TileSmem<S>& sm = *reinterpret_cast<TileSmem<S>*>(smem_tiles);
   const CacheParams& c = p.c;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -115,7 +117,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
   const int64_t begin = sm.plan.begin, end = sm.plan.end;
   int64_t left = begin < end ? end - begin : 0;
   Cursor at = sm.plan.from;
-  PartRecord record = {0, 0, 0, 0};
 
   if (warp < 8) {
     // ------------------------------------------------------------ rows of a tile
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
     if constexpr (!kEight) {
       constexpr int kLag = 2;  // tiles on their way before the oldest is waited for
       int open = 0, open_slot = 0;
-      bool withheld = test_withhold != 0 && blockIdx.x == 0;
+      bool withheld = test_withhold != 0 && begin == 0;
       auto hand_on = [&] {  // the oldest tile, whose copies have landed
         fence_async_smem();
         if (!withheld) warp_arrive(&sm.full[open_slot]);
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
           *reinterpret_cast<uint4*>(to + swizzled(mine * 32 + tok, unit * 2 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
         }
         fence_async_smem();
-        if (test_withhold == 0 || blockIdx.x != 0 || round > 0 || slot > 0) warp_arrive(&sm.full[slot]);
+        if (test_withhold == 0 || begin != 0 || round > 0 || slot > 0) warp_arrive(&sm.full[slot]);
         advance();
       };
       auto largest = [&](uint32_t byte) { return __reduce_max_sync(0xFFFFFFFFu, byte == 255u ? 0u : byte); };
@@ -520,20 +521,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         if (!ok) break;
         left -= n;
         at.tile += n - 1;
-        const Cursor done = at;
         Plan::next_unit(p, at);
-        if (left == 0 && done.tile + 1 < done.t1 && begin <= end - 1 - (done.tile - done.t0)) {
-          record.lane = done.b;
-          record.head = done.h;
-          record.block = done.k;
-          record.parts = Plan::block_of(end - 1 + (done.t1 - done.tile) - 1, sm.plan.total) - static_cast<int>(blockIdx.x) + 1;
-        }
       }
       // Tensor memory is given back only after the last product.
       mma_commit(lead, &sm.drain);
       mbar_wait_bounded(&sm.drain, 0);
       __syncwarp();
-      if (lane == 0 && p.parts != nullptr) p.records[blockIdx.x] = record;
+      if (lane == 0 && p.parts != nullptr) p.records[blockIdx.x] = sm.plan.record;
     }
   }
   __syncthreads();

@@ -9,7 +9,7 @@ namespace specv {
 
 template <typename S>
 PagedVariant rows_variant() {
-  return {reinterpret_cast<void*>(&paged_rows_kernel<S>), S::kRows, S::D, S::kThreads, static_cast<int>(sizeof(RowsSmem<S>)), 0};
+  return {reinterpret_cast<void*>(&paged_rows_kernel<S>), S::kRows, S::D, S::kThreads, static_cast<int>(sizeof(RowsSmem<S>)), S::kRegs};
 }
 template <typename S>
 PagedVariant tile_variant() {

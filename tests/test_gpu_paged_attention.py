@@ -37,6 +37,15 @@ def test_head_layouts(kind, hq, kv):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [7, 8, 9, 12, 15, 16, 17, 24, 25, 31, 32, 33, 64, 65])
+def test_rows_of_a_head(kind, d, rows):
+    """Every number of rows that a kernel's blocks of 8, 16, 32 and 128 end at or beside."""
+    check([1], [150], hq=rows, kv=1, d=d, kind=kind, seed=rows)
+    check([rows], [40], hq=1, kv=1, d=d, kind=kind, seed=rows + 1)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("page", [1, 3, 16, 24, 100, 128, 1000])
 def test_page_sizes(kind, page):
     check([2, 5, 1], [300, 0, 999], page=page, kind=kind, seed=page)

@@ -1,6 +1,6 @@
-"""The tile kernel's bounded waits: a tile that is never handed on ends in a status, not in a hang.
+"""The attention's bounded waits: a copy that never comes ends in a status, not in a hang.
 
-The withheld tile is a switch of the kernel made for this; nothing faults, and the same
+The withheld copy (tile, in the kernel for many rows) is a switch of the kernels made for this; nothing faults, and the same
 process goes on computing right results afterwards."""
 
 import pytest
@@ -19,8 +19,9 @@ def _built():
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-def test_attention_wait_gives_up(monkeypatch, kind):
-    L = Lanes([300, 300], [9000, 9000], kind=kind, kv=1, seed=1)
+@pytest.mark.parametrize("n", [1, 4, 300])
+def test_attention_wait_gives_up(monkeypatch, kind, n):
+    L = Lanes([n, n], [9000, 9000], kind=kind, kv=1, seed=1)
     q = L.queries(8)
 
     def run():
@@ -33,7 +34,7 @@ def test_attention_wait_gives_up(monkeypatch, kind):
     monkeypatch.setenv("SPEC_PAGED_TEST_WITHHOLD_COPY", "1")
     late = run()
     assert late[2] == [sv.SPEC_ERR_TIMEOUT, 0]
-    assert torch.equal(late[0][300:], good[0][300:]) and torch.equal(late[1][300:], good[1][300:])
+    assert torch.equal(late[0][n:], good[0][n:]) and torch.equal(late[1][n:], good[1][n:])
     monkeypatch.delenv("SPEC_PAGED_TEST_WITHHOLD_COPY")
     again = run()
     assert again[2] == [0, 0] and torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
