@@ -53,6 +53,9 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
 // One arrival (of those that the barrier was set up for) when this thread's copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -102,6 +105,7 @@ __device__ __forceinline__ uint32_t eight_to_half2(uint32_t w, int i) {
 }
 
 constexpr int kCopyWarps = 4;
+constexpr int kUnseen = INT32_MIN;  // in a page's place: no row sees the token
 
 template <int TYPE_, int D_, int MT_>
 struct RowsShape {
@@ -118,10 +122,12 @@ struct RowsShape {
   static constexpr int kTokens = (kEight ? MT > 1 : kRowBytes >= 256) ? 16 : 32;  // tokens of a warp's step
   static constexpr int kSub = MT == 1 ? kTokens : 16;                             // of them, scores held at a time
   static constexpr int kTile = kTokens * kWarps;
-  static constexpr int kStage = 2 * kTokens * kPitch + (kEight ? 2 * kTokens * 4 : 0);
+  // A place: keys, values and, with 8 bits, each token's exponents (words that hold them, and where).
+  static constexpr int kExps = 2 * kTokens * kPitch;
+  static constexpr int kStage = kExps + (kEight ? kTokens * 9 : 0);
   // With 32 rows q is read from shared memory for each product (registers are short).
   static constexpr int kFragments = MT > 1 ? MT * (D / 16) * 32 : 0;
-  static constexpr int kRing = (MT == 1 ? 222 : D > 64 ? 214 : 218) * 1024;  // shared memory of all rings
+  static constexpr int kRing = (MT == 1 ? 223 : D > 64 ? 214 : 218) * 1024;  // shared memory of all rings
   static constexpr int kFit = kRing / kWarps / kStage;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kOutCols = 16 * (D + 4) * 4 <= kStage ? D : D / 2;  // columns of sums joined at a time
@@ -183,63 +189,52 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
     const uint8_t* const v_base = c.v + unit * 16;
     Cursor ld = sm.plan.from;
     int64_t left = begin < end ? end - begin : 0;
-    int id[kMine];  // of each warp's step: the page of this lane's token
-    auto look_up = [&] {
+    // Pages are looked up two units ahead: with the memory busy, a load takes as long as that.
+    Cursor ahead = ld;
+    int64_t left_ahead = left;
+    int id[3][kMine];  // of the unit and the next two: the page of this lane's token, kUnseen: none
+    auto look_up = [&](int (&to)[kMine]) {
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int pos = ld.tile * S::kTile + (first_warp + i * kCopyWarps) * kTokens + lane;
-        id[i] = -1;
-        if (left > 0 && lane < kTokens && pos >= ld.lo && pos < ld.hi) {
-          id[i] = __ldg(c.tables + ld.b * c.table_stride + page_of(c, pos));
-          if (static_cast<uint32_t>(id[i]) >= static_cast<uint32_t>(c.pages)) id[i] = -2;
-        }
+        const int pos = ahead.tile * S::kTile + (first_warp + i * kCopyWarps) * kTokens + lane;
+        if (left_ahead > 0 && lane < kTokens && pos >= ahead.lo && pos < ahead.hi)
+          to[i] = __ldg(c.tables + ahead.b * c.table_stride + page_of(c, pos));
+        else
+          to[i] = kUnseen;
       }
-    };
-    // Exponents come by plain loads, which are put into their place a step later.
-    uint32_t pend_k = 127u, pend_v = 127u;
-    int pend_warp = -1, pend_stage = 0;
-    auto settle = [&] {
-      if (kEight && pend_warp >= 0) {
-        if (lane < kTokens) {
-          float* const f = reinterpret_cast<float*>(&sm.ring[pend_warp][pend_stage][2 * kTokens * S::kPitch]);
-          const float nan = __uint_as_float(0x7FC00000u);
-          f[lane] = pend_k == 255u ? nan : __uint_as_float(pend_k << 23);
-          f[kTokens + lane] = pend_v == 255u ? nan : static_cast<float>(static_cast<int>(pend_v) - 127);
-        }
-        warp_arrive(&sm.full[pend_warp][pend_stage]);
-        pend_warp = -1;
-      }
+      if (--left_ahead > 0) Plan::next_unit(p, ahead);
     };
     int stage[kMine] = {}, round[kMine] = {};  // of each warp's ring
     bool ok = true;
-    look_up();
+    look_up(id[0]);
+    look_up(id[1]);
 #pragma unroll 1
-    while (ok && left > 0) {
-      Cursor now = ld;
-      int page_id[kMine];
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) page_id[i] = id[i];
-      --left;
-      if (left > 0) Plan::next_unit(p, ld);
-      look_up();  // of the next unit, which takes its time
+    for (; ok && left > 0; --left) {
+      look_up(id[2]);
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int w = first_warp + i * kCopyWarps, p0 = now.tile * S::kTile + w * kTokens;
-        const bool seen_some = p0 < now.hi && p0 + kTokens > now.lo;  // (if not, a place goes by empty)
-        if (!ok) continue;
-        if (round[i] > 0 && !(ok = warp_wait(&sm.empty[w][stage[i]], (round[i] - 1) & 1, &sm.abort))) continue;
-        uint32_t at = kNowhere, ek = 127u, ev = 127u;
-        if (page_id[i] == -2) lane_failed(c, now.b, SPEC_ERR_LAYOUT);
-        if (page_id[i] >= 0) {
+        const int w = first_warp + i * kCopyWarps, p0 = ld.tile * S::kTile + w * kTokens;
+        const bool seen_some = p0 < ld.hi && p0 + kTokens > ld.lo;  // (if not, a place goes by empty)
+        if (!ok || (round[i] > 0 && !(ok = warp_wait(&sm.empty[w][stage[i]], (round[i] - 1) & 1, &sm.abort)))) continue;
+        uint8_t* const place = sm.ring[w][stage[i]];
+        const int page = id[0][i];
+        uint32_t at = kNowhere;
+        uint8_t where = 255;  // of the exponents in their words: two bits each
+        if (page != kUnseen && static_cast<uint32_t>(page) >= static_cast<uint32_t>(c.pages)) {
+          lane_failed(c, ld.b, SPEC_ERR_LAYOUT);
+        } else if (page != kUnseen) {
           const int pos = p0 + lane, in = pos - page_of(c, pos) * c.page_size;
-          at = head_at(c, page_id[i], in, now.h);
+          at = head_at(c, page, in, ld.h);
           if constexpr (kEight) {
-            const int64_t e = page_id[i] * c.exp_page + in * c.exp_slot + now.h * c.exp_head;
-            ek = c.k_exps[e];
-            ev = c.v_exps[e];
+            const int64_t e = page * c.exp_page + in * c.exp_slot + ld.h * c.exp_head;
+            const uintptr_t ke = reinterpret_cast<uintptr_t>(c.k_exps + e), ve = reinterpret_cast<uintptr_t>(c.v_exps + e);
+            cp_async4(place + S::kExps + lane * 4, reinterpret_cast<const void*>(ke & ~uintptr_t{3}));
+            cp_async4(place + S::kExps + (kTokens + lane) * 4, reinterpret_cast<const void*>(ve & ~uintptr_t{3}));
+            where = static_cast<uint8_t>((ke & 3) | (ve & 3) << 2);
           }
         }
-        const uint32_t to = smem_addr(&sm.ring[w][stage[i]][sub * S::kPitch + unit * 16]);
+        if (kEight && lane < kTokens) place[S::kExps + kTokens * 8 + lane] = where;
+        const uint32_t to = smem_addr(place + sub * S::kPitch + unit * 16);
 #pragma unroll
         for (int j = 0; j < kTokens / kAtOnce && seen_some; ++j) {
           const uint32_t from = __shfl_sync(0xFFFFFFFFu, at, j * kAtOnce + sub);
@@ -251,19 +246,16 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
           }
         }
         if (!(test_withhold != 0 && begin == 0 && w == 0)) cp_async_arrive(&sm.full[w][stage[i]]);
-        // (The step before: no warp waits for it to free a place, as rings have three.)
-        settle();
-        pend_k = ek;
-        pend_v = ev;
-        pend_warp = w;
-        pend_stage = stage[i];
+        if constexpr (kEight) warp_arrive(&sm.full[w][stage[i]]);
         if (++stage[i] == kStages) {
           stage[i] = 0;
           ++round[i];
         }
+        id[0][i] = id[1][i];
+        id[1][i] = id[2][i];
       }
+      if (left > 1) Plan::next_unit(p, ld);
     }
-    settle();
     asm volatile("cp.async.wait_all;" ::: "memory");  // copies end before the thread does
   } else if (begin < end) {
     // ------------------------------------------------------- scores and outputs
@@ -347,6 +339,18 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
       }
       if (!dead) dead = !warp_wait(&sm.full[warp][stage], phase, &sm.abort);
       const uint32_t ks = ring_at + stage * S::kStage, vs = ks + kTokens * S::kPitch;
+      if constexpr (kEight) {
+        // Each lane takes a token's exponents out of their words: 2^e of the key, e of the value.
+        if (lane < kTokens && seen_some && !dead) {
+          uint32_t* const f = reinterpret_cast<uint32_t*>(&ring[stage][S::kExps]);
+          const uint32_t where = ring[stage][S::kExps + kTokens * 8 + lane];
+          const uint32_t kb = where == 255u ? 127u : (f[lane] >> (where & 3) * 8) & 255u;
+          const uint32_t vb = where == 255u ? 127u : (f[kTokens + lane] >> (where >> 2) * 8) & 255u;
+          f[lane] = kb == 255u ? 0x7FC00000u : kb << 23;
+          f[kTokens + lane] = vb == 255u ? 0x7FC00000u : __float_as_uint(static_cast<float>(static_cast<int>(vb) - 127));
+        }
+        __syncwarp();
+      }
       if (seen_some && !dead) {
         const int seen_first = at.before + at.k * S::kRows / p.group;  // the block's first column's position
         const bool whole = p0 + kTokens <= seen_first + 1 && (p.window == 0 || p0 > at.hi - 1 - p.window);
@@ -414,7 +418,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
             }
           }
           // Scores in powers of two (8 bits: with the value's exponent), hidden ones -inf.
-          const float* const exps = reinterpret_cast<const float*>(&ring[stage][2 * kTokens * S::kPitch]) + half * kSub + 2 * t;
+          const float* const exps = reinterpret_cast<const float*>(&ring[stage][S::kExps]) + half * kSub + 2 * t;
 #pragma unroll
           for (int n = 0; n < kSub / 8; ++n) {
             float2 kf, ve;

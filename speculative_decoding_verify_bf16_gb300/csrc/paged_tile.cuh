@@ -312,20 +312,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
     const int mine = warp - 8, used = c.dim * (kEight ? 1 : 2) / 16;
     const int unit = lane % kUnits, sub = lane / kUnits;
     const bool in_head = unit < used;
-    // Where this lane's position of the step at the cursor lies (-1: not seen), and its exponents.
-    int64_t from = -1;
-    uint32_t ek = 0, ev = 0;
+    // Where this lane's position lies is looked up ahead: its page two units (`ahead`), the place of its
+    // head and its exponents one unit before they are used.
+    Cursor ahead = at;
+    int64_t left_ahead = left;
+    int page = kUnseen, next_page = kUnseen;
+    uint32_t from = kNowhere, ek = 0, ev = 0;
     auto look_up = [&] {
-      const int pos = at.tile * S::kTile + mine * 32 + lane;
-      from = -1;
+      const int pos = ahead.tile * S::kTile + mine * 32 + lane;
+      next_page = kUnseen;
+      if (left_ahead > 0 && pos >= ahead.lo && pos < ahead.hi)
+        next_page = __ldg(c.tables + ahead.b * c.table_stride + page_of(c, pos));
+      if (--left_ahead > 0) Plan::next_unit(p, ahead);
+    };
+    // For the unit at the cursor, whose page is `page`.
+    auto locate = [&] {
+      from = kNowhere;
       ek = ev = 127 + SPEC_CACHE_LEAST_EXP;
-      if (pos >= at.lo && pos < at.hi) {
-        const int page = page_of(c, pos);
-        const int id = __ldg(c.tables + at.b * c.table_stride + page), in = pos - page * c.page_size;
-        if (static_cast<uint32_t>(id) < static_cast<uint32_t>(c.pages)) {
-          from = id * c.page + in * c.slot + at.h * c.head;
+      if (page != kUnseen) {
+        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(c.pages)) {
+          const int pos = at.tile * S::kTile + mine * 32 + lane, in = pos - page_of(c, pos) * c.page_size;
+          from = head_at(c, page, in, at.h);
           if constexpr (kEight) {
-            const int64_t e = id * c.exp_page + in * c.exp_slot + at.h * c.exp_head;
+            const int64_t e = page * c.exp_page + in * c.exp_slot + at.h * c.exp_head;
             ek = c.k_exps[e];
             ev = c.v_exps[e];
           }
@@ -334,6 +343,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         }
       }
     };
+    const uint32_t by = 1u << c.unit_shift;
+    look_up();
+    page = next_page;
+    look_up();
     int slot = 0, round = 0;
     bool ok = true;
     auto advance = [&] {
@@ -354,7 +367,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         --open;
       };
 #pragma unroll 1
-      for (; ok && left > 0; --left, Plan::next_unit(p, at)) {
+      for (; ok && left > 0; --left) {
+        locate();
+        page = next_page;
         look_up();
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {
@@ -364,13 +379,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
             if (!(ok = warp_wait(&sm.empty[slot], (round - 1) & 1, &sm.abort))) break;
           }
           const uint32_t to = smem_addr(sm.ring[slot]);
-          const uint8_t* const base = v ? c.v : c.k;
+          const uint8_t* const base = (v ? c.v : c.k) + unit * 16;
 #pragma unroll
           for (int i = 0; i < 32 / kAtOnce; ++i) {
             const int tok = i * kAtOnce + sub;
-            const int64_t f = __shfl_sync(0xFFFFFFFFu, from, tok);
-            const bool on = f >= 0 && in_head;
-            cp_async16_or_zero(to + swizzled(mine * 32 + tok, unit), base + (on ? f + unit * 16 : 0), on);
+            const uint32_t f = __shfl_sync(0xFFFFFFFFu, from, tok);
+            const bool on = f != kNowhere && in_head;
+            cp_async16_or_zero(to + swizzled(mine * 32 + tok, unit), base + (on ? static_cast<uint64_t>(f) * by : 0), on);
           }
           cp_async_commit();
           ++open;
@@ -380,17 +395,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
           }
           advance();
         }
+        if (left > 1) Plan::next_unit(p, at);
       }
       cp_async_wait<0>();
       while (open > 0) hand_on();
     } else {
       constexpr int kLoads = 32 / kAtOnce;  // of a thread and tile
       uint4 kx[kLoads], vx[kLoads];
-      auto fetch = [&](uint4 (&x)[kLoads], const uint8_t* base) {
+      auto fetch = [&](uint4 (&x)[kLoads], const uint8_t* base, uint32_t here) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          const int64_t f = __shfl_sync(0xFFFFFFFFu, from, i * kAtOnce + sub);
-          x[i] = f >= 0 && in_head ? __ldg(reinterpret_cast<const uint4*>(base + f + unit * 16)) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t f = __shfl_sync(0xFFFFFFFFu, here, i * kAtOnce + sub);
+          x[i] = f != kNowhere && in_head ? __ldg(reinterpret_cast<const uint4*>(base + unit * 16 + static_cast<uint64_t>(f) * by))
+                                          : make_uint4(0u, 0u, 0u, 0u);
         }
       };
       // A tile as fp16 into the ring; `byte`: this lane's position's exponent, `ref` the largest.
@@ -428,28 +445,42 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         advance();
       };
       auto largest = [&](uint32_t byte) { return __reduce_max_sync(0xFFFFFFFFu, byte == 255u ? 0u : byte); };
+      // A unit's places and exponents are found while the one before it is fetched.
+      uint32_t kb = 0, vb = 0, here = 0;
+      auto take = [&] {  // what has been located becomes the unit in hand; the next one is located
+        kb = ek;
+        vb = ev;
+        here = from;
+        if (left > 1) {
+          Plan::next_unit(p, at);
+          page = next_page;
+          locate();
+          look_up();
+        }
+      };
       if (left > 0) {
-        look_up();
-        fetch(kx, c.k);
+        locate();
+        page = next_page;
+        take();
+        fetch(kx, c.k, here);
       }
       int step = 0;
 #pragma unroll 1
       while (ok && left > 0) {
-        fetch(vx, c.v);
-        const uint32_t kb = ek, vb = ev, kr = largest(kb), vr = largest(vb);
+        fetch(vx, c.v, here);
+        const uint32_t k0 = kb, v0 = vb, kr = largest(kb), vr = largest(vb);
         if (lane == 0) {
           sm.refs[step % kTileRefs][0][mine] = __uint_as_float(kr << 23);
           sm.refs[step % kTileRefs][1][mine] = static_cast<float>(static_cast<int>(vr) - 127);
         }
         ++step;
-        store(kx, kb, kr);
+        store(kx, k0, kr);
         if (!ok) break;
-        Plan::next_unit(p, at);
         if (--left > 0) {
-          look_up();
-          fetch(kx, c.k);
+          take();
+          fetch(kx, c.k, here);
         }
-        store(vx, vb, vr);
+        store(vx, v0, vr);
       }
     }
   } else {
