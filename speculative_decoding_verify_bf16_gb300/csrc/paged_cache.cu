@@ -211,7 +211,8 @@ PagedVariant variant_for(spec_cache_type type, int dim, int64_t rows, bool tiles
 }
 
 uint64_t scratch_bytes(const PagedVariant& v, int sms) {
-  return static_cast<uint64_t>(sms) * (2 * specv::part_floats(v.rows, v.size) * sizeof(float) + sizeof(specv::PartRecord));
+  // (workers times the heads that each takes: v.heads)
+  return static_cast<uint64_t>(sms) * (2 * specv::part_floats(v.rows * v.heads, v.size) * sizeof(float) + v.heads * sizeof(specv::PartRecord));
 }
 
 void* join_kernel(int size) {
@@ -276,18 +277,26 @@ int spec_paged_attention(const spec_paged_attention_args* a, void* stream) {
   const PagedVariant v = variant_for(a->cache.type, p.c.dim, rows, p.scale >= 0x1p-100f);
   if ((rc = grant_smem(v, dev)) != SPEC_OK) return rc;
   const bool split = a->workspace != nullptr && a->workspace_bytes >= scratch_bytes(v, sms);
+  p.heads = v.heads;
+  while (p.c.kv_heads % p.heads != 0) p.heads /= 2;
+  p.head_groups = p.c.kv_heads / p.heads;
+  p.workers = v.heads / p.heads;
   if (split) {
     p.records = static_cast<specv::PartRecord*>(a->workspace);
-    p.parts = reinterpret_cast<float*>(p.records + sms);
+    p.parts = reinterpret_cast<float*>(p.records + sms * v.heads);
   }
   const char* const withhold = std::getenv("SPEC_PAGED_TEST_WITHHOLD_COPY");
   int test_withhold = withhold != nullptr && std::atoi(withhold) != 0;
   void* args[] = {&p, &test_withhold};
   rc = launch(v.kernel, dim3(static_cast<unsigned>(sms)), static_cast<unsigned>(v.threads), static_cast<size_t>(v.smem), args, stream);
   if (rc != SPEC_OK || !split) return rc;
-  int rows_of = v.rows, slice = v.rows > 32 ? 16 : 4;
-  void* join_args[] = {&p, &rows_of, &slice};
-  return launch(join_kernel(v.size), dim3(static_cast<unsigned>(sms), static_cast<unsigned>((v.rows + slice - 1) / slice)),
+  // Rows of a thread block of the join: one, and more where that would be too many blocks, most of
+  // which find nothing to do.
+  int of_item = v.rows, used = static_cast<int>(rows < v.rows ? rows : v.rows);
+  const int workers = sms * p.workers, tasks = used * p.heads;
+  int per_block = (tasks * p.workers + 31) / 32;
+  void* join_args[] = {&p, &of_item, &used, &per_block};
+  return launch(join_kernel(v.size), dim3(static_cast<unsigned>(workers), static_cast<unsigned>((tasks + per_block - 1) / per_block)),
                 specv::kJoinThreads, 0, join_args, stream);
 }
 

@@ -8,7 +8,8 @@ namespace specv {
 // A kernel over blocks of rows and what it is launched with.
 struct PagedVariant {
   void* kernel;
-  int rows, size;  // rows of an item, head size that the kernel works with
+  int rows, size;  // rows of an item and cache head, head size that the kernel works with
+  int heads;       // cache heads that a thread block can take at a time, a power of two
   int threads, smem;
   int regs;  // registers that the warpgroups share out, four of a thread each (0: none are shared out)
 };

@@ -4,14 +4,14 @@
 // of a row: one pass over keys and values.
 //
 // What bounds it is reading the cache: 2 * dim numbers a token and head, for the rows of all query
-// heads and columns of that head together.  Every computing warp has tokens of its own, which come
-// through a ring of its own in shared memory, and keeps maxima, sums and the outputs' numerators of
-// all rows in registers: warps wait for nobody until an item ends, when their sums are joined
-// in the ring's last place.  Four warps do nothing but look up where tokens lie, one by one (any page
-// size and order will do), and copy them, 16 bytes a thread.  (Bulk copies of whole heads, 128 or 256 bytes
-// each, are fewer instructions, but one took some 19 cycles of an SM: 142 us for 131,000 tokens
-// where these took 109 from within the computing warps.)  Products are 16 x 8 x 16 ones of a warp: 16 rows are
-// a fraction of a 128-row tile of the large tensor cores, and what they save is not short.
+// heads and columns of that head together.  A thread block's computing warps take a cache head each (of
+// a group of heads; where there are fewer heads than warps, of the next worker's units), keep maxima,
+// sums and the outputs' numerators of all its rows in registers, and wait for no other warp.  To each
+// belongs a warp that does nothing but look up where tokens lie, one by one (any page size and order will
+// do), and copy them through a ring in shared memory, 16 bytes a thread: q of an item, then keys
+// and values by turns.  (Bulk copies of whole heads, 128 or 256 bytes each, are fewer instructions, but one
+// took some 19 cycles of an SM.)  Products are 16 x 8 x 16 ones of a warp: 16 rows are a fraction of
+// a 128-row tile of the large tensor cores, and what they save is not short.
 //
 // 8-bit caches: numbers become fp16 in registers, exactly, and products are fp16.  q is
 // taken times a power of two for each row into fp16's range (exactly, but for what is below
@@ -104,7 +104,6 @@ __device__ __forceinline__ uint32_t eight_to_half2(uint32_t w, int i) {
   }
 }
 
-constexpr int kCopyWarps = 4;
 constexpr int kUnseen = INT32_MIN;  // in a page's place: no row sees the token
 
 template <int TYPE_, int D_, int MT_>
@@ -112,56 +111,143 @@ struct RowsShape {
   static constexpr int TYPE = TYPE_, D = D_, MT = MT_;  // cache type, head size (at most), blocks of 16 rows
   static constexpr bool kEight = TYPE != SPEC_CACHE_BF16;
   static constexpr int kRows = 16 * MT;
-  static constexpr int kWarps = D > 128 ? 4 : 8;  // that compute
-  static constexpr int kThreads = 32 * (kWarps + kCopyWarps);
+  static constexpr int kWarps = D > 128 ? 4 : 8;  // that compute; as many copy
+  static constexpr int kThreads = 64 * kWarps;
   // Registers a thread, and what a launch must bring (0: they are not shared out).
-  static constexpr int kRegsRows = kWarps == 8 ? 208 : 0, kRegsCopy = kWarps == 8 ? 88 : 0;
-  static constexpr int kRegs = kWarps / 4 * kRegsRows + kRegsCopy;
+  static constexpr int kRegsRows = kWarps == 8 ? 192 : 0, kRegsCopy = kWarps == 8 ? 64 : 0;
+  static constexpr int kRegs = kWarps / 4 * (kRegsRows + kRegsCopy);
+  static constexpr int kTokens = kEight ? 32 : 16;  // of a unit
   static constexpr int kRowBytes = D * (kEight ? 1 : 2);
-  static constexpr int kPitch = kRowBytes + 16;  // rows on other banks each
-  static constexpr int kTokens = (kEight ? MT > 1 : kRowBytes >= 256) ? 16 : 32;  // tokens of a warp's step
-  static constexpr int kSub = MT == 1 ? kTokens : 16;                             // of them, scores held at a time
-  static constexpr int kTile = kTokens * kWarps;
-  // A place: keys, values and, with 8 bits, each token's exponents (words that hold them, and where).
-  static constexpr int kExps = 2 * kTokens * kPitch;
-  static constexpr int kStage = kExps + (kEight ? kTokens * 9 : 0);
-  // With 32 rows q is read from shared memory for each product (registers are short).
-  static constexpr int kFragments = MT > 1 ? MT * (D / 16) * 32 : 0;
-  static constexpr int kRing = (MT == 1 ? 223 : D > 64 ? 214 : 218) * 1024;  // shared memory of all rings
-  static constexpr int kFit = kRing / kWarps / kStage;
-  static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static constexpr int kOutCols = 16 * (D + 4) * 4 <= kStage ? D : D / 2;  // columns of sums joined at a time
-  static constexpr int kOutPitch = kOutCols + 4;
+  // A place of the ring: the keys or the values of a unit, or 16 rows of q; with 8 bits also each token's
+  // exponents (words that hold the key's and the value's, and where in them).
+  static constexpr int kNumbers = 32 * D;
+  static constexpr int kPlace = kNumbers + (kEight ? kTokens * 9 : 0);
+  // Where registers are short, q's operands lie in shared memory.
+  static constexpr bool kShared = MT > 1 || D > 128;
+  static constexpr int kOperands = kShared ? MT * (D / 16) * 32 : 1;
+  static constexpr int kFit = (223 * 1024 / kWarps - kOperands * 16) / kPlace;
+  static constexpr int kPlaces = kFit > 12 ? 12 : kFit;
   static constexpr int kExtra = 1;  // an item's beginning and end, in units
-  static_assert(kStages >= 3, "the ring has three places at least");
-  static_assert(16 * kOutPitch * 4 <= kStage, "16 rows of sums fit a place of the ring");
-  using Plan = Schedule<kRows, kTile, kExtra>;
+  static_assert(kPlaces >= 4, "the ring holds two units at least");
+  using Plan = Schedule<kRows, kTokens, kExtra, 4>;
 };
 
 template <typename S>
 struct RowsSmem {
-  uint8_t ring[S::kWarps][S::kStages][S::kStage];
-  uint4 q[S::kFragments + 1];
-  float top[S::kWarps][S::kRows], sum[S::kWarps][S::kRows];
+  uint8_t ring[S::kWarps][S::kPlaces][S::kPlace];
+  uint4 q[S::kWarps][S::kOperands];
   typename S::Plan::Shared plan;
-  uint64_t full[S::kWarps][S::kStages], empty[S::kWarps][S::kStages];
+  uint64_t full[S::kWarps][S::kPlaces], empty[S::kWarps][S::kPlaces];
   int abort;
 };
 
+// Which 16-byte unit of row r a unit u goes to, so that neighbouring rows' equal units lie on
+// other banks (8 bits: also those of rows two apart, together with the next unit).
+template <bool EIGHT>
+__device__ __forceinline__ uint32_t mixed(uint32_t r, uint32_t u) {
+  return EIGHT ? u ^ ((r & 2) | (((r >> 2) ^ r) & 1) << 2) : u ^ (r & 7);
+}
+// (heads of 64 numbers of 8 bits: four units a row)
+template <int BYTES, bool EIGHT>
+__device__ __forceinline__ uint32_t unit_at(uint32_t r, uint32_t u) {
+  return r * BYTES + (BYTES > 64 ? mixed<EIGHT>(r, u) : u ^ ((r >> 1) & 3)) * 16;
+}
+__device__ __forceinline__ uint4 load_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 constexpr float kLn2 = 0.693147180559945f;
+
+// A row's parts, joined by a warp: a lane has components 4 lane .. 4 lane + 3 (heads of 64: of every
+// other part; of 256: also those 128 later).  take(i): part i's numerators of the row, its
+// maximum and sum.
+template <int D>
+struct RowSum {
+  static constexpr int kWide = D > 128 ? 2 : 1, kAcross = D / 4 / kWide, kSubs = 32 / kAcross;
+  float top, sum;
+  float4 a[kWide];
+
+  template <typename Rows, typename Stats>
+  __device__ __forceinline__ void take(int first, int parts, int step, const Rows& rows, const Stats& stats) {
+    const int lane = threadIdx.x & 31, sub = lane / kAcross, at = lane % kAcross;
+    top = -INFINITY;
+    sum = 0.f;
+#pragma unroll
+    for (int z = 0; z < kWide; ++z) a[z] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int i0 = first; i0 < parts; i0 += 32 * step) {  // 32 parts at a time
+      const int mine = i0 + lane * step, n = min(32, (parts - i0 + step - 1) / step);
+      float2 ms = make_float2(-INFINITY, 0.f);
+      if (mine < parts) ms = __ldcg(stats(mine));
+      const float most = warp_max_f32(ms.x), raise = fmaxf(most, top), down = top == -INFINITY ? 0.f : ex2_approx(top - raise);
+      const float f = ms.x == -INFINITY ? 0.f : ex2_approx(ms.x - raise);
+      float s = ms.y * f;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+      sum = fmaf(sum, down, s);
+      top = raise;
+#pragma unroll
+      for (int z = 0; z < kWide; ++z) a[z].x *= down, a[z].y *= down, a[z].z *= down, a[z].w *= down;
+      constexpr int kBatch = 8;  // parts on their way at a time
+#pragma unroll 1
+      for (int j0 = 0; j0 < n; j0 += kBatch * kSubs) {
+        float4 b[kBatch][kWide];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)  // (those past the end weigh 0: the last one again)
+#pragma unroll
+          for (int z = 0; z < kWide; ++z)
+            b[j][z] = __ldcg(reinterpret_cast<const float4*>(rows(i0 + min(j0 + j * kSubs + sub, n - 1) * step)) + at + z * 32);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int x = j0 + j * kSubs + sub;
+          const float from = __shfl_sync(0xFFFFFFFFu, f, x & 31), w = x < n ? from : 0.f;
+#pragma unroll
+          for (int z = 0; z < kWide; ++z) {
+            a[z].x = fmaf(b[j][z].x, w, a[z].x), a[z].y = fmaf(b[j][z].y, w, a[z].y);
+            a[z].z = fmaf(b[j][z].z, w, a[z].z), a[z].w = fmaf(b[j][z].w, w, a[z].w);
+          }
+        }
+      }
+    }
+    if constexpr (kSubs == 2) {
+      a[0].x += __shfl_xor_sync(0xFFFFFFFFu, a[0].x, 16);
+      a[0].y += __shfl_xor_sync(0xFFFFFFFFu, a[0].y, 16);
+      a[0].z += __shfl_xor_sync(0xFFFFFFFFu, a[0].z, 16);
+      a[0].w += __shfl_xor_sync(0xFFFFFFFFu, a[0].w, 16);
+    }
+  }
+  // The finished row, of query head `head` and packed row `row`.
+  __device__ __forceinline__ void finish(const AttendParams& p, int lane_of, int64_t row, int head) const {
+    const int lane = threadIdx.x & 31, at = lane % kAcross;
+    if (lane >= kAcross) return;
+    const float inv = 1.f / sum;
+#pragma unroll
+    for (int z = 0; z < kWide; ++z) {
+      const float4 b = make_float4(a[z].x * inv, a[z].y * inv, a[z].z * inv, a[z].w * inv);
+      const int d = 4 * at + 128 * z;
+      if (d < p.c.dim) {
+        *reinterpret_cast<uint2*>(p.out + row * p.out_row + head * p.out_head + d) =
+            make_uint2(to_bf16x2(b.x, b.y), to_bf16x2(b.z, b.w));
+        if (!finite4(b)) lane_failed(p.c, lane_of, SPEC_ERR_NONFINITE);
+      }
+    }
+    if (p.lse != nullptr && lane == 0) p.lse[row * p.lse_row + head] = (top + log2f(sum)) * kLn2;
+  }
+};
 
 template <typename S>
 __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const AttendParams p, const int test_withhold) {
   using Plan = typename S::Plan;
-  constexpr int TYPE = S::TYPE, D = S::D, MT = S::MT, kTokens = S::kTokens, kSub = S::kSub, kStages = S::kStages;
+  constexpr int TYPE = S::TYPE, D = S::D, MT = S::MT, kTokens = S::kTokens, kPlaces = S::kPlaces;
   constexpr bool kEight = S::kEight;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   RowsSmem<S>& sm = *reinterpret_cast<RowsSmem<S>*>(smem_raw);
   const CacheParams& c = p.c;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  if (threadIdx.x < S::kWarps * kStages) {
-    // (a full place: each copying thread's copies and, with 8 bits, its warp's exponents)
+  if (threadIdx.x < S::kWarps * kPlaces) {
+    // (a full place: each copying thread's copies and, with 8 bits, what its warp wrote itself)
     mbar_init(&sm.full[0][0] + threadIdx.x, kEight ? 33 : 32);
     mbar_init(&sm.empty[0][0] + threadIdx.x, 1);
   }
@@ -175,271 +261,300 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
       int first, count, before;
       if (!cache_lane(c, b, first, count, before)) lane_failed(c, b, SPEC_ERR_LAYOUT);
     }
-  const int64_t begin = sm.plan.begin, end = sm.plan.end;
+  const int pair = warp % S::kWarps, worker = pair / p.heads, head_in = pair - worker * p.heads;
+  const int64_t begin = sm.plan.begin[worker], end = sm.plan.end[worker];
+  int64_t left = end - begin;
+  Cursor at = sm.plan.from[worker];
+  uint8_t(&ring)[kPlaces][S::kPlace] = sm.ring[pair];
+  uint64_t(&full)[kPlaces] = sm.full[pair];
+  uint64_t(&empty)[kPlaces] = sm.empty[pair];
+  int place = 0, phase = 0;
+  auto next_place = [&] {
+    if (++place == kPlaces) {
+      place = 0;
+      phase ^= 1;
+    }
+  };
 
   if (warp >= S::kWarps) {
     // ------------------------------------------------------------------ copies
     if constexpr (S::kRegsCopy > 0) registers_shrink<S::kRegsCopy>();
     constexpr int kUnits = S::kRowBytes / 16, kAtOnce = 32 / kUnits;  // 16-byte units of a token; tokens of an access
-    constexpr int kMine = S::kWarps / kCopyWarps;                     // computing warps of this one
-    const int unit = lane % kUnits, sub = lane / kUnits, first_warp = warp - S::kWarps;
+    const int unit = lane % kUnits, sub = lane / kUnits;
     const bool in_head = unit * 16 < c.dim * (kEight ? 1 : 2);
     const uint32_t by = 1u << c.unit_shift;
-    const uint8_t* const k_base = c.k + unit * 16;
-    const uint8_t* const v_base = c.v + unit * 16;
-    Cursor ld = sm.plan.from;
-    int64_t left = begin < end ? end - begin : 0;
     // Pages are looked up two units ahead: with the memory busy, a load takes as long as that.
-    Cursor ahead = ld;
+    Cursor ahead = at;
     int64_t left_ahead = left;
-    int id[3][kMine];  // of the unit and the next two: the page of this lane's token, kUnseen: none
-    auto look_up = [&](int (&to)[kMine]) {
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int pos = ahead.tile * S::kTile + (first_warp + i * kCopyWarps) * kTokens + lane;
-        if (left_ahead > 0 && lane < kTokens && pos >= ahead.lo && pos < ahead.hi)
-          to[i] = __ldg(c.tables + ahead.b * c.table_stride + page_of(c, pos));
-        else
-          to[i] = kUnseen;
-      }
+    auto look_up = [&] {
+      const int pos = ahead.tile * kTokens + lane;
+      int page = kUnseen;
+      if (left_ahead > 0 && lane < kTokens && pos >= ahead.lo && pos < ahead.hi)
+        page = __ldg(c.tables + ahead.b * c.table_stride + page_of(c, pos));
       if (--left_ahead > 0) Plan::next_unit(p, ahead);
+      return page;
     };
-    int stage[kMine] = {}, round[kMine] = {};  // of each warp's ring
-    bool ok = true;
-    look_up(id[0]);
-    look_up(id[1]);
+    const bool withhold = test_withhold != 0 && begin == 0 && head_in == 0;
+    bool ok = true, again = false, fresh = true;  // again: the ring has been gone through
+    auto acquire = [&] { return ok = !again || warp_wait(&empty[place], phase ^ 1, &sm.abort); };
+    auto hand_on = [&] {
+      if (!withhold) cp_async_arrive(&full[place]);
+      if constexpr (kEight) warp_arrive(&full[place]);
+      next_place();
+      again = again || place == 0;
+    };
+    int page0 = look_up(), page1 = look_up();
 #pragma unroll 1
-    for (; ok && left > 0; --left) {
-      look_up(id[2]);
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int w = first_warp + i * kCopyWarps, p0 = ld.tile * S::kTile + w * kTokens;
-        const bool seen_some = p0 < ld.hi && p0 + kTokens > ld.lo;  // (if not, a place goes by empty)
-        if (!ok || (round[i] > 0 && !(ok = warp_wait(&sm.empty[w][stage[i]], (round[i] - 1) & 1, &sm.abort)))) continue;
-        uint8_t* const place = sm.ring[w][stage[i]];
-        const int page = id[0][i];
-        uint32_t at = kNowhere;
-        uint8_t where = 255;  // of the exponents in their words: two bits each
-        if (page != kUnseen && static_cast<uint32_t>(page) >= static_cast<uint32_t>(c.pages)) {
-          lane_failed(c, ld.b, SPEC_ERR_LAYOUT);
-        } else if (page != kUnseen) {
-          const int pos = p0 + lane, in = pos - page_of(c, pos) * c.page_size;
-          at = head_at(c, page, in, ld.h);
+    for (; left > 0; --left) {
+      const int page2 = look_up();
+      if (fresh) {  // the item's rows of q, 16 at a time
+#pragma unroll 1
+        for (int m = 0; m < MT && acquire(); ++m) {
+          constexpr int kQUnits = D / 8, kQAtOnce = kQUnits > 32 ? 1 : 32 / kQUnits;
+          const int r = at.k * S::kRows + m * 16 + (lane & 15), col = r / p.group;
+          int64_t row = -1;
+          if (col < at.count)
+            row = (at.first + col) * p.q_row + ((at.h * p.heads + head_in) * p.group + r - col * p.group) * p.q_head;
+          const uint32_t to = smem_addr(ring[place]);
+#pragma unroll 4
+          for (int j = 0; j < 16 / kQAtOnce; ++j) {
+            const int i = j * kQAtOnce + lane / kQUnits, u = lane % kQUnits;
+            const int64_t f = __shfl_sync(0xFFFFFFFFu, row, i);
+            const bool on = f >= 0 && u * 8 < c.dim;
+            cp_async16_or_zero(to + unit_at<2 * D, false>(i, u), p.q + (on ? f + u * 8 : 0), on);
+          }
+          hand_on();
+        }
+        if (!ok) break;
+      }
+      uint32_t from = kNowhere;
+      uint8_t where = 255;  // of the exponents in their words: two bits each
+      if (!acquire()) break;
+      if (page0 != kUnseen) {
+        if (static_cast<uint32_t>(page0) >= static_cast<uint32_t>(c.pages)) {
+          lane_failed(c, at.b, SPEC_ERR_LAYOUT);
+        } else {
+          const int pos = at.tile * kTokens + lane, in = pos - page_of(c, pos) * c.page_size, head = at.h * p.heads + head_in;
+          from = head_at(c, page0, in, head);
           if constexpr (kEight) {
-            const int64_t e = page * c.exp_page + in * c.exp_slot + ld.h * c.exp_head;
+            const int64_t e = page0 * c.exp_page + in * c.exp_slot + head * c.exp_head;
             const uintptr_t ke = reinterpret_cast<uintptr_t>(c.k_exps + e), ve = reinterpret_cast<uintptr_t>(c.v_exps + e);
-            cp_async4(place + S::kExps + lane * 4, reinterpret_cast<const void*>(ke & ~uintptr_t{3}));
-            cp_async4(place + S::kExps + (kTokens + lane) * 4, reinterpret_cast<const void*>(ve & ~uintptr_t{3}));
+            cp_async4(&ring[place][S::kNumbers + lane * 4], reinterpret_cast<const void*>(ke & ~uintptr_t{3}));
+            cp_async4(&ring[place][S::kNumbers + (kTokens + lane) * 4], reinterpret_cast<const void*>(ve & ~uintptr_t{3}));
             where = static_cast<uint8_t>((ke & 3) | (ve & 3) << 2);
           }
         }
-        if (kEight && lane < kTokens) place[S::kExps + kTokens * 8 + lane] = where;
-        const uint32_t to = smem_addr(place + sub * S::kPitch + unit * 16);
-#pragma unroll
-        for (int j = 0; j < kTokens / kAtOnce && seen_some; ++j) {
-          const uint32_t from = __shfl_sync(0xFFFFFFFFu, at, j * kAtOnce + sub);
-          const bool on = from != kNowhere && in_head;
-          const uint64_t off = on ? static_cast<uint64_t>(from) * by : 0;
-          if (!(test_withhold != 0 && begin == 0 && w == 0 && j == 0)) {
-            cp_async16_or_zero(to + j * kAtOnce * S::kPitch, k_base + off, on);
-            cp_async16_or_zero(to + (kTokens + j * kAtOnce) * S::kPitch, v_base + off, on);
-          }
-        }
-        if (!(test_withhold != 0 && begin == 0 && w == 0)) cp_async_arrive(&sm.full[w][stage[i]]);
-        if constexpr (kEight) warp_arrive(&sm.full[w][stage[i]]);
-        if (++stage[i] == kStages) {
-          stage[i] = 0;
-          ++round[i];
-        }
-        id[0][i] = id[1][i];
-        id[1][i] = id[2][i];
       }
-      if (left > 1) Plan::next_unit(p, ld);
+      if (kEight && lane < kTokens) ring[place][S::kNumbers + kTokens * 8 + lane] = where;
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        if (v == 1 && !acquire()) break;
+        const uint32_t to = smem_addr(ring[place]);
+        const uint8_t* const base = (v ? c.v : c.k) + unit * 16;
+#pragma unroll
+        for (int j = 0; j < kTokens / kAtOnce; ++j) {
+          const int tok = j * kAtOnce + sub;
+          const uint32_t f = __shfl_sync(0xFFFFFFFFu, from, tok);
+          const bool on = f != kNowhere && in_head;
+          cp_async16_or_zero(to + unit_at<S::kRowBytes, kEight>(tok, unit), base + (on ? static_cast<uint64_t>(f) * by : 0), on);
+        }
+        hand_on();
+      }
+      if (!ok) break;
+      page0 = page1;
+      page1 = page2;
+      if (left > 1) {
+        Plan::next_unit(p, at);
+        fresh = at.tile == at.t0;
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // copies end before the thread does
-  } else if (begin < end) {
+  } else {
     // ------------------------------------------------------- scores and outputs
     if constexpr (S::kRegsRows > 0) registers_grow<S::kRegsRows>();
-    Cursor at = sm.plan.from;
-    bool dead = false;  // a wait gave up: the warp only goes along to the barriers
-    uint8_t(&ring)[kStages][S::kStage] = sm.ring[warp];
+    const int g = lane >> 2, t = lane & 3;
     const uint32_t ring_at = smem_addr(&ring[0][0]);
-    auto all_rows = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * S::kWarps) : "memory"); };
-    uint32_t qf[MT == 1 ? D / 16 : 1][4];
-    float o[MT][D / 8][4];
-    float top[MT][2], sum[MT][2], qs[MT][2];
-    int last[MT][2];  // one past the last position that a row sees
-    bool fresh = true, started = false;
-    int stage = 0, phase = 0;  // of the ring
-#pragma unroll 1
-    for (int64_t u = begin; u < end; ++u) {
-      const int p0 = at.tile * S::kTile + warp * kTokens;
-      const bool seen_some = p0 < at.hi && p0 + kTokens > at.lo;
-      if (fresh) {
-        // q as left operands: of each 16 components a thread has four of rows g and g + 8.
-        fresh = false;
-        started = at.tile == at.t0;
+    uint4* const operands = sm.q[pair];
+    auto release = [&](int which) { warp_arrive(&empty[which]); };
+    bool ok = true;
+    while (ok && left > 0) {
+      const int n_units = static_cast<int>(min(static_cast<int64_t>(at.t1 - at.tile), left));
+      const bool started = at.tile == at.t0, ends = at.tile + n_units == at.t1;
+      // q as left operands: of each 16 components a thread has four of rows g and g + 8.
+      uint32_t qf[S::kShared ? 1 : D / 16][4];
+      float qs[MT][2], o[MT][D / 8][4], top[MT][2], sum[MT][2];
+      int last[MT][2];  // one past the last position that a row sees
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint32_t f[D / 16][4];
+      for (int m = 0; m < MT; ++m) {
+        if (!(ok = ok && warp_wait(&full[place], phase, &sm.abort))) break;
+        const uint32_t rows = ring_at + place * S::kPlace;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = at.k * S::kRows + m * 16 + g + 8 * i, col = r / p.group;
-            last[m][i] = at.before + col + 1;
-            top[m][i] = -INFINITY;
-            sum[m][i] = 0.f;
-            const bool on = col < at.count;
-            const __nv_bfloat16* const from =
-                p.q + (on ? (at.first + col) * p.q_row + (at.h * p.group + r - col * p.group) * p.q_head : 0);
+        for (int i = 0; i < 2; ++i) {
+          last[m][i] = at.before + (at.k * S::kRows + m * 16 + g + 8 * i) / p.group + 1;
+          top[m][i] = -INFINITY;
+          sum[m][i] = 0.f;
+        }
+        if constexpr (!kEight) {
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-              // (8 bits: components 16 (t + 4 (s / 4)) + 4 (s % 4) + 0..3)
-              const int d = kEight ? 16 * (t + 4 * (s / 4)) + 4 * (s % 4) : 16 * s + 2 * t;
-              const int d2 = kEight ? d + 2 : d + 8;
-              f[s][i] = on && d < c.dim ? __ldg(reinterpret_cast<const uint32_t*>(from + d)) : 0u;
-              f[s][i + 2] = on && d2 < c.dim ? __ldg(reinterpret_cast<const uint32_t*>(from + d2)) : 0u;
+          for (int s = 0; s < D / 16; ++s) {
+            uint32_t a[4];  // rows 0-7 and 8-15 of components 0-7, then of 8-15
+            ldmatrix_x4(a, rows + unit_at<2 * D, false>(lane & 15, 2 * s + (lane >> 4)));
+            if constexpr (S::kShared) {
+              operands[(m * (D / 16) + s) * 32 + lane] = make_uint4(a[0], a[1], a[2], a[3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) qf[s][j] = a[j];
             }
           }
-          if constexpr (kEight) {
+        } else {
+          // Components 16 (t + 4 (s / 4)) + 4 (s % 4) + 0..3 of each row, as fp16; the row's largest comes
+          // to lie in 2^14 .. 2^15.  (Rows of tiny numbers are left smaller.)
+          uint32_t f[2][D / 8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t most = 0;
+          for (int i = 0; i < 2; ++i) {
+            uint32_t most = 0;
 #pragma unroll
-              for (int s = 0; s < D / 16; ++s) {
-                most = max(most, max(f[s][i] & 0x7FFFu, (f[s][i] >> 16) & 0x7FFFu));
-                most = max(most, max(f[s][i + 2] & 0x7FFFu, (f[s][i + 2] >> 16) & 0x7FFFu));
-              }
-              most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-              most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-              // The largest comes to lie in 2^14 .. 2^15.  (Rows of tiny numbers are left smaller.)
-              const int up = min(127 + 14 - static_cast<int>(most >> 7), 126);
-              const float by = __uint_as_float(static_cast<uint32_t>(127 + max(up, -126)) << 23);
-              qs[m][i] = p.scale / by;
-#pragma unroll
-              for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-                for (int j = i; j < 4; j += 2) f[s][j] = to_halfx2(bf16_lo(f[s][j]) * by, bf16_hi(f[s][j]) * by);
+            for (int u = 0; u < D / 32; ++u) {
+              const uint4 v = load_shared16(rows + unit_at<2 * D, false>(g + 8 * i, 2 * (t + 4 * (u / 2)) + u % 2));
+              f[i][4 * u] = v.x, f[i][4 * u + 1] = v.y, f[i][4 * u + 2] = v.z, f[i][4 * u + 3] = v.w;
             }
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) most = max(most, max(f[i][j] & 0x7FFFu, (f[i][j] >> 16) & 0x7FFFu));
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+            const int up = max(min(127 + 14 - static_cast<int>(most >> 7), 126), -126);
+            const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+            qs[m][i] = p.scale / by;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) f[i][j] = to_halfx2(bf16_lo(f[i][j]) * by, bf16_hi(f[i][j]) * by);
           }
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
-            if constexpr (MT == 1) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) qf[s][j] = f[s][j];
-            } else if (s % S::kWarps == warp) {  // (all warps have the same)
-              sm.q[(m * (D / 16) + s) * 32 + lane] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
+            if constexpr (S::kShared) {
+              operands[(m * (D / 16) + s) * 32 + lane] = make_uint4(f[0][2 * s], f[1][2 * s], f[0][2 * s + 1], f[1][2 * s + 1]);
+            } else {
+              qf[s][0] = f[0][2 * s], qf[s][1] = f[1][2 * s], qf[s][2] = f[0][2 * s + 1], qf[s][3] = f[1][2 * s + 1];
             }
           }
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[m][n][i] = 0.f;
         }
-        if constexpr (MT > 1) all_rows();
+        release(place);
+        next_place();
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[m][n][i] = 0.f;
       }
-      if (!dead) dead = !warp_wait(&sm.full[warp][stage], phase, &sm.abort);
-      const uint32_t ks = ring_at + stage * S::kStage, vs = ks + kTokens * S::kPitch;
-      if constexpr (kEight) {
-        // Each lane takes a token's exponents out of their words: 2^e of the key, e of the value.
-        if (lane < kTokens && seen_some && !dead) {
-          uint32_t* const f = reinterpret_cast<uint32_t*>(&ring[stage][S::kExps]);
-          const uint32_t where = ring[stage][S::kExps + kTokens * 8 + lane];
+      if (!ok) break;
+      const int seen_first = at.before + at.k * S::kRows / p.group;  // the block's first column's position
+#pragma unroll 1
+      for (int unit = 0; unit < n_units; ++unit, ++at.tile) {
+        const int k_place = place;
+        if (!(ok = warp_wait(&full[place], phase, &sm.abort))) break;
+        next_place();
+        const int v_place = place;
+        if (!(ok = warp_wait(&full[place], phase, &sm.abort))) break;
+        next_place();
+        const int p0 = at.tile * kTokens;
+        const uint32_t ks = ring_at + k_place * S::kPlace, vs = ring_at + v_place * S::kPlace;
+        if constexpr (kEight) {
+          // Each lane takes a token's exponents out of their words: 2^e of the key, e of the value.
+          uint32_t* const f = reinterpret_cast<uint32_t*>(&ring[k_place][S::kNumbers]);
+          const uint32_t where = ring[k_place][S::kNumbers + kTokens * 8 + lane];
           const uint32_t kb = where == 255u ? 127u : (f[lane] >> (where & 3) * 8) & 255u;
           const uint32_t vb = where == 255u ? 127u : (f[kTokens + lane] >> (where >> 2) * 8) & 255u;
           f[lane] = kb == 255u ? 0x7FC00000u : kb << 23;
           f[kTokens + lane] = vb == 255u ? 0x7FC00000u : __float_as_uint(static_cast<float>(static_cast<int>(vb) - 127));
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      if (seen_some && !dead) {
-        const int seen_first = at.before + at.k * S::kRows / p.group;  // the block's first column's position
         const bool whole = p0 + kTokens <= seen_first + 1 && (p.window == 0 || p0 > at.hi - 1 - p.window);
-#pragma unroll
-        for (int half = 0; half < kTokens / kSub; ++half) {
-          float x[MT][kSub / 8][4];
+#pragma unroll 1
+        for (int t0 = 0; t0 < kTokens; t0 += 16) {
+          float x[MT][2][4];
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int n = 0; n < kSub / 8; ++n)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
               for (int i = 0; i < 4; ++i) x[m][n][i] = 0.f;
           auto q_of = [&](int m, int s, uint32_t (&a)[4]) {
-            if constexpr (MT == 1) {
+            if constexpr (S::kShared) {
+              const uint4 v = operands[(m * (D / 16) + s) * 32 + lane];
+              a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
+            } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j) a[j] = qf[s][j];
-            } else {
-              const uint4 v = sm.q[(m * (D / 16) + s) * 32 + lane];
-              a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
             }
           };
           if constexpr (!kEight) {
-            const uint32_t base = ks + (half * kSub + (lane >> 4) * 8 + (lane & 7)) * S::kPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
-              uint32_t a[MT][4];
+              uint32_t b[4];
+              ldmatrix_x4(b, ks + unit_at<S::kRowBytes, false>((lane >> 4) * 8 + (lane & 7), 2 * s + ((lane >> 3) & 1)));
 #pragma unroll
-              for (int m = 0; m < MT; ++m) q_of(m, s, a[m]);
-#pragma unroll
-              for (int n = 0; n < kSub / 16; ++n) {
-                uint32_t b[4];
-                ldmatrix_x4(b, base + n * 16 * S::kPitch + s * 32);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                  mma_16816<false>(x[m][2 * n], a[m], b[0], b[1]);
-                  mma_16816<false>(x[m][2 * n + 1], a[m], b[2], b[3]);
-                }
+              for (int m = 0; m < MT; ++m) {
+                uint32_t a[4];
+                q_of(m, s, a);
+                mma_16816<false>(x[m][0], a, b[0], b[1]);
+                mma_16816<false>(x[m][1], a, b[2], b[3]);
               }
             }
           } else {
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
-              uint4 w[kSub / 8];
+              uint4 w[2];
 #pragma unroll
-              for (int n = 0; n < kSub / 8; ++n) {
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w[n].x), "=r"(w[n].y), "=r"(w[n].z), "=r"(w[n].w)
-                             : "r"(ks + (half * kSub + n * 8 + g) * S::kPitch + (t + 4 * i) * 16)
-                             : "memory");
-              }
+              for (int n = 0; n < 2; ++n) w[n] = load_shared16(ks + t0 * S::kRowBytes + unit_at<S::kRowBytes, true>(n * 8 + g, t + 4 * i));
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                uint32_t a[MT][4];
+                uint32_t b[2][2];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) q_of(m, 4 * i + j, a[m]);
-#pragma unroll
-                for (int n = 0; n < kSub / 8; ++n) {
+                for (int n = 0; n < 2; ++n) {
                   uint32_t v = (&w[n].x)[j];
                   if constexpr (TYPE == SPEC_CACHE_INT8) v ^= 0x80808080u;
-                  const uint32_t b0 = eight_to_half2<TYPE>(v, 0), b1 = eight_to_half2<TYPE>(v, 1);
+                  b[n][0] = eight_to_half2<TYPE>(v, 0);
+                  b[n][1] = eight_to_half2<TYPE>(v, 1);
+                }
 #pragma unroll
-                  for (int m = 0; m < MT; ++m) mma_16816<true>(x[m][n], a[m], b0, b1);
+                for (int m = 0; m < MT; ++m) {
+                  uint32_t a[4];
+                  q_of(m, 4 * i + j, a);
+                  mma_16816<true>(x[m][0], a, b[0][0], b[0][1]);
+                  mma_16816<true>(x[m][1], a, b[1][0], b[1][1]);
                 }
               }
             }
           }
           // Scores in powers of two (8 bits: with the value's exponent), hidden ones -inf.
-          const float* const exps = reinterpret_cast<const float*>(&ring[stage][S::kExps]) + half * kSub + 2 * t;
+          const float* const exps = reinterpret_cast<const float*>(&ring[k_place][S::kNumbers]) + t0 + 2 * t;
+          float2 ve[2];
 #pragma unroll
-          for (int n = 0; n < kSub / 8; ++n) {
-            float2 kf, ve;
+          for (int n = 0; n < 2; ++n) {
+            float2 kf;
             if constexpr (kEight) {
               kf = *reinterpret_cast<const float2*>(exps + n * 8);
-              ve = *reinterpret_cast<const float2*>(exps + kTokens + n * 8);
+              ve[n] = *reinterpret_cast<const float2*>(exps + kTokens + n * 8);
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 if constexpr (kEight)
-                  x[m][n][i] = fmaf(x[m][n][i] * ((i & 1) ? kf.y : kf.x), qs[m][i >> 1], (i & 1) ? ve.y : ve.x);
+                  x[m][n][i] = fmaf(x[m][n][i] * ((i & 1) ? kf.y : kf.x), qs[m][i >> 1], (i & 1) ? ve[n].y : ve[n].x);
                 else
                   x[m][n][i] *= p.scale;
-                if (!whole) {
-                  const int pos = p0 + half * kSub + n * 8 + 2 * t + (i & 1), lim = last[m][i >> 1];
+              }
+          }
+          if (!whole) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int pos = p0 + t0 + n * 8 + 2 * t + (i & 1), lim = last[m][i >> 1];
                   const bool seen = pos < lim && pos >= at.lo && (p.window == 0 || pos >= lim - p.window);
                   x[m][n][i] = seen ? x[m][n][i] : -INFINITY;
                 }
-              }
           }
           float raise[MT][2];
           bool any = false;
@@ -447,9 +562,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float most = -INFINITY;
-#pragma unroll
-              for (int n = 0; n < kSub / 8; ++n) most = fmaxf(most, fmaxf(x[m][n][2 * i], x[m][n][2 * i + 1]));
+              float most = fmaxf(fmaxf(x[m][0][2 * i], x[m][0][2 * i + 1]), fmaxf(x[m][1][2 * i], x[m][1][2 * i + 1]));
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
               raise[m][i] = most > top[m][i] + kRowsSlack ? most : top[m][i];
@@ -470,204 +583,201 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
                 top[m][i] = raise[m][i];
               }
           }
-          uint32_t w[MT][kSub / 16][4];
+          uint32_t w[MT][4];
 #pragma unroll
-          for (int n = 0; n < kSub / 8; ++n) {
-            float2 vi;  // 2^-e
-            if constexpr (kEight) {
-              const float2 ve = *reinterpret_cast<const float2*>(exps + kTokens + n * 8);
-              vi = make_float2(power_of_minus(ve.x), power_of_minus(ve.y));
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float from = top[m][i] == -INFINITY ? 0.f : top[m][i];
-                const float e0 = ex2_approx(x[m][n][2 * i] - from), e1 = ex2_approx(x[m][n][2 * i + 1] - from);
-                if constexpr (kEight) {
-                  sum[m][i] = fmaf(e0, vi.x, fmaf(e1, vi.y, sum[m][i]));
-                  w[m][n / 2][(n & 1) * 2 + i] = to_halfx2(e0, e1);
-                } else {
-                  sum[m][i] += e0 + e1;
-                  w[m][n / 2][(n & 1) * 2 + i] = to_bf16x2(e0, e1);
-                }
-              }
-          }
-          // Outputs' numerators: tokens are the products' inner dimension.
-#pragma unroll
-          for (int k16 = 0; k16 < kSub / 16; ++k16) {
-            const int tok = half * kSub + k16 * 16;
-            if constexpr (!kEight) {
-              const uint32_t base = vs + (tok + ((lane >> 3) & 1) * 8 + (lane & 7)) * S::kPitch + (lane >> 4) * 16;
-#pragma unroll
-              for (int n = 0; n < D / 16; ++n) {
-                uint32_t b[4];
-                ldmatrix_x4_trans(b, base + n * 32);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                  mma_16816<false>(o[m][2 * n], w[m][k16], b[0], b[1]);
-                  mma_16816<false>(o[m][2 * n + 1], w[m][k16], b[2], b[3]);
-                }
-              }
-            } else {
-              constexpr int kBytes = D >= 128 ? 16 : 8;  // neighbouring components of a thread
-#pragma unroll
-              for (int i = 0; i < D / (8 * kBytes); ++i) {
-                uint32_t y[4][kBytes / 4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-                  const uint32_t from = vs + (tok + 2 * t + (k & 1) + (k >> 1) * 8) * S::kPitch + (g + 8 * i) * kBytes;
-                  if constexpr (kBytes == 16)
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(y[k][0]), "=r"(y[k][1]), "=r"(y[k][2]), "=r"(y[k][3])
-                                 : "r"(from)
-                                 : "memory");
-                  else
-                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(y[k][0]), "=r"(y[k][1]) : "r"(from) : "memory");
-                  if constexpr (TYPE == SPEC_CACHE_INT8)
-#pragma unroll
-                    for (int j = 0; j < kBytes / 4; ++j) y[k][j] ^= 0x80808080u;
-                }
-#pragma unroll
-                for (int j = 0; j < kBytes / 4; ++j)
-#pragma unroll
-                  for (int z = 0; z < 2; ++z) {
-                    const uint32_t a = __byte_perm(y[0][j], y[1][j], z ? 0x7362 : 0x5140);
-                    const uint32_t b = __byte_perm(y[2][j], y[3][j], z ? 0x7362 : 0x5140);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                      const uint32_t b0 = eight_to_half2<TYPE>(a, e), b1 = eight_to_half2<TYPE>(b, e);
-#pragma unroll
-                      for (int m = 0; m < MT; ++m)
-                        mma_16816<true>(o[m][i * kBytes + j * 4 + z * 2 + e], w[m][k16], b0, b1);
-                    }
-                  }
-              }
-            }
-          }
-        }
-      }
-      if (at.tile + 1 == at.t1 || u + 1 == end) {
-        // The item ends here, or goes on in the next thread block: the warps' sums are joined, 16
-        // rows at a time, in the places of the ring that the warps have just read.
-        const bool ends = at.tile + 1 == at.t1;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float s = sum[m][i];
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-            if (t == 0) {
-              sm.top[warp][m * 16 + g + 8 * i] = top[m][i];
-              sm.sum[warp][m * 16 + g + 8 * i] = s;
-            }
-          }
-        all_rows();
-        float* const part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (started ? 1 : 0)) * part_floats(S::kRows, D);
-        constexpr int kCols = S::kOutCols;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          float factor[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float most = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) most = fmaxf(most, sm.top[w][m * 16 + g + 8 * i]);
-            factor[i] = top[m][i] == -INFINITY ? 0.f : ex2_approx(top[m][i] - most);
-          }
-#pragma unroll
-          for (int d0 = 0; d0 < D; d0 += kCols) {
-            // (8 bits: a thread's numbers of n = 0, 8, .. go to components all over the head: those of
-            // a half are the ones whose place in it is even or odd, n % 8 below 4 or not)
-            float* const mine = reinterpret_cast<float*>(&ring[stage][0]);
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float* const to = mine + (g + 8 * i) * S::kOutPitch;
-              const float f = factor[i];
-              if constexpr (!kEight) {
+              const float from = top[m][i] == -INFINITY ? 0.f : top[m][i];
 #pragma unroll
-                for (int n = d0 / 8; n < (d0 + kCols) / 8; ++n)
-                  *reinterpret_cast<float2*>(to + n * 8 - d0 + 2 * t) = make_float2(o[m][n][2 * i] * f, o[m][n][2 * i + 1] * f);
-              } else {
-                constexpr int kBytes = D >= 128 ? 16 : 8;
+              for (int n = 0; n < 2; ++n) {
+                const float e0 = ex2_approx(x[m][n][2 * i] - from), e1 = ex2_approx(x[m][n][2 * i + 1] - from);
+                if constexpr (kEight) {
+                  sum[m][i] = fmaf(e0, power_of_minus(ve[n].x), fmaf(e1, power_of_minus(ve[n].y), sum[m][i]));
+                  w[m][n * 2 + i] = to_halfx2(e0, e1);
+                } else {
+                  sum[m][i] += e0 + e1;
+                  w[m][n * 2 + i] = to_bf16x2(e0, e1);
+                }
+              }
+            }
+          // Outputs' numerators: tokens are the products' inner dimension.
+          if constexpr (!kEight) {
 #pragma unroll
-                for (int n = 0; n < D / 8; n += 4)
+            for (int n = 0; n < D / 16; ++n) {
+              uint32_t b[4];
+              ldmatrix_x4_trans(b, vs + unit_at<S::kRowBytes, false>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * n + (lane >> 4)));
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma_16816<false>(o[m][2 * n], w[m], b[0], b[1]);
+                mma_16816<false>(o[m][2 * n + 1], w[m], b[2], b[3]);
+              }
+            }
+          } else {
+            constexpr int kBytes = D >= 128 ? 16 : 8;  // neighbouring components of a thread
+#pragma unroll
+            for (int i = 0; i < D / (8 * kBytes); ++i) {
+              uint32_t y[4][kBytes / 4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+                const uint32_t r = 2 * t + (k & 1) + (k >> 1) * 8, d = (g + 8 * i) * kBytes;
+                const uint32_t from = vs + t0 * S::kRowBytes + unit_at<S::kRowBytes, true>(r, d / 16) + d % 16;
+                if constexpr (kBytes == 16) {
+                  const uint4 v = load_shared16(from);
+                  y[k][0] = v.x, y[k][1] = v.y, y[k][2] = v.z, y[k][3] = v.w;
+                } else {
+                  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(y[k][0]), "=r"(y[k][1]) : "r"(from) : "memory");
+                }
+                if constexpr (TYPE == SPEC_CACHE_INT8)
+#pragma unroll
+                  for (int j = 0; j < kBytes / 4; ++j) y[k][j] ^= 0x80808080u;
+              }
+#pragma unroll
+              for (int j = 0; j < kBytes / 4; ++j)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const uint32_t a = __byte_perm(y[0][j], y[1][j], z ? 0x7362 : 0x5140);
+                  const uint32_t b = __byte_perm(y[2][j], y[3][j], z ? 0x7362 : 0x5140);
 #pragma unroll
                   for (int e = 0; e < 2; ++e) {
-                    // Components 4 y .. 4 y + 3 of the head; a half takes every other four.
-                    const int y = (2 * t + e + 8 * (n / kBytes)) * (kBytes / 4) + n % kBytes / 4;
-                    if (kCols == D || (n / 4) % 2 == d0 / kCols)
-                      *reinterpret_cast<float4*>(to + (kCols == D ? y : y / 2) * 4) =
-                          make_float4(o[m][n][2 * i + e] * f, o[m][n + 1][2 * i + e] * f, o[m][n + 2][2 * i + e] * f,
-                                      o[m][n + 3][2 * i + e] * f);
+                    const uint32_t b0 = eight_to_half2<TYPE>(a, e), b1 = eight_to_half2<TYPE>(b, e);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) mma_16816<true>(o[m][i * kBytes + j * 4 + z * 2 + e], w[m], b0, b1);
                   }
-              }
-            }
-            all_rows();
-#pragma unroll 1
-            for (int x = threadIdx.x; x < 16 * (kCols / 4); x += 32 * S::kWarps) {
-              const int r = x / (kCols / 4), y = x % (kCols / 4);
-              const int d = kCols == D ? y * 4 : kEight ? (2 * y + d0 / kCols) * 4 : d0 + y * 4;
-              float most = -INFINITY, total = 0.f;
-#pragma unroll
-              for (int w = 0; w < S::kWarps; ++w) most = fmaxf(most, sm.top[w][m * 16 + r]);
-              float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-              for (int w = 0; w < S::kWarps; ++w) {
-                const float mw = sm.top[w][m * 16 + r];
-                total += mw == -INFINITY ? 0.f : sm.sum[w][m * 16 + r] * ex2_approx(mw - most);
-                const float4 b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(&sm.ring[w][stage][0]) +
-                                                                  r * S::kOutPitch + y * 4);
-                a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
-              }
-              if (started && ends) {
-                const int row = at.k * S::kRows + m * 16 + r, col = row / p.group, head = at.h * p.group + row - col * p.group;
-                if (col < at.count && d < c.dim) {
-                  const float inv = 1.f / total;
-                  a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
-                  *reinterpret_cast<uint2*>(p.out + (at.first + col) * p.out_row + head * p.out_head + d) =
-                      make_uint2(to_bf16x2(a.x, a.y), to_bf16x2(a.z, a.w));
-                  if (!finite4(a)) lane_failed(c, at.b, SPEC_ERR_NONFINITE);
-                  if (p.lse != nullptr && d == 0)
-                    p.lse[(at.first + col) * p.lse_row + head] = (most + log2f(total)) * kLn2;
                 }
-              } else {
-                *reinterpret_cast<float4*>(part + (m * 16 + r) * D + d) = a;
-                if (d == 0) {
-                  part[S::kRows * D + 2 * (m * 16 + r)] = most;
-                  part[S::kRows * D + 2 * (m * 16 + r) + 1] = total;
-                }
-              }
             }
-            all_rows();
           }
         }
-        fresh = true;
+        release(k_place);
+        release(v_place);
       }
+      if (!ok) break;
+      // The item ends here, or goes on with the next worker.
+      const int head = at.h * p.heads + head_in;
+      float* const part = p.parts + (2 * (static_cast<int64_t>(blockIdx.x) * p.workers + worker) + (started ? 1 : 0)) *
+                                        part_floats(S::kRows * p.heads, D);
+      const bool direct = started && ends;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float s = sum[m][i];
+          s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+          s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+          const int r = m * 16 + g + 8 * i, row = at.k * S::kRows + r, col = row / p.group;
+          if (col >= at.count) continue;
+          const int q_head = head * p.group + row - col * p.group;
+          __nv_bfloat16* const out = p.out + (at.first + col) * p.out_row + q_head * p.out_head;
+          float* const to = part + (head_in * S::kRows + r) * D;
+          const float f = direct ? 1.f / s : 1.f;
+          bool fine = true;
+          constexpr int kBytes = D >= 128 ? 16 : 8;
+          // (8 bits: four by four, components of the head that lie side by side)
+#pragma unroll
+          for (int n = 0; n < D / 8; n += kEight ? 4 : 1)
+#pragma unroll
+            for (int e = 0; e < (kEight ? 2 : 1); ++e) {
+              const int d = kEight ? (2 * t + e + 8 * (n / kBytes)) * kBytes + n % kBytes : n * 8 + 2 * t;
+              float4 a;
+              if constexpr (kEight)
+                a = make_float4(o[m][n][2 * i + e] * f, o[m][n + 1][2 * i + e] * f, o[m][n + 2][2 * i + e] * f, o[m][n + 3][2 * i + e] * f);
+              else
+                a = make_float4(o[m][n][2 * i] * f, o[m][n][2 * i + 1] * f, 0.f, 0.f);
+              if (direct) {
+                if (d < c.dim) {
+                  if constexpr (kEight)
+                    *reinterpret_cast<uint2*>(out + d) = make_uint2(to_bf16x2(a.x, a.y), to_bf16x2(a.z, a.w));
+                  else
+                    *reinterpret_cast<uint32_t*>(out + d) = to_bf16x2(a.x, a.y);
+                  fine = fine && finite4(a);
+                }
+              } else if constexpr (kEight) {
+                *reinterpret_cast<float4*>(to + d) = a;
+              } else {
+                *reinterpret_cast<float2*>(to + d) = make_float2(a.x, a.y);
+              }
+            }
+          if (direct) {
+            if (!fine) lane_failed(c, at.b, SPEC_ERR_NONFINITE);
+            if (p.lse != nullptr && t == 0) p.lse[(at.first + col) * p.lse_row + q_head] = (top[m][i] + log2f(s)) * kLn2;
+          } else if (t == 0) {
+            *reinterpret_cast<float2*>(part + S::kRows * p.heads * D + 2 * (head_in * S::kRows + r)) = make_float2(top[m][i], s);
+          }
+        }
+      left -= n_units;
+      --at.tile;
       Plan::next_unit(p, at);
-      warp_arrive(&sm.empty[warp][stage]);
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    if (p.parts != nullptr) p.records[blockIdx.x] = sm.plan.record;
-    if (sm.abort && c.status != nullptr) {  // a wait gave up: all lanes of the block's range
-      Cursor x = sm.plan.from;
-      for (int64_t u = begin; u < end; ++u, Plan::next_unit(p, x)) c.status[x.b] = SPEC_ERR_TIMEOUT;
+  const int64_t worker0 = static_cast<int64_t>(blockIdx.x) * p.workers;
+  if (p.parts != nullptr && p.workers > 1) {
+    // Parts of one item that several of the block's workers hold become one part (or the output).
+    const int64_t size = part_floats(S::kRows * p.heads, D);
+    auto goes_on = [&](int w) {  // worker w begins inside an item
+      return w < p.workers && sm.plan.begin[w] < sm.plan.end[w] && sm.plan.from[w].tile != sm.plan.from[w].t0;
+    };
+#pragma unroll 1
+    for (int run = -1; run < p.workers; ++run) {
+      // An item that goes on from before the block, then those that its workers begin: workers w0 to w1,
+      // the first one's part in its first or later place.
+      const int w0 = max(run, 0), later = run < 0 ? 0 : 1, parts = later ? sm.plan.record[w0].parts : 0;
+      int w1 = w0;
+      if (later) {
+        w1 += min(parts, p.workers - w0) - 1;
+      } else if (goes_on(0)) {
+        while (sm.plan.record[w1].parts == 0 && goes_on(w1 + 1)) ++w1;
+      }
+      if (w1 <= w0) continue;
+      const Cursor x = sm.plan.from[w1];
+      float* const first = p.parts + (2 * (worker0 + w0) + later) * size;
+      const float* const rest = p.parts + 2 * worker0 * size;
+      const int used = min(S::kRows, x.count * p.group - x.k * S::kRows);
+      const bool done = later && w1 - w0 + 1 == parts;
+      auto part = [&](int i) { return i == 0 ? static_cast<const float*>(first) : rest + 2 * (w0 + i) * size; };
+#pragma unroll 1
+      for (int y = warp; y < used * p.heads; y += 2 * S::kWarps) {
+        const int h = y / used, r = y - h * used, in = h * S::kRows + r;
+        RowSum<D> sum;
+        sum.take(0, w1 - w0 + 1, 1, [&](int i) { return part(i) + static_cast<int64_t>(in) * D; },
+                 [&](int i) { return reinterpret_cast<const float2*>(part(i) + S::kRows * p.heads * D + 2 * in); });
+        __syncwarp();  // (the first part's numbers have been read)
+        if (done) {
+          const int row = x.k * S::kRows + r, col = row / p.group;
+          sum.finish(p, x.b, x.first + col, (x.h * p.heads + h) * p.group + row - col * p.group);
+        } else if (lane < RowSum<D>::kAcross) {
+#pragma unroll
+          for (int z = 0; z < RowSum<D>::kWide; ++z)
+            reinterpret_cast<float4*>(first + static_cast<int64_t>(in) * D)[lane + z * 32] = sum.a[z];
+          if (lane == 0)
+            *reinterpret_cast<float2*>(first + S::kRows * p.heads * D + 2 * in) = make_float2(sum.top, sum.sum);
+        }
+      }
     }
+  }
+  if (p.parts != nullptr && threadIdx.x < p.workers) {
+    // How many thread blocks hold parts.
+    PartRecord record = sm.plan.record[threadIdx.x];
+    if (record.parts > 0) record.parts = (static_cast<int>(threadIdx.x) + record.parts - 1) / p.workers + 1;
+    p.records[worker0 + threadIdx.x] = record;
+  }
+  if (sm.abort && threadIdx.x < p.workers && c.status != nullptr) {  // a wait gave up: all lanes of the block's units
+    Cursor x = sm.plan.from[threadIdx.x];
+    for (int64_t u = sm.plan.begin[threadIdx.x]; u < sm.plan.end[threadIdx.x]; ++u, Plan::next_unit(p, x))
+      c.status[x.b] = SPEC_ERR_TIMEOUT;
   }
 }
 
-// Joins the parts of items that were split.  blockIdx.x: the thread block that an item begins in;
-// blockIdx.y: a slice of its rows.
-constexpr int kJoinThreads = 128;
+// Joins the parts of items that were split over thread blocks.  blockIdx.x: the worker that an item
+// begins with; blockIdx.y: some of its rows, of which there are `rows` for a head, at most `used` of
+// them in use.  A warp takes a row; of many parts, all warps a share each.
+constexpr int kJoinThreads = 128, kJoinAlone = 32;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttendParams p, int rows, int slice) {
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttendParams p, int rows, int used, int per_block) {
+  constexpr int kWarps = kJoinThreads / 32;
+  using Sum = RowSum<D>;
+  __shared__ float4 sums[kWarps][D / 4];
+  __shared__ float2 stats[kWarps];
   griddep_wait();
   griddep_launch_dependents();
   const PartRecord record = p.records[blockIdx.x];
@@ -675,34 +785,53 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttendPa
   const CacheParams& c = p.c;
   int first, count, before;
   if (!cache_lane(c, record.lane, first, count, before)) return;
-  const int64_t size = part_floats(rows, D);
-  // Part i: the first block's later place, the others' first place.
-  const float* const base = p.parts + 2 * static_cast<int64_t>(blockIdx.x) * size;
-  auto part = [&](int i) { return base + (i == 0 ? size : 2 * i * size); };
-  for (int x = threadIdx.x; x < slice * (D / 4); x += kJoinThreads) {
-    const int r = blockIdx.y * slice + x / (D / 4), d = x % (D / 4) * 4;
-    const int row = record.block * rows + r, col = row / p.group;
-    if (r >= rows || col >= count || d >= c.dim) continue;
-    const int head = record.head * p.group + row - col * p.group;
-    float most = -INFINITY;
-#pragma unroll 4
-    for (int i = 0; i < record.parts; ++i) most = fmaxf(most, __ldcg(part(i) + rows * D + 2 * r));
-    float total = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < record.parts; ++i) {
-      const float2 ms = __ldcg(reinterpret_cast<const float2*>(part(i) + rows * D + 2 * r));
-      const float4 b = __ldcg(reinterpret_cast<const float4*>(part(i) + r * D + d));
-      const float f = ms.x == -INFINITY ? 0.f : ex2_approx(ms.x - most);
-      total = fmaf(ms.y, f, total);
-      a.x = fmaf(b.x, f, a.x), a.y = fmaf(b.y, f, a.y), a.z = fmaf(b.z, f, a.z), a.w = fmaf(b.w, f, a.w);
+  const int64_t size = part_floats(rows * p.heads, D);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Part 0: the first worker's later place; the others: the first place of the next thread blocks' first
+  // worker.
+  const float* const part0 = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + 1) * size;
+  const float* const others = p.parts + 2 * static_cast<int64_t>(blockIdx.x / p.workers) * p.workers * size;
+  auto part = [&](int i) { return i == 0 ? part0 : others + 2 * static_cast<int64_t>(i) * p.workers * size; };
+  const int y1 = min(static_cast<int>(blockIdx.y + 1) * per_block, used * p.heads);
+  const bool alone = record.parts <= kJoinAlone;
+#pragma unroll 1
+  for (int y = blockIdx.y * per_block + (alone ? warp : 0); y < y1; y += alone ? kWarps : 1) {
+    const int h = y / used, r = y - h * used, row = record.block * rows + r, col = row / p.group, in = h * rows + r;
+    if (col >= count) continue;  // (the same for all threads that go on together)
+    const int head = (record.head * p.heads + h) * p.group + row - col * p.group;
+    Sum sum;
+    sum.take(alone ? 0 : warp, record.parts, alone ? 1 : kWarps, [&](int i) { return part(i) + static_cast<int64_t>(in) * D; },
+             [&](int i) { return reinterpret_cast<const float2*>(part(i) + rows * p.heads * D + 2 * in); });
+    if (!alone) {
+      if (lane < Sum::kAcross)
+#pragma unroll
+        for (int z = 0; z < Sum::kWide; ++z) sums[warp][lane + z * 32] = sum.a[z];
+      if (lane == 0) stats[warp] = make_float2(sum.top, sum.sum);
+      __syncthreads();
+      if (warp == 0) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w].x);
+        Sum all{};
+        all.top = top;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = stats[w].x == -INFINITY ? 0.f : ex2_approx(stats[w].x - top);
+          all.sum = fmaf(stats[w].y, f, all.sum);
+          if (lane < Sum::kAcross)
+#pragma unroll
+            for (int z = 0; z < Sum::kWide; ++z) {
+              const float4 b = sums[w][lane + z * 32];
+              all.a[z].x = fmaf(b.x, f, all.a[z].x), all.a[z].y = fmaf(b.y, f, all.a[z].y);
+              all.a[z].z = fmaf(b.z, f, all.a[z].z), all.a[z].w = fmaf(b.w, f, all.a[z].w);
+            }
+        }
+        all.finish(p, record.lane, first + col, head);
+      }
+      __syncthreads();  // (sums and stats have been read)
+    } else {
+      sum.finish(p, record.lane, first + col, head);
     }
-    const float inv = 1.f / total;
-    a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
-    *reinterpret_cast<uint2*>(p.out + (first + col) * p.out_row + head * p.out_head + d) =
-        make_uint2(to_bf16x2(a.x, a.y), to_bf16x2(a.z, a.w));
-    if (!finite4(a)) lane_failed(c, record.lane, SPEC_ERR_NONFINITE);
-    if (p.lse != nullptr && d == 0) p.lse[(first + col) * p.lse_row + head] = (most + log2f(total)) * kLn2;
   }
 }
 

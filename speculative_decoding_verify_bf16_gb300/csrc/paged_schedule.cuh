@@ -1,14 +1,14 @@
 // paged_schedule.cuh -- how the attention over a paged cache is shared out to thread blocks.
 //
 // The query heads of one cache head and a lane's columns make up its rows: row r is column
-// r / group, query head r % group of the group.  An item is a block of rows of a lane and cache
-// head, a unit an item's step over a tile of positions.  All units stand in one order (lanes, heads,
-// row blocks, tiles); an item costs its units and EXTRA for what it takes to begin and to end it, and thread
-// block c of g takes what lies between total * c / g and total * (c + 1) / g of the costs: all have
-// the same work to within a unit, however ragged the lanes are.  An item whose units
-// fall to several blocks leaves partial sums, which a second launch joins; without scratch
-// memory for them the borders move up to the next item.  Lanes' lengths are read on the device,
-// so that a captured launch serves every round.
+// r / group, query head r % group of the group.  An item is a block of rows of a lane and of some cache heads,
+// a unit an item's step over a tile of positions.  All units stand in one order (lanes, heads,
+// row blocks, tiles); an item costs its units and EXTRA for what it takes to begin and to end it, and
+// worker c of g (a thread block, or some of its warps) takes what lies between total * c / g
+// and total * (c + 1) / g of the costs: all have the same work to within a unit, however ragged the
+// lanes are.  An item whose units fall to several workers leaves partial sums, which a second launch
+// joins; without scratch memory for them the borders move up to the next item.  Lanes' lengths are
+// read on the device, so that a captured launch serves every round.
 #pragma once
 
 #include <cstdint>
@@ -17,8 +17,9 @@
 
 namespace specv {
 
-// What a thread block leaves of an item that goes on in the next one: how many blocks hold parts of
-// it, this one the first.
+// What a worker leaves of an item that goes on in the next one: how many workers hold parts of
+// it, this one the first.  (parts 0: nothing.)  The parts of a thread block's workers are joined at its
+// end, into the place of the first of them.
 struct PartRecord {
   int32_t lane, head, block, parts;
 };
@@ -31,20 +32,23 @@ struct AttendParams {
   float* lse;
   int64_t lse_row;
   int32_t group, window;
-  float scale;          // times log2(e)
-  float* parts;         // two places for each thread block, part_floats() each; NULL: items stay whole
-  PartRecord* records;  // one for each thread block
+  int32_t heads, head_groups;  // cache heads of an item (a power of two), and how many such groups there are
+  int32_t workers;             // of a thread block
+  float scale;                 // times log2(e)
+  float* parts;                // two places for each worker, part_floats() each; NULL: items stay whole
+  PartRecord* records;         // one for each worker
 };
+constexpr int kMostWorkers = 8;  // of a thread block
 
-// Partial sums of a block of rows: the outputs' numerators [rows][size], then (maximum, sum) of
-// each row.
+// Partial sums of an item (rows: of all its heads): the outputs' numerators [rows][size], then
+// (maximum, sum) of each row.
 __host__ __device__ constexpr int64_t part_floats(int rows, int size) {
   return static_cast<int64_t>(rows) * (size + 2);
 }
 
 // A place in the order of units.  (b == lanes: past the end.)
 struct Cursor {
-  int b, h, k, blocks;       // lane, cache head, block of rows, blocks of the lane
+  int b, h, k, blocks;       // lane, group of cache heads, block of rows, blocks of the lane
   int first, count, before;  // the lane's rows, and tokens before them
   int lo, hi;                // positions that the block's rows see
   int tile, t0, t1;          // tiles of positions
@@ -56,7 +60,8 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
   return n / d;
 }
 
-template <int ROWS, int TILE, int EXTRA>
+// LEAST: costs that a worker takes at least (more workers leave more parts to join).
+template <int ROWS, int TILE, int EXTRA, int LEAST>
 struct Schedule {
   static __device__ __forceinline__ void set_block(const AttendParams& p, Cursor& x) {
     const int i0 = x.k * ROWS / p.group, i1 = min(x.count - 1, (x.k * ROWS + ROWS - 1) / p.group);
@@ -77,7 +82,7 @@ struct Schedule {
   static __device__ __forceinline__ void next_item(const AttendParams& p, Cursor& x) {
     if (++x.k < x.blocks) {
       set_block(p, x);
-    } else if (++x.h < p.c.kv_heads) {
+    } else if (++x.h < p.head_groups) {
       x.k = 0;
       set_block(p, x);
     } else {
@@ -103,21 +108,24 @@ struct Schedule {
     x.b = b;
     units = cost = 0;
     if (!try_lane(p, x)) return;
-    units = head_units(p, x) * p.c.kv_heads;
-    cost = units + static_cast<int64_t>(EXTRA) * x.blocks * p.c.kv_heads;
+    units = head_units(p, x) * p.head_groups;
+    cost = units + static_cast<int64_t>(EXTRA) * x.blocks * p.head_groups;
   }
 
   struct Shared {
     int64_t units[32], cost[32];
-    int64_t begin, end;  // units of this thread block
-    Cursor from;         // at the first of them
-    PartRecord record;
+    int64_t begin[kMostWorkers], end[kMostWorkers];  // units of this thread block's workers
+    Cursor from[kMostWorkers];                       // at the first of them
+    PartRecord record[kMostWorkers];
   };
 
-  // Thread blocks that get work: each a cost of one at least.
-  static __device__ __forceinline__ int64_t blocks_for(int64_t total, int64_t grid) { return total < grid ? total : grid; }
-  // The thread block that a cost falls to.
-  static __device__ __forceinline__ int block_of(int64_t u, int64_t total, int64_t g) {
+  // Workers that get work.
+  static __device__ __forceinline__ int64_t workers_for(int64_t total, int64_t most) {
+    const int64_t n = (total + LEAST - 1) / LEAST;
+    return n < most ? n : most;
+  }
+  // The worker that a cost falls to.
+  static __device__ __forceinline__ int worker_of(int64_t u, int64_t total, int64_t g) {
     return static_cast<int>(quotient((u + 1) * g - 1, total));
   }
 
@@ -157,7 +165,7 @@ struct Schedule {
     return before + left - EXTRA;
   }
 
-  // The whole thread block: its range of units and the cursor at the first of them.
+  // The whole thread block: its workers' ranges of units and the cursors at the first of them.
   static __device__ void plan(const AttendParams& p, Shared& sh) {
     const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.c.lanes + threads - 1) / threads;
@@ -181,9 +189,9 @@ struct Schedule {
       sh.units[warp] = run_units;
       sh.cost[warp] = run_cost;
     }
-    if (threadIdx.x == 0) {
-      sh.begin = sh.end = 0;
-      sh.record.parts = 0;
+    if (threadIdx.x < kMostWorkers) {
+      sh.begin[threadIdx.x] = sh.end[threadIdx.x] = 0;
+      sh.record[threadIdx.x].parts = 0;
     }
     __syncthreads();
     int64_t total = 0, all_units = 0, before = run_cost - cost, before_units = run_units - units;
@@ -193,29 +201,30 @@ struct Schedule {
       total += sh.cost[w];
       all_units += sh.units[w];
     }
-    const int64_t g = blocks_for(total, gridDim.x), c = blockIdx.x;
-    if (c < g) {
-      const int64_t border[2] = {quotient(total * c, g), quotient(total * (c + 1), g)};
+    const int64_t g = workers_for(total, static_cast<int64_t>(gridDim.x) * p.workers);
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * p.workers;
+    int64_t last = 0;
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        const int64_t u = border[i];
-        if (u == total) {
-          if (threadIdx.x == 0) sh.end = all_units;
-        } else if (u >= before && u < before + cost) {  // the border lies in one of this thread's lanes
-          Cursor x;
-          int64_t in, all;
-          const int64_t at = before_units + find(p, b0, u - before, x, in, all);
-          if (i == 0) {
-            sh.begin = at;
-            sh.from = x;
-          } else {
-            sh.end = at;
-            // An item that goes on, and that this block begins.
-            if (p.parts != nullptr && in > EXTRA && border[0] <= u - in + EXTRA)
-              sh.record = {x.b, x.h, x.k, block_of(u - in + all - 1, total, g) - static_cast<int>(c) + 1};
-          }
+    for (int i = 0; i <= p.workers && c + i <= g && c < g; ++i) {
+      const int64_t u = quotient(total * (c + i), g);  // where worker i begins and the one before it ends
+      if (u == total) {
+        if (threadIdx.x == 0 && i > 0) sh.end[i - 1] = all_units;
+      } else if (u >= before && u < before + cost) {  // in one of this thread's lanes
+        Cursor x;
+        int64_t in, all;
+        const int64_t at = before_units + find(p, b0, u - before, x, in, all);
+        if (i < p.workers) {
+          sh.begin[i] = at;
+          sh.from[i] = x;
+        }
+        if (i > 0) {
+          sh.end[i - 1] = at;
+          // An item that goes on, and that worker i - 1 begins.
+          if (p.parts != nullptr && in > EXTRA && last <= u - in + EXTRA)
+            sh.record[i - 1] = {x.b, x.h, x.k, worker_of(u - in + all - 1, total, g) - static_cast<int>(c + i - 1) + 1};
         }
       }
+      last = u;
     }
     __syncthreads();
   }

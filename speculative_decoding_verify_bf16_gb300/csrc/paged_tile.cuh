@@ -49,7 +49,7 @@ struct TileShape {
   static constexpr int kBytes = kTileHalf * (D / 64);
   static constexpr int kStages = D > 64 ? 5 : 8;
   static constexpr int kExtra = 2;  // an item's beginning and end, in units
-  using Plan = Schedule<kRows, kTile, kExtra>;
+  using Plan = Schedule<kRows, kTile, kExtra, 1>;
 };
 
 template <typename S>
@@ -114,9 +114,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       if (!cache_lane(c, b, first, count, before)) lane_failed(c, b, SPEC_ERR_LAYOUT);
     }
   const uint32_t tm = sm.tmem;
-  const int64_t begin = sm.plan.begin, end = sm.plan.end;
+  const int64_t begin = sm.plan.begin[0], end = sm.plan.end[0];
   int64_t left = begin < end ? end - begin : 0;
-  Cursor at = sm.plan.from;
+  Cursor at = sm.plan.from[0];
 
   if (warp < 8) {
     // ------------------------------------------------------------ rows of a tile
@@ -558,13 +558,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       mma_commit(lead, &sm.drain);
       mbar_wait_bounded(&sm.drain, 0);
       __syncwarp();
-      if (lane == 0 && p.parts != nullptr) p.records[blockIdx.x] = sm.plan.record;
+      if (lane == 0 && p.parts != nullptr) p.records[blockIdx.x] = sm.plan.record[0];
     }
   }
   __syncthreads();
   // A wait gave up: all lanes of the block's range.
   if (sm.abort && threadIdx.x == 0) {
-    at = sm.plan.from;
+    at = sm.plan.from[0];
     for (int64_t u = begin; u < end; ++u, Plan::next_unit(p, at))
       if (c.status != nullptr) c.status[at.b] = SPEC_ERR_TIMEOUT;
   }

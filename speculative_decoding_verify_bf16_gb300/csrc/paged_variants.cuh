@@ -9,11 +9,11 @@ namespace specv {
 
 template <typename S>
 PagedVariant rows_variant() {
-  return {reinterpret_cast<void*>(&paged_rows_kernel<S>), S::kRows, S::D, S::kThreads, static_cast<int>(sizeof(RowsSmem<S>)), S::kRegs};
+  return {reinterpret_cast<void*>(&paged_rows_kernel<S>), S::kRows, S::D, S::kWarps, S::kThreads, static_cast<int>(sizeof(RowsSmem<S>)), S::kRegs};
 }
 template <typename S>
 PagedVariant tile_variant() {
-  return {reinterpret_cast<void*>(&paged_tile_kernel<S>), S::kRows, S::D, kTileThreads, static_cast<int>(sizeof(TileSmem<S>)), kTileRegs};
+  return {reinterpret_cast<void*>(&paged_tile_kernel<S>), S::kRows, S::D, 1, kTileThreads, static_cast<int>(sizeof(TileSmem<S>)), kTileRegs};
 }
 
 template <int TYPE>
