@@ -33,24 +33,25 @@ struct CacheParams {
   int32_t most;  // most positions of a lane
 };
 
-// p / page_size for 0 <= p < 2^31.  With 2^s < page_size < 2^(s + 1) and the magic number m =
-// floor(2^(32 + s) / page_size) + 1, p m / 2^(32 + s) exceeds p / page_size by at most p / 2^(32 + s)
-// < 1 / page_size, so its whole part is the same.  Powers of two have magic number 0.
-__host__ __device__ inline int32_t page_of(const CacheParams& c, int32_t p) {
+// n / d for 0 <= n < 2^31 by a product.  With 2^s < d < 2^(s + 1) and the magic number m =
+// floor(2^(32 + s) / d) + 1, n m / 2^(32 + s) exceeds n / d by at most n / 2^(32 + s) < 1 / d, so
+// its whole part is the same.  Powers of two have magic number 0.
+__host__ __device__ inline int32_t by_magic(int32_t n, uint32_t magic, uint32_t shift) {
 #ifdef __CUDA_ARCH__
-  return c.page_magic == 0 ? p >> c.page_shift : static_cast<int32_t>(__umulhi(p, c.page_magic) >> c.page_shift);
+  return magic == 0 ? n >> shift : static_cast<int32_t>(__umulhi(n, magic) >> shift);
 #else
-  return c.page_magic == 0 ? p >> c.page_shift
-                           : static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(p)) * c.page_magic >> 32) >> c.page_shift);
+  return magic == 0 ? n >> shift : static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * magic >> 32) >> shift);
 #endif
 }
+inline void set_magic(int32_t d, uint32_t& magic, uint32_t& shift) {
+  shift = 0;
+  while ((int64_t{2} << shift) <= d) ++shift;
+  magic = (d & (d - 1)) == 0 ? 0u : static_cast<uint32_t>((uint64_t{1} << (32 + shift)) / static_cast<uint32_t>(d)) + 1u;
+}
+__host__ __device__ inline int32_t page_of(const CacheParams& c, int32_t p) { return by_magic(p, c.page_magic, c.page_shift); }
 inline void set_page_size(CacheParams& c, int32_t page_size) {
   c.page_size = page_size;
-  c.page_shift = 0;
-  while ((int64_t{2} << c.page_shift) <= page_size) ++c.page_shift;
-  c.page_magic = (page_size & (page_size - 1)) == 0
-                     ? 0u
-                     : static_cast<uint32_t>((uint64_t{1} << (32 + c.page_shift)) / static_cast<uint32_t>(page_size)) + 1u;
+  set_magic(page_size, c.page_magic, c.page_shift);
 }
 
 // A lane's rows and the tokens before them; false for a lane that is laid out wrongly.

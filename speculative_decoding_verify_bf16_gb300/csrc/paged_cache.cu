@@ -267,6 +267,7 @@ int spec_paged_attention(const spec_paged_attention_args* a, void* stream) {
   p.lse = a->lse;
   p.lse_row = a->lse_row_stride;
   p.group = a->q_heads / p.c.kv_heads;
+  specv::set_magic(p.group, p.group_magic, p.group_shift);
   p.window = a->window;
   p.scale = a->scale * 1.44269504088896f;
   if (a->max_context > 0 && a->max_context < p.c.most) p.c.most = a->max_context;

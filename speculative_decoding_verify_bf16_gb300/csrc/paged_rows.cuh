@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
 #pragma unroll 1
         for (int m = 0; m < MT && acquire(); ++m) {
           constexpr int kQUnits = D / 8, kQAtOnce = kQUnits > 32 ? 1 : 32 / kQUnits;
-          const int r = at.k * S::kRows + m * 16 + (lane & 15), col = r / p.group;
+          const int r = at.k * S::kRows + m * 16 + (lane & 15), col = column_of(p, r);
           int64_t row = -1;
           if (col < at.count)
             row = (at.first + col) * p.q_row + ((at.h * p.heads + head_in) * p.group + r - col * p.group) * p.q_head;
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
         const uint32_t rows = ring_at + place * S::kPlace;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          last[m][i] = at.before + (at.k * S::kRows + m * 16 + g + 8 * i) / p.group + 1;
+          last[m][i] = at.before + column_of(p, at.k * S::kRows + m * 16 + g + 8 * i) + 1;
           top[m][i] = -INFINITY;
           sum[m][i] = 0.f;
         }
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
           for (int i = 0; i < 4; ++i) o[m][n][i] = 0.f;
       }
       if (!ok) break;
-      const int seen_first = at.before + at.k * S::kRows / p.group;  // the block's first column's position
+      const int seen_first = at.before + column_of(p, at.k * S::kRows);  // the block's first column's position
 #pragma unroll 1
       for (int unit = 0; unit < n_units; ++unit, ++at.tile) {
         const int k_place = place;
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
           float s = sum[m][i];
           s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
           s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-          const int r = m * 16 + g + 8 * i, row = at.k * S::kRows + r, col = row / p.group;
+          const int r = m * 16 + g + 8 * i, row = at.k * S::kRows + r, col = column_of(p, row);
           if (col >= at.count) continue;
           const int q_head = head * p.group + row - col * p.group;
           __nv_bfloat16* const out = p.out + (at.first + col) * p.out_row + q_head * p.out_head;
@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
                  [&](int i) { return reinterpret_cast<const float2*>(part(i) + S::kRows * p.heads * D + 2 * in); });
         __syncwarp();  // (the first part's numbers have been read)
         if (done) {
-          const int row = x.k * S::kRows + r, col = row / p.group;
+          const int row = x.k * S::kRows + r, col = column_of(p, row);
           sum.finish(p, x.b, x.first + col, (x.h * p.heads + h) * p.group + row - col * p.group);
         } else if (lane < RowSum<D>::kAcross) {
 #pragma unroll
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttendPa
   const bool alone = record.parts <= kJoinAlone;
 #pragma unroll 1
   for (int y = blockIdx.y * per_block + (alone ? warp : 0); y < y1; y += alone ? kWarps : 1) {
-    const int h = y / used, r = y - h * used, row = record.block * rows + r, col = row / p.group, in = h * rows + r;
+    const int h = y / used, r = y - h * used, row = record.block * rows + r, col = column_of(p, row), in = h * rows + r;
     if (col >= count) continue;  // (the same for all threads that go on together)
     const int head = (record.head * p.heads + h) * p.group + row - col * p.group;
     Sum sum;

@@ -32,12 +32,14 @@ struct AttendParams {
   float* lse;
   int64_t lse_row;
   int32_t group, window;
+  uint32_t group_magic, group_shift;
   int32_t heads, head_groups;  // cache heads of an item (a power of two), and how many such groups there are
   int32_t workers;             // of a thread block
   float scale;                 // times log2(e)
   float* parts;                // two places for each worker, part_floats() each; NULL: items stay whole
   PartRecord* records;         // one for each worker
 };
+__device__ __forceinline__ int column_of(const AttendParams& p, int row) { return by_magic(row, p.group_magic, p.group_shift); }
 constexpr int kMostWorkers = 8;  // of a thread block
 
 // Partial sums of an item (rows: of all its heads): the outputs' numerators [rows][size], then
@@ -64,7 +66,7 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
 template <int ROWS, int TILE, int EXTRA, int LEAST>
 struct Schedule {
   static __device__ __forceinline__ void set_block(const AttendParams& p, Cursor& x) {
-    const int i0 = x.k * ROWS / p.group, i1 = min(x.count - 1, (x.k * ROWS + ROWS - 1) / p.group);
+    const int i0 = column_of(p, x.k * ROWS), i1 = min(x.count - 1, column_of(p, x.k * ROWS + ROWS - 1));
     x.hi = x.before + i1 + 1;
     x.lo = p.window > 0 ? max(0, x.before + i0 - p.window + 1) : 0;
     x.t0 = x.lo / TILE;
@@ -93,25 +95,6 @@ struct Schedule {
   static __device__ __forceinline__ void next_unit(const AttendParams& p, Cursor& x) {
     if (++x.tile == x.t1) next_item(p, x);
   }
-  // Units of one head of the lane at x (whose block moves on the way).
-  static __device__ __forceinline__ int64_t head_units(const AttendParams& p, Cursor& x) {
-    int64_t n = 0;
-    for (x.k = 0; x.k < x.blocks; ++x.k) {
-      set_block(p, x);
-      n += x.t1 - x.t0;
-    }
-    return n;
-  }
-  // Units and costs of lane b.
-  static __device__ __forceinline__ void lane_sums(const AttendParams& p, int b, int64_t& units, int64_t& cost) {
-    Cursor x;
-    x.b = b;
-    units = cost = 0;
-    if (!try_lane(p, x)) return;
-    units = head_units(p, x) * p.head_groups;
-    cost = units + static_cast<int64_t>(EXTRA) * x.blocks * p.head_groups;
-  }
-
   struct Shared {
     int64_t units[32], cost[32];
     int64_t begin[kMostWorkers], end[kMostWorkers];  // units of this thread block's workers
@@ -129,31 +112,22 @@ struct Schedule {
     return static_cast<int>(quotient((u + 1) * g - 1, total));
   }
 
-  // What lies `left` costs behind the beginning of lane b0: the cursor there (in an item's EXTRA: at its
-  // first unit; where items stay whole and one has begun: at the next), and the units
-  // before it.  `in`: costs of the item up to there, `all`: its costs.
-  static __device__ __forceinline__ int64_t find(const AttendParams& p, int b0, int64_t left, Cursor& x, int64_t& in,
-                                                 int64_t& all) {
-    int64_t before = 0;
-    x.b = b0;
-    for (;; ++x.b) {
-      int64_t units, cost;
-      lane_sums(p, x.b, units, cost);
-      if (left < cost) break;
-      left -= cost;
-      before += units;
-    }
-    try_lane(p, x);
-    const int64_t per_units = head_units(p, x), per_cost = per_units + static_cast<int64_t>(EXTRA) * x.blocks;
+  // What lies `left` costs behind the beginning of the lane at x (at its first item; `units` and `cost`: all of
+  // the lane's): the cursor there (in an item's EXTRA: at its first unit; where items stay whole and one has
+  // begun: at the next), and the units before it.  `in`: costs of the item up to there, `all`: its costs.
+  static __device__ __forceinline__ int64_t find(const AttendParams& p, int64_t left, int64_t units, int64_t cost, Cursor& x,
+                                                 int64_t& in, int64_t& all) {
+    all = x.t1 - x.t0 + EXTRA;
+    const bool one = x.blocks == 1;
+    const int64_t per_cost = one ? all : quotient(cost, p.head_groups);
     x.h = static_cast<int>(quotient(left, per_cost));
     left -= x.h * per_cost;
-    before += x.h * per_units;
-    for (x.k = 0;; ++x.k) {
-      set_block(p, x);
-      all = x.t1 - x.t0 + EXTRA;
-      if (left < all) break;
+    int64_t before = x.h * (one ? all - EXTRA : quotient(units, p.head_groups));
+    for (; !one && left >= all; all = x.t1 - x.t0 + EXTRA) {
       left -= all;
       before += all - EXTRA;
+      ++x.k;
+      set_block(p, x);
     }
     in = left;
     if (left <= EXTRA) return before;
@@ -165,54 +139,20 @@ struct Schedule {
     return before + left - EXTRA;
   }
 
-  // The whole thread block: its workers' ranges of units and the cursors at the first of them.
-  static __device__ void plan(const AttendParams& p, Shared& sh) {
-    const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (p.c.lanes + threads - 1) / threads;
-    const int b0 = min(p.c.lanes, static_cast<int>(threadIdx.x) * per), b1 = min(p.c.lanes, b0 + per);
-    int64_t units = 0, cost = 0;
-    for (int b = b0; b < b1; ++b) {
-      int64_t u, n;
-      lane_sums(p, b, u, n);
-      units += u;
-      cost += n;
-    }
-    int64_t run_units = units, run_cost = cost;
-    if (warp * 32 * per < p.c.lanes)
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, run_units, d), n = __shfl_up_sync(0xFFFFFFFFu, run_cost, d);
-        run_units += lane >= d ? u : 0;
-        run_cost += lane >= d ? n : 0;
-      }
-    if (lane == 31) {
-      sh.units[warp] = run_units;
-      sh.cost[warp] = run_cost;
-    }
-    if (threadIdx.x < kMostWorkers) {
-      sh.begin[threadIdx.x] = sh.end[threadIdx.x] = 0;
-      sh.record[threadIdx.x].parts = 0;
-    }
-    __syncthreads();
-    int64_t total = 0, all_units = 0, before = run_cost - cost, before_units = run_units - units;
-    for (int w = 0; w < threads / 32; ++w) {
-      before += w < warp ? sh.cost[w] : 0;
-      before_units += w < warp ? sh.units[w] : 0;
-      total += sh.cost[w];
-      all_units += sh.units[w];
-    }
+  // The borders of this block's workers that lie in the lane at x, which begins at `before`.
+  static __device__ __forceinline__ void mark(const AttendParams& p, Shared& sh, const Cursor& lane, bool on, int64_t before,
+                                              int64_t before_units, int64_t units, int64_t cost, int64_t total) {
+    if (!on || cost == 0) return;
     const int64_t g = workers_for(total, static_cast<int64_t>(gridDim.x) * p.workers);
     const int64_t c = static_cast<int64_t>(blockIdx.x) * p.workers;
     int64_t last = 0;
 #pragma unroll 1
     for (int i = 0; i <= p.workers && c + i <= g && c < g; ++i) {
       const int64_t u = quotient(total * (c + i), g);  // where worker i begins and the one before it ends
-      if (u == total) {
-        if (threadIdx.x == 0 && i > 0) sh.end[i - 1] = all_units;
-      } else if (u >= before && u < before + cost) {  // in one of this thread's lanes
-        Cursor x;
+      if (u >= before && u < before + cost) {
+        Cursor x = lane;
         int64_t in, all;
-        const int64_t at = before_units + find(p, b0, u - before, x, in, all);
+        const int64_t at = before_units + find(p, u - before, units, cost, x, in, all);
         if (i < p.workers) {
           sh.begin[i] = at;
           sh.from[i] = x;
@@ -226,6 +166,78 @@ struct Schedule {
       }
       last = u;
     }
+  }
+
+  // The whole thread block: its workers' ranges of units and the cursors at the first of them.  (One
+  // launch's first instructions come from far: few of them, and each thread reads one lane.)
+  static __device__ void plan(const AttendParams& p, Shared& sh) {
+    const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x < kMostWorkers) {
+      sh.begin[threadIdx.x] = sh.end[threadIdx.x] = 0;
+      sh.record[threadIdx.x].parts = 0;
+    }
+    // Lanes in rounds of as many as there are threads: first all for the sums, then, unless that was
+    // one round, again for the borders.
+    int64_t total = 0, all_units = 0;
+#pragma unroll 1
+    for (int find_at = p.c.lanes <= threads ? 1 : 0, again = find_at; again < 2; find_at = 1, ++again) {
+      int64_t base = 0, base_units = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < p.c.lanes; b0 += threads) {
+        Cursor x;
+        x.b = b0 + threadIdx.x;
+        int64_t units = 0, cost = 0, of_units = 0, of_cost = 0;  // of the lane; of the warp's lanes before it
+        const int warps = min(threads, p.c.lanes - b0 + 31) / 32;  // that have lanes
+        if (warp < warps) {
+          if (x.b < p.c.lanes && try_lane(p, x)) {
+            int64_t n = x.t1 - x.t0;
+            if (x.blocks > 1) {
+#pragma unroll 1
+              while (++x.k < x.blocks) {
+                set_block(p, x);
+                n += x.t1 - x.t0;
+              }
+              x.k = 0;
+              set_block(p, x);
+            }
+            units = n * p.head_groups;
+            cost = units + static_cast<int64_t>(EXTRA) * x.blocks * p.head_groups;
+          }
+          int64_t run_units = units, run_cost = cost;
+#pragma unroll 1
+          for (int d = 1; d < 32; d <<= 1) {
+            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, run_units, d), n = __shfl_up_sync(0xFFFFFFFFu, run_cost, d);
+            run_units += lane >= d ? u : 0;
+            run_cost += lane >= d ? n : 0;
+          }
+          if (lane == 31) {
+            sh.units[warp] = run_units;
+            sh.cost[warp] = run_cost;
+          }
+          of_units = run_units - units;
+          of_cost = run_cost - cost;
+        }
+        __syncthreads();
+        int64_t before = base, before_units = base_units;
+#pragma unroll 1
+        for (int w = 0; w < warps; ++w) {
+          before += w < warp ? sh.cost[w] : 0;
+          before_units += w < warp ? sh.units[w] : 0;
+          base += sh.cost[w];
+          base_units += sh.units[w];
+        }
+        if (b0 + threads >= p.c.lanes) {
+          total = base;
+          all_units = base_units;
+        }
+        if (find_at == 1) mark(p, sh, x, warp < warps, before + of_cost, before_units + of_units, units, cost, total);
+        if (p.c.lanes > threads) __syncthreads();  // (the sums have been read)
+      }
+    }
+    // The last border is nobody's lane's.
+    const int64_t most = static_cast<int64_t>(gridDim.x) * p.workers, g = workers_for(total, most);
+    const int64_t last = g - static_cast<int64_t>(blockIdx.x) * p.workers;  // workers from this block's first on
+    if (threadIdx.x == 0 && total > 0 && last >= 1 && last <= p.workers) sh.end[last - 1] = all_units;
     __syncthreads();
   }
 };

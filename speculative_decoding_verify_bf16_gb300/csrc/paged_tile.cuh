@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
     // This thread's row of q.  (A tile without rows is left out.)
     auto has_rows = [&] { return at.count * p.group - at.k * S::kRows > w * 128; };
     auto load_q = [&] {
-      const int r = at.k * S::kRows + w * 128 + row, col = r / p.group;
+      const int r = at.k * S::kRows + w * 128 + row, col = column_of(p, r);
       const bool on = col < at.count;
       const __nv_bfloat16* const from =
           p.q + (on ? (at.first + col) * p.q_row + (at.h * p.group + r - col * p.group) * p.q_head : 0);
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         if (left > 0 && has_rows()) load_q();
         continue;
       }
-      const int r = at.k * S::kRows + w * 128 + row, col = r / p.group;
+      const int r = at.k * S::kRows + w * 128 + row, col = column_of(p, r);
       const int lim = at.before + col + 1, low = p.window > 0 ? lim - p.window : 0;
       float top = -INFINITY, sum = 0.f;
       int p0 = at.tile * S::kTile;
