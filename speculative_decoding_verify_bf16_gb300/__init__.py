@@ -10,7 +10,6 @@ fallback.
 import ctypes
 import os
 import struct
-from typing import NamedTuple, Optional
 
 import torch
 
@@ -751,15 +750,46 @@ SPEC_CACHE_MOST_EXP = 48
 _CACHE_TYPES = {torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.int8: 3}
 
 
-class PagedCache(NamedTuple):
+class PagedCache:
     """Keys and values [pages, page_size, kv_heads, dim] (bf16, float8_e4m3fn or int8; any
     strides, the same for both, with a contiguous last dimension) and, for the 8-bit types,
-    their exponents' bytes, uint8 [pages, page_size, kv_heads]."""
+    their exponents' bytes, uint8 [pages, page_size, kv_heads].  Checked once, when it is made;
+    ``k, v, k_exps, v_exps = cache`` gives the tensors back."""
 
-    k: torch.Tensor
-    v: torch.Tensor
-    k_exps: Optional[torch.Tensor] = None
-    v_exps: Optional[torch.Tensor] = None
+    __slots__ = ("_tensors", "_pools", "_sizes", "_heads", "_code", "_device")
+
+    def __init__(self, k, v, k_exps=None, v_exps=None):
+        code = _CACHE_TYPES.get(k.dtype)
+        shape, strides, dev = k.shape, k.stride(), k.get_device()
+        if code is None or len(shape) != 4:
+            raise ValueError("k must be a bf16, float8_e4m3fn or int8 [pages, page_size, kv_heads, dim] tensor")
+        if v.dtype is not k.dtype or v.shape != shape or v.stride() != strides or v.get_device() != dev:
+            raise ValueError("v must match k's dtype, device, shape and strides")
+        if strides[3] != 1:
+            raise ValueError("k and v must have unit inner stride")
+        ek = ev = 0
+        es = (0, 0, 0)
+        if code != 1:
+            for t, name in ((k_exps, "k_exps"), (v_exps, "v_exps")):
+                if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or t.get_device() != dev or t.shape != shape[:3]:
+                    raise ValueError(f"{name} must be a uint8 [pages, page_size, kv_heads] tensor on k's device")
+            es = k_exps.stride()
+            if v_exps.stride() != es:
+                raise ValueError("v_exps must have k_exps' strides")
+            ek, ev = k_exps.data_ptr(), v_exps.data_ptr()
+        elif k_exps is not None or v_exps is not None:
+            raise ValueError("a bf16 cache has no exponents")
+        self._tensors = (k, v, k_exps, v_exps)
+        self._pools = (k.data_ptr(), v.data_ptr(), *strides[:3], ek, ev, *es)
+        self._sizes, self._heads, self._code, self._device = shape[:2], shape[2:], code, dev
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_exps = property(lambda self: self._tensors[2])
+    v_exps = property(lambda self: self._tensors[3])
+
+    def __iter__(self):
+        return iter(self._tensors)
 
 
 def new_paged_cache(pages, page_size, kv_heads, dim, dtype, device):
@@ -776,41 +806,37 @@ def new_paged_cache(pages, page_size, kv_heads, dim, dtype, device):
 
 
 def _cache_fields(cache, block_tables, cached_lens, row_offsets, lane_status, rows, max_len, dev):
-    """The fields of a spec_paged_cache, in order, and (kv_heads, dim)."""
-    k, v, k_exps, v_exps = cache
-    code = _CACHE_TYPES.get(k.dtype)
-    shape, strides = k.shape, k.stride()
-    if code is None or len(shape) != 4 or k.get_device() != dev:
-        raise ValueError(f"cache.k must be a bf16, float8_e4m3fn or int8 [pages, page_size, kv_heads, dim] tensor on cuda:{dev}")
-    if v.dtype is not k.dtype or v.shape != shape or v.stride() != strides or v.get_device() != dev:
-        raise ValueError("cache.v must match cache.k's dtype, device, shape and strides")
-    if strides[3] != 1:
-        raise ValueError("cache.k and cache.v must have unit inner stride")
-    ek = ev = 0
-    es = (0, 0, 0)
-    if code != 1:
-        for t, name in ((k_exps, "k_exps"), (v_exps, "v_exps")):
-            if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or t.get_device() != dev or t.shape != shape[:3]:
-                raise ValueError(f"cache.{name} must be a uint8 [pages, page_size, kv_heads] tensor on cuda:{dev}")
-        es = k_exps.stride()
-        if v_exps.stride() != es:
-            raise ValueError("cache.v_exps must have cache.k_exps' strides")
-        ek, ev = k_exps.data_ptr(), v_exps.data_ptr()
-    elif k_exps is not None or v_exps is not None:
-        raise ValueError("a bf16 cache has no exponents")
+    """The fields of a spec_paged_cache, in order."""
+    if not isinstance(cache, PagedCache) or cache._device != dev:
+        raise ValueError(f"cache must be a PagedCache on cuda:{dev}, like the rows")
     if row_offsets is None or cached_lens is None or block_tables is None:
         raise ValueError("block_tables, cached_lens and row_offsets are required")
     offsets = _at(row_offsets, "row_offsets", torch.int32, dev, 1)
     lanes = row_offsets.numel() - 1
-    if block_tables.dtype is not torch.int32 or block_tables.get_device() != dev or block_tables.dim() != 2 \
-            or block_tables.shape[0] != lanes or (block_tables.stride(1) != 1 and block_tables.shape[1] > 1 and lanes > 0):
-        raise ValueError(f"block_tables must be an int32 [lanes, width] tensor on cuda:{dev} with unit inner stride")
-    width = block_tables.shape[1]
-    stride = block_tables.stride(0) if lanes > 1 else max(block_tables.stride(0), width)
-    return (k.data_ptr(), v.data_ptr(), strides[0], strides[1], strides[2], ek, ev, es[0], es[1], es[2],
-            block_tables.data_ptr(), stride, _at(cached_lens, "cached_lens", torch.int32, dev, lanes), offsets,
-            _at(lane_status, "lane_status", torch.int32, dev, lanes), code, shape[0], shape[1], width, lanes, rows, max_len,
-            shape[2], shape[3])
+    shape = block_tables.shape
+    if block_tables.dtype is not torch.int32 or block_tables.get_device() != dev or len(shape) != 2 or shape[0] != lanes:
+        raise ValueError(f"block_tables must be an int32 [lanes, width] tensor on cuda:{dev}")
+    width, (stride, inner) = shape[1], block_tables.stride()
+    if inner != 1 and width > 1 and lanes > 0:
+        raise ValueError("block_tables must have unit inner stride")
+    if lanes <= 1 and stride < width:  # (a size of one leaves its stride free)
+        stride = width
+    pages, page_size = cache._sizes
+    kv_heads, dim = cache._heads
+    return (*cache._pools, block_tables.data_ptr(), stride, _at(cached_lens, "cached_lens", torch.int32, dev, lanes), offsets,
+            _at(lane_status, "lane_status", torch.int32, dev, lanes), cache._code, pages, page_size, width, lanes, rows,
+            max_len, kv_heads, dim)
+
+
+def _call(entry, what, args, stream, dev):
+    """The library's call on the tensors' device, whichever is the current one."""
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            rc = entry(args, _raw_stream(stream, dev))
+    else:
+        rc = entry(args, _raw_stream(stream, dev))
+    if rc != SPEC_OK:
+        raise SpecError(rc, what)
 
 
 def _cache_rows_call(entry, what, cache, block_tables, cached_lens, row_offsets, k, v, max_len, lane_status, stream):
@@ -824,15 +850,13 @@ def _cache_rows_call(entry, what, cache, block_tables, cached_lens, row_offsets,
     if ks[2] != 1 or vs[2] != 1:
         raise ValueError("k and v must have unit inner stride")
     fields = _cache_fields(cache, block_tables, cached_lens, row_offsets, lane_status, shape[0], int(max_len), dev)
-    if shape[1:] != fields[-2:]:
+    if shape[1:] != cache._heads:
         raise ValueError("k and v must have the cache's heads and head size")
     try:
         args = _CACHE_ROWS_LAYOUT.pack(*fields, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], code)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"{what}: a size does not fit 32 bits ({e})") from None
-    rc = entry(args, _raw_stream(stream, dev))
-    if rc != SPEC_OK:
-        raise SpecError(rc, what)
+    _call(entry, what, args, stream, dev)
 
 
 def spec_cache_write(cache, block_tables, cached_lens, row_offsets, k, v, max_len, lane_status=None, stream=None):
@@ -906,7 +930,7 @@ def spec_paged_attention(q, cache, block_tables, cached_lens, row_offsets, out, 
     max_len = int(max_len)
     fields = _cache_fields(cache, block_tables, cached_lens, row_offsets, lane_status, rows, max_len, dev)
     kv = fields[-2]
-    if dim != fields[-1] or kv == 0 or hq == 0 or hq % kv:
+    if dim != fields[-1] or kv == 0 or hq == 0 or hq % kv:  # (checked again by the library, but for dim)
         raise ValueError("q must have the cache's head size and a multiple of its heads")
     lse_ptr = lse_row = 0
     if lse is not None:
@@ -924,6 +948,4 @@ def spec_paged_attention(q, cache, block_tables, cached_lens, row_offsets, out, 
             int(max_context), dim ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.numel())
     except (struct.error, OverflowError) as e:
         raise ValueError(f"spec_paged_attention: a size does not fit 32 bits, or scale is no number ({e})") from None
-    rc = lib.spec_paged_attention(args, _raw_stream(stream, dev))
-    if rc != SPEC_OK:
-        raise SpecError(rc, "spec_paged_attention")
+    _call(lib.spec_paged_attention, "spec_paged_attention", args, stream, dev)

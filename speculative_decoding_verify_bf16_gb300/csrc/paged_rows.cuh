@@ -116,11 +116,11 @@ struct RowsShape {
   // Registers a thread, and what a launch must bring (0: they are not shared out).
   static constexpr int kRegsRows = kWarps == 8 ? 192 : 0, kRegsCopy = kWarps == 8 ? 64 : 0;
   static constexpr int kRegs = kWarps / 4 * (kRegsRows + kRegsCopy);
-  static constexpr int kTokens = kEight ? 32 : 16;  // of a unit
+  static constexpr int kTokens = kEight || D <= 64 ? 32 : 16;  // of a unit
   static constexpr int kRowBytes = D * (kEight ? 1 : 2);
   // A place of the ring: the keys or the values of a unit, or 16 rows of q; with 8 bits also each token's
   // exponents (words that hold the key's and the value's, and where in them).
-  static constexpr int kNumbers = 32 * D;
+  static constexpr int kNumbers = kTokens * kRowBytes > 32 * D ? kTokens * kRowBytes : 32 * D;
   static constexpr int kPlace = kNumbers + (kEight ? kTokens * 9 : 0);
   // Where registers are short, q's operands lie in shared memory.
   static constexpr bool kShared = MT > 1 || D > 128;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
               uint32_t b[4];
-              ldmatrix_x4(b, ks + unit_at<S::kRowBytes, false>((lane >> 4) * 8 + (lane & 7), 2 * s + ((lane >> 3) & 1)));
+              ldmatrix_x4(b, ks + t0 * S::kRowBytes + unit_at<S::kRowBytes, false>((lane >> 4) * 8 + (lane & 7), 2 * s + ((lane >> 3) & 1)));
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
                 uint32_t a[4];
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) {
               uint32_t b[4];
-              ldmatrix_x4_trans(b, vs + unit_at<S::kRowBytes, false>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * n + (lane >> 4)));
+              ldmatrix_x4_trans(b, vs + t0 * S::kRowBytes + unit_at<S::kRowBytes, false>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * n + (lane >> 4)));
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
                 mma_16816<false>(o[m][2 * n], w[m], b[0], b[1]);
