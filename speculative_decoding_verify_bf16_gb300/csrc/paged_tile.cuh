@@ -38,6 +38,8 @@ constexpr int kTileThreads = 512;
 // Registers a thread of each warpgroup; their sum is what a launch must bring (4 x 128).
 constexpr int kTileRegsRows = 176, kTileRegsCopy = 104, kTileRegsIssue = 56;
 constexpr int kTileRegs = 2 * kTileRegsRows + kTileRegsCopy + kTileRegsIssue;
+static_assert(kTileRegs <= 4 * 128 && kTileRegsCopy <= 128 && kTileRegsIssue <= 128 && kTileRegsRows >= 128,
+              "shares within what the launch brings; those that shrink below it");
 constexpr int kTileHalf = 128 * 128;  // bytes of 128 rows of 64 numbers
 constexpr int kTileRefs = 8;          // steps whose exponents are held: more than the ring has steps
 
@@ -48,7 +50,7 @@ struct TileShape {
   static constexpr int kRows = 256, kTile = 128;
   static constexpr int kBytes = kTileHalf * (D / 64);
   static constexpr int kStages = D > 64 ? 5 : 8;
-  static constexpr int kExtra = 2;  // an item's beginning and end, in units
+  static constexpr int kExtra = 4;  // an item's beginning and end, in units
   using Plan = Schedule<kRows, kTile, kExtra, 1>;
 };
 
@@ -56,6 +58,7 @@ template <typename S>
 struct TileSmem {
   uint8_t q[2][S::kBytes];
   uint8_t ring[S::kStages][S::kBytes];
+  Cursor cursor[13], ahead[4];  // of each warp (registers are short)
   float refs[kTileRefs][2][4];  // of a step's keys and values: each 32 positions' exponent
   typename S::Plan::Shared plan;
   uint64_t full[S::kStages], empty[S::kStages];
@@ -116,7 +119,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
   const uint32_t tm = sm.tmem;
   const int64_t begin = sm.plan.begin[0], end = sm.plan.end[0];
   int64_t left = begin < end ? end - begin : 0;
-  Cursor at = sm.plan.from[0];
+  // Where the warp is: its first lane moves on, after all have read.
+  Cursor& at = sm.cursor[min(warp, 12)];
+  auto place = [&](Cursor& x) {
+    if (lane == 0) x = sm.plan.from[0];
+    __syncwarp();
+  };
+  auto move_on = [&](Cursor& x, int units) {  // within the item, or to the next one's first
+    __syncwarp();
+    if (lane == 0) {
+      x.tile += units - 1;
+      Plan::next_unit(p, x);
+    }
+    __syncwarp();
+  };
+  if (warp < 13) place(at);
 
   if (warp < 8) {
     // ------------------------------------------------------------ rows of a tile
@@ -168,8 +185,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       if (!has_rows()) {
         refs += n;
         left -= n;
-        at.tile += n - 1;
-        Plan::next_unit(p, at);
+        move_on(at, n);
         if (left > 0 && has_rows()) load_q();
         continue;
       }
@@ -258,16 +274,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       if (!ok) break;
       // The last scores are there, so q's tile is free: the next item's comes while the last
       // products run.
-      const Cursor done = at;
+      const bool whole = starts && ends, on = col < at.count;
+      const int head = at.h * p.group + r - col * p.group, b_done = at.b;
+      const int64_t row_done = at.first + col;
       left -= n;
-      at.tile += n - 1;
-      Plan::next_unit(p, at);
+      move_on(at, n);
       if (left > 0 && has_rows()) load_q();
       if (!(ok = warp_wait(&sm.o_full[w], items++ & 1, &sm.abort))) break;
       tc_fence_after();
-      const bool whole = starts && ends, on = col < done.count;
-      const int head = done.h * p.group + r - col * p.group;
-      __nv_bfloat16* const out = p.out + (on ? (done.first + col) * p.out_row + head * p.out_head : 0);
+      __nv_bfloat16* const out = p.out + (on ? row_done * p.out_row + head * p.out_head : 0);
       float* const part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0)) * part_floats(S::kRows, D);
       const float inv = 1.f / sum;
       bool fine = true;
@@ -297,8 +312,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       }
       tc_fence_before();
       if (whole) {
-        if (!fine) lane_failed(c, done.b, SPEC_ERR_NONFINITE);
-        if (on && p.lse != nullptr) p.lse[(done.first + col) * p.lse_row + head] = (top + log2f(sum)) * kLn2;
+        if (!fine) lane_failed(c, b_done, SPEC_ERR_NONFINITE);
+        if (on && p.lse != nullptr) p.lse[row_done * p.lse_row + head] = (top + log2f(sum)) * kLn2;
       } else {
         part[S::kRows * D + 2 * (w * 128 + row)] = top;
         part[S::kRows * D + 2 * (w * 128 + row) + 1] = sum;
@@ -314,7 +329,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
     const bool in_head = unit < used;
     // Where this lane's position lies is looked up ahead: its page two units (`ahead`), the place of its
     // head and its exponents one unit before they are used.
-    Cursor ahead = at;
+    Cursor& ahead = sm.ahead[mine];
+    place(ahead);
     int64_t left_ahead = left;
     int page = kUnseen, next_page = kUnseen;
     uint32_t from = kNowhere, ek = 0, ev = 0;
@@ -323,7 +339,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       next_page = kUnseen;
       if (left_ahead > 0 && pos >= ahead.lo && pos < ahead.hi)
         next_page = __ldg(c.tables + ahead.b * c.table_stride + page_of(c, pos));
-      if (--left_ahead > 0) Plan::next_unit(p, ahead);
+      if (--left_ahead > 0) move_on(ahead, 1);
     };
     // For the unit at the cursor, whose page is `page`.
     auto locate = [&] {
@@ -395,7 +411,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
           }
           advance();
         }
-        if (left > 1) Plan::next_unit(p, at);
+        if (left > 1) move_on(at, 1);
       }
       cp_async_wait<0>();
       while (open > 0) hand_on();
@@ -452,7 +468,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         vb = ev;
         here = from;
         if (left > 1) {
-          Plan::next_unit(p, at);
+          move_on(at, 1);
           page = next_page;
           locate();
           look_up();
@@ -551,8 +567,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         }
         if (!ok) break;
         left -= n;
-        at.tile += n - 1;
-        Plan::next_unit(p, at);
+        move_on(at, n);
       }
       // Tensor memory is given back only after the last product.
       mma_commit(lead, &sm.drain);
@@ -564,9 +579,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
   __syncthreads();
   // A wait gave up: all lanes of the block's range.
   if (sm.abort && threadIdx.x == 0) {
-    at = sm.plan.from[0];
-    for (int64_t u = begin; u < end; ++u, Plan::next_unit(p, at))
-      if (c.status != nullptr) c.status[at.b] = SPEC_ERR_TIMEOUT;
+    Cursor x = sm.plan.from[0];
+    for (int64_t u = begin; u < end; ++u, Plan::next_unit(p, x))
+      if (c.status != nullptr) c.status[x.b] = SPEC_ERR_TIMEOUT;
   }
   tc_fence_after();
   if (warp == 12) tmem_dealloc(tm, 512);
