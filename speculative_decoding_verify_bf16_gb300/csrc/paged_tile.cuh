@@ -15,8 +15,10 @@
 // with the 128-byte swizzle, so that a tile serves along either dimension.
 //
 // Warps: 0-3 and 4-7 a tile's rows, a thread each (q into shared memory, weights, rescaling,
-// outputs); 8-11 bring keys and values, 32 positions of a step each, looked up one by one, so that any page size and
-// order will do; 12 issues the products.
+// outputs); 8-11 bring keys and 12-15 values, 32 positions of a step each, looked up one by one, so
+// that any page size and order will do; 16 issues the products.  Scores are read from tensor memory half
+// a row at a time, the second half twice, for its maximum and for its weights: that leaves registers
+// for eight copying warps, which 8-bit caches need (four took 5,800 cycles a step).
 //
 // 8-bit caches become fp16 on the way to shared memory, times 2^(e - r) with r the largest of a warp's 32
 // exponents, and q becomes fp16 times a power of two for each row.  2^r multiplies the keys' scores; the
@@ -34,12 +36,12 @@
 
 namespace specv {
 
-constexpr int kTileThreads = 512;
-// Registers a thread of each warpgroup; their sum is what a launch must bring (4 x 128).
-constexpr int kTileRegsRows = 176, kTileRegsCopy = 104, kTileRegsIssue = 56;
-constexpr int kTileRegs = 2 * kTileRegsRows + kTileRegsCopy + kTileRegsIssue;
-static_assert(kTileRegs <= 4 * 128 && kTileRegsCopy <= 128 && kTileRegsIssue <= 128 && kTileRegsRows >= 128,
-              "shares within what the launch brings; those that shrink below it");
+constexpr int kTileThreads = 640;
+// Registers a thread of each warpgroup; their sum is what a launch must bring (5 x 96).
+constexpr int kTileRegsRows = 128, kTileRegsCopy = 88, kTileRegsIssue = 48;
+constexpr int kTileRegs = 2 * kTileRegsRows + 2 * kTileRegsCopy + kTileRegsIssue;
+static_assert(kTileRegs <= 5 * 96 && kTileRegsCopy <= 96 && kTileRegsIssue <= 96 && kTileRegsRows >= 96,
+              "shares within what the launch brings; those that shrink are below it, those that grow above");
 constexpr int kTileHalf = 128 * 128;  // bytes of 128 rows of 64 numbers
 constexpr int kTileRefs = 8;          // steps whose exponents are held: more than the ring has steps
 
@@ -58,7 +60,7 @@ template <typename S>
 struct TileSmem {
   uint8_t q[2][S::kBytes];
   uint8_t ring[S::kStages][S::kBytes];
-  Cursor cursor[13], ahead[4];  // of each warp (registers are short)
+  Cursor cursor[17], ahead[8];  // of each warp (registers are short)
   float refs[kTileRefs][2][4];  // of a step's keys and values: each 32 positions' exponent
   typename S::Plan::Shared plan;
   uint64_t full[S::kStages], empty[S::kStages];
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
     sm.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
     tc_fence_before();
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
   const int64_t begin = sm.plan.begin[0], end = sm.plan.end[0];
   int64_t left = begin < end ? end - begin : 0;
   // Where the warp is: its first lane moves on, after all have read.
-  Cursor& at = sm.cursor[min(warp, 12)];
+  Cursor& at = sm.cursor[min(warp, 16)];
   auto place = [&](Cursor& x) {
     if (lane == 0) x = sm.plan.from[0];
     __syncwarp();
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
     }
     __syncwarp();
   };
-  if (warp < 13) place(at);
+  if (warp < 17) place(at);
 
   if (warp < 8) {
     // ------------------------------------------------------------ rows of a tile
@@ -197,35 +199,36 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       for (int j = 0; j < n; ++j, p0 += S::kTile, ++refs) {
         if (!(ok = warp_wait(&sm.s_full[w], steps++ & 1, &sm.abort))) break;
         tc_fence_after();
-        uint32_t x[4][32];
+        // Of 32 positions each: a score's factor, and what its exponent gets.
+        auto factor = [&](int i) { return kEight ? qs * sm.refs[refs % kTileRefs][0][i] : qs; };
+        auto addend = [&](int i) { return kEight ? sm.refs[refs % kTileRefs][1][i] : 0.f; };
+        const bool part_hidden = __any_sync(0xFFFFFFFFu, p0 + S::kTile > lim || p0 < low);
+        uint32_t x[2][32];
+        auto load = [&](int half) {
+          tmem_ld32(x[0], tms + half * 64);
+          tmem_ld32(x[1], tms + half * 64 + 32);
+          tmem_wait_ld();
+          if (part_hidden) {
+            const int i0 = low - p0 - half * 64, i1 = lim - p0 - half * 64;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(x[i], tms + i * 32);
-        tmem_wait_ld();
-        if (__any_sync(0xFFFFFFFFu, p0 + S::kTile > lim || p0 < low)) {
-          const int i0 = low - p0, i1 = lim - p0;
-#pragma unroll
-          for (int i = 0; i < 128; ++i) x[i / 32][i % 32] = i >= i0 && i < i1 ? x[i / 32][i % 32] : 0xFF800000u;
-        }
-        float by[4], add[4];  // of each 32 positions: a score's factor, and what its exponent gets
+            for (int i = 0; i < 64; ++i) x[i / 32][i % 32] = i >= i0 && i < i1 ? x[i / 32][i % 32] : 0xFF800000u;
+          }
+        };
         float most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float m[4];
+        for (int half = 1; half >= 0; --half) {  // (the first half stays in registers)
+          load(half);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) m[k] = fmaxf(__uint_as_float(x[i][k]), __uint_as_float(x[i][k + 4]));
+          for (int i = 0; i < 2; ++i) {
+            float m[4];
 #pragma unroll
-          for (int k = 8; k < 32; k += 8)
+            for (int k = 0; k < 4; ++k) m[k] = fmaxf(__uint_as_float(x[i][k]), __uint_as_float(x[i][k + 4]));
 #pragma unroll
-            for (int l = 0; l < 4; ++l) m[l] = fmaxf(m[l], fmaxf(__uint_as_float(x[i][k + l]), __uint_as_float(x[i][k + l + 4])));
-          const float mi = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-          if constexpr (kEight) {
-            by[i] = qs * sm.refs[refs % kTileRefs][0][i];
-            add[i] = sm.refs[refs % kTileRefs][1][i];
-            most = fmaxf(most, fmaf(mi, by[i], add[i]));
-          } else {
-            by[i] = qs;
-            add[i] = 0.f;
-            most = fmaxf(most, mi * qs);
+            for (int k = 8; k < 32; k += 8)
+#pragma unroll
+              for (int l = 0; l < 4; ++l) m[l] = fmaxf(m[l], fmaxf(__uint_as_float(x[i][k + l]), __uint_as_float(x[i][k + l + 4])));
+            const float mi = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            most = fmaxf(most, kEight ? fmaf(mi, factor(half * 2 + i), addend(half * 2 + i)) : mi * qs);
           }
         }
         const float raise = most > top + kRowsSlack ? most : top;
@@ -248,22 +251,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         const float from = top == -INFINITY ? 0.f : top;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          // (the second half's weights come to lie where its scores are not: columns 32 to 63)
+          if (half == 1) load(1);
           uint32_t y[32];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int q4 = half * 2 + i;
-            const f32x2 mul = pair(by[q4], by[q4]), off = pair(add[q4] - from, add[q4] - from);
+            const float by = factor(half * 2 + i), add = addend(half * 2 + i);
+            const f32x2 mul = pair(by, by), off = pair(add - from, add - from);
             f32x2 part[2] = {0ull, 0ull};
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
-              const f32x2 e = fma2(pair(__uint_as_float(x[q4][k]), __uint_as_float(x[q4][k + 1])), mul, off);
+              const f32x2 e = fma2(pair(__uint_as_float(x[i][k]), __uint_as_float(x[i][k + 1])), mul, off);
               const float e0 = ex2_approx(first_of(e)), e1 = ex2_approx(second_of(e));
               part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], pair(e0, e1));
               y[i * 16 + k / 2] = kEight ? to_halfx2(e0, e1) : to_bf16x2(e0, e1);
             }
             part[0] = add2(part[0], part[1]);
             const float s = first_of(part[0]) + second_of(part[0]);
-            sum = kEight ? fmaf(s, power_of_minus(add[q4]), sum) : sum + s;
+            sum = kEight ? fmaf(s, power_of_minus(add), sum) : sum + s;
           }
           tmem_st32(tms + half * 32, y);
         }
@@ -319,17 +324,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         part[S::kRows * D + 2 * (w * 128 + row) + 1] = sum;
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ------------------------------------------------------------ keys and values
     registers_shrink<kTileRegsCopy>();
     constexpr int kUnits = D * (kEight ? 1 : 2) / 16;  // 16-byte units of a token in the cache
     constexpr int kAtOnce = 32 / kUnits;               // tokens of a warp's access
-    const int mine = warp - 8, used = c.dim * (kEight ? 1 : 2) / 16;
+    const int mine = warp & 3, which = (warp - 8) >> 2;  // positions of a step; keys or values
+    const int used = c.dim * (kEight ? 1 : 2) / 16;
     const int unit = lane % kUnits, sub = lane / kUnits;
     const bool in_head = unit < used;
     // Where this lane's position lies is looked up ahead: its page two units (`ahead`), the place of its
     // head and its exponents one unit before they are used.
-    Cursor& ahead = sm.ahead[mine];
+    Cursor& ahead = sm.ahead[warp - 8];
     place(ahead);
     int64_t left_ahead = left;
     int page = kUnseen, next_page = kUnseen;
@@ -363,71 +369,68 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
     look_up();
     page = next_page;
     look_up();
-    int slot = 0, round = 0;
+    const uint8_t* const base = (which ? c.v : c.k) + unit * 16;
+    int slot = which, round = 0;  // every other place of the ring
     bool ok = true;
     auto advance = [&] {
-      if (++slot == kStages) {
-        slot = 0;
+      if ((slot += 2) >= kStages) {
+        slot -= kStages;
         ++round;
       }
     };
+    const bool withhold = test_withhold != 0 && begin == 0 && which == 0;
     if constexpr (!kEight) {
-      constexpr int kLag = 2;  // tiles on their way before the oldest is waited for
-      int open = 0, open_slot = 0;
-      bool withheld = test_withhold != 0 && begin == 0;
-      auto hand_on = [&] {  // the oldest tile, whose copies have landed
+      // A tile on its way while the next is asked for.
+      int open_slot = -1;
+      bool withheld = withhold;
+      auto hand_on = [&] {  // the open tile, whose copies have landed
         fence_async_smem();
         if (!withheld) warp_arrive(&sm.full[open_slot]);
         withheld = false;
-        if (++open_slot == kStages) open_slot = 0;
-        --open;
+        open_slot = -1;
       };
 #pragma unroll 1
       for (; ok && left > 0; --left) {
         locate();
         page = next_page;
         look_up();
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v) {
-          if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_try_wait(&sm.empty[slot], (round - 1) & 1))) {
-            cp_async_wait<0>();
-            while (open > 0) hand_on();
-            if (!(ok = warp_wait(&sm.empty[slot], (round - 1) & 1, &sm.abort))) break;
-          }
-          const uint32_t to = smem_addr(sm.ring[slot]);
-          const uint8_t* const base = (v ? c.v : c.k) + unit * 16;
-#pragma unroll
-          for (int i = 0; i < 32 / kAtOnce; ++i) {
-            const int tok = i * kAtOnce + sub;
-            const uint32_t f = __shfl_sync(0xFFFFFFFFu, from, tok);
-            const bool on = f != kNowhere && in_head;
-            cp_async16_or_zero(to + swizzled(mine * 32 + tok, unit), base + (on ? static_cast<uint64_t>(f) * by : 0), on);
-          }
-          cp_async_commit();
-          ++open;
-          if (open > kLag) {
-            cp_async_wait<kLag>();
-            hand_on();
-          }
-          advance();
+        if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_try_wait(&sm.empty[slot], (round - 1) & 1))) {
+          cp_async_wait<0>();
+          if (open_slot >= 0) hand_on();
+          if (!(ok = warp_wait(&sm.empty[slot], (round - 1) & 1, &sm.abort))) break;
         }
+        const uint32_t to = smem_addr(sm.ring[slot]);
+#pragma unroll
+        for (int i = 0; i < 32 / kAtOnce; ++i) {
+          const int tok = i * kAtOnce + sub;
+          const uint32_t f = __shfl_sync(0xFFFFFFFFu, from, tok);
+          const bool on = f != kNowhere && in_head;
+          cp_async16_or_zero(to + swizzled(mine * 32 + tok, unit), base + (on ? static_cast<uint64_t>(f) * by : 0), on);
+        }
+        cp_async_commit();
+        if (open_slot >= 0) {
+          cp_async_wait<1>();
+          hand_on();
+        }
+        open_slot = slot;
+        advance();
         if (left > 1) move_on(at, 1);
       }
       cp_async_wait<0>();
-      while (open > 0) hand_on();
+      if (open_slot >= 0) hand_on();
     } else {
       constexpr int kLoads = 32 / kAtOnce;  // of a thread and tile
-      uint4 kx[kLoads], vx[kLoads];
-      auto fetch = [&](uint4 (&x)[kLoads], const uint8_t* base, uint32_t here) {
+      uint4 x[kLoads];
+      auto fetch = [&](uint32_t here) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const uint32_t f = __shfl_sync(0xFFFFFFFFu, here, i * kAtOnce + sub);
-          x[i] = f != kNowhere && in_head ? __ldg(reinterpret_cast<const uint4*>(base + unit * 16 + static_cast<uint64_t>(f) * by))
+          x[i] = f != kNowhere && in_head ? __ldg(reinterpret_cast<const uint4*>(base + static_cast<uint64_t>(f) * by))
                                           : make_uint4(0u, 0u, 0u, 0u);
         }
       };
       // A tile as fp16 into the ring; `byte`: this lane's position's exponent, `ref` the largest.
-      auto store = [&](uint4 (&x)[kLoads], uint32_t byte, uint32_t ref) {
+      auto store = [&](uint32_t byte, uint32_t ref) {
         if (round > 0 && !(ok = warp_wait(&sm.empty[slot], (round - 1) & 1, &sm.abort))) return;
         uint8_t* const to = sm.ring[slot];
         const float f = byte == 255u ? __uint_as_float(0x7FC00000u)
@@ -457,7 +460,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
           *reinterpret_cast<uint4*>(to + swizzled(mine * 32 + tok, unit * 2 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
         }
         fence_async_smem();
-        if (test_withhold == 0 || begin != 0 || round > 0 || slot > 0) warp_arrive(&sm.full[slot]);
+        if (!withhold || round > 0 || slot > 0) warp_arrive(&sm.full[slot]);
         advance();
       };
       auto largest = [&](uint32_t byte) { return __reduce_max_sync(0xFFFFFFFFu, byte == 255u ? 0u : byte); };
@@ -477,32 +480,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       if (left > 0) {
         locate();
         page = next_page;
-        take();
-        fetch(kx, c.k, here);
       }
       int step = 0;
 #pragma unroll 1
-      while (ok && left > 0) {
-        fetch(vx, c.v, here);
-        const uint32_t k0 = kb, v0 = vb, kr = largest(kb), vr = largest(vb);
-        if (lane == 0) {
+      for (; ok && left > 0; --left, ++step) {
+        take();
+        fetch(here);
+        const uint32_t kr = largest(kb), vr = largest(vb);
+        if (which == 0 && lane == 0) {
           sm.refs[step % kTileRefs][0][mine] = __uint_as_float(kr << 23);
           sm.refs[step % kTileRefs][1][mine] = static_cast<float>(static_cast<int>(vr) - 127);
         }
-        ++step;
-        store(kx, k0, kr);
-        if (!ok) break;
-        if (--left > 0) {
-          take();
-          fetch(kx, c.k, here);
-        }
-        store(vx, v0, vr);
+        store(which ? vb : kb, which ? vr : kr);
       }
     }
   } else {
     // ------------------------------------------------------------------ products
     registers_shrink<kTileRegsIssue>();
-    if (warp == 12) {
+    if (warp == 16) {
       const uint32_t lead = elect_one();
       const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0);
       constexpr uint32_t kScores = mma_desc_of(kEight, 128, 128, false), kOuts = mma_desc_of(kEight, 128, D, true);
@@ -584,7 +579,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       if (c.status != nullptr) c.status[x.b] = SPEC_ERR_TIMEOUT;
   }
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tm, 512);
+  if (warp == 16) tmem_dealloc(tm, 512);
 }
 
 }  // namespace specv
