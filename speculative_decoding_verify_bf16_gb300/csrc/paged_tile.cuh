@@ -38,7 +38,7 @@ namespace specv {
 
 constexpr int kTileThreads = 640;
 // Registers a thread of each warpgroup; their sum is what a launch must bring (5 x 96).
-constexpr int kTileRegsRows = 128, kTileRegsCopy = 88, kTileRegsIssue = 48;
+constexpr int kTileRegsRows = 136, kTileRegsCopy = 80, kTileRegsIssue = 48;
 constexpr int kTileRegs = 2 * kTileRegsRows + 2 * kTileRegsCopy + kTileRegsIssue;
 static_assert(kTileRegs <= 5 * 96 && kTileRegsCopy <= 96 && kTileRegsIssue <= 96 && kTileRegsRows >= 96,
               "shares within what the launch brings; those that shrink are below it, those that grow above");
@@ -64,7 +64,7 @@ struct TileSmem {
   float refs[kTileRefs][2][4];  // of a step's keys and values: each 32 positions' exponent
   typename S::Plan::Shared plan;
   uint64_t full[S::kStages], empty[S::kStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], drain;
   uint32_t tmem;
   int abort;
 };
@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 4);
       mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_half[i], 4);
       mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.o_full[i], 1);
     }
@@ -271,10 +272,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
             sum = kEight ? fmaf(s, power_of_minus(add), sum) : sum + s;
           }
           tmem_st32(tms + half * 32, y);
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(half ? &sm.p_full[w] : &sm.p_half[w]);  // (products begin with the first half)
         }
-        tmem_wait_st();
-        tc_fence_before();
-        warp_arrive(&sm.p_full[w]);
       }
       if (!ok) break;
       // The last scores are there, so q's tile is free: the next item's comes while the last
@@ -544,12 +545,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
           if (j + 1 < n && !(ok = warp_wait(&sm.full[sk], phase, &sm.abort))) break;
 #pragma unroll 1
           for (int w = 0; w < tiles; ++w) {
-            if (!(ok = warp_wait(&sm.p_full[w], (parity >> w) & 1, &sm.abort))) break;
-            parity ^= 1u << w;
-            tc_fence_after();
+#pragma unroll 1
+            for (int half = 0; half < 2 && ok; ++half) {
+              if (!(ok = warp_wait(half ? &sm.p_full[w] : &sm.p_half[w], (parity >> w) & 1, &sm.abort))) break;
+              tc_fence_after();
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-              mma_ts(lead, tmu + kColO + w * 128, tmu + kColS + w * 128 + s * 8, vd + s * (2048 / 16), kOuts, s + j > 0);
+              for (int s = 0; s < 4; ++s)
+                mma_ts(lead, tmu + kColO + w * 128, tmu + kColS + w * 128 + half * 32 + s * 8, vd + (half * 4 + s) * (2048 / 16),
+                       kOuts, half + s + j > 0);
+            }
+            if (!ok) break;
+            parity ^= 1u << w;
             if (w + 1 == tiles) mma_commit(lead, &sm.empty[sv]);
             if (j + 1 < n) {
               scores(w, kd);
