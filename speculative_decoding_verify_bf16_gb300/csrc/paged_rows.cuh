@@ -129,7 +129,7 @@ struct RowsShape {
   static constexpr int kPlaces = kFit > 12 ? 12 : kFit;
   static constexpr int kExtra = 1;  // an item's beginning and end, in units
   static_assert(kPlaces >= 4, "the ring holds two units at least");
-  using Plan = Schedule<kRows, kTokens, kExtra, 4>;
+  using Plan = Schedule<kRows, kTokens, kExtra, 2>;
 };
 
 template <typename S>
@@ -283,15 +283,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
     const int unit = lane % kUnits, sub = lane / kUnits;
     const bool in_head = unit * 16 < c.dim * (kEight ? 1 : 2);
     const uint32_t by = 1u << c.unit_shift;
-    // Pages are looked up two units ahead: with the memory busy, a load takes as long as that.
-    Cursor ahead = at;
-    int64_t left_ahead = left;
-    auto look_up = [&] {
-      const int pos = ahead.tile * kTokens + lane;
+    // Pages are looked up two units ahead, within the item: with the memory busy, a load takes as long as
+    // that.
+    auto look_up = [&](int ahead) {
+      const int pos = (at.tile + ahead) * kTokens + lane;
       int page = kUnseen;
-      if (left_ahead > 0 && lane < kTokens && pos >= ahead.lo && pos < ahead.hi)
-        page = __ldg(c.tables + ahead.b * c.table_stride + page_of(c, pos));
-      if (--left_ahead > 0) Plan::next_unit(p, ahead);
+      if (ahead < left && at.tile + ahead < at.t1 && lane < kTokens && pos >= at.lo && pos < at.hi)
+        page = __ldg(c.tables + at.b * c.table_stride + page_of(c, pos));
       return page;
     };
     const bool withhold = test_withhold != 0 && begin == 0 && head_in == 0;
@@ -303,10 +301,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
       next_place();
       again = again || place == 0;
     };
-    int page0 = look_up(), page1 = look_up();
+    int page0 = kUnseen, page1 = kUnseen;
 #pragma unroll 1
     for (; left > 0; --left) {
-      const int page2 = look_up();
+      if (fresh) {
+        page0 = look_up(0);
+        page1 = look_up(1);
+      }
+      const int page2 = look_up(2);
       if (fresh) {  // the item's rows of q, 16 at a time
 #pragma unroll 1
         for (int m = 0; m < MT && acquire(); ++m) {
