@@ -169,9 +169,33 @@ struct RowSum {
   float top, sum;
   float4 a[kWide];
 
-  template <typename Rows, typename Stats>
-  __device__ __forceinline__ void take(int first, int parts, int step, const Rows& rows, const Stats& stats) {
+  // Parts i0, i0 + step, .. of n, lane j's weight the j-th's; BATCH of them on their way at a time.
+  template <int BATCH, typename Rows>
+  __device__ __forceinline__ void add(int i0, int n, int step, float f, const Rows& rows) {
     const int lane = threadIdx.x & 31, sub = lane / kAcross, at = lane % kAcross;
+#pragma unroll 1
+    for (int j0 = 0; j0 < n; j0 += BATCH * kSubs) {
+      float4 b[BATCH][kWide];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)  // (those past the end weigh 0: the last one again)
+#pragma unroll
+        for (int z = 0; z < kWide; ++z)
+          b[j][z] = __ldcg(reinterpret_cast<const float4*>(rows(i0 + min(j0 + j * kSubs + sub, n - 1) * step)) + at + z * 32);
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        const int x = j0 + j * kSubs + sub;
+        const float from = __shfl_sync(0xFFFFFFFFu, f, x & 31), w = x < n ? from : 0.f;
+#pragma unroll
+        for (int z = 0; z < kWide; ++z) {
+          a[z].x = fmaf(b[j][z].x, w, a[z].x), a[z].y = fmaf(b[j][z].y, w, a[z].y);
+          a[z].z = fmaf(b[j][z].z, w, a[z].z), a[z].w = fmaf(b[j][z].w, w, a[z].w);
+        }
+      }
+    }
+  }
+  template <int BATCH, typename Rows, typename Stats>
+  __device__ __forceinline__ void take(int first, int parts, int step, const Rows& rows, const Stats& stats) {
+    const int lane = threadIdx.x & 31;
     top = -INFINITY;
     sum = 0.f;
 #pragma unroll
@@ -190,26 +214,10 @@ struct RowSum {
       top = raise;
 #pragma unroll
       for (int z = 0; z < kWide; ++z) a[z].x *= down, a[z].y *= down, a[z].z *= down, a[z].w *= down;
-      constexpr int kBatch = 8;  // parts on their way at a time
-#pragma unroll 1
-      for (int j0 = 0; j0 < n; j0 += kBatch * kSubs) {
-        float4 b[kBatch][kWide];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)  // (those past the end weigh 0: the last one again)
-#pragma unroll
-          for (int z = 0; z < kWide; ++z)
-            b[j][z] = __ldcg(reinterpret_cast<const float4*>(rows(i0 + min(j0 + j * kSubs + sub, n - 1) * step)) + at + z * 32);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int x = j0 + j * kSubs + sub;
-          const float from = __shfl_sync(0xFFFFFFFFu, f, x & 31), w = x < n ? from : 0.f;
-#pragma unroll
-          for (int z = 0; z < kWide; ++z) {
-            a[z].x = fmaf(b[j][z].x, w, a[z].x), a[z].y = fmaf(b[j][z].y, w, a[z].y);
-            a[z].z = fmaf(b[j][z].z, w, a[z].z), a[z].w = fmaf(b[j][z].w, w, a[z].w);
-          }
-        }
-      }
+      if (BATCH > 4 && n > 8)
+        add<BATCH>(i0, n, step, f, rows);
+      else
+        add<4>(i0, n, step, f, rows);
     }
     if constexpr (kSubs == 2) {
       a[0].x += __shfl_xor_sync(0xFFFFFFFFu, a[0].x, 16);
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
       for (int y = warp; y < used * p.heads; y += 2 * S::kWarps) {
         const int h = y / used, r = y - h * used, in = h * S::kRows + r;
         RowSum<D> sum;
-        sum.take(0, w1 - w0 + 1, 1, [&](int i) { return part(i) + static_cast<int64_t>(in) * D; },
+        sum.template take<4>(0, w1 - w0 + 1, 1, [&](int i) { return part(i) + static_cast<int64_t>(in) * D; },
                  [&](int i) { return reinterpret_cast<const float2*>(part(i) + S::kRows * p.heads * D + 2 * in); });
         __syncwarp();  // (the first part's numbers have been read)
         if (done) {
@@ -772,7 +780,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
 
 // Joins the parts of items that were split over thread blocks.  blockIdx.x: the worker that an item
 // begins with; blockIdx.y: some of its rows, of which there are `rows` for a head, at most `used` of
-// them in use.  A warp takes a row; of many parts, all warps a share each.
+// them in use.  A warp takes a row; of many parts, and where a block has one row, all warps a share each.
 constexpr int kJoinThreads = 128, kJoinAlone = 32;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttendParams p, int rows, int used, int per_block) {
@@ -795,14 +803,14 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttendPa
   const float* const others = p.parts + 2 * static_cast<int64_t>(blockIdx.x / p.workers) * p.workers * size;
   auto part = [&](int i) { return i == 0 ? part0 : others + 2 * static_cast<int64_t>(i) * p.workers * size; };
   const int y1 = min(static_cast<int>(blockIdx.y + 1) * per_block, used * p.heads);
-  const bool alone = record.parts <= kJoinAlone;
+  const bool alone = record.parts <= kJoinAlone || per_block > 1;
 #pragma unroll 1
   for (int y = blockIdx.y * per_block + (alone ? warp : 0); y < y1; y += alone ? kWarps : 1) {
     const int h = y / used, r = y - h * used, row = record.block * rows + r, col = column_of(p, row), in = h * rows + r;
     if (col >= count) continue;  // (the same for all threads that go on together)
     const int head = (record.head * p.heads + h) * p.group + row - col * p.group;
     Sum sum;
-    sum.take(alone ? 0 : warp, record.parts, alone ? 1 : kWarps, [&](int i) { return part(i) + static_cast<int64_t>(in) * D; },
+    sum.template take<D <= 128 ? 16 : 8>(alone ? 0 : warp, record.parts, alone ? 1 : kWarps, [&](int i) { return part(i) + static_cast<int64_t>(in) * D; },
              [&](int i) { return reinterpret_cast<const float2*>(part(i) + rows * p.heads * D + 2 * in); });
     if (!alone) {
       if (lane < Sum::kAcross)
