@@ -15,7 +15,7 @@
 
 namespace specv {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 constexpr int kRowsMost = 32;  // rows of a CTA
 
 struct CacheRowsParams {
@@ -68,24 +68,28 @@ __device__ __forceinline__ uint32_t exponent_byte(uint32_t top_bits) {
   return e < 127 + SPEC_CACHE_LEAST_EXP ? 127 + SPEC_CACHE_LEAST_EXP : e;
 }
 
+// A thread has eight numbers of a head in two fours, at `d` and `e`: in bf16 rows side by side, 16 bytes; in
+// fp32 rows so that each four, 16 bytes too, lies beside the next thread's.
 template <typename T>
-__device__ __forceinline__ void load8(float (&x)[8], const uint8_t* from) {
+__device__ __forceinline__ void load_fours(float (&x)[8], const uint8_t* from, int d, int e, bool on_d, bool on_e) {
   if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(from)), b = __ldcs(reinterpret_cast<const float4*>(from) + 1);
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 a = on_d ? __ldcs(reinterpret_cast<const float4*>(from + 4 * d)) : zero;
+    const float4 b = on_e ? __ldcs(reinterpret_cast<const float4*>(from + 4 * e)) : zero;
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   } else {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(from));
+    const uint4 a = on_d ? __ldcs(reinterpret_cast<const uint4*>(from + 2 * d)) : make_uint4(0u, 0u, 0u, 0u);
     x[0] = bf16_lo(a.x), x[1] = bf16_hi(a.x), x[2] = bf16_lo(a.y), x[3] = bf16_hi(a.y);
     x[4] = bf16_lo(a.z), x[5] = bf16_hi(a.z), x[6] = bf16_lo(a.w), x[7] = bf16_hi(a.w);
   }
 }
 template <typename T>
-__device__ __forceinline__ void store8(uint8_t* to, const float (&x)[8]) {
+__device__ __forceinline__ void store_fours(uint8_t* to, const float (&x)[8], int d, int e, bool on_d, bool on_e) {
   if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(to)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    *reinterpret_cast<uint4*>(to) =
+    if (on_d) *reinterpret_cast<float4*>(to + 4 * d) = make_float4(x[0], x[1], x[2], x[3]);
+    if (on_e) *reinterpret_cast<float4*>(to + 4 * e) = make_float4(x[4], x[5], x[6], x[7]);
+  } else if (on_d) {
+    *reinterpret_cast<uint4*>(to + 2 * d) =
         make_uint4(to_bf16x2(x[0], x[1]), to_bf16x2(x[2], x[3]), to_bf16x2(x[4], x[5]), to_bf16x2(x[6], x[7]));
   }
 }
@@ -128,24 +132,21 @@ __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRows
     }
   __syncthreads();
   const int unit = threadIdx.x % GROUP, heads = mine * c.kv_heads;
-  const bool in_head = unit * 8 < c.dim;
-  constexpr int kSize = TYPE == SPEC_CACHE_BF16 ? 2 : 1;
-#pragma unroll 2
+  const int d = sizeof(T) == 4 ? 4 * unit : 8 * unit, e = sizeof(T) == 4 ? d + 4 * GROUP : d + 4;
+#pragma unroll 1
   for (int base = 0; base < heads; base += kRowThreads / GROUP) {
     const int i = base + threadIdx.x / GROUP;
     const int r = i / c.kv_heads, h = i - r * c.kv_heads;
     const int b = i < heads ? lane_at[r] : -1;
-    const bool on = b >= 0 && in_head;
-    const int64_t at = b < 0 ? 0 : slot_at[r] + h * c.head + unit * (8 * kSize);
+    const bool on_d = b >= 0 && d < c.dim, on_e = b >= 0 && e < c.dim;
+    const int64_t at = b < 0 ? 0 : slot_at[r] + h * c.head;
     const int64_t ea = b < 0 ? 0 : exp_at[r] + h * c.exp_head;
-    uint8_t* const kr = p.k + (row0 + r) * p.k_row + h * p.k_head + unit * (8 * static_cast<int>(sizeof(T)));
-    uint8_t* const vr = p.v + (row0 + r) * p.v_row + h * p.v_head + unit * (8 * static_cast<int>(sizeof(T)));
-    float x[2][8] = {};
+    uint8_t* const kr = p.k + (row0 + r) * p.k_row + h * p.k_head;
+    uint8_t* const vr = p.v + (row0 + r) * p.v_row + h * p.v_head;
+    float x[2][8];
     if constexpr (WRITE) {
-      if (on) {
-        load8<T>(x[0], kr);
-        load8<T>(x[1], vr);
-      }
+      load_fours<T>(x[0], kr, d, e, on_d, on_e);
+      load_fours<T>(x[1], vr, d, e, on_d, on_e);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         uint8_t* const to = (s ? c.v : c.k) + at;
@@ -155,12 +156,18 @@ __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRows
         for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
         bool bad;
         if constexpr (TYPE == SPEC_CACHE_BF16) {
-          bad = top > 0x7F7F7FFFu;  // rounds to an infinity in bf16, or is one or NaN
-          if (on) store8<__nv_bfloat16>(to, x[s]);
-          bad = bad && on;
+          bad = top > 0x7F7F7FFFu;  // rounds to an infinity in bf16, or is one or NaN (what is not there is 0)
+          const uint2 lo = make_uint2(to_bf16x2(x[s][0], x[s][1]), to_bf16x2(x[s][2], x[s][3]));
+          const uint2 hi = make_uint2(to_bf16x2(x[s][4], x[s][5]), to_bf16x2(x[s][6], x[s][7]));
+          if constexpr (sizeof(T) == 4) {
+            if (on_d) *reinterpret_cast<uint2*>(to + 2 * d) = lo;
+            if (on_e) *reinterpret_cast<uint2*>(to + 2 * e) = hi;
+          } else if (on_d) {
+            *reinterpret_cast<uint4*>(to + 2 * d) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          }
         } else {
 #pragma unroll
-          for (int d = 1; d < GROUP; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          for (int z = 1; z < GROUP; z <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, z));
           const uint32_t byte = exponent_byte<TYPE>(top);
           const float inverse = __uint_as_float((254u - (byte == 255u ? 127u : byte)) << 23);
           uint32_t w[2];
@@ -174,33 +181,49 @@ __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRows
             for (int j = 0; j < 2; ++j) {
               uint32_t y[4];
 #pragma unroll
-              for (int i2 = 0; i2 < 4; ++i2) y[i2] = static_cast<uint32_t>(__float2int_rn(x[s][4 * j + i2] * inverse)) & 255u;
+              for (int z = 0; z < 4; ++z) y[z] = static_cast<uint32_t>(__float2int_rn(x[s][4 * j + z] * inverse)) & 255u;
               w[j] = y[0] | y[1] << 8 | y[2] << 16 | y[3] << 24;
             }
           }
-          if (on) {
-            *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-            if (unit == 0) (s ? c.v_exps : c.k_exps)[ea] = static_cast<uint8_t>(byte);
+          if constexpr (sizeof(T) == 4) {
+            if (on_d) *reinterpret_cast<uint32_t*>(to + d) = w[0];
+            if (on_e) *reinterpret_cast<uint32_t*>(to + e) = w[1];
+          } else if (on_d) {
+            *reinterpret_cast<uint2*>(to + d) = make_uint2(w[0], w[1]);
           }
+          if (on_d && unit == 0) (s ? c.v_exps : c.k_exps)[ea] = static_cast<uint8_t>(byte);
           bad = byte == 255u && b >= 0 && unit == 0;
         }
         if (bad) lane_failed(c, b, SPEC_ERR_NONFINITE);
       }
     } else {
       if constexpr (TYPE == SPEC_CACHE_BF16) {
-        if (on) {
-          load8<__nv_bfloat16>(x[0], c.k + at);
-          load8<__nv_bfloat16>(x[1], c.v + at);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint8_t* const from = (s ? c.v : c.k) + at;
+          uint4 a = make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (sizeof(T) == 4) {
+            if (on_d) *reinterpret_cast<uint2*>(&a.x) = __ldcs(reinterpret_cast<const uint2*>(from + 2 * d));
+            if (on_e) *reinterpret_cast<uint2*>(&a.z) = __ldcs(reinterpret_cast<const uint2*>(from + 2 * e));
+          } else if (on_d) {
+            a = __ldcs(reinterpret_cast<const uint4*>(from + 2 * d));
+          }
+          x[s][0] = bf16_lo(a.x), x[s][1] = bf16_hi(a.x), x[s][2] = bf16_lo(a.y), x[s][3] = bf16_hi(a.y);
+          x[s][4] = bf16_lo(a.z), x[s][5] = bf16_hi(a.z), x[s][6] = bf16_lo(a.w), x[s][7] = bf16_hi(a.w);
         }
       } else {
         uint2 w[2] = {};
         uint32_t byte[2] = {};
-        if (on) {
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            w[s] = __ldcs(reinterpret_cast<const uint2*>((s ? c.v : c.k) + at));
-            byte[s] = (s ? c.v_exps : c.k_exps)[ea];
+        for (int s = 0; s < 2; ++s) {
+          const uint8_t* const from = (s ? c.v : c.k) + at;
+          if constexpr (sizeof(T) == 4) {
+            if (on_d) w[s].x = __ldcs(reinterpret_cast<const uint32_t*>(from + d));
+            if (on_e) w[s].y = __ldcs(reinterpret_cast<const uint32_t*>(from + e));
+          } else {
+            w[s] = on_d ? __ldcs(reinterpret_cast<const uint2*>(from + d)) : make_uint2(0u, 0u);
           }
+          byte[s] = on_d ? (s ? c.v_exps : c.k_exps)[ea] : 0u;
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -220,10 +243,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRows
           }
         }
       }
-      if (on) {
-        store8<T>(kr, x[0]);
-        store8<T>(vr, x[1]);
-      }
+      store_fours<T>(kr, x[0], d, e, on_d, on_e);
+      store_fours<T>(vr, x[1], d, e, on_d, on_e);
     }
   }
 }

@@ -114,7 +114,8 @@ struct RowsShape {
   static constexpr int kWarps = D > 128 ? 4 : 8;  // that compute; as many copy
   static constexpr int kThreads = 64 * kWarps;
   // Registers a thread, and what a launch must bring (0: they are not shared out).
-  static constexpr int kRegsRows = kWarps == 8 ? 192 : 0, kRegsCopy = kWarps == 8 ? 64 : 0;
+  // (8 x 8 columns over e4m3: 82 us with 192 and 64 for both types; bf16 76 us, with 200 and 56 79)
+  static constexpr int kRegsRows = kWarps != 8 ? 0 : kEight ? 200 : 192, kRegsCopy = kWarps != 8 ? 0 : kEight ? 56 : 64;
   static constexpr int kRegs = kWarps / 4 * (kRegsRows + kRegsCopy);
   static constexpr int kTokens = kEight || D <= 64 ? 32 : 16;  // of a unit
   static constexpr int kRowBytes = D * (kEight ? 1 : 2);
