@@ -21,7 +21,8 @@
  * for y 2^e.  e is the least integer of SPEC_CACHE_LEAST_EXP or more with
  * top * 2^e >= max |x|, and y is x / 2^e rounded to nearest, ties to even: to an e4m3
  * number (top 448) or to an integer (top 127).  A head that holds NaN, an infinity or a number beyond
- * top * 2^SPEC_CACHE_MOST_EXP gets the byte 255 and reads back as NaN.  With a power of two every step but
+ * top * 2^SPEC_CACHE_MOST_EXP gets the byte 255 and reads back as NaN.  (Attention
+ * takes these bytes; what others give is unspecified.)  With a power of two every step but
  * the rounding is exact: what is stored is a function of the numbers alone, and it reads back exactly,
  * in bf16 too.
  *
@@ -143,7 +144,8 @@ typedef struct {
 /*
  * spec_paged_attention_workspace -- the most scratch memory, in bytes, that
  * spec_paged_attention can use with these heads and up to max_len columns a lane on the
- * current device (host-only; 0 for sizes that it refuses).  It does not depend on lanes or contexts.
+ * current device (host-only; 0 for sizes that it refuses).  It does not depend on lanes or contexts,
+ * and a buffer for more columns serves fewer.
  */
 uint64_t spec_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t max_len);
 
@@ -153,7 +155,7 @@ uint64_t spec_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int32
  * Column i of a lane sees positions 0 .. cached_lens + i (the last window of them):
  * its own and what is before it, which spec_cache_write has put there.  Every column
  * sees one position at least.  Slots that no column of the lane sees may hold anything, NaN
- * included, and rows behind the last lane's are left as they are.
+ * included, and rows behind the last lane's are left as they are.  out must not overlap q.
  *
  * Scores, sums and the output's sum are fp32; the weights enter the second product
  * rounded to bf16 (8-bit caches: to fp16), the output is rounded once more.

@@ -750,6 +750,16 @@ SPEC_CACHE_MOST_EXP = 48
 _CACHE_TYPES = {torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.int8: 3}
 
 
+def _free_strides(shape, strides):
+    """Strides of all dimensions but the last; those of a size of one, which are free, as for a
+    packed tensor."""
+    out, packed = [], shape[-1]
+    for n, s in zip(shape[-2::-1], strides[-2::-1]):
+        out.append(s if n > 1 else packed)
+        packed = max(packed, out[-1] * n)
+    return out[::-1]
+
+
 class PagedCache:
     """Keys and values [pages, page_size, kv_heads, dim] (bf16, float8_e4m3fn or int8; any
     strides, the same for both, with a contiguous last dimension) and, for the 8-bit types,
@@ -780,7 +790,7 @@ class PagedCache:
         elif k_exps is not None or v_exps is not None:
             raise ValueError("a bf16 cache has no exponents")
         self._tensors = (k, v, k_exps, v_exps)
-        self._pools = (k.data_ptr(), v.data_ptr(), *strides[:3], ek, ev, *es)
+        self._pools = (k.data_ptr(), v.data_ptr(), *_free_strides(shape, strides), ek, ev, *es)
         self._sizes, self._heads, self._code, self._device = shape[:2], shape[2:], code, dev
 
     k = property(lambda self: self._tensors[0])
@@ -852,6 +862,8 @@ def _cache_rows_call(entry, what, cache, block_tables, cached_lens, row_offsets,
     fields = _cache_fields(cache, block_tables, cached_lens, row_offsets, lane_status, shape[0], int(max_len), dev)
     if shape[1:] != cache._heads:
         raise ValueError("k and v must have the cache's heads and head size")
+    if shape[0] < 2 or shape[1] < 2:
+        ks, vs = _free_strides(shape, ks), _free_strides(shape, vs)
     try:
         args = _CACHE_ROWS_LAYOUT.pack(*fields, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], code)
     except (struct.error, OverflowError) as e:
@@ -932,6 +944,8 @@ def spec_paged_attention(q, cache, block_tables, cached_lens, row_offsets, out, 
     kv = fields[-2]
     if dim != fields[-1] or kv == 0 or hq == 0 or hq % kv:  # (checked again by the library, but for dim)
         raise ValueError("q must have the cache's head size and a multiple of its heads")
+    if rows < 2 or hq < 2:
+        qs, os_ = _free_strides(shape, qs), _free_strides(shape, os_)
     lse_ptr = lse_row = 0
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (rows, hq) or (lse.stride(1) != 1 and hq > 1):

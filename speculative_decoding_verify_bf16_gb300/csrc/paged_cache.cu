@@ -211,8 +211,10 @@ PagedVariant variant_for(spec_cache_type type, int dim, int64_t rows, bool tiles
 }
 
 uint64_t scratch_bytes(const PagedVariant& v, int sms) {
-  // (workers times the heads that each takes: v.heads)
-  return static_cast<uint64_t>(sms) * (2 * specv::part_floats(v.rows * v.heads, v.size) * sizeof(float) + v.heads * sizeof(specv::PartRecord));
+  // A thread block's workers times the heads that each takes are v.heads.  (Records for the most workers, so
+  // that more columns never want less.)
+  return static_cast<uint64_t>(sms) *
+         (2 * specv::part_floats(v.rows * v.heads, v.size) * sizeof(float) + specv::kMostWorkers * sizeof(specv::PartRecord));
 }
 
 void* join_kernel(int size) {
@@ -284,7 +286,7 @@ int spec_paged_attention(const spec_paged_attention_args* a, void* stream) {
   p.workers = v.heads / p.heads;
   if (split) {
     p.records = static_cast<specv::PartRecord*>(a->workspace);
-    p.parts = reinterpret_cast<float*>(p.records + sms * v.heads);
+    p.parts = reinterpret_cast<float*>(p.records + sms * specv::kMostWorkers);
   }
   const char* const withhold = std::getenv("SPEC_PAGED_TEST_WITHHOLD_COPY");
   int test_withhold = withhold != nullptr && std::atoi(withhold) != 0;

@@ -22,6 +22,8 @@ namespace specv {
 // end, into the place of the first of them.
 struct PartRecord {
   int32_t lane, head, block, parts;
+  int32_t first, count;  // the lane's rows
+  int32_t unused[2];
 };
 
 struct AttendParams {
@@ -161,7 +163,7 @@ struct Schedule {
           sh.end[i - 1] = at;
           // An item that goes on, and that worker i - 1 begins.
           if (p.parts != nullptr && in > EXTRA && last <= u - in + EXTRA)
-            sh.record[i - 1] = {x.b, x.h, x.k, worker_of(u - in + all - 1, total, g) - static_cast<int>(c + i - 1) + 1};
+            sh.record[i - 1] = {x.b, x.h, x.k, worker_of(u - in + all - 1, total, g) - static_cast<int>(c + i - 1) + 1, x.first, x.count, {0, 0}};
         }
       }
       last = u;

@@ -336,3 +336,46 @@ def test_a_buffer_for_more_columns_serves_fewer():
     ws = sv.new_paged_attention_workspace(8, 2, 128, 600, DEV)
     for n in (1, 3, 8, 100, 600):
         check([n], [3000], hq=8, kv=2, workspace=ws, seed=n)
+
+
+def test_scratch_memory_grows_with_the_columns():
+    for hq, kv, d in ((8, 2, 128), (32, 8, 128), (16, 1, 64), (8, 8, 256), (24, 3, 96)):
+        sizes = [sv.spec_paged_attention_workspace(hq, kv, d, n) for n in (1, 2, 3, 4, 8, 9, 16, 33, 64, 600, 5000)]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+@pytest.mark.parametrize("n", [1, 3])
+def test_strides_of_dimensions_of_one_are_free(n):
+    """One head, one row, one slot a page: their strides are never used, whatever they are."""
+    L = Lanes([n], [20], kv=1, d=64, page=1, seed=26)
+    odd = lambda t, strides: torch.as_strided(t, t.shape, strides)
+    L.cache = sv.PagedCache(odd(L.cache.k, (64, 7, 3, 1)), odd(L.cache.v, (64, 7, 3, 1)))
+    q = odd(L.queries(1), (5 if n == 1 else 64, 3, 1))
+    out, lse, status = attend(L, q, out=odd(torch.zeros(n, 1, 64, dtype=torch.bfloat16, device=DEV), (5 if n == 1 else 64, 3, 1)))
+    torch.cuda.synchronize()
+    assert status.tolist() == [0]
+    check_lane(L, 0, q, out, lse)
+
+
+def test_refusals_of_the_binding():
+    L = Lanes([2], [20], seed=27)
+    q = L.queries(4)
+    out = torch.empty_like(q)
+    bad = [dict(q=q.float()), dict(q=q[0]), dict(out=out[:1]), dict(out=out.float()), dict(q=q.transpose(1, 2), out=out.transpose(1, 2)),
+           dict(q=q[:, :3], out=out[:, :3]), dict(q=q[..., :64], out=out[..., :64]), dict(lse=torch.empty(2, 3, device=DEV)),
+           dict(lane_status=torch.zeros(1, device=DEV)), dict(tables=L.tables.long()), dict(tables=L.tables[0]),
+           dict(tables=L.tables.repeat(2, 1)), dict(cached=None), dict(offsets=None), dict(cache=tuple(L.cache)), dict(scale="1"),
+           dict(max_len=2 ** 40), dict(workspace=torch.empty(9, device=DEV))]
+    for kw in bad:
+        a = dict(q=q, cache=L.cache, tables=L.tables, cached=L.cached, offsets=L.offsets, out=out, max_len=2) | kw
+        with pytest.raises((ValueError, TypeError)):
+            sv.spec_paged_attention(a.pop("q"), a.pop("cache"), a.pop("tables"), a.pop("cached"), a.pop("offsets"), a.pop("out"),
+                                    a.pop("max_len"), **a)
+    k, v, _, _ = L.cache
+    for args in ((k, v[:1]), (k, v.float()), (k.float(), v.float()), (k[0], v[0]), (k, v, torch.zeros(1)), (k.view(torch.int8), v.view(torch.int8))):
+        with pytest.raises(ValueError):
+            sv.PagedCache(*args)
+    rows = torch.zeros(2, L.kv, L.d, device=DEV)
+    for kk, vv in ((rows.half(), rows.half()), (rows[:, :1], rows[:, :1]), (rows, rows[:1]), (rows.transpose(1, 2), rows.transpose(1, 2))):
+        with pytest.raises(ValueError):
+            sv.spec_cache_write(*L.where(), kk, vv, 2)
