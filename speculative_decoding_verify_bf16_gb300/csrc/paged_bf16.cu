@@ -2,5 +2,5 @@
 #include "paged_variants.cuh"
 
 namespace specv {
-PagedVariant paged_bf16(int dim, int64_t rows, bool tiles) { return paged_variant<SPEC_CACHE_BF16>(dim, rows, tiles); }
+PagedVariant paged_bf16(int dim, int64_t rows, bool tiles, bool few) { return paged_variant<SPEC_CACHE_BF16>(dim, rows, tiles, few); }
 }  // namespace specv

@@ -204,10 +204,10 @@ int cache_rows(const spec_cache_rows_args* a, void* stream) {
 // ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
-PagedVariant variant_for(spec_cache_type type, int dim, int64_t rows, bool tiles) {
-  if (type == SPEC_CACHE_BF16) return specv::paged_bf16(dim, rows, tiles);
-  if (type == SPEC_CACHE_E4M3) return specv::paged_e4m3(dim, rows, tiles);
-  return specv::paged_int8(dim, rows, tiles);
+PagedVariant variant_for(spec_cache_type type, int dim, int64_t rows, bool tiles, bool few) {
+  if (type == SPEC_CACHE_BF16) return specv::paged_bf16(dim, rows, tiles, few);
+  if (type == SPEC_CACHE_E4M3) return specv::paged_e4m3(dim, rows, tiles, few);
+  return specv::paged_int8(dim, rows, tiles, few);
 }
 
 uint64_t scratch_bytes(const PagedVariant& v, int sms) {
@@ -239,8 +239,10 @@ uint64_t spec_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int32
   const int64_t rows = static_cast<int64_t>(max_len) * (q_heads / kv_heads);
   uint64_t most = 0;
   for (spec_cache_type type : {SPEC_CACHE_BF16, SPEC_CACHE_E4M3, SPEC_CACHE_INT8}) {
-    const uint64_t n = scratch_bytes(variant_for(type, dim, rows, true), sms);
-    most = n > most ? n : most;
+    for (const bool few : {false, true}) {
+      const uint64_t n = scratch_bytes(variant_for(type, dim, rows, true, few), sms);
+      most = n > most ? n : most;
+    }
   }
   return most;
 }
@@ -277,7 +279,8 @@ int spec_paged_attention(const spec_paged_attention_args* a, void* stream) {
   if ((rc = device_sms(&dev, &sms)) != SPEC_OK) return rc;
   // The tiles' kernel takes its maxima from unscaled scores: not for a scale of 0 or below (or NaN),
   // nor for one that is nothing beside the largest numbers.
-  const PagedVariant v = variant_for(a->cache.type, p.c.dim, rows, p.scale >= 0x1p-100f);
+  const bool few = static_cast<int64_t>(p.c.lanes) * p.c.kv_heads <= sms / 4;
+  const PagedVariant v = variant_for(a->cache.type, p.c.dim, rows, p.scale >= 0x1p-100f, few);
   if ((rc = grant_smem(v, dev)) != SPEC_OK) return rc;
   const bool split = a->workspace != nullptr && a->workspace_bytes >= scratch_bytes(v, sms);
   p.heads = v.heads;

@@ -2,5 +2,5 @@
 #include "paged_variants.cuh"
 
 namespace specv {
-PagedVariant paged_int8(int dim, int64_t rows, bool tiles) { return paged_variant<SPEC_CACHE_INT8>(dim, rows, tiles); }
+PagedVariant paged_int8(int dim, int64_t rows, bool tiles, bool few) { return paged_variant<SPEC_CACHE_INT8>(dim, rows, tiles, few); }
 }  // namespace specv

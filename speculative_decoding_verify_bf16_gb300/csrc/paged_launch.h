@@ -15,9 +15,9 @@ struct PagedVariant {
 };
 
 // The kernel for heads of `dim` and up to `rows` rows of a lane and cache head; `tiles`: the
-// one of large tiles may be taken.
-PagedVariant paged_bf16(int dim, int64_t rows, bool tiles);
-PagedVariant paged_e4m3(int dim, int64_t rows, bool tiles);
-PagedVariant paged_int8(int dim, int64_t rows, bool tiles);
+// one of large tiles may be taken; `few`: there are few lanes and heads.
+PagedVariant paged_bf16(int dim, int64_t rows, bool tiles, bool few);
+PagedVariant paged_e4m3(int dim, int64_t rows, bool tiles, bool few);
+PagedVariant paged_int8(int dim, int64_t rows, bool tiles, bool few);
 
 }  // namespace specv

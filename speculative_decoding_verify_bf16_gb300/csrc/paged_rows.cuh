@@ -1,7 +1,9 @@
 // paged_rows.cuh -- attention of a few rows (decoding, a verify round) over a paged cache.
 //
 // o = sum_j w_j v_j / sum_j w_j,  w_j = 2^(x_j - M),  x_j = scale * log2(e) * q . k_j, with the running maximum M
-// of a row: one pass over keys and values.
+// of a row: one pass over keys and values.  Scores, sums of weights and numerators are fp32; for the
+// second product a weight is rounded to the operands' type, bf16 (an error like that of the output's own
+// rounding, and independent of it) or, with an 8-bit cache, fp16 (an eighth of that).
 //
 // What bounds it is reading the cache: 2 * dim numbers a token and head, for the rows of all query
 // heads and columns of that head together.  A thread block's computing warps take a cache head each (of

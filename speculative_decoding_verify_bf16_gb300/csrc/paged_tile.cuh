@@ -3,7 +3,7 @@
 //
 //   S = q k^T (fp32, tensor memory)     P = 2^(scale log2(e) S - M), hidden ones 0     O += P v
 //
-// A row's running maximum M is raised, and O in tensor memory rescaled, only where a score exceeds
+// P is rounded to bf16 (8-bit caches: fp16) as the few rows' kernel's weights are.  A row's running maximum M is raised, and O in tensor memory rescaled, only where a score exceeds
 // it by more than 2^8; sums of weights are fp32, in the thread that has the row.
 //
 // Products of a step and tile take 2 x 512 cycles on the tensor cores (heads of 128), the two tiles'

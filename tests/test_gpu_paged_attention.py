@@ -72,6 +72,19 @@ def test_columns(kind, lens):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [48, 64, 128])
+@pytest.mark.parametrize("window,whole", [(0, False), (50, False), (0, True)])
+def test_rounds_of_many_lanes(kind, d, window, whole):
+    """17 to 32 rows of a head and many lanes (few of them take the tiles), split and whole."""
+    rng = np.random.default_rng(d)
+    lens = rng.integers(0, 5, 44).tolist()
+    before = rng.integers(0, 700, 44).tolist()
+    workspace = torch.empty(0, dtype=torch.uint8, device=DEV) if whole else None
+    check(lens, before, hq=8, kv=1, d=d, kind=kind, page=24, window=window, workspace=workspace, seed=d)
+    check([4], [900], hq=8, kv=1, d=d, kind=kind, scale=-0.1, window=window, workspace=workspace, seed=d + 1)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("n,before,d", [(255, 0, 128), (256, 1, 64), (257, 300, 128), (700, 130, 96), (512, 1500, 128), (300, 10, 256)])
 def test_prompts(kind, n, before, d):
     check([n], [before], hq=2, kv=1, d=d, kind=kind, seed=n)
