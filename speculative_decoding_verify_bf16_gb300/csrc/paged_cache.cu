@@ -277,10 +277,10 @@ int spec_paged_attention(const spec_paged_attention_args* a, void* stream) {
   if (a->max_context > 0 && a->max_context < p.c.most) p.c.most = a->max_context;
   int dev, sms;
   if ((rc = device_sms(&dev, &sms)) != SPEC_OK) return rc;
-  // The tiles' kernel takes its maxima from unscaled scores: not for a scale of 0 or below (or NaN),
-  // nor for one that is nothing beside the largest numbers.
+  // The tiles' kernel takes its maxima from unscaled scores: not for a scale of 0 or below (or NaN, or
+  // infinite), nor for one that is nothing beside the largest numbers.
   const bool few = static_cast<int64_t>(p.c.lanes) * p.c.kv_heads <= sms / 4;
-  const PagedVariant v = variant_for(a->cache.type, p.c.dim, rows, p.scale >= 0x1p-100f, few);
+  const PagedVariant v = variant_for(a->cache.type, p.c.dim, rows, p.scale >= 0x1p-100f && p.scale <= 0x1.fffffep127f, few);
   if ((rc = grant_smem(v, dev)) != SPEC_OK) return rc;
   const bool split = a->workspace != nullptr && a->workspace_bytes >= scratch_bytes(v, sms);
   p.heads = v.heads;

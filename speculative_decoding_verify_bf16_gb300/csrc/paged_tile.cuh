@@ -208,8 +208,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       for (int j = 0; j < n; ++j, p0 += S::kTile, ++refs) {
         if (!(ok = warp_wait(&sm.s_full[w], steps++ & 1, &sm.abort))) break;
         tc_fence_after();
-        // Of 32 positions each: a score's factor, and what its exponent gets.
-        auto factor = [&](int i) { return kEight ? qs * sm.refs[refs % kTileRefs][0][i] : qs; };
+        // Of 32 positions each: a score's factor, and what its exponent gets.  (The factor is kept above 0 and
+        // finite: hidden scores, -inf, must stay that, and scores of 0 too.  Where it is kept at 2^-126, scores
+        // are below 2^-60; where at the largest number, others are beyond fp32.)
+        auto factor = [&](int i) {
+          return kEight ? fminf(fmaxf(qs * sm.refs[refs % kTileRefs][0][i], 0x1p-126f), 0x1.fffffep127f) : qs;
+        };
         auto addend = [&](int i) { return kEight ? sm.refs[refs % kTileRefs][1][i] : 0.f; };
         const bool part_hidden = __any_sync(0xFFFFFFFFu, p0 + S::kTile > lim || p0 < low);
         uint32_t x[2][32];
