@@ -29,9 +29,10 @@
 // 8-bit caches: numbers become fp16 in registers, exactly, and products are fp16.  q is
 // taken times a power of two for each row into fp16's range (exactly, but for what is below
 // 2^-38 of the row's largest).  The key's power of two multiplies its scores; the value's, 2^e,
-// goes into the weight's exponent, w = 2^(x + e - M), and out of the sum of weights again.  (Exponents lie
-// within -48..48, so a weight that vanishes beside the largest is below 2^-30 of it in the
-// sum.)  The components' order is free in both products: a thread takes sixteen neighbouring
+// goes into the weight's exponent, w = 2^(x + e - M), and out of the sum of weights again.  M stays seven
+// below the running maximum of x + e, so that fp16's 2^-25, below which a weight is lost, is 2^-32 of the
+// largest: many small ones together count.  (Weights stay below 2^15; exponents lie within -48..48, so sums
+// are within fp32.)  The components' order is free in both products: a thread takes sixteen neighbouring
 // bytes of a token at a time.
 #pragma once
 
@@ -48,7 +49,10 @@
 
 namespace specv {
 
-constexpr float kRowsSlack = 8.f;           // a maximum is raised when it is exceeded by more: weights stay below 2^8
+constexpr float kRowsSlack = 8.f;  // a maximum is raised when a score, in powers of two, exceeds it by more
+// M, from which scores are taken, lies so far below the maximum: fp16 weights use the type's upper range.
+template <bool EIGHT>
+constexpr float kRowsBelow = EIGHT ? 7.f : 0.f;
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
       const bool started = at.tile == at.t0, ends = at.tile + n_units == at.t1;
       // q as left operands: of each 16 components a thread has four of rows g and g + 8.
       uint32_t qf[S::kShared ? 1 : D / 16][4];
-      float qs[MT][2], o[MT][D / 8][4], top[MT][2], sum[MT][2];
+      float qs[MT][2], o[MT][D / 8][4], top[MT][2], sum[MT][2];  // (top: M)
       int last[MT][2];  // one past the last position that a row sees
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -591,7 +595,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
               float most = fmaxf(fmaxf(x[m][0][2 * i], x[m][0][2 * i + 1]), fmaxf(x[m][1][2 * i], x[m][1][2 * i + 1]));
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-              raise[m][i] = most > top[m][i] + kRowsSlack ? most : top[m][i];
+              raise[m][i] = most > top[m][i] + (kRowsSlack + kRowsBelow<kEight>) ? most - kRowsBelow<kEight> : top[m][i];
               any |= raise[m][i] != top[m][i];
             }
           if (__any_sync(0xFFFFFFFFu, any)) {

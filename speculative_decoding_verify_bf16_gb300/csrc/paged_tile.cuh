@@ -3,8 +3,9 @@
 //
 //   S = q k^T (fp32, tensor memory)     P = 2^(scale log2(e) S - M), hidden ones 0     O += P v
 //
-// P is rounded to bf16 (8-bit caches: fp16) as the few rows' kernel's weights are.  A row's running maximum M is raised, and O in tensor memory rescaled, only where a score exceeds
-// it by more than 2^8; sums of weights are fp32, in the thread that has the row.
+// P is rounded to bf16 (8-bit caches: fp16) as the few rows' kernel's weights are, and M is taken as there.
+// It is raised, and O in tensor memory rescaled, only where a score (in powers of two) exceeds the row's running
+// maximum by more than 8; sums of weights are fp32, in the thread that has the row.
 //
 // Products of a step and tile take 2 x 512 cycles on the tensor cores (heads of 128), the two tiles'
 // take turns: while one's run, the other's scores become weights.  Per step and tile a warp does 32 x 128
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       }
       const int r = at.k * S::kRows + w * 128 + row, col = column_of(p, r);
       const int lim = at.before + col + 1, low = p.window > 0 ? lim - p.window : 0;
-      float top = -INFINITY, sum = 0.f;
+      float top = -INFINITY, sum = 0.f;  // (top: M)
       int p0 = at.tile * S::kTile;
 #pragma unroll 1
       for (int j = 0; j < n; ++j, p0 += S::kTile, ++refs) {
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
             most = fmaxf(most, kEight ? fmaf(mi, factor(half * 2 + i), addend(half * 2 + i)) : mi * qs);
           }
         }
-        const float raise = most > top + kRowsSlack ? most : top;
+        const float raise = most > top + (kRowsSlack + kRowsBelow<kEight>) ? most - kRowsBelow<kEight> : top;
         if (__any_sync(0xFFFFFFFFu, raise != top)) {
           const float f = raise == top ? 1.f : ex2_approx(top - raise);
           top = raise;
