@@ -158,8 +158,8 @@ uint64_t spec_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int32
  * included, and rows behind the last lane's are left as they are.  out must not overlap q.
  *
  * Scores, sums and the output's sum are fp32; the weights enter the second product
- * rounded to bf16 (8-bit caches: with the value's 2^e to fp16, at most 2^-32 of a row's largest beside
- * 2^-11 of their own), the output is rounded once more.
+ * rounded to bf16 (8-bit caches: with the value's 2^e to fp16, off by 2^-11 of their own or, with many
+ * columns, 2^-25 of the row's largest, 2^-32 with few), the output is rounded once more.
  * SPEC_ERR_NONFINITE for a lane with an output that is not finite, as when a query, or a
  * key or value that one of its columns sees, is not.  SPEC_ERR_TIMEOUT: a bounded wait gave up.
  *

@@ -64,8 +64,9 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
   return n / d;
 }
 
-// LEAST: costs that a worker takes at least (more workers leave more parts to join).
-template <int ROWS, int TILE, int EXTRA, int LEAST>
+// LEAST: costs that a worker takes at least (more workers leave more parts to join).  WORKERS: of a thread
+// block, at most.
+template <int ROWS, int TILE, int EXTRA, int LEAST, int WORKERS = kMostWorkers>
 struct Schedule {
   static __device__ __forceinline__ void set_block(const AttendParams& p, Cursor& x) {
     const int i0 = column_of(p, x.k * ROWS), i1 = min(x.count - 1, column_of(p, x.k * ROWS + ROWS - 1));
@@ -99,9 +100,9 @@ struct Schedule {
   }
   struct Shared {
     int64_t units[32], cost[32];
-    int64_t begin[kMostWorkers], end[kMostWorkers];  // units of this thread block's workers
-    Cursor from[kMostWorkers];                       // at the first of them
-    PartRecord record[kMostWorkers];
+    int64_t begin[WORKERS], end[WORKERS];  // units of this thread block's workers
+    Cursor from[WORKERS];                       // at the first of them
+    PartRecord record[WORKERS];
   };
 
   // Workers that get work.
@@ -174,7 +175,7 @@ struct Schedule {
   // launch's first instructions come from far: few of them, and each thread reads one lane.)
   static __device__ void plan(const AttendParams& p, Shared& sh) {
     const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x < kMostWorkers) {
+    if (threadIdx.x < WORKERS) {
       sh.begin[threadIdx.x] = sh.end[threadIdx.x] = 0;
       sh.record[threadIdx.x].parts = 0;
     }

@@ -31,8 +31,10 @@
 //
 // 8-bit caches become fp16 on the way to shared memory, times 2^(e - r) with r the largest of a warp's 32
 // exponents, and q becomes fp16 times a power of two for each row.  2^r multiplies the keys' scores; the
-// values' r goes into the weights' exponents and out of their sum.  All of it is exact but for numbers
-// more than 2^14 below the largest of their 32 positions, which keep 24 bits behind that one's first.
+// values' r goes into the weights' exponents and out of their sum.  All of it is exact: keys' exponents may be
+// 15 below r (e4m3's least number is then fp16's, 2^-24), and values' 7, so that M, which r enters, takes no
+// more than that off the small weights.  A group of 32 positions with larger differences is taken apart: its
+// numbers come as they are, and each score gets its own position's exponents, as in the few rows' kernel.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -52,7 +54,8 @@ constexpr int kTileRegs = 2 * kTileRegsRows + 2 * kTileRegsCopy + kTileRegsIssue
 static_assert(kTileRegs <= 5 * 96 && kTileRegsCopy <= 96 && kTileRegsIssue <= 96 && kTileRegsRows >= 96,
               "shares within what the launch brings; those that shrink are below it, those that grow above");
 constexpr int kTileHalf = 128 * 128;  // bytes of 128 rows of 64 numbers
-constexpr int kTileRefs = 8;          // steps whose exponents are held: more than the ring has steps
+// Differences of exponents within 32 positions up to which these are taken together.
+constexpr uint32_t kKeysTogether = 15, kValuesTogether = 7;
 
 template <int TYPE_, int D_>
 struct TileShape {
@@ -62,7 +65,11 @@ struct TileShape {
   static constexpr int kBytes = kTileHalf * (D / 64);
   static constexpr int kStages = D > 64 ? 5 : 8;
   static constexpr int kExtra = 4;  // an item's beginning and end, in units (12 e4m3 prompts: 364 us with 1, 319 with 2, 301 with 4, 314 with 7)
-  using Plan = Schedule<kRows, kTile, kExtra, 1>;
+  using Plan = Schedule<kRows, kTile, kExtra, 1, 1>;
+  // Steps whose exponents are held.  A step's are written when its keys' place in the ring is free: five places
+  // before it lie the values of the third step back, eight before it the keys of the fourth, whose scores follow
+  // the weights of the fifth.  What is older has been read.
+  static constexpr int kHeld = kStages / 2 + 1;
 };
 
 template <typename S>
@@ -70,7 +77,9 @@ struct TileSmem {
   uint8_t q[2][S::kBytes];
   uint8_t ring[S::kStages][S::kBytes];
   Cursor cursor[17], ahead[8];  // of each warp (registers are short)
-  float refs[kTileRefs][2][4];  // of a step's keys and values: each 32 positions' exponent
+  // Of a step's 32 positions each: 2^r of the keys, r of the values, 2^-r of them; -1, 0, 0: taken apart.
+  alignas(16) float refs[S::kHeld][3][4];
+  alignas(8) uint8_t own[S::kEight ? S::kHeld : 1][2][S::kTile];  // exponents' bytes of positions taken apart
   typename S::Plan::Shared plan;
   uint64_t full[S::kStages], empty[S::kStages];
   uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], drain;
@@ -86,6 +95,53 @@ __host__ __device__ constexpr uint32_t mma_desc_of(bool half, int M, int N, bool
 // Byte offset of 16-byte unit u of row r: pieces of 64 numbers one after the other.
 __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t u) {
   return (u >> 3) * kTileHalf + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+}
+
+// A row's scores of positions taken apart (32 each; those whose `refs` are negative): with the positions' own
+// exponents, their bytes in `own`, back to tensor memory at `at`, and the sum of their weights into `sum`.
+// The row sees positions first .. end - 1 of the tile; gives back M and the sum.  (A function of its own: in place,
+// although it never ran, 2,048 tokens behind 30,000 in e4m3 took 987 us instead of 886, 12 ragged prompts 268
+// instead of 253; without it 875 and 245.)
+static __device__ __noinline__ float2 tile_apart(uint32_t at, const float* refs, const uint8_t (*own)[128], float qs, int first, int end,
+                                          float top, float sum) {
+  auto byte_of = [](uint2 bytes, int k) { return ((k < 4 ? bytes.x : bytes.y) >> (8 * (k & 3))) & 255u; };
+  float most = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < 128; i += 8) {
+    if (!(refs[i / 32] < 0.f)) continue;
+    const uint2 kb = *reinterpret_cast<const uint2*>(own[0] + i), vb = *reinterpret_cast<const uint2*>(own[1] + i);
+    uint32_t x[8];
+    tmem_ld8(x, at + i);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float s = fmaf(__uint_as_float(x[k]) * __uint_as_float(byte_of(kb, k) << 23), qs,
+                           static_cast<float>(static_cast<int>(byte_of(vb, k)) - 127));
+      x[k] = __float_as_uint(s);
+      if (i + k >= first && i + k < end) most = fmaxf(most, s);
+    }
+    tmem_st8(at + i, x);
+  }
+  tmem_wait_st();
+  if (most > top + (kRowsSlack + kRowsBelow<true>)) {
+    sum *= ex2_approx(top - (most - kRowsBelow<true>));
+    top = most - kRowsBelow<true>;
+  }
+  __syncwarp();
+  const float from = top == -INFINITY ? 0.f : top;
+#pragma unroll 1
+  for (int i = 0; i < 128; i += 8) {
+    if (!(refs[i / 32] < 0.f)) continue;
+    const uint2 vb = *reinterpret_cast<const uint2*>(own[1] + i);
+    uint32_t x[8];
+    tmem_ld8(x, at + i);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i + k >= first && i + k < end)
+        sum = fmaf(ex2_approx(__uint_as_float(x[k]) - from), power_of_minus(static_cast<float>(static_cast<int>(byte_of(vb, k)) - 127)), sum);
+  }
+  return make_float2(top, sum);
 }
 
 template <typename S>
@@ -212,10 +268,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         // Of 32 positions each: a score's factor, and what its exponent gets.  (The factor is kept above 0 and
         // finite: hidden scores, -inf, must stay that, and scores of 0 too.  Where it is kept at 2^-126, scores
         // are below 2^-60; where at the largest number, others are beyond fp32.)
+        const int held = kEight ? refs % S::kHeld : 0;
         auto factor = [&](int i) {
-          return kEight ? fminf(fmaxf(qs * sm.refs[refs % kTileRefs][0][i], 0x1p-126f), 0x1.fffffep127f) : qs;
+          if (!kEight) return qs;
+          const float ref = sm.refs[held][0][i];
+          return ref < 0.f ? 1.f : fminf(fmaxf(qs * ref, 0x1p-126f), 0x1.fffffep127f);
         };
-        auto addend = [&](int i) { return kEight ? sm.refs[refs % kTileRefs][1][i] : 0.f; };
+        auto addend = [&](int i) { return kEight ? sm.refs[held][1][i] : 0.f; };
+        const float before = top;
+        if constexpr (kEight) {
+          const float4 r = *reinterpret_cast<const float4*>(sm.refs[held][0]);
+          if (fminf(fminf(r.x, r.y), fminf(r.z, r.w)) < 0.f) {
+            const float2 now = tile_apart(tms, sm.refs[held][0], sm.own[held], qs, low - p0, lim - p0, top, sum);
+            top = now.x;
+            sum = now.y;
+          }
+        }
         const bool part_hidden = __any_sync(0xFFFFFFFFu, p0 + S::kTile > lim || p0 < low);
         uint32_t x[2][32];
         auto load = [&](int half) {
@@ -246,10 +314,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
           }
         }
         const float raise = most > top + (kRowsSlack + kRowsBelow<kEight>) ? most - kRowsBelow<kEight> : top;
-        if (__any_sync(0xFFFFFFFFu, raise != top)) {
-          const float f = raise == top ? 1.f : ex2_approx(top - raise);
+        if (__any_sync(0xFFFFFFFFu, raise != before)) {
+          const float f = raise == before ? 1.f : ex2_approx(before - raise);
+          sum *= kEight ? raise == top ? 1.f : ex2_approx(top - raise) : f;
           top = raise;
-          sum *= f;
           if (j > 0) {
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
@@ -282,7 +350,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
             }
             part[0] = add2(part[0], part[1]);
             const float s = first_of(part[0]) + second_of(part[0]);
-            sum = kEight ? fmaf(s, power_of_minus(add), sum) : sum + s;
+            sum = kEight ? fmaf(s, sm.refs[held][2][half * 2 + i], sum) : sum + s;
           }
           tmem_st32(tms + half * 32, y);
           tmem_wait_st();
@@ -443,9 +511,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
                                           : make_uint4(0u, 0u, 0u, 0u);
         }
       };
-      // A tile as fp16 into the ring; `byte`: this lane's position's exponent, `ref` the largest.
-      auto store = [&](uint32_t byte, uint32_t ref) {
+      // A tile as fp16 into the ring; `byte`: this lane's position's exponent, `ref` the largest (or the same: the
+      // numbers as they are).  `tell` leaves word of the exponents.
+      auto store = [&](uint32_t byte, uint32_t ref, auto tell) {
         if (round > 0 && !(ok = warp_wait(&sm.empty[slot], (round - 1) & 1, &sm.abort))) return;
+        tell();
         uint8_t* const to = sm.ring[slot];
         const float f = byte == 255u ? __uint_as_float(0x7FC00000u)
                                      : __uint_as_float(static_cast<uint32_t>(max(127 + static_cast<int>(byte) - static_cast<int>(ref), 0)) << 23);
@@ -495,17 +565,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
         locate();
         page = next_page;
       }
-      int step = 0;
+      int held = 0;
 #pragma unroll 1
-      for (; ok && left > 0; --left, ++step) {
+      for (; ok && left > 0; --left, held = held + 1 == S::kHeld ? 0 : held + 1) {
         take();
         fetch(here);
         const uint32_t kr = largest(kb), vr = largest(vb);
-        if (which == 0 && lane == 0) {
-          sm.refs[step % kTileRefs][0][mine] = __uint_as_float(kr << 23);
-          sm.refs[step % kTileRefs][1][mine] = static_cast<float>(static_cast<int>(vr) - 127);
-        }
-        store(which ? vb : kb, which ? vr : kr);
+        // (positions that no row of the item sees hold zeros)
+        const bool apart = __any_sync(0xFFFFFFFFu, here != kNowhere && (kb + kKeysTogether < kr || vb + kValuesTogether < vr));
+        const uint32_t byte = which ? vb : kb;
+        store(byte, apart ? byte : which ? vr : kr, [&] {
+          if (which != 0) return;
+          if (apart) {
+            sm.own[held][0][mine * 32 + lane] = static_cast<uint8_t>(kb);
+            sm.own[held][1][mine * 32 + lane] = static_cast<uint8_t>(vb);
+          }
+          if (lane == 0) {
+            const float r = static_cast<float>(static_cast<int>(vr) - 127);
+            sm.refs[held][0][mine] = apart ? -1.f : __uint_as_float(kr << 23);
+            sm.refs[held][1][mine] = apart ? 0.f : r;
+            sm.refs[held][2][mine] = apart ? 0.f : power_of_minus(r);
+          }
+        });
       }
     }
   } else {
