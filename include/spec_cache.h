@@ -69,8 +69,9 @@ typedef struct {
   /* Lane b owns rows row_offsets[b] .. row_offsets[b + 1] - 1 (none: nothing to do).
    * [lanes + 1], ascending, within 0..rows. */
   const int32_t* row_offsets;
-  /* Read and updated in place, may be NULL: a lane whose status is not SPEC_OK on entry is
-   * left out.  SPEC_ERR_LAYOUT: row_offsets descend, leave 0..rows or give the lane more
+  /* Read and updated in place (to be read when the call's work is done), may be NULL: a lane whose
+   * status, one of spec_verify.h's, is not SPEC_OK on entry is left out, and its status stays.  Otherwise a
+   * lane's first error is reported.  SPEC_ERR_LAYOUT: row_offsets descend, leave 0..rows or give the lane more
    * than max_len rows; cached_lens is negative or the lane's last position lies beyond
    * its table; a page that the lane needs is outside 0..pages - 1 (never read or
    * written).  SPEC_ERR_NONFINITE, SPEC_ERR_TIMEOUT: see the calls.  A failed lane's

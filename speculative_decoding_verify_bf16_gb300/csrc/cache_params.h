@@ -27,6 +27,8 @@ struct CacheParams {
   const int32_t* cached;
   const int32_t* offsets;
   int32_t* status;
+  const int32_t* entry;  // status, or any other words where there is none; the bits of a word that count
+  uint32_t entry_bits;
   int32_t pages, page_size;
   uint32_t page_magic, page_shift;  // p / page_size, see page_of
   int32_t lanes, rows, max_len, kv_heads, dim;
@@ -69,9 +71,26 @@ __device__ __forceinline__ uint32_t head_at(const CacheParams& c, int page, int 
 }
 constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 
+__device__ __forceinline__ int lane_status(const CacheParams& c, int b) {
+  return c.status != nullptr ? *static_cast<volatile int32_t*>(c.status + b) : SPEC_OK;
+}
 // The first error of a lane stays.
 __device__ __forceinline__ void lane_failed(const CacheParams& c, int b, int code) {
-  if (c.status != nullptr && *static_cast<volatile int32_t*>(c.status + b) == SPEC_OK) c.status[b] = code;
+  if (c.status != nullptr && lane_status(c, b) == SPEC_OK) c.status[b] = code;
+}
+// The attention's thread blocks, which may not all begin at once, have to agree on the lanes that had failed before
+// the launch.  An error of its own stands in the status' highest four bits until its last launch moves it down.
+constexpr int kFreshShift = 28;
+constexpr uint32_t kEntryBits = (1u << kFreshShift) - 1;
+__device__ __forceinline__ void lane_fails_now(const CacheParams& c, int b, int code) { lane_failed(c, b, code << kFreshShift); }
+__device__ __forceinline__ bool failed_before(const CacheParams& c, int b) { return (c.entry[b] & c.entry_bits) != 0; }
+// Moves all lanes' errors down (a thread block's threads).
+__device__ __forceinline__ void settle_errors(const CacheParams& c) {
+  if (c.status == nullptr) return;
+  for (int b = threadIdx.x; b < c.lanes; b += blockDim.x) {
+    const int status = lane_status(c, b);
+    if (status != SPEC_OK && (status & kEntryBits) == 0) c.status[b] = static_cast<uint32_t>(status) >> kFreshShift;
+  }
 }
 
 }  // namespace specv

@@ -65,6 +65,8 @@ int check_cache(const spec_paged_cache& a, CacheParams* c) {
   c->cached = a.cached_lens;
   c->offsets = a.row_offsets;
   c->status = a.lane_status;
+  c->entry = a.lane_status != nullptr ? a.lane_status : a.row_offsets;
+  c->entry_bits = a.lane_status != nullptr ? specv::kEntryBits : 0u;
   c->pages = a.pages;
   specv::set_page_size(*c, a.page_size);
   c->lanes = a.lanes;
@@ -204,6 +206,14 @@ int cache_rows(const spec_cache_rows_args* a, void* stream) {
 // ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
+// The last launch where no item was split.
+constexpr int kStatusThreads = 128;
+__global__ void __launch_bounds__(kStatusThreads) paged_status_kernel(const CacheParams c) {
+  specv::griddep_wait();
+  specv::griddep_launch_dependents();
+  specv::settle_errors(c);
+}
+
 PagedVariant variant_for(spec_cache_type type, int dim, int64_t rows, bool tiles, bool few) {
   if (type == SPEC_CACHE_BF16) return specv::paged_bf16(dim, rows, tiles, few);
   if (type == SPEC_CACHE_E4M3) return specv::paged_e4m3(dim, rows, tiles, few);
@@ -295,7 +305,11 @@ int spec_paged_attention(const spec_paged_attention_args* a, void* stream) {
   int test_withhold = withhold != nullptr && std::atoi(withhold) != 0;
   void* args[] = {&p, &test_withhold};
   rc = launch(v.kernel, dim3(static_cast<unsigned>(sms)), static_cast<unsigned>(v.threads), static_cast<size_t>(v.smem), args, stream);
-  if (rc != SPEC_OK || !split) return rc;
+  if (rc != SPEC_OK || (!split && p.c.status == nullptr)) return rc;
+  if (!split) {
+    void* status_args[] = {&p.c};
+    return launch(reinterpret_cast<void*>(&paged_status_kernel), dim3(1), kStatusThreads, 0, status_args, stream);
+  }
   // Rows of a thread block of the join: one, and more where that would be too many blocks, most of
   // which find nothing to do.
   int of_item = v.rows, used = static_cast<int>(rows < v.rows ? rows : v.rows);

@@ -246,7 +246,8 @@ struct RowSum {
       a[0].w += __shfl_xor_sync(0xFFFFFFFFu, a[0].w, 16);
     }
   }
-  // The finished row, of query head `head` and packed row `row`.
+  // The finished row, of query head `head` and packed row `row`.  (SHIFT: of the errors, 0 in the last launch.)
+  template <int SHIFT>
   __device__ __forceinline__ void finish(const AttendParams& p, int lane_of, int64_t row, int head) const {
     const int lane = threadIdx.x & 31, at = lane % kAcross;
     if (lane >= kAcross) return;
@@ -258,7 +259,7 @@ struct RowSum {
       if (d < p.c.dim) {
         *reinterpret_cast<uint2*>(p.out + row * p.out_row + head * p.out_head + d) =
             make_uint2(to_bf16x2(b.x, b.y), to_bf16x2(b.z, b.w));
-        if (!finite4(b)) lane_failed(p.c, lane_of, SPEC_ERR_NONFINITE);
+        if (!finite4(b)) lane_failed(p.c, lane_of, SPEC_ERR_NONFINITE << SHIFT);
       }
     }
     if (p.lse != nullptr && lane == 0) p.lse[row * p.lse_row + head] = (top + log2f(sum)) * kLn2;
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
   if (blockIdx.x == 0)  // lanes laid out wrongly have no units
     for (int b = threadIdx.x; b < c.lanes; b += S::kThreads) {
       int first, count, before;
-      if (!cache_lane(c, b, first, count, before)) lane_failed(c, b, SPEC_ERR_LAYOUT);
+      if (!cache_lane(c, b, first, count, before)) lane_fails_now(c, b, SPEC_ERR_LAYOUT);
     }
   const int pair = warp % S::kWarps, worker = pair / p.heads, head_in = pair - worker * p.heads;
   const int64_t begin = sm.plan.begin[worker], end = sm.plan.end[worker];
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
       if (!acquire()) break;
       if (page0 != kUnseen) {
         if (static_cast<uint32_t>(page0) >= static_cast<uint32_t>(c.pages)) {
-          lane_failed(c, at.b, SPEC_ERR_LAYOUT);
+          lane_fails_now(c, at.b, SPEC_ERR_LAYOUT);
         } else {
           const int pos = at.tile * kTokens + lane, in = pos - page_of(c, pos) * c.page_size, head = at.h * p.heads + head_in;
           from = head_at(c, page0, in, head);
@@ -728,7 +729,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
               }
             }
           if (direct) {
-            if (!fine) lane_failed(c, at.b, SPEC_ERR_NONFINITE);
+            if (!fine) lane_fails_now(c, at.b, SPEC_ERR_NONFINITE);
             if (p.lse != nullptr && t == 0) p.lse[(at.first + col) * p.lse_row + q_head] = (top[m][i] + log2f(s)) * kLn2;
           } else if (t == 0) {
             *reinterpret_cast<float2*>(part + S::kRows * p.heads * D + 2 * (head_in * S::kRows + r)) = make_float2(top[m][i], s);
@@ -741,7 +742,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
   }
   __syncthreads();
   const int64_t worker0 = static_cast<int64_t>(blockIdx.x) * p.workers;
-  if (p.parts != nullptr && p.workers > 1) {
+  if (sm.abort) {  // a wait gave up: all lanes of the block's units (and nothing to join)
+    if (threadIdx.x < p.workers && c.status != nullptr) {
+      Cursor x = sm.plan.from[threadIdx.x];
+      for (int64_t u = sm.plan.begin[threadIdx.x]; u < sm.plan.end[threadIdx.x]; ++u, Plan::next_unit(p, x))
+        lane_fails_now(c, x.b, SPEC_ERR_TIMEOUT);
+    }
+  } else if (p.parts != nullptr && p.workers > 1) {
     // Parts of one item that several of the block's workers hold become one part (or the output).
     const int64_t size = part_floats(S::kRows * p.heads, D);
     auto goes_on = [&](int w) {  // worker w begins inside an item
@@ -774,7 +781,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
         __syncwarp();  // (the first part's numbers have been read)
         if (done) {
           const int row = x.k * S::kRows + r, col = column_of(p, row);
-          sum.finish(p, x.b, x.first + col, (x.h * p.heads + h) * p.group + row - col * p.group);
+          sum.template finish<kFreshShift>(p, x.b, x.first + col, (x.h * p.heads + h) * p.group + row - col * p.group);
         } else if (lane < RowSum<D>::kAcross) {
 #pragma unroll
           for (int z = 0; z < RowSum<D>::kWide; ++z)
@@ -791,11 +798,6 @@ __global__ void __launch_bounds__(S::kThreads, 1) paged_rows_kernel(const Attend
     if (record.parts > 0) record.parts = (static_cast<int>(threadIdx.x) + record.parts - 1) / p.workers + 1;
     p.records[worker0 + threadIdx.x] = record;
   }
-  if (sm.abort && threadIdx.x < p.workers && c.status != nullptr) {  // a wait gave up: all lanes of the block's units
-    Cursor x = sm.plan.from[threadIdx.x];
-    for (int64_t u = sm.plan.begin[threadIdx.x]; u < sm.plan.end[threadIdx.x]; ++u, Plan::next_unit(p, x))
-      c.status[x.b] = SPEC_ERR_TIMEOUT;
-  }
 }
 
 // Joins the parts of items that were split over thread blocks.  blockIdx.x: the worker that an item
@@ -810,6 +812,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttendPa
   __shared__ float2 stats[kWarps];
   griddep_wait();
   griddep_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0) settle_errors(p.c);
   const PartRecord record = p.records[blockIdx.x];
   if (record.parts < 2) return;
   const int first = record.first, count = record.count;
@@ -854,11 +857,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttendPa
               all.a[z].z = fmaf(b.z, f, all.a[z].z), all.a[z].w = fmaf(b.w, f, all.a[z].w);
             }
         }
-        all.finish(p, record.lane, first + col, head);
+        all.template finish<0>(p, record.lane, first + col, head);
       }
       __syncthreads();  // (sums and stats have been read)
     } else {
-      sum.finish(p, record.lane, first + col, head);
+      sum.template finish<0>(p, record.lane, first + col, head);
     }
   }
 }

@@ -76,9 +76,10 @@ struct Schedule {
     x.t1 = (x.hi + TILE - 1) / TILE;
     x.tile = x.t0;
   }
-  // The lane at x.b, if it has work, at its first item.
+  // The lane at x.b, if it has work and had not failed before the launch, at its first item.
   static __device__ __forceinline__ bool try_lane(const AttendParams& p, Cursor& x) {
-    if (!cache_lane(p.c, x.b, x.first, x.count, x.before) || x.count == 0) return false;
+    const bool failed = failed_before(p.c, x.b);
+    if (!cache_lane(p.c, x.b, x.first, x.count, x.before) || x.count == 0 || failed) return false;
     x.blocks = (x.count * p.group + ROWS - 1) / ROWS;
     x.h = x.k = 0;
     set_block(p, x);

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
   if (blockIdx.x == 0)  // lanes laid out wrongly have no units
     for (int b = threadIdx.x; b < c.lanes; b += kTileThreads) {
       int first, count, before;
-      if (!cache_lane(c, b, first, count, before)) lane_failed(c, b, SPEC_ERR_LAYOUT);
+      if (!cache_lane(c, b, first, count, before)) lane_fails_now(c, b, SPEC_ERR_LAYOUT);
     }
   const uint32_t tm = sm.tmem;
   const int64_t begin = sm.plan.begin[0], end = sm.plan.end[0];
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
       }
       tc_fence_before();
       if (whole) {
-        if (!fine) lane_failed(c, b_done, SPEC_ERR_NONFINITE);
+        if (!fine) lane_fails_now(c, b_done, SPEC_ERR_NONFINITE);
         if (on && p.lse != nullptr) p.lse[row_done * p.lse_row + head] = (top + log2f(sum)) * kLn2;
       } else {
         part[S::kRows * D + 2 * (w * 128 + row)] = top;
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
             ev = c.v_exps[e];
           }
         } else {
-          lane_failed(c, at.b, SPEC_ERR_LAYOUT);
+          lane_fails_now(c, at.b, SPEC_ERR_LAYOUT);
         }
       }
     };
@@ -673,10 +673,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_tile_kernel(const Atten
   }
   __syncthreads();
   // A wait gave up: all lanes of the block's range.
-  if (sm.abort && threadIdx.x == 0) {
+  if (sm.abort && threadIdx.x == 0 && c.status != nullptr) {
     Cursor x = sm.plan.from[0];
-    for (int64_t u = begin; u < end; ++u, Plan::next_unit(p, x))
-      if (c.status != nullptr) c.status[x.b] = SPEC_ERR_TIMEOUT;
+    for (int64_t u = begin; u < end; ++u, Plan::next_unit(p, x)) lane_fails_now(c, x.b, SPEC_ERR_TIMEOUT);
   }
   tc_fence_after();
   if (warp == 16) tmem_dealloc(tm, 512);
