@@ -67,7 +67,8 @@ typedef struct {
   int64_t table_stride;
   const int32_t* cached_lens;  /* [lanes] */
   /* Lane b owns rows row_offsets[b] .. row_offsets[b + 1] - 1 (none: nothing to do).
-   * [lanes + 1], ascending, within 0..rows. */
+   * [lanes + 1], ascending, within 0..rows.  (Where they are not, each lane goes by its own two; what a row
+   * of two lanes is given, is one of theirs.) */
   const int32_t* row_offsets;
   /* Read and updated in place (to be read when the call's work is done), may be NULL: a lane whose
    * status, one of spec_verify.h's, is not SPEC_OK on entry is left out, and its status stays.  Otherwise a

@@ -32,8 +32,7 @@ struct CacheRowsParams {
   int32_t rows_per_cta;
 };
 
-// The row's lane, by bisection of the offsets (which may be in no order at all: then
-// whatever is found does not hold the row, or is laid out rightly for it).
+// The row's lane, by bisection of offsets that ascend.
 __device__ __forceinline__ int lane_of_row(const CacheParams& c, int row) {
   int lo = 0, hi = c.lanes;  // offsets[lo] <= row < offsets[hi], in good order
   while (hi - lo > 1) {
@@ -100,18 +99,27 @@ __device__ __forceinline__ void store_fours(uint8_t* to, const float (&x)[8], in
   }
 }
 
-// GROUP threads a head (dim <= 8 * GROUP).  WRITE: rows to slots; otherwise slots to rows.
+// GROUP threads a head (dim <= 8 * GROUP).  WRITE: rows to slots; otherwise slots to rows.  (Registers as for one
+// pass over the rows: the loop over lanes alone would take 48 instead of 40, and a write 6 % longer.)
 template <typename T, int TYPE, int GROUP, bool WRITE>
-__global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRowsParams p) {
+__global__ void __launch_bounds__(kRowThreads, WRITE ? 12 : 16) cache_rows_kernel(const CacheRowsParams p) {
   const CacheParams& c = p.c;
   __shared__ int64_t slot_at[kRowsMost], exp_at[kRowsMost];
   __shared__ int lane_at[kRowsMost];  // -1: nothing to do
+  __shared__ volatile int turn;       // the next lane, where lanes take turns; -1: they do not
+  if (threadIdx.x == 0) turn = -1;
   griddep_wait();
   griddep_launch_dependents();
   const int row0 = blockIdx.x * p.rows_per_cta;
   const int mine = min(p.rows_per_cta, c.rows - row0);
-  if (static_cast<int>(threadIdx.x) < mine) {
-    const int row = row0 + threadIdx.x, b = lane_of_row(c, row);
+  // A row has one lane at most where offsets ascend.  Where some descend, the lanes are gone through one after
+  // the other, each by its own.
+  bool descend = false;
+  if (threadIdx.x >= kRowsMost)  // (by the threads that look no row up)
+#pragma unroll 1
+    for (int b = threadIdx.x - kRowsMost; b < c.lanes; b += kRowThreads - kRowsMost)
+      descend |= __ldg(c.offsets + b) > __ldg(c.offsets + b + 1);
+  auto look_up = [&](int row, int b) {
     int first, count, before, lane = -1;
     int64_t at = 0, ea = 0;
     if (cache_lane(c, b, first, count, before) && row >= first && row < first + count &&
@@ -129,129 +137,144 @@ __global__ void __launch_bounds__(kRowThreads) cache_rows_kernel(const CacheRows
     lane_at[threadIdx.x] = lane;
     slot_at[threadIdx.x] = at;
     exp_at[threadIdx.x] = ea;
-  }
+  };
+  if (static_cast<int>(threadIdx.x) < mine) look_up(row0 + threadIdx.x, lane_of_row(c, row0 + threadIdx.x));
   // Lanes laid out wrongly own no row for certain: the first CTA looks at all of them.
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < c.lanes; b += kRowThreads) {
       int first, count, before;
       if (!cache_lane(c, b, first, count, before)) lane_failed(c, b, SPEC_ERR_LAYOUT);
     }
-  __syncthreads();
+  if (__syncthreads_or(descend)) {
+    if (threadIdx.x < kRowsMost) lane_at[threadIdx.x] = -1;
+    if (threadIdx.x == 0) turn = 0;
+    __syncthreads();
+  }
   const int unit = threadIdx.x % GROUP, heads = mine * c.kv_heads;
   const int d = sizeof(T) == 4 ? 4 * unit : 8 * unit, e = sizeof(T) == 4 ? d + 4 * GROUP : d + 4;
 #pragma unroll 1
-  for (int base = 0; base < heads; base += kRowThreads / GROUP) {
-    const int i = base + threadIdx.x / GROUP;
-    const int r = i / c.kv_heads, h = i - r * c.kv_heads;
-    const int b = i < heads ? lane_at[r] : -1;
-    const bool on_d = b >= 0 && d < c.dim, on_e = b >= 0 && e < c.dim;
-    const int64_t at = b < 0 ? 0 : slot_at[r] + h * c.head;
-    const int64_t ea = b < 0 ? 0 : exp_at[r] + h * c.exp_head;
-    uint8_t* const kr = p.k + (row0 + r) * p.k_row + h * p.k_head;
-    uint8_t* const vr = p.v + (row0 + r) * p.v_row + h * p.v_head;
-    float x[2][8];
-    if constexpr (WRITE) {
-      load_fours<T>(x[0], kr, d, e, on_d, on_e);
-      load_fours<T>(x[1], vr, d, e, on_d, on_e);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        uint8_t* const to = (s ? c.v : c.k) + at;
-        // Magnitudes order as their bits, NaN above all.
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
-        bool bad;
-        if constexpr (TYPE == SPEC_CACHE_BF16) {
-          bad = top > 0x7F7F7FFFu;  // rounds to an infinity in bf16, or is one or NaN (what is not there is 0)
-          const uint2 lo = make_uint2(to_bf16x2(x[s][0], x[s][1]), to_bf16x2(x[s][2], x[s][3]));
-          const uint2 hi = make_uint2(to_bf16x2(x[s][4], x[s][5]), to_bf16x2(x[s][6], x[s][7]));
-          if constexpr (sizeof(T) == 4) {
-            if (on_d) *reinterpret_cast<uint2*>(to + 2 * d) = lo;
-            if (on_e) *reinterpret_cast<uint2*>(to + 2 * e) = hi;
-          } else if (on_d) {
-            *reinterpret_cast<uint4*>(to + 2 * d) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-          }
-        } else {
-#pragma unroll
-          for (int z = 1; z < GROUP; z <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, z));
-          const uint32_t byte = exponent_byte<TYPE>(top);
-          const float inverse = __uint_as_float((254u - (byte == 255u ? 127u : byte)) << 23);
-          uint32_t w[2];
-          if constexpr (TYPE == SPEC_CACHE_E4M3) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              w[j] = to_e4m3x2(x[s][4 * j] * inverse, x[s][4 * j + 1] * inverse) |
-                     to_e4m3x2(x[s][4 * j + 2] * inverse, x[s][4 * j + 3] * inverse) << 16;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t y[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) y[z] = static_cast<uint32_t>(__float2int_rn(x[s][4 * j + z] * inverse)) & 255u;
-              w[j] = y[0] | y[1] << 8 | y[2] << 16 | y[3] << 24;
-            }
-          }
-          if constexpr (sizeof(T) == 4) {
-            if (on_d) *reinterpret_cast<uint32_t*>(to + d) = w[0];
-            if (on_e) *reinterpret_cast<uint32_t*>(to + e) = w[1];
-          } else if (on_d) {
-            *reinterpret_cast<uint2*>(to + d) = make_uint2(w[0], w[1]);
-          }
-          if (on_d && unit == 0) (s ? c.v_exps : c.k_exps)[ea] = static_cast<uint8_t>(byte);
-          bad = byte == 255u && b >= 0 && unit == 0;
-        }
-        if (bad) lane_failed(c, b, SPEC_ERR_NONFINITE);
-      }
-    } else {
-      if constexpr (TYPE == SPEC_CACHE_BF16) {
+  for (;;) {
+#pragma unroll 1
+    for (int base = 0; base < heads; base += kRowThreads / GROUP) {
+      const int i = base + threadIdx.x / GROUP;
+      const int r = i / c.kv_heads, h = i - r * c.kv_heads;
+      const int b = i < heads ? lane_at[r] : -1;
+      const bool on_d = b >= 0 && d < c.dim, on_e = b >= 0 && e < c.dim;
+      const int64_t at = b < 0 ? 0 : slot_at[r] + h * c.head;
+      const int64_t ea = b < 0 ? 0 : exp_at[r] + h * c.exp_head;
+      uint8_t* const kr = p.k + (row0 + r) * p.k_row + h * p.k_head;
+      uint8_t* const vr = p.v + (row0 + r) * p.v_row + h * p.v_head;
+      float x[2][8];
+      if constexpr (WRITE) {
+        load_fours<T>(x[0], kr, d, e, on_d, on_e);
+        load_fours<T>(x[1], vr, d, e, on_d, on_e);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const uint8_t* const from = (s ? c.v : c.k) + at;
-          uint4 a = make_uint4(0u, 0u, 0u, 0u);
-          if constexpr (sizeof(T) == 4) {
-            if (on_d) *reinterpret_cast<uint2*>(&a.x) = __ldcs(reinterpret_cast<const uint2*>(from + 2 * d));
-            if (on_e) *reinterpret_cast<uint2*>(&a.z) = __ldcs(reinterpret_cast<const uint2*>(from + 2 * e));
-          } else if (on_d) {
-            a = __ldcs(reinterpret_cast<const uint4*>(from + 2 * d));
+          uint8_t* const to = (s ? c.v : c.k) + at;
+          // Magnitudes order as their bits, NaN above all.
+          uint32_t top = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
+          bool bad;
+          if constexpr (TYPE == SPEC_CACHE_BF16) {
+            bad = top > 0x7F7F7FFFu;  // rounds to an infinity in bf16, or is one or NaN (what is not there is 0)
+            const uint2 lo = make_uint2(to_bf16x2(x[s][0], x[s][1]), to_bf16x2(x[s][2], x[s][3]));
+            const uint2 hi = make_uint2(to_bf16x2(x[s][4], x[s][5]), to_bf16x2(x[s][6], x[s][7]));
+            if constexpr (sizeof(T) == 4) {
+              if (on_d) *reinterpret_cast<uint2*>(to + 2 * d) = lo;
+              if (on_e) *reinterpret_cast<uint2*>(to + 2 * e) = hi;
+            } else if (on_d) {
+              *reinterpret_cast<uint4*>(to + 2 * d) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+          } else {
+#pragma unroll
+            for (int z = 1; z < GROUP; z <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, z));
+            const uint32_t byte = exponent_byte<TYPE>(top);
+            const float inverse = __uint_as_float((254u - (byte == 255u ? 127u : byte)) << 23);
+            uint32_t w[2];
+            if constexpr (TYPE == SPEC_CACHE_E4M3) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                w[j] = to_e4m3x2(x[s][4 * j] * inverse, x[s][4 * j + 1] * inverse) |
+                       to_e4m3x2(x[s][4 * j + 2] * inverse, x[s][4 * j + 3] * inverse) << 16;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                uint32_t y[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) y[z] = static_cast<uint32_t>(__float2int_rn(x[s][4 * j + z] * inverse)) & 255u;
+                w[j] = y[0] | y[1] << 8 | y[2] << 16 | y[3] << 24;
+              }
+            }
+            if constexpr (sizeof(T) == 4) {
+              if (on_d) *reinterpret_cast<uint32_t*>(to + d) = w[0];
+              if (on_e) *reinterpret_cast<uint32_t*>(to + e) = w[1];
+            } else if (on_d) {
+              *reinterpret_cast<uint2*>(to + d) = make_uint2(w[0], w[1]);
+            }
+            if (on_d && unit == 0) (s ? c.v_exps : c.k_exps)[ea] = static_cast<uint8_t>(byte);
+            bad = byte == 255u && b >= 0 && unit == 0;
           }
-          x[s][0] = bf16_lo(a.x), x[s][1] = bf16_hi(a.x), x[s][2] = bf16_lo(a.y), x[s][3] = bf16_hi(a.y);
-          x[s][4] = bf16_lo(a.z), x[s][5] = bf16_hi(a.z), x[s][6] = bf16_lo(a.w), x[s][7] = bf16_hi(a.w);
+          if (bad) lane_failed(c, b, SPEC_ERR_NONFINITE);
         }
       } else {
-        uint2 w[2] = {};
-        uint32_t byte[2] = {};
+        if constexpr (TYPE == SPEC_CACHE_BF16) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const uint8_t* const from = (s ? c.v : c.k) + at;
-          if constexpr (sizeof(T) == 4) {
-            if (on_d) w[s].x = __ldcs(reinterpret_cast<const uint32_t*>(from + d));
-            if (on_e) w[s].y = __ldcs(reinterpret_cast<const uint32_t*>(from + e));
-          } else {
-            w[s] = on_d ? __ldcs(reinterpret_cast<const uint2*>(from + d)) : make_uint2(0u, 0u);
+          for (int s = 0; s < 2; ++s) {
+            const uint8_t* const from = (s ? c.v : c.k) + at;
+            uint4 a = make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (sizeof(T) == 4) {
+              if (on_d) *reinterpret_cast<uint2*>(&a.x) = __ldcs(reinterpret_cast<const uint2*>(from + 2 * d));
+              if (on_e) *reinterpret_cast<uint2*>(&a.z) = __ldcs(reinterpret_cast<const uint2*>(from + 2 * e));
+            } else if (on_d) {
+              a = __ldcs(reinterpret_cast<const uint4*>(from + 2 * d));
+            }
+            x[s][0] = bf16_lo(a.x), x[s][1] = bf16_hi(a.x), x[s][2] = bf16_lo(a.y), x[s][3] = bf16_hi(a.y);
+            x[s][4] = bf16_lo(a.z), x[s][5] = bf16_hi(a.z), x[s][6] = bf16_lo(a.w), x[s][7] = bf16_hi(a.w);
           }
-          byte[s] = on_d ? (s ? c.v_exps : c.k_exps)[ea] : 0u;
-        }
+        } else {
+          uint2 w[2] = {};
+          uint32_t byte[2] = {};
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const float scale = byte[s] == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte[s] << 23);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t two = ((j < 2 ? w[s].x : w[s].y) >> (16 * (j & 1))) & 0xFFFFu;
-            if constexpr (TYPE == SPEC_CACHE_E4M3) {
-              const uint32_t hh = e4m3_to_half2(two);
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-              x[s][2 * j] = f.x * scale;
-              x[s][2 * j + 1] = f.y * scale;
+          for (int s = 0; s < 2; ++s) {
+            const uint8_t* const from = (s ? c.v : c.k) + at;
+            if constexpr (sizeof(T) == 4) {
+              if (on_d) w[s].x = __ldcs(reinterpret_cast<const uint32_t*>(from + d));
+              if (on_e) w[s].y = __ldcs(reinterpret_cast<const uint32_t*>(from + e));
             } else {
-              x[s][2 * j] = static_cast<float>(static_cast<int8_t>(two & 255u)) * scale;
-              x[s][2 * j + 1] = static_cast<float>(static_cast<int8_t>(two >> 8)) * scale;
+              w[s] = on_d ? __ldcs(reinterpret_cast<const uint2*>(from + d)) : make_uint2(0u, 0u);
+            }
+            byte[s] = on_d ? (s ? c.v_exps : c.k_exps)[ea] : 0u;
+          }
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const float scale = byte[s] == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte[s] << 23);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t two = ((j < 2 ? w[s].x : w[s].y) >> (16 * (j & 1))) & 0xFFFFu;
+              if constexpr (TYPE == SPEC_CACHE_E4M3) {
+                const uint32_t hh = e4m3_to_half2(two);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+                x[s][2 * j] = f.x * scale;
+                x[s][2 * j + 1] = f.y * scale;
+              } else {
+                x[s][2 * j] = static_cast<float>(static_cast<int8_t>(two & 255u)) * scale;
+                x[s][2 * j + 1] = static_cast<float>(static_cast<int8_t>(two >> 8)) * scale;
+              }
             }
           }
         }
+        store_fours<T>(kr, x[0], d, e, on_d, on_e);
+        store_fours<T>(vr, x[1], d, e, on_d, on_e);
       }
-      store_fours<T>(kr, x[0], d, e, on_d, on_e);
-      store_fours<T>(vr, x[1], d, e, on_d, on_e);
     }
+    const int next = turn;
+    if (next < 0) break;
+    __syncthreads();
+    if (next == c.lanes) break;
+    if (static_cast<int>(threadIdx.x) < mine) look_up(row0 + threadIdx.x, next);
+    if (threadIdx.x == 0) turn = next + 1;
+    __syncthreads();
   }
 }
 
