@@ -162,8 +162,9 @@ uint64_t spec_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int32
  * Scores, sums and the output's sum are fp32; the weights enter the second product
  * rounded to bf16 (8-bit caches: with the value's 2^e to fp16, off by 2^-11 of their own or, with many
  * columns, 2^-25 of the row's largest, 2^-32 with few), the output is rounded once more.
- * SPEC_ERR_NONFINITE for a lane with an output that is not finite, as when a query, or a
- * key or value that one of its columns sees, is not.  SPEC_ERR_TIMEOUT: a bounded wait gave up.
+ * SPEC_ERR_NONFINITE for a lane with an output that is not finite, as when a query, or a value that one of its
+ * columns sees, is not, or a key that makes a score NaN or +inf.  (A score of -inf is no error: its position
+ * weighs nothing.)  SPEC_ERR_TIMEOUT: a bounded wait gave up.
  *
  * Errors: SPEC_ERR_INVALID_ARG as above, for q_heads that are no multiple of kv_heads, a
  * negative window or max_context or a misaligned workspace; SPEC_ERR_CUDA if a launch fails.
