@@ -7,8 +7,9 @@
 // It is bound by HBM.  Measured (device time): a lane of 40,001 tokens from int8 to fp32, 410 MB, 65
 // us, 6.3 TB/s, 0.93 of the copy rate (83 us with each thread's fp32 numbers side by side: stores of 16
 // bytes at every 32); 24 prompts of 0 to 3000 tokens in bf16 into e4m3 slots and back, 496 MB in two calls,
-// 91 us, 5.5 TB/s (95 with CTAs of 256 threads, two rounds of loads at a time; 146 with four,
-// whose registers cost too many CTAs); one row there and back 4.9 us, two launches.
+// 94 us, 5.3 TB/s (4 % more with CTAs of 256 threads, two rounds of loads at a time; 60 % with four,
+// whose registers cost too many CTAs), into bf16 slots and back, 660 MB, 107 us, 6.2 TB/s; one row there
+// and back 5.1 us, two launches.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -16,11 +16,11 @@
 // a 128-row tile of the large tensor cores, and what they save is not short.
 //
 // Measured (device time, heads of 128): one lane of 131,000 tokens, 8 cache heads in bf16, 537 MB,
-// 93 us, 5.8 TB/s, 0.85 of the copy rate; 64 lanes of up to 8,192 tokens in int8, 514 MB, 108 us, 4.8 TB/s
-// (in bf16 165 us, 6.2 TB/s): without the arithmetic 92 of 93, 92 of 108 and 160 of 165 us are left.  8
-// lanes x 8 columns of 4 heads a cache head (32 rows) in e4m3 75 us (56 without arithmetic: 32 rows' products
-// and conversions take 5,300 cycles a unit, its copies at the HBM rate 2,800); 64 lanes x 1 to 4 columns of 8 heads of
-// 64 through a window of 1,000 36 us (31): ten of copies, the rest begins, ends and joins items; one
+// 92 us, 5.8 TB/s, 0.86 of the copy rate; 64 lanes of up to 8,192 tokens in int8, 514 MB, 109 us, 4.7 TB/s
+// (in bf16 162 us, 6.3 TB/s): without the arithmetic 92, 92 and 160 us are left.  8
+// lanes x 8 columns of 4 heads a cache head (32 rows) in e4m3 77 us (56 without arithmetic: 32 rows' products
+// and conversions take 5,300 cycles a unit, its copies at the HBM rate 2,800), in bf16 78; 64 lanes x 1 to 4 columns
+// of 8 heads of 64 through a window of 1,000 37 us (31): ten of copies, the rest begins, ends and joins items; one
 // lane of 1,500 tokens 12 us: a chain of latencies, and of fetching code (some 110 cycles for each 128
 // bytes that a launch runs first), which is why inner loops are short.
 // Four copying warps for eight that compute, sums joined through shared memory at each item's end:
@@ -131,7 +131,8 @@ struct RowsShape {
   static constexpr int kWarps = D > 128 ? 4 : 8;  // that compute; as many copy
   static constexpr int kThreads = 64 * kWarps;
   // Registers a thread, and what a launch must bring (0: they are not shared out).
-  // (8 x 8 columns over e4m3: 82 us with 192 and 64 for both types; bf16 76 us, with 200 and 56 79)
+  // (8 x 8 columns: over e4m3 83 us with 192 and 64, 77 with 200 and 56; over bf16 78 and 77, but 8 x 4 64.6
+  // and 65.1, one lane 11.9 and 12.1)
   static constexpr int kRegsRows = kWarps != 8 ? 0 : kEight ? 200 : 192, kRegsCopy = kWarps != 8 ? 0 : kEight ? 56 : 64;
   static constexpr int kRegs = kWarps / 4 * (kRegsRows + kRegsCopy);
   static constexpr int kTokens = kEight || D <= 64 ? 32 : 16;  // of a unit
@@ -147,8 +148,8 @@ struct RowsShape {
   static constexpr int kPlaces = kFit > 12 ? 12 : kFit;
   static constexpr int kExtra = 1;  // an item's beginning and end, in units
   static_assert(kPlaces >= 4, "the ring holds two units at least");
-  // (a worker takes two units at least: one lane of 1,500 tokens 11.7 us, with four 13.7; 8 x 8 columns of e4m3
-  // behind 1,000 tokens 31 us against 42)
+  // (a worker takes two units at least: one lane of 1,500 tokens 11.9 us, with four 14.2; 8 x 8 columns of e4m3
+  // behind 1,000 tokens 30 us against 40)
   using Plan = Schedule<kRows, kTokens, kExtra, 2>;
 };
 

@@ -22,19 +22,20 @@
 // for eight copying warps, which 8-bit caches need (four took 5,800 cycles a step).
 //
 // Measured (device time): 2,048 tokens behind 30,000, 32 heads of 128 for 8 of a bf16 cache, 730 to 745 us, 1.4
-// PFLOP/s, 0.75 of a library product's rate (801 in a row of calls that the power limit slows), in
-// e4m3 868; 12 prompts of 0 to 1,500 tokens behind 0 to 3,000, 16 heads for 2 in e4m3, 244 us (in bf16
-// 216): short items, whose beginnings and ends do not overlap as their steps do.  A step of two tiles
-// takes 2,900 cycles (8-bit caches: 3,900) where the products take 2,048: waits between scores, weights and the
+// PFLOP/s, 0.75 of a library product's rate (801 to 812, 0.69, in a row of calls that the power limit slows), in
+// e4m3 890; 12 prompts of 0 to 1,500 tokens behind 0 to 3,000, 16 heads for 2 in e4m3, 255 us (in bf16
+// 218): short items, whose beginnings and ends do not overlap as their steps do.  A step of two tiles
+// takes 2,900 cycles (8-bit caches: 4,000) where the products take 2,048: waits between scores, weights and the
 // second product, and 57 % of the issue slots in use.  Whole rows of scores in registers, and four copying
-// warps: 718 us in bf16, but 1,341 in e4m3 and 304 for the 12 prompts.
+// warps, took 718 us in bf16, but 1,341 in e4m3 (868 then) and 304 for the 12 prompts (244).
 //
 // 8-bit caches become fp16 on the way to shared memory, times 2^(e - r) with r the largest of a warp's 32
 // exponents, and q becomes fp16 times a power of two for each row.  2^r multiplies the keys' scores; the
 // values' r goes into the weights' exponents and out of their sum.  All of it is exact: keys' exponents may be
 // 15 below r (e4m3's least number is then fp16's, 2^-24), and values' 7, so that M, which r enters, takes no
 // more than that off the small weights.  A group of 32 positions with larger differences is taken apart: its
-// numbers come as they are, and each score gets its own position's exponents, as in the few rows' kernel.
+// numbers come as they are, and each score gets its own position's exponents, as in the few rows' kernel.  (With
+// every group taken apart 2,048 tokens behind 30,000 take 4,050 us; activations have hardly any such group.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -64,7 +65,7 @@ struct TileShape {
   static constexpr int kRows = 256, kTile = 128;
   static constexpr int kBytes = kTileHalf * (D / 64);
   static constexpr int kStages = D > 64 ? 5 : 8;
-  static constexpr int kExtra = 4;  // an item's beginning and end, in units (12 e4m3 prompts: 364 us with 1, 319 with 2, 301 with 4, 314 with 7)
+  static constexpr int kExtra = 4;  // an item's beginning and end, in units (12 e4m3 prompts: 323 us with 1, 282 with 2, 255 with 4, 257 with 7)
   using Plan = Schedule<kRows, kTile, kExtra, 1, 1>;
   // Steps whose exponents are held.  A step's are written when its keys' place in the ring is free: five places
   // before it lie the values of the third step back, eight before it the keys of the fourth, whose scores follow
